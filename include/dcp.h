@@ -394,6 +394,80 @@ dcp_status_t dcp_mla_decode_partial_noalloc(
     float* O_part, float* lse_part,
     int32_t* dev_error, void* stream);
 
+/*
+ * The general form of dcp_decode_concat_cache: the latent rows are written
+ * into a bf16 or an FP8 E4M3 cache, with the decode query or without it (a
+ * prefill's tokens) ["perf(mla): fuse K3 DCP verification queries", review
+ * follow-up: fp8 KV verify plans].
+ *
+ *   kv_dtype     DCP_KV_BF16: kv_cache bf16 [num_slots, 576], kv_scale is not
+ *                used.  DCP_KV_FP8_E4M3: kv_cache uint8 codes [num_slots, 576]
+ *                and kv_scale fp32 [num_slots] (required, else
+ *                DCP_ERR_INVALID_ARG).  Other values: DCP_ERR_UNSUPPORTED_DTYPE.
+ *                A written slot gets, from its row x = [kv_c | k_pe],
+ *                  scale = 2^e, the least power of two with
+ *                          max |x_i| <= 256 * scale (over the finite x_i; 1
+ *                          when they are all zero),
+ *                  code_i = x_i / scale rounded to the nearest E4M3 value,
+ *                          ties to even (x_i / scale is exact); NaN and
+ *                          infinities give the NaN code.
+ *                Scales that are powers of two make the decode's widening to
+ *                bf16 exact.
+ *   H            0 writes the cache alone; then ql_nope, q_pe and q_out must
+ *                be NULL and their strides are not used.
+ * Everything else as for dcp_decode_concat_cache.
+ */
+dcp_status_t dcp_decode_concat_cache_v2(
+    const void* ql_nope, int64_t ql_nope_stride_tok, int64_t ql_nope_stride_head,
+    const void* q_pe, int64_t q_pe_stride_tok, int64_t q_pe_stride_head,
+    const void* kv_c, int64_t kv_c_stride_tok,
+    const void* k_pe, int64_t k_pe_stride_tok,
+    const int64_t* slot_mapping, int32_t T, int32_t H,
+    void* q_out, int64_t q_out_stride_tok,
+    void* kv_cache, dcp_kv_dtype_t kv_dtype, float* kv_scale, int64_t num_slots,
+    int32_t* dev_error, void* stream);
+
+/*
+ * Reads context ranges of the requests back out of the paged cache, as dense
+ * rows: what a prefill over a cached prefix attends to, or what moves to
+ * another cache.  (The pages' prefill side gathers its context this way; its
+ * form is not on them.)
+ *
+ * For request b and cu_lens[b] <= n < cu_lens[b + 1], output row n is the
+ * latent row of position p = seq_starts[b] + n - cu_lens[b]:
+ *   out[n, 0:576] = kv(p)   (bf16 cache: a copy, or widened to fp32;
+ *                            fp8 cache: code x scale in fp32, rounded to
+ *                            nearest even for a bf16 output)
+ * with kv(p) found as in the decode.  Rows of positions that shards outside
+ * [shard_begin, shard_begin + shard_count) own are zeros, so that the outputs
+ * of DCP ranks add up to the whole.  Output rows before cu_lens[0] or from
+ * cu_lens[B] on are left as they are.  A position that has no table column, a
+ * negative one, or a block id outside the cache gives a zero row and sets
+ * DCP_DEVERR_BAD_BLOCK in *dev_error.
+ *
+ *   kv_cache, kv_dtype, kv_scale, num_blocks, block_size, block_table,
+ *   bt_width, bt_stride, per_shard_tables, bt_shard_stride, D, interleave,
+ *   shard_begin, shard_count
+ *                as for dcp_mla_decode_partial_v2.
+ *   seq_starts   int32 [B], first position of each request's range; NULL: 0.
+ *   cu_lens      int32 [B + 1], non-decreasing: output row offsets.
+ *   B, N         requests, and rows of `out` (cu_lens[B] <= N; rows past N
+ *                are not written).
+ *   out          bf16 or fp32 [N, 576], rows out_stride elements apart
+ *                (>= 576, whole 16-byte units), 16-byte aligned; must not
+ *                overlap the cache.
+ * B == 0 or N == 0 returns DCP_OK without launching anything.
+ */
+dcp_status_t dcp_latent_cache_read(
+    const void* kv_cache, dcp_kv_dtype_t kv_dtype, const float* kv_scale,
+    int32_t num_blocks, int32_t block_size,
+    const int32_t* block_table, int32_t bt_width, int64_t bt_stride,
+    int32_t per_shard_tables, int64_t bt_shard_stride,
+    int32_t D, int32_t interleave, int32_t shard_begin, int32_t shard_count,
+    const int32_t* seq_starts, const int32_t* cu_lens, int32_t B, int64_t N,
+    void* out, dcp_dtype_t out_dtype, int64_t out_stride,
+    int32_t* dev_error, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,6 +11,7 @@ The library is loaded on first use; if it has not been built the call raises
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -70,6 +71,12 @@ EXPORTS = [
     ("dcp_mla_decode_partial_noalloc", ctypes.c_int,
      [_P, _I64, _P, _I32, _I32, _P, _I32, _I64, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F,
       _P, _P, _P, _P]),
+    ("dcp_decode_concat_cache_v2", ctypes.c_int,
+     [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _I32, _I32, _P, _I64, _P, ctypes.c_int, _P, _I64, _P,
+      _P]),
+    ("dcp_latent_cache_read", ctypes.c_int,
+     [_P, ctypes.c_int, _P, _I32, _I32, _P, _I32, _I64, _I32, _I64, _I32, _I32, _I32, _I32, _P, _P, _I32, _I64, _P,
+      ctypes.c_int, _I64, _P, _P]),
 ]
 
 _lib = None
@@ -443,6 +450,139 @@ def dcp_decode_concat_cache(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q_out, kv_c
     _check(st, "dcp_decode_concat_cache")
 
 
+def _same_device(device, **tensors):
+    """A context in which `device` is the current one (the library launches on
+    the current device); tensors elsewhere are refused."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s is on %s, kv_cache on %s" % (name, t.device, device))
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _cache_format(kv_cache, kv_scale):
+    """Check a paged cache [num_blocks, block_size, 576] (bf16, or uint8 FP8
+    E4M3 codes with kv_scale fp32 [num_blocks, block_size]) and return
+    whether it is FP8."""
+    if not isinstance(kv_cache, torch.Tensor) or kv_cache.dtype not in (torch.bfloat16, torch.uint8):
+        raise TypeError("kv_cache must be a bfloat16 or uint8 (FP8 E4M3 codes) tensor")
+    if kv_cache.dim() != 3 or kv_cache.shape[2] != KV_DIM:
+        raise ValueError("kv_cache must be [num_blocks, block_size, 576]")
+    fp8 = kv_cache.dtype == torch.uint8
+    if fp8:
+        if not isinstance(kv_scale, torch.Tensor) or kv_scale.dtype != torch.float32:
+            raise TypeError("an FP8 kv_cache needs kv_scale, a float32 tensor")
+        if tuple(kv_scale.shape) != tuple(kv_cache.shape[:2]):
+            raise ValueError("kv_scale must be [num_blocks, block_size]")
+    elif kv_scale is not None:
+        raise ValueError("kv_scale is given for a bf16 kv_cache")
+    return fp8
+
+
+def dcp_decode_concat_cache_v2(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q_out, kv_cache, *,
+                               kv_scale: Optional[torch.Tensor] = None, dev_error: Optional[torch.Tensor] = None,
+                               stream=None) -> None:
+    """The general form of dcp_decode_concat_cache: kv_cache bf16, or uint8 FP8
+    E4M3 codes with kv_scale fp32 [num_blocks, block_size] (each written row
+    gets its own power-of-two scale).  ql_nope, q_pe and q_out may all be None
+    to write the cache alone."""
+    query = ql_nope is not None or q_pe is not None or q_out is not None
+    args = [("kv_c", kv_c, 2, LATENT_DIM), ("k_pe", k_pe, 2, ROPE_DIM)]
+    if query:
+        args += [("ql_nope", ql_nope, 3, LATENT_DIM), ("q_pe", q_pe, 3, ROPE_DIM), ("q_out", q_out, 3, KV_DIM)]
+    for name, t, dims, last in args:
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+            raise TypeError("%s must be a %s tensor" % (name, torch.bfloat16))
+        if t.dim() != dims or t.shape[-1] != last or t.stride(-1) != 1:
+            raise ValueError("%s must have %d dims, last of size %d with unit stride" % (name, dims, last))
+    T = kv_c.shape[0]
+    H = ql_nope.shape[1] if query else 0
+    if k_pe.shape[0] != T or (query and (tuple(ql_nope.shape[:2]) != (T, H) or tuple(q_pe.shape[:2]) != (T, H))):
+        raise ValueError("ql_nope, q_pe, kv_c and k_pe disagree on T or H")
+    if query and (H < 1 or tuple(q_out.shape[:2]) != (T, H) or (H > 1 and q_out.stride(1) != KV_DIM)):
+        raise ValueError("q_out must be [T, H, 576] with dense heads")
+    if not isinstance(slot_mapping, torch.Tensor) or slot_mapping.dtype != torch.int64 or \
+            tuple(slot_mapping.shape) != (T,):
+        raise ValueError("slot_mapping must be an int64 [T] tensor")
+    fp8 = _cache_format(kv_cache, kv_scale)
+    for name, t, _, _ in args:
+        _need(t, name, torch.bfloat16, contiguous=False)
+    _need(slot_mapping, "slot_mapping", torch.int64)
+    _need(kv_cache, "kv_cache", kv_cache.dtype)
+    if fp8:
+        _need(kv_scale, "kv_scale", torch.float32)
+    _need_opt(dev_error, "dev_error", torch.int32)
+    guard = _same_device(kv_cache.device, kv_c=kv_c, k_pe=k_pe, ql_nope=ql_nope, q_pe=q_pe, q_out=q_out,
+                         slot_mapping=slot_mapping, kv_scale=kv_scale, dev_error=dev_error)
+    if T == 0:
+        return
+
+    def step(t, dim):  # the stride of a dimension of one element is never used
+        return t.stride(dim) if t is not None and t.shape[dim] > 1 else 0
+    q_step = H * KV_DIM if T == 1 else step(q_out, 0)
+    with guard, _Range("dcp_decode_concat_cache_v2"):
+        st = lib().dcp_decode_concat_cache_v2(
+            _ptr(ql_nope), step(ql_nope, 0), step(ql_nope, 1), _ptr(q_pe), step(q_pe, 0), step(q_pe, 1), _ptr(kv_c),
+            step(kv_c, 0), _ptr(k_pe), step(k_pe, 0), _ptr(slot_mapping), T, H, _ptr(q_out), q_step,
+            _ptr(kv_cache), KV_FP8_E4M3 if fp8 else KV_BF16, _ptr(kv_scale),
+            kv_cache.shape[0] * kv_cache.shape[1], _ptr(dev_error), _stream(stream))
+    _check(st, "dcp_decode_concat_cache_v2")
+
+
+def dcp_latent_cache_read(kv_cache, block_table, cu_lens, out, *, seq_starts: Optional[torch.Tensor] = None,
+                          kv_scale: Optional[torch.Tensor] = None, D: int = 1, interleave: int = 1,
+                          shard_begin: int = 0, shard_count: Optional[int] = None,
+                          dev_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Read context ranges back out of the paged cache (bf16, or uint8 FP8
+    E4M3 codes with kv_scale): out bf16 or fp32 [N, 576] (rows may be strided)
+    gets request b's positions seq_starts[b] + i in rows cu_lens[b] + i.
+    block_table is [B, W] or per-shard [shard_count, B, W]; rows of positions
+    that other shards own are zeros, rows past cu_lens[B] are left alone."""
+    if shard_count is None:
+        shard_count = D - shard_begin
+    fp8 = _cache_format(kv_cache, kv_scale)
+    ints = [("block_table", block_table), ("cu_lens", cu_lens)] + \
+        ([("seq_starts", seq_starts)] if seq_starts is not None else [])
+    for name, t in ints:
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+            raise TypeError("%s must be an int32 tensor" % name)
+    if not isinstance(out, torch.Tensor) or out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out must be a bfloat16 or float32 tensor")
+    if out.dim() != 2 or out.shape[1] != KV_DIM or out.stride(1) != 1:
+        raise ValueError("out must be [N, 576] with unit column stride")
+    if cu_lens.dim() != 1 or cu_lens.shape[0] < 1:
+        raise ValueError("cu_lens must be [B + 1]")
+    B, N = cu_lens.shape[0] - 1, out.shape[0]
+    local = block_table.dim() == 3
+    if block_table.dim() not in (2, 3) or block_table.stride(-1) != 1 or block_table.shape[-2] != B or \
+            (local and block_table.shape[0] != shard_count):
+        raise ValueError("block_table must be [B, W] or [shard_count, B, W] with unit column stride")
+    if seq_starts is not None and tuple(seq_starts.shape) != (B,):
+        raise ValueError("seq_starts must be [B]")
+    if D < 1 or D > MAX_SHARDS or shard_begin < 0 or shard_count < 1 or shard_begin + shard_count > D:
+        raise ValueError("shards [shard_begin, shard_begin + shard_count) must lie in [0, D), D <= %d" % MAX_SHARDS)
+    _need(kv_cache, "kv_cache", kv_cache.dtype)
+    if fp8:
+        _need(kv_scale, "kv_scale", torch.float32)
+    for name, t in ints:
+        _need(t, name, torch.int32, contiguous=name != "block_table")
+    _need(out, "out", out.dtype, contiguous=False)
+    _need_opt(dev_error, "dev_error", torch.int32)
+    guard = _same_device(kv_cache.device, kv_scale=kv_scale, out=out, dev_error=dev_error, **dict(ints))
+    if B == 0 or N == 0:
+        return
+    with guard, _Range("dcp_latent_cache_read"):
+        st = lib().dcp_latent_cache_read(
+            _ptr(kv_cache), KV_FP8_E4M3 if fp8 else KV_BF16, _ptr(kv_scale), kv_cache.shape[0], kv_cache.shape[1],
+            _ptr(block_table), block_table.shape[-1], block_table.stride(-2), 1 if local else 0,
+            block_table.stride(0) if local else 0, D, interleave, shard_begin, shard_count, _ptr(seq_starts),
+            _ptr(cu_lens), B, N, _ptr(out), DTYPE_F32 if out.dtype == torch.float32 else DTYPE_BF16,
+            out.stride(0) if N > 1 else KV_DIM,
+            _ptr(dev_error), _stream(stream))
+    _check(st, "dcp_latent_cache_read")
+
+
 # ----------------------------------------------------------------------------
 # allocating conveniences
 # ----------------------------------------------------------------------------
@@ -494,11 +634,39 @@ def lse_combine(O_part, lse_part, seq_lens, query_start_loc, out_dtype=torch.bfl
     return out, out_lse
 
 
-def decode_concat_cache(ql_nope, q_pe, kv_c, k_pe, slot_mapping, kv_cache, dev_error=None, stream=None):
+def decode_concat_cache(ql_nope, q_pe, kv_c, k_pe, slot_mapping, kv_cache, dev_error=None, stream=None,
+                        kv_scale: Optional[torch.Tensor] = None):
     """Allocating form: returns the decode query q bf16 [T, H, 576]; writes
-    the step's latent rows into kv_cache in place."""
+    the step's latent rows into kv_cache in place (bf16, or FP8 E4M3 codes and
+    their scales with kv_scale)."""
     T, H = ql_nope.shape[0], ql_nope.shape[1]
     q = torch.empty((T, H, KV_DIM), dtype=torch.bfloat16, device=ql_nope.device)
+    if kv_scale is not None:
+        dcp_decode_concat_cache_v2(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q, kv_cache, kv_scale=kv_scale,
+                                   dev_error=dev_error, stream=stream)
+        return q
     dcp_decode_concat_cache(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q, kv_cache, dev_error=dev_error,
                             stream=stream)
     return q
+
+
+def latent_cache_write(kv_c, k_pe, slot_mapping, kv_cache, kv_scale: Optional[torch.Tensor] = None, dev_error=None,
+                       stream=None) -> None:
+    """Write tokens' latent rows into the paged cache in place, without a
+    query (a prefill's tokens): kv_cache bf16, or FP8 E4M3 codes with
+    kv_scale."""
+    dcp_decode_concat_cache_v2(None, None, kv_c, k_pe, slot_mapping, None, kv_cache, kv_scale=kv_scale,
+                               dev_error=dev_error, stream=stream)
+
+
+def latent_cache_read(kv_cache, block_table, cu_lens, num_rows: int, seq_starts: Optional[torch.Tensor] = None,
+                      kv_scale: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, D: int = 1,
+                      interleave: int = 1, shard_begin: int = 0, shard_count: Optional[int] = None, dev_error=None,
+                      stream=None):
+    """Allocating form: returns out [num_rows, 576] of out_dtype, num_rows =
+    cu_lens[B] (known on the host; rows past cu_lens[B] are undefined)."""
+    out = torch.empty((num_rows, KV_DIM), dtype=out_dtype, device=kv_cache.device)
+    dcp_latent_cache_read(kv_cache, block_table, cu_lens, out, seq_starts=seq_starts, kv_scale=kv_scale, D=D,
+                          interleave=interleave, shard_begin=shard_begin, shard_count=shard_count,
+                          dev_error=dev_error, stream=stream)
+    return out

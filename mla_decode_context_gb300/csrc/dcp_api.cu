@@ -389,4 +389,82 @@ dcp_status_t dcp_decode_concat_cache(const void* ql_nope, int64_t ql_nope_stride
   return dcp::launch_concat_cache(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DCP_OK : DCP_ERR_CUDA;
 }
 
+dcp_status_t dcp_decode_concat_cache_v2(const void* ql_nope, int64_t ql_nope_stride_tok, int64_t ql_nope_stride_head,
+                                        const void* q_pe, int64_t q_pe_stride_tok, int64_t q_pe_stride_head,
+                                        const void* kv_c, int64_t kv_c_stride_tok, const void* k_pe,
+                                        int64_t k_pe_stride_tok, const int64_t* slot_mapping, int32_t T, int32_t H,
+                                        void* q_out, int64_t q_out_stride_tok, void* kv_cache,
+                                        dcp_kv_dtype_t kv_dtype, float* kv_scale, int64_t num_slots,
+                                        int32_t* dev_error, void* stream) {
+  if (T < 0 || H < 0 || num_slots < 1) return DCP_ERR_INVALID_ARG;
+  if (kv_dtype != DCP_KV_BF16 && kv_dtype != DCP_KV_FP8_E4M3) return DCP_ERR_UNSUPPORTED_DTYPE;
+  if (T == 0) return DCP_OK;
+  const bool fp8 = kv_dtype == DCP_KV_FP8_E4M3, query = H > 0;
+  if (!kv_c || !k_pe || !slot_mapping || !kv_cache || (fp8 && !kv_scale)) return DCP_ERR_INVALID_ARG;
+  if (query ? (!ql_nope || !q_pe || !q_out) : (ql_nope || q_pe || q_out)) return DCP_ERR_INVALID_ARG;
+  if (kv_c_stride_tok < 0 || k_pe_stride_tok < 0) return DCP_ERR_INVALID_ARG;
+  if (kv_c_stride_tok % 8 != 0 || k_pe_stride_tok % 8 != 0) return DCP_ERR_MISALIGNED;  // 16-byte units
+  if (!aligned16(kv_c) || !aligned16(k_pe) || !aligned16(kv_cache) || (fp8 && reinterpret_cast<uintptr_t>(kv_scale) % 4 != 0))
+    return DCP_ERR_MISALIGNED;
+  if (query) {
+    if (ql_nope_stride_tok < 0 || ql_nope_stride_head < 0 || q_pe_stride_tok < 0 || q_pe_stride_head < 0 ||
+        q_out_stride_tok < static_cast<int64_t>(H) * DCP_KV_DIM)
+      return DCP_ERR_INVALID_ARG;
+    const int64_t strides[] = {ql_nope_stride_tok, ql_nope_stride_head, q_pe_stride_tok, q_pe_stride_head,
+                               q_out_stride_tok};
+    for (int64_t st : strides)
+      if (st % 8 != 0) return DCP_ERR_MISALIGNED;
+    if (!aligned16(ql_nope) || !aligned16(q_pe) || !aligned16(q_out)) return DCP_ERR_MISALIGNED;
+  }
+  dcp::ConcatCacheArgs a{};
+  a.ql_nope = ql_nope; a.ql_nope_stride_tok = ql_nope_stride_tok; a.ql_nope_stride_head = ql_nope_stride_head;
+  a.q_pe = q_pe; a.q_pe_stride_tok = q_pe_stride_tok; a.q_pe_stride_head = q_pe_stride_head;
+  a.kv_c = kv_c; a.kv_c_stride_tok = kv_c_stride_tok;
+  a.k_pe = k_pe; a.k_pe_stride_tok = k_pe_stride_tok;
+  a.slot_mapping = slot_mapping;
+  a.T = T; a.H = H;
+  a.q_out = q_out; a.q_out_stride_tok = q_out_stride_tok;
+  a.kv_cache = kv_cache; a.num_slots = num_slots;
+  a.kv_scale = fp8 ? kv_scale : nullptr;
+  a.dev_error = dev_error;
+  return dcp::launch_concat_cache_v2(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DCP_OK : DCP_ERR_CUDA;
+}
+
+dcp_status_t dcp_latent_cache_read(const void* kv_cache, dcp_kv_dtype_t kv_dtype, const float* kv_scale,
+                                   int32_t num_blocks, int32_t block_size, const int32_t* block_table,
+                                   int32_t bt_width, int64_t bt_stride, int32_t per_shard_tables,
+                                   int64_t bt_shard_stride, int32_t D, int32_t interleave, int32_t shard_begin,
+                                   int32_t shard_count, const int32_t* seq_starts, const int32_t* cu_lens, int32_t B,
+                                   int64_t N, void* out, dcp_dtype_t out_dtype, int64_t out_stride,
+                                   int32_t* dev_error, void* stream) {
+  if (B < 0 || N < 0 || D < 1 || D > DCP_MAX_SHARDS || interleave < 1) return DCP_ERR_INVALID_ARG;
+  if ((kv_dtype != DCP_KV_BF16 && kv_dtype != DCP_KV_FP8_E4M3) ||
+      (out_dtype != DCP_DTYPE_F32 && out_dtype != DCP_DTYPE_BF16))
+    return DCP_ERR_UNSUPPORTED_DTYPE;
+  if (B == 0 || N == 0) return DCP_OK;
+  const bool fp8 = kv_dtype == DCP_KV_FP8_E4M3, f32 = out_dtype == DCP_DTYPE_F32;
+  if (!kv_cache || !block_table || !cu_lens || !out || (fp8 && !kv_scale)) return DCP_ERR_INVALID_ARG;
+  if (num_blocks < 1 || block_size < 1 || bt_width < 1 || bt_stride < bt_width || out_stride < DCP_KV_DIM)
+    return DCP_ERR_INVALID_ARG;
+  if (shard_begin < 0 || shard_count < 1 || shard_begin + static_cast<int64_t>(shard_count) > D) return DCP_ERR_INVALID_ARG;
+  if (per_shard_tables && shard_count > 1 && bt_shard_stride < static_cast<int64_t>(B - 1) * bt_stride + bt_width)
+    return DCP_ERR_INVALID_ARG;  // shards' tables would overlap
+  if (!aligned16(kv_cache) || !aligned16(out) || out_stride % (f32 ? 4 : 8) != 0) return DCP_ERR_MISALIGNED;
+  dcp::CacheReadArgs a{};
+  a.kv = kv_cache;
+  a.kv_scale = fp8 ? kv_scale : nullptr;
+  a.num_blocks = num_blocks; a.block_size = block_size;
+  a.block_table = block_table; a.bt_width = bt_width; a.bt_stride = bt_stride;
+  a.local_tables = per_shard_tables ? 1 : 0;
+  a.bt_shard_stride = per_shard_tables ? bt_shard_stride : 0;
+  a.D = D; a.I = interleave; a.d0 = shard_begin; a.Dn = shard_count;
+  a.div_I = dcp::make_fastdiv(interleave);
+  a.div_bs = dcp::make_fastdiv(block_size);
+  a.div_D = dcp::make_fastdiv(D);
+  a.seq_starts = seq_starts; a.cu_lens = cu_lens; a.B = B; a.N = N;
+  a.out = out; a.out_stride = out_stride; a.out_f32 = f32 ? 1 : 0;
+  a.dev_error = dev_error;
+  return dcp::launch_cache_read(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DCP_OK : DCP_ERR_CUDA;
+}
+
 }  // extern "C"

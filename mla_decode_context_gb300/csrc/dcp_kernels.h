@@ -125,11 +125,38 @@ struct ConcatCacheArgs {
   int32_t T, H;
   void* q_out;          // bf16 [T, H, 576]
   int64_t q_out_stride_tok;
-  void* kv_cache;       // bf16 [num_slots, 576]
+  void* kv_cache;       // bf16 [num_slots, 576], or (v2, kv_scale set) E4M3 codes
   int64_t num_slots;
   int32_t* dev_error;
+  float* kv_scale;      // v2 only: fp32 [num_slots] for an FP8 cache, else nullptr
 };
 cudaError_t launch_concat_cache(const ConcatCacheArgs& a, cudaStream_t st);
+// The general form: bf16 or FP8 cache; H == 0 writes the cache alone.
+cudaError_t launch_concat_cache_v2(const ConcatCacheArgs& a, cudaStream_t st);
+
+// Context ranges of the paged cache read back as dense rows (validated by
+// the C ABI).
+struct CacheReadArgs {
+  const void* kv;        // bf16 rows, or E4M3 codes when kv_scale is set
+  const float* kv_scale;
+  int32_t num_blocks, block_size;
+  const int32_t* block_table;
+  int32_t bt_width;
+  int64_t bt_stride;
+  int32_t local_tables;
+  int64_t bt_shard_stride;
+  int32_t D, I, d0, Dn;
+  FastDiv div_I, div_bs, div_D;
+  const int32_t* seq_starts;  // may be nullptr (0)
+  const int32_t* cu_lens;
+  int32_t B;
+  int64_t N;
+  void* out;
+  int64_t out_stride;  // elements between output rows
+  int32_t out_f32;
+  int32_t* dev_error;
+};
+cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t st);
 
 // Tensor-core decode (tcgen05/TMEM/TMA, 2-CTA clusters).  Supported when
 // H <= 128 and the shard layout tiles into whole TMA boxes: block_size a

@@ -51,7 +51,8 @@ __all__ = [
     "bf16_to_f64", "row_lengths", "shard_of", "local_len", "shard_positions",
     "physical_rows", "physical_rows_local", "gather_latents", "scores", "shard_partial",
     "decode_partial_row", "decode_partial", "lse_combine", "attention", "concat_cache",
-    "fp8_e4m3_to_f64", "kv_rows_f64",
+    "fp8_e4m3_to_f64", "kv_rows_f64", "quantize_rows", "concat_cache_fp8", "cache_read",
+    "visible_positions", "decode_partial_select",
 ]
 
 
@@ -364,3 +365,116 @@ def kv_rows_f64(inp: dict) -> np.ndarray:
         scale = np.asarray(inp["kv_scale"], dtype=np.float32).astype(np.float64).reshape(nb * bs, 1)
         return fp8_e4m3_to_f64(kv.reshape(nb * bs, kd)) * scale
     return bf16_to_f64(kv.reshape(nb * bs, kd))
+
+
+def quantize_rows(bits: np.ndarray):
+    """FP8 E4M3 codes and power-of-two scales of bf16 rows (uint16 [n, 576]):
+    per row the least 2^e with max |x| <= 256 * 2^e over the finite x (1 when
+    they are all zero), and the code nearest to x / 2^e, ties to the even
+    code; NaN and infinities give the NaN code 0x7F.  Nearest is found by
+    comparing with the midpoints of the format's 127 non-negative values."""
+    x = bf16_to_f64(bits)
+    grid = fp8_e4m3_to_f64(np.arange(127, dtype=np.uint8))  # increasing, index = code
+    mid = (grid[1:] + grid[:-1]) / 2
+    n = x.shape[0]
+    codes = np.full(x.shape, 0x7F, dtype=np.uint8)
+    scale = np.ones(n)
+    for r in range(n):
+        ok = np.isfinite(x[r])
+        top = np.abs(x[r][ok]).max(initial=0.0)
+        if top > 0:
+            e = -160
+            while 256.0 * 2.0 ** e < top:
+                e += 1
+            scale[r] = 2.0 ** e
+        y = np.abs(x[r][ok]) / scale[r]
+        lo = np.searchsorted(mid, y, side="left")   # midpoints below y
+        hi = np.searchsorted(mid, y, side="right")  # midpoints at or below y
+        c = np.where(lo == hi, lo, np.where(lo % 2 == 0, lo, hi))
+        codes[r, ok] = c | np.where(np.signbit(x[r][ok]), 0x80, 0)
+    return codes, scale.astype(np.float32)
+
+
+def concat_cache_fp8(kv_c, k_pe, slot_mapping, codes, scale):
+    """The cache side of ``concat_cache`` for an FP8 cache: (codes, scale)
+    after each token's quantised row went to its slot (negative: skipped)."""
+    codes, scale = np.array(codes, copy=True), np.array(scale, copy=True)
+    flat, fs = codes.reshape(-1, KDIM), scale.reshape(-1)
+    c, s = quantize_rows(np.concatenate([kv_c, k_pe], axis=1))
+    for t, slot in enumerate(slot_mapping):
+        if slot >= 0:
+            flat[int(slot)], fs[int(slot)] = c[t], s[t]
+    return codes, scale
+
+
+def cache_read(rows_f64: np.ndarray, table: np.ndarray, block_size: int, starts, cu_lens, D: int = 1, I: int = 1,
+               shards=None, local: bool = False) -> np.ndarray:
+    """float64 [cu_lens[B], 576]: request b's positions starts[b] + i, each
+    walked by itself (global table [B, W], or per-shard tables [len(shards),
+    B, W]); positions of shards not in ``shards`` are zero rows."""
+    shards = list(range(D)) if shards is None else list(shards)
+    out = np.zeros((int(cu_lens[-1]), KDIM))
+    for b in range(len(cu_lens) - 1):
+        for n in range(int(cu_lens[b]), int(cu_lens[b + 1])):
+            p = int(starts[b]) + n - int(cu_lens[b])
+            d = int(shard_of(p, D, I))
+            if d not in shards:
+                continue
+            j = int(np.searchsorted(shard_positions(p + 1, d, D, I), p)) if local else p
+            row = table[shards.index(d), b] if local else table[b]
+            out[n] = rows_f64[int(row[j // block_size]) * block_size + j % block_size]
+    return out
+
+
+# ---------------------------------------------------------------------------
+# selected context: sliding window with sinks, trees of drafted tokens
+# ---------------------------------------------------------------------------
+def visible_positions(seq: int, q_len: int, i: int, window: int = 0, sinks: int = 0, tree_bits=None) -> np.ndarray:
+    """The positions row i of a q_len-row request sees, in the order of the
+    row's own sequence: the causal context (a chain), or with ``tree_bits``
+    (bool [q_len], the row of the tree mask) the prefix of seq - q_len tokens
+    followed by the row's visible tree tokens.  With a window, the first
+    ``sinks`` and the last ``window`` of that sequence."""
+    if tree_bits is None:
+        mine = np.arange(max(0, seq - (q_len - 1 - i)))
+    else:
+        base = seq - q_len
+        tree = [base + k for k in range(q_len) if tree_bits[k] and base + k >= 0]
+        mine = np.concatenate([np.arange(max(0, base)), np.asarray(tree, dtype=np.int64)])
+    if window > 0:
+        k = np.arange(len(mine))
+        mine = mine[(k < sinks) | (k >= len(mine) - window)]
+    return mine.astype(np.int64)
+
+
+def decode_partial_select(inp: dict, window: int = 0, sinks: int = 0, tree=None):
+    """Oracle of the windowed and tree decodes on a workload dict: as
+    ``decode_partial``, each row over its ``visible_positions``.  ``tree`` is
+    bool [T, max_q_len] (row r: which of its request's rows it sees).
+    Empty (row, shard) pairs: lse -inf, O NaN."""
+    T, H, D, I, bs = inp["T"], inp["H"], inp["D"], inp["interleave"], inp["block_size"]
+    local = inp.get("layout", "global") == "local"
+    kv = kv_rows_f64(inp)
+    O = np.full((D, T, H, LATENT), np.nan)
+    lse = np.full((D, T, H), -np.inf)
+    req, _, padding = row_lengths(inp["seq_lens"], inp["query_start_loc"], T)
+    for r in range(T):
+        b = int(req[r])
+        if b < 0 or padding[r]:
+            continue
+        q0, q1 = (int(x) for x in inp["query_start_loc"][b:b + 2])
+        pos = visible_positions(int(inp["seq_lens"][b]), q1 - q0, r - q0, window, sinks,
+                                None if tree is None else tree[r])
+        q = bf16_to_f64(inp["q"][r])
+        for d in range(D):
+            mine = pos[shard_of(pos, D, I) == d]
+            if mine.size == 0:
+                continue
+            if local:
+                j = np.searchsorted(shard_positions(int(mine.max()) + 1, d, D, I), mine)
+                rows = inp["block_table"][d, b].astype(np.int64)[j // bs] * bs + j % bs
+            else:
+                rows = physical_rows(inp["block_table"][b], bs, mine)
+            latents = kv[rows]
+            O[d, r], lse[d, r] = shard_partial(scores(q, latents, inp["scale"]), latents[:, :LATENT])
+    return O, lse
