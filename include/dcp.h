@@ -68,6 +68,7 @@ extern "C" {
 #define DCP_ROPE_DIM 64
 #define DCP_KV_DIM 576
 #define DCP_MAX_SHARDS 32
+#define DCP_MAX_TREE_ROWS 256 /* rows of a request under a tree mask */
 
 /* Device-side error bits ORed into *dev_error. */
 #define DCP_DEVERR_BAD_BLOCK 1    /* a referenced block id is outside [0, num_blocks) */
@@ -467,6 +468,89 @@ dcp_status_t dcp_latent_cache_read(
     const int32_t* seq_starts, const int32_t* cu_lens, int32_t B, int64_t N,
     void* out, dcp_dtype_t out_dtype, int64_t out_stride,
     int32_t* dev_error, void* stream);
+
+/*
+ * The decode over a sliding window and the first tokens of the context (a
+ * window layer whose "sink" tokens stay visible): dcp_mla_decode_partial_v2
+ * with, for row i of a request and its own context length
+ * L = max(0, seq_len - (q_len - 1 - i)),
+ *   S = { p < L : (p < num_sinks or p >= L - window), shard(p) == d }.
+ * (The pages decode over the whole context; this form is for models whose
+ * layers do not.)
+ *
+ *   window      last tokens of its context, itself included, that a row sees;
+ *               0: all of them (then num_sinks has no effect).
+ *   num_sinks   first tokens of the context that it sees besides.
+ *               Negative values: DCP_ERR_INVALID_ARG.
+ *   max_q_len   rows of a request past max_q_len get -inf / 0 (and set
+ *               DCP_DEVERR_BAD_ROWS).  It sizes the launch: pass the step's
+ *               largest verification width, not a loose bound.
+ *   workspace   >= dcp_decode_select_workspace_size(...) bytes.
+ * Only blocks that hold a visible token of some row are read: table entries of
+ * blocks that have left every window may hold anything.  Split partials in
+ * the workspace are fp32 for every o_dtype.  Everything else as for
+ * dcp_mla_decode_partial_v2.
+ */
+dcp_status_t dcp_mla_decode_partial_window(
+    const void* q, int64_t q_stride_tok,
+    const void* kv_cache, dcp_kv_dtype_t kv_dtype, const float* kv_scale,
+    int32_t num_blocks, int32_t block_size,
+    const int32_t* block_table, int32_t bt_width, int64_t bt_stride,
+    int32_t per_shard_tables, int64_t bt_shard_stride, int32_t shard_begin, int32_t shard_count,
+    const int32_t* seq_lens, const int32_t* query_start_loc,
+    int32_t B, int32_t T, int32_t H, int32_t max_seq_len, int32_t max_q_len,
+    int32_t D, int32_t interleave, float scale,
+    int32_t window, int32_t num_sinks,
+    void* O_part, dcp_dtype_t o_dtype, float* lse_part,
+    void* workspace, size_t workspace_bytes,
+    int32_t* dev_error, void* stream);
+
+/*
+ * The decode of a tree of drafted tokens (tree-shaped speculation; the pages
+ * verify a chain, [PR565] Summary).  A request's q_len rows are its tree
+ * tokens: row k sits at position seq_len - q_len + k of the cache (written
+ * before the call, like a chain's) and sees the context before the tree, the
+ * first seq_len - q_len positions, and those rows k' of its request whose bit
+ * is set in its mask row: its ancestors, and itself where its own bit is set.
+ *   own sequence of row r, n tokens in order:
+ *       p = 0 .. seq_len - q_len - 1, then the set bits k' in increasing order
+ *       at positions seq_len - q_len + k' (those >= 0)
+ *   S = { the tokens of rank < num_sinks or >= n - window : shard(p) == d }
+ * (window 0: all of them).  An empty mask row sees the context alone; a row
+ * with nothing to see gives -inf / 0.
+ *
+ *   tree_mask    uint64 device words, 8-byte aligned: bit k' % 64 of word
+ *                tree_mask[r * mask_stride + k' / 64], r the query row (of
+ *                all T).  Bits at or past the request's q_len are ignored.
+ *                Rows past query_start_loc[B] are not read.
+ *   mask_stride  words between rows, >= ceil(max_q_len / 64), else
+ *                DCP_ERR_INVALID_ARG.
+ *   max_q_len    <= DCP_MAX_TREE_ROWS, else DCP_ERR_INVALID_ARG.
+ * Everything else as for dcp_mla_decode_partial_window.
+ */
+dcp_status_t dcp_mla_decode_partial_tree(
+    const void* q, int64_t q_stride_tok,
+    const void* kv_cache, dcp_kv_dtype_t kv_dtype, const float* kv_scale,
+    int32_t num_blocks, int32_t block_size,
+    const int32_t* block_table, int32_t bt_width, int64_t bt_stride,
+    int32_t per_shard_tables, int64_t bt_shard_stride, int32_t shard_begin, int32_t shard_count,
+    const int32_t* seq_lens, const int32_t* query_start_loc,
+    int32_t B, int32_t T, int32_t H, int32_t max_seq_len, int32_t max_q_len,
+    int32_t D, int32_t interleave, float scale,
+    const uint64_t* tree_mask, int64_t mask_stride,
+    int32_t window, int32_t num_sinks,
+    void* O_part, dcp_dtype_t o_dtype, float* lse_part,
+    void* workspace, size_t workspace_bytes,
+    int32_t* dev_error, void* stream);
+
+/*
+ * Bytes of device workspace the windowed and tree decodes need for these
+ * sizes on the CURRENT device (D = shard_count), an upper bound over every
+ * interleave.  Returns (size_t)-1 on invalid arguments.
+ */
+size_t dcp_decode_select_workspace_size(int32_t B, int32_t T, int32_t H, int32_t D,
+                                        int32_t max_seq_len, int32_t max_q_len,
+                                        int32_t window, int32_t num_sinks);
 
 #ifdef __cplusplus
 }

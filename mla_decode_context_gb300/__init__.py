@@ -24,6 +24,7 @@ LATENT_DIM = 512
 ROPE_DIM = 64
 KV_DIM = 576
 MAX_SHARDS = 32
+MAX_TREE_ROWS = 256
 
 DEVERR_BAD_BLOCK = 1
 DEVERR_SEQ_TOO_LONG = 2
@@ -77,6 +78,13 @@ EXPORTS = [
     ("dcp_latent_cache_read", ctypes.c_int,
      [_P, ctypes.c_int, _P, _I32, _I32, _P, _I32, _I64, _I32, _I64, _I32, _I32, _I32, _I32, _P, _P, _I32, _I64, _P,
       ctypes.c_int, _I64, _P, _P]),
+    ("dcp_mla_decode_partial_window", ctypes.c_int,
+     [_P, _I64, _P, ctypes.c_int, _P, _I32, _I32, _P, _I32, _I64, _I32, _I64, _I32, _I32, _P, _P, _I32, _I32, _I32,
+      _I32, _I32, _I32, _I32, _F, _I32, _I32, _P, ctypes.c_int, _P, _P, _SZ, _P, _P]),
+    ("dcp_mla_decode_partial_tree", ctypes.c_int,
+     [_P, _I64, _P, ctypes.c_int, _P, _I32, _I32, _P, _I32, _I64, _I32, _I64, _I32, _I32, _P, _P, _I32, _I32, _I32,
+      _I32, _I32, _I32, _I32, _F, _P, _I64, _I32, _I32, _P, ctypes.c_int, _P, _P, _SZ, _P, _P]),
+    ("dcp_decode_select_workspace_size", _SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32]),
 ]
 
 _lib = None
@@ -336,6 +344,87 @@ def dcp_mla_decode_partial_v2(q, kv_cache, block_table, seq_lens, query_start_lo
             scale, _ptr(O_part), DTYPE_BF16 if O_part.dtype == torch.bfloat16 else DTYPE_F32, _ptr(lse_part),
             _ptr(workspace), ws_bytes, _ptr(dev_error), _stream(stream))
     _check(st, "dcp_mla_decode_partial_v2")
+
+
+def dcp_decode_select_workspace_size(B: int, T: int, H: int, D: int, max_seq_len: int, max_q_len: int,
+                                     window: int = 0, num_sinks: int = 0) -> int:
+    n = lib().dcp_decode_select_workspace_size(B, T, H, D, max_seq_len, max_q_len, window, num_sinks)
+    if n == ctypes.c_size_t(-1).value:
+        raise DCPError(1, "dcp_decode_select_workspace_size")
+    return n
+
+
+def _decode_select(where, tree_mask, q, kv_cache, block_table, seq_lens, query_start_loc, O_part, lse_part, D,
+                   interleave, scale, window, num_sinks, max_seq_len, max_q_len, kv_scale, shard_begin, shard_count,
+                   workspace, dev_error, stream) -> None:
+    if shard_count is None:
+        shard_count = D - shard_begin
+    local = isinstance(block_table, torch.Tensor) and block_table.dim() == 3
+    extra = []
+    if where == "dcp_mla_decode_partial_tree":
+        if not isinstance(tree_mask, torch.Tensor) or tree_mask.dtype != torch.int64:
+            raise TypeError("tree_mask must be an int64 tensor (see pack_tree_mask)")
+        words = (max_q_len + 63) // 64
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != q.shape[0] or tree_mask.shape[1] < words or \
+                (tree_mask.shape[1] > 1 and tree_mask.stride(1) != 1):
+            raise ValueError("tree_mask must be [T, >= %d] words with unit column stride" % words)
+        extra = [_ptr(tree_mask), tree_mask.stride(0) if tree_mask.shape[0] > 1 else words]
+    B, T, H = _decode_geometry(q, kv_cache, block_table, seq_lens, query_start_loc, O_part, lse_part, shard_count,
+                               local=local)
+    fp8 = _cache_format(kv_cache, kv_scale)
+    if fp8:
+        _need(kv_scale, "kv_scale", torch.float32)
+    if extra:
+        _need(tree_mask, "tree_mask", torch.int64, contiguous=False)
+    _need_opt(workspace, "workspace", allow_empty=True)
+    if workspace is not None and workspace.numel() == 0:
+        workspace = None
+    _need_opt(dev_error, "dev_error", torch.int32)
+    guard = _same_device(kv_cache.device, q=q, block_table=block_table, seq_lens=seq_lens,
+                         query_start_loc=query_start_loc, O_part=O_part, lse_part=lse_part, kv_scale=kv_scale,
+                         tree_mask=tree_mask, workspace=workspace, dev_error=dev_error)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with guard, _Range(where):
+        st = getattr(lib(), where)(
+            _ptr(q), q.stride(0) if T > 1 else H * KV_DIM, _ptr(kv_cache), KV_FP8_E4M3 if fp8 else KV_BF16,
+            _ptr(kv_scale), kv_cache.shape[0], kv_cache.shape[1], _ptr(block_table), block_table.shape[-1],
+            block_table.stride(-2), 1 if local else 0, block_table.stride(0) if local else 0, shard_begin,
+            shard_count, _ptr(seq_lens), _ptr(query_start_loc), B, T, H, max_seq_len, max_q_len, D, interleave,
+            scale, *extra, window, num_sinks, _ptr(O_part),
+            DTYPE_BF16 if O_part.dtype == torch.bfloat16 else DTYPE_F32, _ptr(lse_part), _ptr(workspace), ws_bytes,
+            _ptr(dev_error), _stream(stream))
+    _check(st, where)
+
+
+def dcp_mla_decode_partial_window(q, kv_cache, block_table, seq_lens, query_start_loc, O_part, lse_part, *,
+                                  D: int, interleave: int, scale: float, window: int, num_sinks: int = 0,
+                                  max_seq_len: int, max_q_len: int, kv_scale: Optional[torch.Tensor] = None,
+                                  shard_begin: int = 0, shard_count: Optional[int] = None,
+                                  workspace: Optional[torch.Tensor] = None,
+                                  dev_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The decode over a sliding window: each row sees the last ``window``
+    tokens of its own context (0: all) and its first ``num_sinks``.  Other
+    arguments as for dcp_mla_decode_partial_v2."""
+    _decode_select("dcp_mla_decode_partial_window", None, q, kv_cache, block_table, seq_lens, query_start_loc, O_part,
+                   lse_part, D, interleave, scale, window, num_sinks, max_seq_len, max_q_len, kv_scale, shard_begin,
+                   shard_count, workspace, dev_error, stream)
+
+
+def dcp_mla_decode_partial_tree(q, kv_cache, block_table, seq_lens, query_start_loc, tree_mask, O_part, lse_part, *,
+                                D: int, interleave: int, scale: float, window: int = 0, num_sinks: int = 0,
+                                max_seq_len: int, max_q_len: int, kv_scale: Optional[torch.Tensor] = None,
+                                shard_begin: int = 0, shard_count: Optional[int] = None,
+                                workspace: Optional[torch.Tensor] = None,
+                                dev_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The decode of trees of drafted tokens: a request's rows are its tree
+    tokens (the last q_len positions of its context), and each sees the
+    context before the tree and the rows k of its request whose bit k is set
+    in its row of tree_mask (int64 words [T, >= max_q_len / 64], see
+    pack_tree_mask).  window and num_sinks as for the window decode, over the
+    row's own sequence.  Other arguments as for dcp_mla_decode_partial_v2."""
+    _decode_select("dcp_mla_decode_partial_tree", tree_mask, q, kv_cache, block_table, seq_lens, query_start_loc,
+                   O_part, lse_part, D, interleave, scale, window, num_sinks, max_seq_len, max_q_len, kv_scale,
+                   shard_begin, shard_count, workspace, dev_error, stream)
 
 
 def dcp_mla_decode_partial_noalloc(q, kv_cache, block_table, seq_lens, query_start_loc, O_part, lse_part, *,
@@ -670,3 +759,59 @@ def latent_cache_read(kv_cache, block_table, cu_lens, num_rows: int, seq_starts:
                           interleave=interleave, shard_begin=shard_begin, shard_count=shard_count,
                           dev_error=dev_error, stream=stream)
     return out
+
+
+def pack_tree_mask(visible: torch.Tensor) -> torch.Tensor:
+    """Bool [T, n] (row r sees row k of its request) -> the int64 words
+    [T, ceil(n / 64)] of the tree decode's mask, on the same device."""
+    if visible.dtype != torch.bool or visible.dim() != 2:
+        raise TypeError("visible must be a bool [T, n] tensor")
+    T, n = visible.shape
+    words = max(1, (n + 63) // 64)
+    bits = torch.zeros((T, words * 64), dtype=torch.int64, device=visible.device)
+    bits[:, :n] = visible.to(torch.int64)
+    return (bits.view(T, words, 64) << torch.arange(64, device=visible.device)).sum(-1)
+
+
+def _decode_select_alloc(entry, masks, q, kv_cache, block_table, seq_lens, query_start_loc, D, interleave, scale,
+                         window, num_sinks, max_seq_len, max_q_len, kv_scale, out_dtype, workspace, dev_error, stream):
+    T, H = q.shape[0], q.shape[1]
+    if max_seq_len is None:
+        max_seq_len = block_table.shape[-1] * kv_cache.shape[1] * (D if block_table.dim() == 3 else 1)
+    if max_q_len is None:
+        max_q_len = max(1, T)
+    O = torch.empty((D, T, H, LATENT_DIM), dtype=out_dtype, device=q.device)
+    lse = torch.empty((D, T, H), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        n = dcp_decode_select_workspace_size(seq_lens.shape[0], T, H, D, max_seq_len, max_q_len, window, num_sinks)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    entry(q, kv_cache, block_table, seq_lens, query_start_loc, *masks, O, lse, D=D, interleave=interleave,
+          scale=scale, window=window, num_sinks=num_sinks, max_seq_len=max_seq_len, max_q_len=max_q_len,
+          kv_scale=kv_scale, workspace=workspace, dev_error=dev_error, stream=stream)
+    return O, lse
+
+
+def decode_partial_window(q, kv_cache, block_table, seq_lens, query_start_loc, D: int, interleave: int, scale: float,
+                          window: int, num_sinks: int = 0, max_seq_len: Optional[int] = None,
+                          max_q_len: Optional[int] = None, kv_scale: Optional[torch.Tensor] = None,
+                          out_dtype=torch.float32, workspace: Optional[torch.Tensor] = None,
+                          dev_error: Optional[torch.Tensor] = None, stream=None):
+    """Allocating form of dcp_mla_decode_partial_window: returns (O_part
+    [D, T, H, 512] of out_dtype, lse_part fp32 [D, T, H]); merge them with
+    lse_combine."""
+    return _decode_select_alloc(dcp_mla_decode_partial_window, (), q, kv_cache, block_table, seq_lens,
+                                query_start_loc, D, interleave, scale, window, num_sinks, max_seq_len, max_q_len,
+                                kv_scale, out_dtype, workspace, dev_error, stream)
+
+
+def decode_partial_tree(q, kv_cache, block_table, seq_lens, query_start_loc, tree_mask, D: int, interleave: int,
+                        scale: float, window: int = 0, num_sinks: int = 0, max_seq_len: Optional[int] = None,
+                        max_q_len: Optional[int] = None, kv_scale: Optional[torch.Tensor] = None,
+                        out_dtype=torch.float32, workspace: Optional[torch.Tensor] = None,
+                        dev_error: Optional[torch.Tensor] = None, stream=None):
+    """Allocating form of dcp_mla_decode_partial_tree: returns (O_part
+    [D, T, H, 512] of out_dtype, lse_part fp32 [D, T, H]); merge them with
+    lse_combine."""
+    return _decode_select_alloc(dcp_mla_decode_partial_tree, (tree_mask,), q, kv_cache, block_table, seq_lens,
+                                query_start_loc, D, interleave, scale, window, num_sinks, max_seq_len, max_q_len,
+                                kv_scale, out_dtype, workspace, dev_error, stream)

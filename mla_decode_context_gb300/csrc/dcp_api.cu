@@ -2,6 +2,7 @@
 // kernel launches.  No allocation, no synchronisation, no global state.
 #include "dcp_kernels.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -35,28 +36,41 @@ int current_sm_count() {
 // Most splits a (row, shard) pair with up to `lmax` local tokens may use:
 // enough (row, shard, split) units to give every SM work when there are few
 // rows (long-context B=1 decode), never splits shorter than kMinSplitTokens.
-static int64_t split_cap(int32_t T, int32_t D, int64_t lmax, int sm_count) {
-  const int64_t units = static_cast<int64_t>(T) * D * kTargetCtasPerUnit;
-  int64_t want = sm_count / units;  // whole waves only
+static int64_t split_cap_units(int64_t units, int64_t lmax, int sm_count) {
+  int64_t want = sm_count / (units * kTargetCtasPerUnit);  // whole waves only
   const int64_t cap_len = (lmax + kMinSplitTokens - 1) / kMinSplitTokens;
   if (want > cap_len) want = cap_len;
   if (want > kMaxSplits) want = kMaxSplits;
   return want < 1 ? 1 : want;
 }
+static int64_t split_cap(int32_t T, int32_t D, int64_t lmax, int sm_count) {
+  return split_cap_units(static_cast<int64_t>(T) * D, lmax, sm_count);
+}
 
-// Split-KV plan: pure function of its arguments (and the SM count).
-SplitPlan plan_splits(int32_t T, int32_t D, int32_t I, int32_t d0, int32_t Dn, int32_t max_seq_len, int sm_count) {
+// `units` units of at most `lmax` tokens, cut into splits of whole tiles.
+static SplitPlan cut(int64_t lmax, int64_t want) {
   SplitPlan p{1, kSplitRound};
-  // the first computed shard is the largest of them
-  const int32_t lmax = local_len(max_seq_len < 0 ? 0 : max_seq_len, d0, D, I);
-  if (lmax <= 0) return p;
-  const int64_t want = split_cap(T, Dn, lmax, sm_count);
   int64_t chunk = (lmax + want - 1) / want;
   chunk = (chunk + kSplitRound - 1) / kSplitRound * kSplitRound;
   p.chunk = static_cast<int32_t>(chunk);
   p.splits = static_cast<int32_t>((lmax + chunk - 1) / chunk);  // <= want
   if (p.splits < 1) p.splits = 1;
   return p;
+}
+static int32_t max_splits_units(int64_t units, int64_t lmax, int sm_count) {
+  return static_cast<int32_t>(split_cap_units(units, lmax, sm_count));
+}
+SplitPlan plan_units(int64_t units, int64_t lmax, int sm_count) {
+  if (lmax <= 0 || units <= 0) return SplitPlan{1, kSplitRound};
+  return cut(lmax, split_cap_units(units, lmax, sm_count));
+}
+
+// Split-KV plan: pure function of its arguments (and the SM count).
+SplitPlan plan_splits(int32_t T, int32_t D, int32_t I, int32_t d0, int32_t Dn, int32_t max_seq_len, int sm_count) {
+  // the first computed shard is the largest of them
+  const int32_t lmax = local_len(max_seq_len < 0 ? 0 : max_seq_len, d0, D, I);
+  if (lmax <= 0) return SplitPlan{1, kSplitRound};
+  return cut(lmax, split_cap(T, Dn, lmax, sm_count));
 }
 
 // Tail of the workspace for the units' launch order (one int32 per unit).
@@ -107,6 +121,38 @@ DecodeLaunch decode_launch(int32_t T, int32_t H, int32_t D, int32_t interleave, 
   const int resident = dcp::decode_tc_resident_ctas();  // 0: no device to size against
   L.use_order = !L.simt && resident > 0 && units > resident / 2 && have_workspace &&
                 workspace_bytes >= L.need + L.obytes;
+  return L;
+}
+
+// The windowed and tree decodes.  A unit is a group of rows of one request
+// (as many as fit the tensor-core kernel's 128 lanes), one shard and one split
+// of what they may see; `lmax` bounds that per shard.
+int32_t select_group(int32_t H, int32_t max_q_len) {
+  const int32_t fit = H <= 128 ? 128 / H : 1;
+  return std::max(1, std::min(std::min(fit, dcp::kMaxGroup), max_q_len));
+}
+
+// Most of n consecutive positions that one shard owns.
+int64_t most_owned(int64_t n, int32_t D, int32_t I) {
+  const int64_t period = static_cast<int64_t>(D) * I;
+  return n / period * I + std::min<int64_t>(n % period, I);
+}
+
+DecodeLaunch select_launch(int32_t B, int32_t T, int32_t H, int32_t D, int32_t interleave, int32_t d0, int32_t Dn,
+                           int32_t max_seq_len, int32_t max_q_len, const dcp::SelectArgs& sel, bool have_workspace,
+                           size_t workspace_bytes) {
+  DecodeLaunch L{};
+  const int sms = dcp::current_sm_count();
+  int64_t lmax = dcp::local_len(max_seq_len, d0, D, interleave);
+  if (sel.window > 0)  // the sinks, and a window for each row of the request
+    lmax = std::min(lmax, most_owned(sel.sinks, D, interleave) +
+                              most_owned(static_cast<int64_t>(sel.window) + max_q_len, D, interleave));
+  const int64_t units = static_cast<int64_t>(B) * sel.chunks * Dn;
+  L.plan = dcp::plan_units(units, lmax, sms);
+  L.need = dcp::split_workspace_bytes(L.plan, T, H, Dn);
+  L.obytes = 0;
+  L.simt = true;
+  L.use_order = false;
   return L;
 }
 }  // namespace
@@ -162,7 +208,7 @@ static dcp_status_t decode_partial_impl(const void* q, int64_t q_stride_tok, con
                                         int32_t T, int32_t H, int32_t max_seq_len, int32_t max_q_len, int32_t D,
                                         int32_t interleave, float scale, void* O_part, dcp_dtype_t o_dtype,
                                         float* lse_part, void* workspace, size_t workspace_bytes, int32_t* dev_error,
-                                        void* stream) {
+                                        void* stream, const dcp::SelectArgs* select = nullptr) {
   if (B < 0 || T < 0 || H < 1 || H > 1024 || D < 1 || D > DCP_MAX_SHARDS || interleave < 1 ||
       max_seq_len < 0 || max_q_len < 1 || !std::isfinite(scale))
     return DCP_ERR_INVALID_ARG;
@@ -185,9 +231,18 @@ static dcp_status_t decode_partial_impl(const void* q, int64_t q_stride_tok, con
   const int64_t covered = local ? dcp::local_len(max_seq_len, d0, D, interleave) : max_seq_len;
   if ((covered + block_size - 1) / block_size > bt_width) return DCP_ERR_TABLE_TOO_NARROW;
 
+  dcp::SelectArgs sel{};
+  if (select) {
+    sel = *select;
+    sel.on = 1;
+    sel.group = select_group(H, max_q_len);
+    sel.chunks = (max_q_len - 1) / sel.group + 1;
+  }
   const DecodeLaunch launch =
-      decode_launch(T, H, D, interleave, d0, Dn, max_seq_len, workspace != nullptr, workspace_bytes,
-                    kv_dtype == DCP_KV_FP8_E4M3);
+      select ? select_launch(B, T, H, D, interleave, d0, Dn, max_seq_len, max_q_len, sel, workspace != nullptr,
+                             workspace_bytes)
+             : decode_launch(T, H, D, interleave, d0, Dn, max_seq_len, workspace != nullptr, workspace_bytes,
+                             kv_dtype == DCP_KV_FP8_E4M3);
   const dcp::SplitPlan plan = launch.plan;
   const size_t need = launch.need;
   if (need > 0 && (workspace_bytes < need || !workspace)) return DCP_ERR_WORKSPACE_TOO_SMALL;
@@ -200,7 +255,10 @@ static dcp_status_t decode_partial_impl(const void* q, int64_t q_stride_tok, con
   a.kv = kv_cache;
   a.kv_fp8 = kv_dtype == DCP_KV_FP8_E4M3 ? 1 : 0;
   a.kv_scale = kv_scale;
-  a.o_bf16 = o_dtype == DCP_DTYPE_BF16 ? 1 : 0;
+  // (split partials are in the output's dtype; those of the windowed and tree
+  // decodes are fp32, so that a bf16 output is rounded once)
+  a.o_bf16 = o_dtype == DCP_DTYPE_BF16 && !(select && launch.plan.splits > 1) ? 1 : 0;
+  a.sel = sel;
   a.num_blocks = num_blocks;
   a.block_size = block_size;
   a.block_table = block_table;
@@ -255,7 +313,7 @@ static dcp_status_t decode_partial_impl(const void* q, int64_t q_stride_tok, con
   if (plan.splits > 1) {
     const int64_t pairs = static_cast<int64_t>(Dn) * T * H;
     e = dcp::launch_lse_merge(ws_O, a.o_bf16 != 0, ws_lse, pairs * DCP_LATENT_DIM, pairs, plan.splits, pairs, H,
-                              nullptr, nullptr, 0, /*row_mask=*/false, O_part, a.o_bf16 != 0, lse_part, st);
+                              nullptr, nullptr, 0, /*row_mask=*/false, O_part, o_dtype == DCP_DTYPE_BF16, lse_part, st);
     if (e != cudaSuccess) return DCP_ERR_CUDA;
   }
   return DCP_OK;
@@ -304,6 +362,77 @@ dcp_status_t dcp_mla_decode_partial_v2(const void* q, int64_t q_stride_tok, cons
                              bt_width, bt_stride, per_shard_tables != 0, bt_shard_stride, shard_begin, shard_count,
                              seq_lens, query_start_loc, B, T, H, max_seq_len, max_q_len, D, interleave, scale, O_part,
                              o_dtype, lse_part, workspace, workspace_bytes, dev_error, stream);
+}
+
+static dcp_status_t select_impl(const dcp::SelectArgs& sel, const void* q, int64_t q_stride_tok, const void* kv_cache,
+                                dcp_kv_dtype_t kv_dtype, const float* kv_scale, int32_t num_blocks,
+                                int32_t block_size, const int32_t* block_table, int32_t bt_width, int64_t bt_stride,
+                                int32_t per_shard_tables, int64_t bt_shard_stride, int32_t shard_begin,
+                                int32_t shard_count, const int32_t* seq_lens, const int32_t* query_start_loc,
+                                int32_t B, int32_t T, int32_t H, int32_t max_seq_len, int32_t max_q_len, int32_t D,
+                                int32_t interleave, float scale, void* O_part, dcp_dtype_t o_dtype, float* lse_part,
+                                void* workspace, size_t workspace_bytes, int32_t* dev_error, void* stream) {
+  if (sel.window < 0 || sel.sinks < 0) return DCP_ERR_INVALID_ARG;
+  return decode_partial_impl(q, q_stride_tok, kv_cache, kv_dtype, kv_scale, num_blocks, block_size, block_table,
+                             bt_width, bt_stride, per_shard_tables != 0, bt_shard_stride, shard_begin, shard_count,
+                             seq_lens, query_start_loc, B, T, H, max_seq_len, max_q_len, D, interleave, scale, O_part,
+                             o_dtype, lse_part, workspace, workspace_bytes, dev_error, stream, &sel);
+}
+
+dcp_status_t dcp_mla_decode_partial_window(
+    const void* q, int64_t q_stride_tok, const void* kv_cache, dcp_kv_dtype_t kv_dtype, const float* kv_scale,
+    int32_t num_blocks, int32_t block_size, const int32_t* block_table, int32_t bt_width, int64_t bt_stride,
+    int32_t per_shard_tables, int64_t bt_shard_stride, int32_t shard_begin, int32_t shard_count,
+    const int32_t* seq_lens, const int32_t* query_start_loc, int32_t B, int32_t T, int32_t H, int32_t max_seq_len,
+    int32_t max_q_len, int32_t D, int32_t interleave, float scale, int32_t window, int32_t num_sinks, void* O_part,
+    dcp_dtype_t o_dtype, float* lse_part, void* workspace, size_t workspace_bytes, int32_t* dev_error, void* stream) {
+  dcp::SelectArgs sel{};
+  sel.window = window;
+  sel.sinks = num_sinks;
+  return select_impl(sel, q, q_stride_tok, kv_cache, kv_dtype, kv_scale, num_blocks, block_size, block_table, bt_width,
+                     bt_stride, per_shard_tables, bt_shard_stride, shard_begin, shard_count, seq_lens,
+                     query_start_loc, B, T, H, max_seq_len, max_q_len, D, interleave, scale, O_part, o_dtype, lse_part,
+                     workspace, workspace_bytes, dev_error, stream);
+}
+
+dcp_status_t dcp_mla_decode_partial_tree(
+    const void* q, int64_t q_stride_tok, const void* kv_cache, dcp_kv_dtype_t kv_dtype, const float* kv_scale,
+    int32_t num_blocks, int32_t block_size, const int32_t* block_table, int32_t bt_width, int64_t bt_stride,
+    int32_t per_shard_tables, int64_t bt_shard_stride, int32_t shard_begin, int32_t shard_count,
+    const int32_t* seq_lens, const int32_t* query_start_loc, int32_t B, int32_t T, int32_t H, int32_t max_seq_len,
+    int32_t max_q_len, int32_t D, int32_t interleave, float scale, const uint64_t* tree_mask, int64_t mask_stride,
+    int32_t window, int32_t num_sinks, void* O_part, dcp_dtype_t o_dtype, float* lse_part, void* workspace,
+    size_t workspace_bytes, int32_t* dev_error, void* stream) {
+  if (max_q_len > DCP_MAX_TREE_ROWS) return DCP_ERR_INVALID_ARG;
+  if (B > 0 && T > 0) {
+    if (!tree_mask || (T > 1 && mask_stride < (max_q_len + 63) / 64)) return DCP_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(tree_mask) % 8 != 0) return DCP_ERR_MISALIGNED;
+  }
+  dcp::SelectArgs sel{};
+  sel.window = window;
+  sel.sinks = num_sinks;
+  sel.tree = reinterpret_cast<const unsigned long long*>(tree_mask);
+  sel.tree_stride = mask_stride;
+  return select_impl(sel, q, q_stride_tok, kv_cache, kv_dtype, kv_scale, num_blocks, block_size, block_table, bt_width,
+                     bt_stride, per_shard_tables, bt_shard_stride, shard_begin, shard_count, seq_lens,
+                     query_start_loc, B, T, H, max_seq_len, max_q_len, D, interleave, scale, O_part, o_dtype, lse_part,
+                     workspace, workspace_bytes, dev_error, stream);
+}
+
+size_t dcp_decode_select_workspace_size(int32_t B, int32_t T, int32_t H, int32_t D, int32_t max_seq_len,
+                                        int32_t max_q_len, int32_t window, int32_t num_sinks) {
+  if (B < 0 || T < 0 || H < 1 || H > 1024 || D < 1 || D > DCP_MAX_SHARDS || max_seq_len < 0 || max_q_len < 1 ||
+      window < 0 || num_sinks < 0)
+    return static_cast<size_t>(-1);
+  if (B == 0 || T == 0) return 0;
+  // An upper bound over every interleave: a shard owns at most every visible
+  // token, and the split count grows with that bound.
+  int64_t lmax = max_seq_len;
+  if (window > 0) lmax = std::min(lmax, static_cast<int64_t>(window) + num_sinks + max_q_len);
+  const int32_t group = select_group(H, max_q_len);
+  const int64_t units = static_cast<int64_t>(B) * ((max_q_len - 1) / group + 1) * D;
+  const dcp::SplitPlan p{dcp::max_splits_units(units, lmax, dcp::current_sm_count()), 0};
+  return dcp::split_workspace_bytes(p, T, H, D);
 }
 
 int32_t dcp_decode_kernel_launches(int32_t B, int32_t T, int32_t H, int32_t D, int32_t interleave,

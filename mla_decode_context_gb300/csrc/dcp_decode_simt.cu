@@ -11,7 +11,12 @@
 // cache is staged as its codes (576 bytes a row) with each row's scale, and
 // widened on use (exactly: every E4M3 value is a half) before the scale is
 // applied; partial outputs may be written in bf16.
+//
+// kSel: the windowed and tree decodes.  A tile walks the row's dense index of
+// visible tokens (dcp_select.cuh); tokens of that range that the row does not
+// see are staged as zeros and masked, like bad blocks, but not flagged.
 #include "dcp_kernels.h"
+#include "dcp_select.cuh"
 
 #include <cuda_fp8.h>
 #include <cmath>
@@ -43,6 +48,7 @@ __device__ __forceinline__ float2 fp8x2_to_float2(uint16_t v) {
 __device__ __forceinline__ float bf16lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
+template <bool kSel>
 __global__ void __launch_bounds__(kThreads)
 decode_simt_kernel(DecodeArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -59,10 +65,27 @@ decode_simt_kernel(DecodeArgs a) {
   const int64_t dst_pair = ((static_cast<int64_t>(s) * a.Dn + (d - a.d0)) * a.T + r) * a.H + h;
   const bool fp8 = a.kv_fp8 != 0;
 
-  const RowInfo ri = resolve_row(a.seq_lens, a.qsl, a.B, r, a.max_seq_len, a.max_q_len);
+  RowInfo ri{};
+  SelRows rows{};
+  SelSpan span{};
+  SelRow own{};
+  int32_t own_len = 0, n_local = 0;
+  if constexpr (kSel) {
+    rows = sel_rows_of_row(a, r);
+    ri.b = rows.b;
+    ri.err = rows.err;
+    if (rows.n > 0) {
+      span = sel_span(a, rows, d);
+      own_len = a.sel.tree ? sel_tree_len(a, rows, rows.i0) : sel_chain_len(rows, rows.i0);
+      own = sel_row(a, rows, span, rows.i0, own_len, d);
+      n_local = span.nv;
+    }
+  } else {
+    ri = resolve_row(a.seq_lens, a.qsl, a.B, r, a.max_seq_len, a.max_q_len);
+    n_local = ri.padding ? 0 : local_len(ri.L, d, a.D, a.I);
+  }
   if (ri.err && threadIdx.x == 0 && hg == 0 && blockIdx.y == 0 && a.dev_error)
     atomicOr(a.dev_error, static_cast<int32_t>(ri.err));
-  const int32_t n_local = ri.padding ? 0 : local_len(ri.L, d, a.D, a.I);
   const int32_t lo = s * a.plan.chunk;
   const int32_t hi = min(n_local, lo + a.plan.chunk);
 
@@ -89,9 +112,19 @@ decode_simt_kernel(DecodeArgs a) {
     for (int32_t t0 = lo; t0 < hi; t0 += kTile) {
       __syncthreads();  // previous tile fully consumed (and q staged)
       if (threadIdx.x < kTile) {
-        const int32_t j = t0 + threadIdx.x;
+        int32_t j = t0 + threadIdx.x;
         int64_t phys = -1;
-        if (j < hi) {
+        bool in = j < hi;
+        if constexpr (kSel) {
+          if (in) {
+            const int32_t v = j;
+            j = span.token_of(v);
+            in = v < span.vb ? v < own.vend && (v < span.vs || v >= own.vlo)
+                             : sel_tree_bit(a, rows, rows.i0, own_len,
+                                            static_cast<int32_t>(local_to_global(j, d, a.D, a.I)) - (rows.seq - rows.q_len));
+          }
+        }
+        if (in) {
           // table index: the shard token's position, or its local index (per-shard layout)
           const int64_t p = a.local_tables ? j : local_to_global(j, d, a.D, a.I);
           const int32_t blk = __ldg(trow + p / a.block_size);
@@ -224,8 +257,11 @@ cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t st) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
-      cudaError_t e = cudaFuncSetAttribute(decode_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      cudaError_t e = cudaFuncSetAttribute(decode_simt_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+      e = cudaFuncSetAttribute(decode_simt_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(smem));
       if (e != cudaSuccess) return e;
       done[dev] = true;
     }
@@ -234,7 +270,8 @@ cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t st) {
   const int64_t gy = static_cast<int64_t>(a.Dn) * a.plan.splits;
   if (gx > 0x7fffffffLL || gy > 65535) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
-  decode_simt_kernel<<<grid, kThreads, smem, st>>>(a);
+  if (a.sel.on) decode_simt_kernel<true><<<grid, kThreads, smem, st>>>(a);
+  else decode_simt_kernel<false><<<grid, kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -31,6 +31,22 @@ __device__ __forceinline__ int32_t fast_div(int32_t n, const FastDiv& f) {
 }
 #endif
 
+constexpr int kMaxTree = 256;  // rows of a request under a tree mask
+constexpr int kMaxGroup = 16;  // rows of a request in one unit of a windowed or tree decode
+
+// What the rows of a windowed or tree decode see (dcp_select.cuh); on = 0: a
+// decode over each row's whole causal context.
+struct SelectArgs {
+  int32_t on;
+  int32_t window;                  // last tokens of a row's own sequence it sees; 0: all
+  int32_t sinks;                   // first tokens it sees besides
+  const unsigned long long* tree;  // tree mask rows (bit k: row k of the request), nullptr: a chain
+  int64_t tree_stride;             // words between rows
+  // tensor-core kernel: rows of a request that share a unit's 128 lanes, and
+  // such groups per request (max_q_len / group, rounded up)
+  int32_t group, chunks;
+};
+
 // Everything one decode launch needs (validated by the C ABI).
 struct DecodeArgs {
   const __nv_bfloat16* q;
@@ -77,6 +93,7 @@ struct DecodeArgs {
   // completes, so every unit ends through its bounded waits and reports
   // DCP_DEVERR_TIMEOUT.
   int32_t stall_test;
+  SelectArgs sel;
 };
 
 // The (row, shard - d0, split) of unit u of the tensor-core decode, with the

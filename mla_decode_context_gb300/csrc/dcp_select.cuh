@@ -1,0 +1,129 @@
+// Row selection of the windowed and tree decodes: which tokens of a shard the
+// rows of a request see.
+//
+// Row i of a q_len-row request has its own sequence of tokens, in order:
+//   chain  the first L_i = seq_len - (q_len - 1 - i) positions;
+//   tree   the prefix of P = max(0, seq_len - q_len) positions, then the tree
+//          tokens k (position seq_len - q_len + k) whose bit is set in the
+//          row's mask.
+// Without a window it sees all of them; with one, the first `sinks` and the
+// last `window` of them.
+//
+// The rows of a unit (one row, or a group of rows of one request that share
+// their tiles) read the union of what they see, so a unit walks a dense index
+// v over the shard's tokens j that any of its rows may see:
+//   v in [0, vs)    the sinks below the window, j = v;
+//   v in [vs, vb)   the window's stretch of the prefix, j = v + gap;
+//   v in [vb, nv)   the tree tokens (tree only; a chain has vb = nv).
+// A row then sees v < vb iff v < vend and (v < vs or v >= vlo), and a tree
+// token iff its bit says so.  Everything is a shard-local count in closed
+// form, so no index list is read or built, and tokens that have left every
+// window are never touched (their blocks may be gone).
+#pragma once
+
+#include "dcp_kernels.h"
+
+namespace dcp {
+
+// The rows r0 .. r0 + n - 1 (i0, i0 + 1, .. of their request); n == 0: none.
+struct SelRows {
+  int32_t r0, n, b, i0, q_len, seq;
+  uint32_t err;
+};
+
+// What the rows may see of shard d, as local counts.
+struct SelSpan {
+  int32_t vs, vb, nv, gap;
+  __device__ __forceinline__ int32_t index_of(int32_t j) const {  // v of the first visible token at or after j
+    return j <= vs ? j : max(vs, j - gap);
+  }
+  __device__ __forceinline__ int32_t token_of(int32_t v) const { return v < vs ? v : v + gap; }
+};
+
+// One row's part of the span's prefix.
+struct SelRow {
+  int32_t vlo, vend;
+};
+
+#ifdef __CUDACC__
+__device__ __forceinline__ int32_t sel_prefix(const SelRows& R) { return max(0, R.seq - R.q_len); }
+
+// Own length of chain row i.
+__device__ __forceinline__ int32_t sel_chain_len(const SelRows& R, int32_t i) {
+  return max(0, R.seq - (R.q_len - 1 - i));
+}
+
+__device__ __forceinline__ SelSpan sel_span(const DecodeArgs& a, const SelRows& R, int32_t d) {
+  const SelectArgs& s = a.sel;
+  const bool tree = s.tree != nullptr;
+  // the rows' prefix ends at P; no row's window starts before `start`
+  const int32_t P = tree ? sel_prefix(R) : sel_chain_len(R, R.i0 + R.n - 1);
+  const int32_t shortest = tree ? P : sel_chain_len(R, R.i0);
+  const int32_t start = s.window > 0 ? max(0, shortest - s.window) : 0;
+  const int32_t ns = local_len(min(s.sinks, P), d, a.D, a.I);
+  const int32_t lo = s.window > 0 ? max(ns, local_len(start, d, a.D, a.I)) : ns;
+  const int32_t nb = local_len(P, d, a.D, a.I);
+  const int32_t ne = tree ? local_len(max(0, R.seq), d, a.D, a.I) : nb;
+  return SelSpan{ns, nb - (lo - ns), ne - (lo - ns), lo - ns};
+}
+
+// Words of a row's mask that hold its request's rows, and word w with the bits
+// past the request's rows, or of positions before the context, dropped.
+__device__ __forceinline__ int32_t sel_words(const DecodeArgs& a, const SelRows& R) {
+  return (min(R.q_len, a.max_q_len) + 63) / 64;
+}
+__device__ __forceinline__ unsigned long long sel_word(const DecodeArgs& a, const SelRows& R, int32_t i, int32_t w) {
+  unsigned long long m = __ldg(a.sel.tree + static_cast<int64_t>(R.r0 - R.i0 + i) * a.sel.tree_stride + w);
+  const int32_t hi = min(R.q_len, a.max_q_len) - 64 * w;  // bits below hi exist
+  if (hi < 64) m &= (1ull << max(hi, 0)) - 1ull;
+  const int32_t lo = R.q_len - R.seq - 64 * w;            // bits from lo on have a position >= 0
+  if (lo > 0) m &= lo < 64 ? ~0ull << lo : 0ull;
+  return m;
+}
+
+// Own length of tree row i: the prefix and its visible tree tokens.
+__device__ __forceinline__ int32_t sel_tree_len(const DecodeArgs& a, const SelRows& R, int32_t i) {
+  int32_t n = sel_prefix(R);
+  for (int32_t w = 0; w < sel_words(a, R); ++w) n += __popcll(sel_word(a, R, i, w));
+  return n;
+}
+
+// Row i's part of the prefix; len: its own length (chain or tree).
+__device__ __forceinline__ SelRow sel_row(const DecodeArgs& a, const SelRows& R, const SelSpan& S, int32_t i,
+                                          int32_t len, int32_t d) {
+  const int32_t P = a.sel.tree ? sel_prefix(R) : len;
+  SelRow r;
+  r.vend = a.sel.tree ? S.vb : S.index_of(local_len(P, d, a.D, a.I));
+  r.vlo = a.sel.window > 0 ? S.index_of(local_len(min(max(0, len - a.sel.window), P), d, a.D, a.I)) : 0;
+  return r;
+}
+
+// Whether tree row i of own length len sees tree token k.
+__device__ __forceinline__ bool sel_tree_bit(const DecodeArgs& a, const SelRows& R, int32_t i, int32_t len, int32_t k) {
+  if (k < 0 || k >= min(R.q_len, a.max_q_len)) return false;
+  const unsigned long long m = sel_word(a, R, i, k >> 6);
+  if (!((m >> (k & 63)) & 1ull)) return false;
+  if (a.sel.window <= 0) return true;
+  int32_t rank = sel_prefix(R) + __popcll(m & ((1ull << (k & 63)) - 1ull));
+  for (int32_t w = 0; w < (k >> 6); ++w) rank += __popcll(sel_word(a, R, i, w));
+  return rank < a.sel.sinks || rank >= len - a.sel.window;
+}
+
+// The one row r (rows past max_q_len of their request count as padding).
+__device__ __forceinline__ SelRows sel_rows_of_row(const DecodeArgs& a, int32_t r) {
+  SelRows R{r, 0, -1, 0, 0, 0, 0u};
+  const RequestOfRow q = request_of_row(a.seq_lens, a.qsl, a.B, r, a.max_q_len);
+  if (q.b < 0) return R;
+  R.b = q.b;
+  R.i0 = r - q.q0;
+  R.q_len = q.q1 - q.q0;
+  if (R.q_len > a.max_q_len) R.err |= DCP_DEVERR_BAD_ROWS;
+  R.seq = q.seq;
+  if (R.seq <= 0) return R;
+  if (R.seq > a.max_seq_len) { R.err |= DCP_DEVERR_SEQ_TOO_LONG; R.seq = a.max_seq_len; }
+  R.n = R.i0 < a.max_q_len ? 1 : 0;
+  return R;
+}
+#endif
+
+}  // namespace dcp
