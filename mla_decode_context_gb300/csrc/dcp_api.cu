@@ -124,6 +124,8 @@ DecodeLaunch decode_launch(int32_t T, int32_t H, int32_t D, int32_t interleave, 
   return L;
 }
 
+size_t order_bytes(int64_t units) { return (static_cast<size_t>(units) * sizeof(int32_t) + 255) / 256 * 256; }
+
 // The windowed and tree decodes.  A unit is a group of rows of one request
 // (as many as fit the tensor-core kernel's 128 lanes), one shard and one split
 // of what they may see; `lmax` bounds that per shard.
@@ -150,9 +152,16 @@ DecodeLaunch select_launch(int32_t B, int32_t T, int32_t H, int32_t D, int32_t i
   const int64_t units = static_cast<int64_t>(B) * sel.chunks * Dn;
   L.plan = dcp::plan_units(units, lmax, sms);
   L.need = dcp::split_workspace_bytes(L.plan, T, H, Dn);
-  L.obytes = 0;
-  L.simt = true;
-  L.use_order = false;
+  const int64_t all = (units + static_cast<int64_t>(sel.chunks) * Dn) * L.plan.splits;  // and the rows of no request
+  L.obytes = order_bytes(all);
+  dcp::DecodeArgs a{};
+  a.H = H;
+  a.plan = L.plan;
+  const char* force = std::getenv("DCP_FORCE_SIMT");
+  L.simt = (force && force[0] == '1') || !dcp::decode_tc_supported(a);
+  const int resident = dcp::decode_tc_resident_ctas();
+  L.use_order = !L.simt && resident > 0 && all > resident / 2 && all <= 0x3fffffff && have_workspace &&
+                workspace_bytes >= L.need + L.obytes;
   return L;
 }
 }  // namespace
@@ -302,7 +311,8 @@ static dcp_status_t decode_partial_impl(const void* q, int64_t q_stride_tok, con
     // more units than clusters that fit at once: start the long ones first
     // (the order lives in the workspace past the split partials; a workspace
     // without room for it keeps index order)
-    const int64_t units = static_cast<int64_t>(T) * Dn * plan.splits;
+    const int64_t units =
+        (select ? (static_cast<int64_t>(B) + 1) * sel.chunks : static_cast<int64_t>(T)) * Dn * plan.splits;
     int32_t* order = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + need);
     e = dcp::launch_unit_order(a, static_cast<int32_t>(units), order, st);
     if (e != cudaSuccess) return DCP_ERR_CUDA;
@@ -432,7 +442,8 @@ size_t dcp_decode_select_workspace_size(int32_t B, int32_t T, int32_t H, int32_t
   const int32_t group = select_group(H, max_q_len);
   const int64_t units = static_cast<int64_t>(B) * ((max_q_len - 1) / group + 1) * D;
   const dcp::SplitPlan p{dcp::max_splits_units(units, lmax, dcp::current_sm_count()), 0};
-  return dcp::split_workspace_bytes(p, T, H, D);
+  return dcp::split_workspace_bytes(p, T, H, D) +
+         order_bytes((units + static_cast<int64_t>((max_q_len - 1) / group + 1) * D) * p.splits);
 }
 
 int32_t dcp_decode_kernel_launches(int32_t B, int32_t T, int32_t H, int32_t D, int32_t interleave,

@@ -188,6 +188,7 @@ decode_simt_kernel(DecodeArgs a) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) tmax = fmaxf(tmax, __shfl_xor_sync(kFull, tmax, o));
       const float m_new = fmaxf(m, tmax);
+      if (kSel && __any_sync(kFull, isnan(s2))) l = NAN;  // the row's result is NaN (fmaxf passes NaNs over)
       if (m_new == -INFINITY) continue;  // nothing valid yet
       const float alpha = exp2f(m - m_new);
       const float p = valid ? exp2f(s2 - m_new) : 0.f;
@@ -229,7 +230,8 @@ decode_simt_kernel(DecodeArgs a) {
   }
   if (!head_ok) return;
   // empty shard / split, or padding row: masked at the source (0 / -inf)
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const bool live = kSel ? l != 0.f : l > 0.f;
+  const float inv = live ? 1.f / l : 0.f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const float4 v = make_float4(acc[4 * k] * inv, acc[4 * k + 1] * inv, acc[4 * k + 2] * inv, acc[4 * k + 3] * inv);
@@ -241,7 +243,7 @@ decode_simt_kernel(DecodeArgs a) {
           make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
     }
   }
-  if (lane == 0) a.lse_dst[dst_pair] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (lane == 0) a.lse_dst[dst_pair] = live ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 }  // namespace

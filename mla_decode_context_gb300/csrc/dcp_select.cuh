@@ -124,6 +124,74 @@ __device__ __forceinline__ SelRows sel_rows_of_row(const DecodeArgs& a, int32_t 
   R.n = R.i0 < a.max_q_len ? 1 : 0;
   return R;
 }
+
+// Unit (b, c) of the tensor-core kernel: rows c * group .. of request b, the
+// first max_q_len of the request at most.  n rows are written, live says
+// whether they see anything at all; `extra` rows from extra0 on have no unit
+// of their own and are written as padding (a request's rows past max_q_len by
+// its last unit; b == B: the rows of no request, dealt to `chunks` units).
+struct SelUnit {
+  SelRows R;
+  bool live;
+  int32_t extra0, extra;
+};
+__device__ __forceinline__ SelUnit sel_unit(const DecodeArgs& a, int32_t b, int32_t c) {
+  SelUnit U{};
+  U.R.b = b;
+  if (b >= a.B) {
+    const int32_t first = min(max(__ldg(a.qsl), 0), a.T), last = min(max(__ldg(a.qsl + a.B), 0), a.T);
+    // [0, first) before the first request and [last, T) after the last one,
+    // as one list of first + T - last rows, an even share per unit
+    const int32_t share = (first + a.T - last + a.sel.chunks - 1) / a.sel.chunks;
+    const int32_t x0 = c * share, x1 = min(x0 + share, first + a.T - last);
+    // (a share that straddles both parts: its first part here, the rest as rows of R)
+    const int32_t h1 = min(x1, first);
+    U.R.r0 = x0 < first ? x0 : 0;
+    U.R.n = max(0, h1 - x0);
+    const int32_t t0 = max(x0, first);
+    U.extra0 = last + (t0 - first);
+    U.extra = max(0, x1 - t0);
+    return U;
+  }
+  const int32_t q0 = __ldg(a.qsl + b), q1 = __ldg(a.qsl + b + 1), seq = __ldg(a.seq_lens + b);
+  SelRows& R = U.R;
+  R.q_len = q1 - q0;
+  R.i0 = c * a.sel.group;
+  R.r0 = q0 + R.i0;
+  if (R.q_len < 0 || q0 < 0 || q0 > a.T) {
+    R.err |= DCP_DEVERR_BAD_ROWS;
+    return U;
+  }
+  const int32_t rows = min(R.q_len, a.max_q_len);
+  R.n = max(0, min(min(a.sel.group, rows - R.i0), a.T - R.r0));
+  if (R.q_len > a.max_q_len) {
+    R.err |= DCP_DEVERR_BAD_ROWS;
+    if (c == a.sel.chunks - 1) {
+      U.extra0 = q0 + rows;
+      U.extra = max(0, min(q1, a.T) - U.extra0);
+    }
+  }
+  R.seq = seq;
+  if (seq > a.max_seq_len) { R.err |= DCP_DEVERR_SEQ_TOO_LONG; R.seq = a.max_seq_len; }
+  U.live = seq > 0 && R.n > 0;
+  return U;
+}
+
+// (request, group, shard - d0, split) of unit u: a request's groups innermost,
+// so that they read each tile from L2 at the same time.
+struct SelCoords {
+  int32_t b, c, dd, s;
+};
+__device__ __forceinline__ SelCoords sel_coords(const DecodeArgs& a, int64_t u) {
+  SelCoords k;
+  k.c = static_cast<int32_t>(u % a.sel.chunks);
+  u /= a.sel.chunks;
+  k.s = static_cast<int32_t>(u % a.plan.splits);
+  u /= a.plan.splits;
+  k.dd = static_cast<int32_t>(u % a.Dn);
+  k.b = static_cast<int32_t>(u / a.Dn);
+  return k;
+}
 #endif
 
 }  // namespace dcp

@@ -216,6 +216,8 @@ def test_latents_behind_a_mask_may_be_anything(kernel, H):
         keep = np.arange(8) != bad
         got, gl = O.cpu().numpy()[:, keep], lse.cpu().numpy()[:, keep]
         G.check_partials(got, gl, ref[0][:, keep], ref[1][:, keep], "bad token %d" % bad)
+        if fill == 0x7FC0:  # and the row that sees a NaN does not hide it
+            assert np.isnan(O.cpu().numpy()[:, bad]).all() and np.isnan(lse.cpu().numpy()[:, bad]).all()
     # a chain's window: token 60 is behind the last rows' windows only
     kv = inp["kv_cache"].copy()
     kv[inp["block_table"][0, 60 // 16], 60 % 16] = 0x7FC0
