@@ -36,15 +36,13 @@ int current_sm_count() {
 // Most splits a (row, shard) pair with up to `lmax` local tokens may use:
 // enough (row, shard, split) units to give every SM work when there are few
 // rows (long-context B=1 decode), never splits shorter than kMinSplitTokens.
-static int64_t split_cap_units(int64_t units, int64_t lmax, int sm_count) {
-  int64_t want = sm_count / (units * kTargetCtasPerUnit);  // whole waves only
+static int64_t split_cap(int32_t T, int32_t D, int64_t lmax, int sm_count) {
+  const int64_t units = static_cast<int64_t>(T) * D * kTargetCtasPerUnit;
+  int64_t want = sm_count / units;  // whole waves only
   const int64_t cap_len = (lmax + kMinSplitTokens - 1) / kMinSplitTokens;
   if (want > cap_len) want = cap_len;
   if (want > kMaxSplits) want = kMaxSplits;
   return want < 1 ? 1 : want;
-}
-static int64_t split_cap(int32_t T, int32_t D, int64_t lmax, int sm_count) {
-  return split_cap_units(static_cast<int64_t>(T) * D, lmax, sm_count);
 }
 
 // `units` units of at most `lmax` tokens, cut into splits of whole tiles.
@@ -57,12 +55,37 @@ static SplitPlan cut(int64_t lmax, int64_t want) {
   if (p.splits < 1) p.splits = 1;
   return p;
 }
-static int32_t max_splits_units(int64_t units, int64_t lmax, int sm_count) {
-  return static_cast<int32_t>(split_cap_units(units, lmax, sm_count));
+// Splits of the windowed and tree decodes: `units` units of at most `lmax`
+// tokens on `clusters` resident clusters.  A unit costs about kUnitUs besides
+// its tiles (measured: 64 requests x 8 shards on a 64-token window take 102 us
+// of 7.2 waves, and 0.68 us more per 32-token tile), a split adds a partial to
+// write and read, and lengths are only known to be at most lmax (kFill of it
+// on average).  While all units run at once, the time is a unit's; beyond
+// that, list scheduling's: the work per cluster and one unit at the end.  So
+// few long units are cut until they fill the GPU, ragged ones until the last
+// one no longer shows (16 requests of 1,000 to 16,384 tokens: 391 us uncut),
+// and many short ones not at all.
+constexpr double kTileUs = 0.68, kUnitUs = 14.0, kMergeUs = 4.0, kPartialUs = 0.06, kFill = 0.6;
+constexpr int64_t kMinSelectSplit = 128;
+static int64_t select_splits(int64_t units, int64_t lmax, int sm_count) {
+  const double clusters = std::max(1, sm_count / kTargetCtasPerUnit);
+  const int64_t most = std::min<int64_t>(kMaxSplits, (lmax + kMinSelectSplit - 1) / kMinSelectSplit);
+  int64_t best = 1;
+  double least = 0;
+  for (int64_t s = 1; s <= most; ++s) {
+    const double n = static_cast<double>(units) * s, unit = kTileUs * ((lmax + s * kSplitRound - 1) / (s * kSplitRound));
+    double t = unit + kUnitUs + (s > 1 ? kMergeUs + kPartialUs * n : 0.0);
+    if (n > clusters) t += n / clusters * (kFill * unit + kUnitUs);
+    if (s == 1 || t < least) {
+      best = s;
+      least = t;
+    }
+  }
+  return best;
 }
-SplitPlan plan_units(int64_t units, int64_t lmax, int sm_count) {
+static SplitPlan plan_select(int64_t units, int64_t lmax, int sm_count) {
   if (lmax <= 0 || units <= 0) return SplitPlan{1, kSplitRound};
-  return cut(lmax, split_cap_units(units, lmax, sm_count));
+  return cut(lmax, select_splits(units, lmax, sm_count));
 }
 
 // Split-KV plan: pure function of its arguments (and the SM count).
@@ -150,7 +173,7 @@ DecodeLaunch select_launch(int32_t B, int32_t T, int32_t H, int32_t D, int32_t i
     lmax = std::min(lmax, most_owned(sel.sinks, D, interleave) +
                               most_owned(static_cast<int64_t>(sel.window) + max_q_len, D, interleave));
   const int64_t units = static_cast<int64_t>(B) * sel.chunks * Dn;
-  L.plan = dcp::plan_units(units, lmax, sms);
+  L.plan = dcp::plan_select(units, lmax, sms);
   L.need = dcp::split_workspace_bytes(L.plan, T, H, Dn);
   const int64_t all = (units + static_cast<int64_t>(sel.chunks) * Dn) * L.plan.splits;  // and the rows of no request
   L.obytes = order_bytes(all);
@@ -158,7 +181,9 @@ DecodeLaunch select_launch(int32_t B, int32_t T, int32_t H, int32_t D, int32_t i
   a.H = H;
   a.plan = L.plan;
   const char* force = std::getenv("DCP_FORCE_SIMT");
-  L.simt = (force && force[0] == '1') || !dcp::decode_tc_supported(a);
+  // (the tensor-core kernel counts in 32 bits)
+  L.simt = (force && force[0] == '1') || !dcp::decode_tc_supported(a) ||
+           static_cast<int64_t>(D) * interleave > 0x7fffffffLL;
   const int resident = dcp::decode_tc_resident_ctas();
   L.use_order = !L.simt && resident > 0 && all > resident / 2 && all <= 0x3fffffff && have_workspace &&
                 workspace_bytes >= L.need + L.obytes;
@@ -267,6 +292,13 @@ static dcp_status_t decode_partial_impl(const void* q, int64_t q_stride_tok, con
   // (split partials are in the output's dtype; those of the windowed and tree
   // decodes are fp32, so that a bf16 output is rounded once)
   a.o_bf16 = o_dtype == DCP_DTYPE_BF16 && !(select && launch.plan.splits > 1) ? 1 : 0;
+  if (select) {
+    sel.div_chunks = dcp::make_fastdiv(sel.chunks);
+    sel.div_splits = dcp::make_fastdiv(launch.plan.splits);
+    sel.div_Dn = dcp::make_fastdiv(Dn);
+    sel.div_period = dcp::make_fastdiv(static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(D) * interleave, 0x7fffffff)));
+    sel.div_H = dcp::make_fastdiv(H);
+  }
   a.sel = sel;
   a.num_blocks = num_blocks;
   a.block_size = block_size;
@@ -441,7 +473,7 @@ size_t dcp_decode_select_workspace_size(int32_t B, int32_t T, int32_t H, int32_t
   if (window > 0) lmax = std::min(lmax, static_cast<int64_t>(window) + num_sinks + max_q_len);
   const int32_t group = select_group(H, max_q_len);
   const int64_t units = static_cast<int64_t>(B) * ((max_q_len - 1) / group + 1) * D;
-  const dcp::SplitPlan p{dcp::max_splits_units(units, lmax, dcp::current_sm_count()), 0};
+  const dcp::SplitPlan p{static_cast<int32_t>(dcp::select_splits(units, lmax, dcp::current_sm_count())), 0};
   return dcp::split_workspace_bytes(p, T, H, D) +
          order_bytes((units + static_cast<int64_t>((max_q_len - 1) / group + 1) * D) * p.splits);
 }

@@ -75,9 +75,9 @@ decode_simt_kernel(DecodeArgs a) {
     ri.b = rows.b;
     ri.err = rows.err;
     if (rows.n > 0) {
-      span = sel_span(a, rows, d);
+      span = sel_span<false>(a, rows, d);
       own_len = a.sel.tree ? sel_tree_len(a, rows, rows.i0) : sel_chain_len(rows, rows.i0);
-      own = sel_row(a, rows, span, rows.i0, own_len, d);
+      own = sel_row<false>(a, rows, span, rows.i0, own_len, d);
       n_local = span.nv;
     }
   } else {
@@ -121,7 +121,7 @@ decode_simt_kernel(DecodeArgs a) {
             j = span.token_of(v);
             in = v < span.vb ? v < own.vend && (v < span.vs || v >= own.vlo)
                              : sel_tree_bit(a, rows, rows.i0, own_len,
-                                            static_cast<int32_t>(local_to_global(j, d, a.D, a.I)) - (rows.seq - rows.q_len));
+                                            sel_position<false>(a, j, d) - (rows.seq - rows.q_len));
           }
         }
         if (in) {

@@ -341,14 +341,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
   SelUnit su{};
   SelSpan span{};
   if constexpr (kSel) {
-    const SelCoords k = sel_coords(a, unit);
+    const SelCoords k = sel_coords(a, static_cast<int32_t>(unit));
     su = sel_unit(a, k.b, k.c);
     r = su.R.r0;
     d = a.d0 + k.dd;
     s = k.s;
     nl = su.R.n * a.H;
     if (su.R.err && threadIdx.x == 0 && score && k.c == 0 && k.dd == 0 && s == 0) report(a.dev_error, su.R.err);
-    if (su.live) span = sel_span(a, su.R, d);
+    if (su.live) span = sel_span<true>(a, su.R, d);
   } else {
     const UnitCoords uc = unit_coords(a, unit);
     r = uc.r;
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
       const int hh = p / 72, u = p - hh * 72;
       const int us = (u & ~7) | ((u & 7) ^ (hh & 7));
       if constexpr (kSel) {  // lane hh: head hh % H of the group's row hh / H
-        const int i = hh < nl ? hh / a.H : 0;
+        const int i = hh < nl ? fast_div(hh, a.sel.div_H) : 0;
         cp_async16_zfill(qs + hh * 1152 + us * 16,
                          qb + 2 * i * a.q_stride_tok + (hh < nl ? hh - i * a.H : 0) * 1152 + u * 16, hh < nl ? 16u : 0u);
       } else {
@@ -486,11 +486,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
       for (int i = warp - kSmWarp1; i < su.R.n; i += 4) {
         const int32_t row = su.R.i0 + i;
         const int32_t len = tree ? sel_tree_len(a, su.R, row) : sel_chain_len(su.R, row);
-        if (lane == 0) bar.row[i] = sel_row(a, su.R, span, row, len, d);
-        for (int w = 0; tree && w < kMaxTree / 32; ++w) {
+        if (lane == 0) bar.row[i] = sel_row<true>(a, su.R, span, row, len, d);
+        // (words past the request's tree tokens of this shard are zero)
+        const int nw = tree ? min((span.nv - span.vb + 31) / 32, kMaxTree / 32) : 0;
+        if (lane >= nw && lane < kMaxTree / 32) bar.tree[i][lane] = 0;
+        for (int w = 0; w < nw; ++w) {
           const int32_t t = 32 * w + lane;
-          const int32_t k = static_cast<int32_t>(local_to_global(span.token_of(span.vb + t), d, a.D, a.I)) -
-                            (su.R.seq - su.R.q_len);
+          const int32_t k = sel_position<true>(a, span.token_of(span.vb + t), d) - (su.R.seq - su.R.q_len);
           const uint32_t m = __ballot_sync(0xffffffffu, span.vb + t < span.nv && sel_tree_bit(a, su.R, row, len, k));
           if (lane == 0) bar.tree[i][w] = m;
         }
@@ -929,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
     float m_used = -INFINITY, l_sum = 0.f;
     const int sw = (h >> 1) & 3;  // 64-byte swizzle of row h
     // kSel: what this lane's row sees of the unit's index
-    const int row_i = kSel && h < nl ? h / a.H : 0;
+    const int row_i = kSel && h < nl ? fast_div(h, a.sel.div_H) : 0;
     SelRow see{0, 0};
     if (kSel && h < nl) see = bar.row[row_i];
     const uint32_t p_row = static_cast<uint32_t>((h >> 3) * 512 + (h & 7) * 64);
@@ -1263,6 +1265,41 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
       // warp's 16-byte writes and reads then hit 4 banks groups at most)
       float* scr = reinterpret_cast<float*>(smem + kOffStages) + warp * (32 * 36);
       const int nrows = min(32, nl - q4 * 32);
+      if (kSel && a.o_bf16) {
+        // bf16, two 32-column blocks at a time: rounded (to nearest even) in
+        // registers, so the transpose moves half the bytes and each row's
+        // store is a whole 128-byte line (8 lanes of 16 bytes)
+        unsigned char* buf = smem + kOffStages + warp * (32 * 144);
+        __nv_bfloat16* orow0 = static_cast<__nv_bfloat16*>(a.O_dst) + (pair0 + q4 * 32) * kLatent;
+        for (int c = c0; c < c0 + 8; c += 2) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t o[32];
+            tmem_ld32(lane_addr + kColO + 32 * (c + half), o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * i]) * inv,
+                                                               __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
+                w[i] = *reinterpret_cast<const uint32_t*>(&b);
+              }
+              *reinterpret_cast<uint4*>(buf + lane * 144 + 64 * half + 16 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            const int rr = 4 * m + (lane >> 3);
+            if (rr < nrows)
+              *reinterpret_cast<uint4*>(orow0 + rr * kLatent + 32 * c + 8 * (lane & 7)) =
+                  *reinterpret_cast<const uint4*>(buf + rr * 144 + 16 * (lane & 7));
+          }
+          __syncwarp();
+        }
+      } else
       for (int c = c0; c < c0 + 8; ++c) {
         uint32_t o[32];
         tmem_ld32(lane_addr + kColO + 32 * c, o);
@@ -1343,7 +1380,7 @@ __global__ void __launch_bounds__(1024) unit_order_kernel(DecodeArgs a, int32_t 
     if (a.sel.on) {
       const SelCoords k = sel_coords(a, u);
       const SelUnit U = sel_unit(a, k.b, k.c);
-      n = U.live ? sel_span(a, U.R, a.d0 + k.dd).nv : 0;
+      n = U.live ? sel_span<true>(a, U.R, a.d0 + k.dd).nv : 0;
       s = k.s;
     } else {
       const UnitCoords uc = unit_coords(a, u);

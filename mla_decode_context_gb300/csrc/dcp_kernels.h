@@ -45,6 +45,9 @@ struct SelectArgs {
   // tensor-core kernel: rows of a request that share a unit's 128 lanes, and
   // such groups per request (max_q_len / group, rounded up)
   int32_t group, chunks;
+  // (tensor-core kernel) division by the unit index's factors, the interleave
+  // period D x I (< 2^31 there) and H
+  FastDiv div_chunks, div_splits, div_Dn, div_period, div_H;
 };
 
 // Everything one decode launch needs (validated by the C ABI).

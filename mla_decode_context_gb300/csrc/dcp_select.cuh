@@ -46,6 +46,24 @@ struct SelRow {
 };
 
 #ifdef __CUDACC__
+// local_len and local_to_global with the launch's divisors: 64-bit divisions
+// by runtime values took half of a unit's set-up (8.5 us with them, 3.5 us
+// without).  kFast needs D x I < 2^31 (the tensor-core kernel); the CUDA-core
+// kernel takes any.
+template <bool kFast>
+__device__ __forceinline__ int32_t sel_local_len(const DecodeArgs& a, int32_t L, int32_t d) {
+  if constexpr (!kFast) return local_len(L, d, a.D, a.I);
+  const int32_t q = fast_div(L, a.sel.div_period);
+  const int32_t rem = L - q * static_cast<int32_t>(a.sel.div_period.d) - d * a.I;
+  return q * a.I + min(max(rem, 0), a.I);
+}
+template <bool kFast>
+__device__ __forceinline__ int32_t sel_position(const DecodeArgs& a, int32_t j, int32_t d) {
+  if constexpr (!kFast) return static_cast<int32_t>(local_to_global(j, d, a.D, a.I));
+  const int32_t q = fast_div(j, a.div_I);
+  return q * static_cast<int32_t>(a.sel.div_period.d) + d * a.I + (j - q * a.I);
+}
+
 __device__ __forceinline__ int32_t sel_prefix(const SelRows& R) { return max(0, R.seq - R.q_len); }
 
 // Own length of chain row i.
@@ -53,6 +71,7 @@ __device__ __forceinline__ int32_t sel_chain_len(const SelRows& R, int32_t i) {
   return max(0, R.seq - (R.q_len - 1 - i));
 }
 
+template <bool kFast>
 __device__ __forceinline__ SelSpan sel_span(const DecodeArgs& a, const SelRows& R, int32_t d) {
   const SelectArgs& s = a.sel;
   const bool tree = s.tree != nullptr;
@@ -60,10 +79,10 @@ __device__ __forceinline__ SelSpan sel_span(const DecodeArgs& a, const SelRows& 
   const int32_t P = tree ? sel_prefix(R) : sel_chain_len(R, R.i0 + R.n - 1);
   const int32_t shortest = tree ? P : sel_chain_len(R, R.i0);
   const int32_t start = s.window > 0 ? max(0, shortest - s.window) : 0;
-  const int32_t ns = local_len(min(s.sinks, P), d, a.D, a.I);
-  const int32_t lo = s.window > 0 ? max(ns, local_len(start, d, a.D, a.I)) : ns;
-  const int32_t nb = local_len(P, d, a.D, a.I);
-  const int32_t ne = tree ? local_len(max(0, R.seq), d, a.D, a.I) : nb;
+  const int32_t ns = sel_local_len<kFast>(a, min(s.sinks, P), d);
+  const int32_t lo = s.window > 0 ? max(ns, sel_local_len<kFast>(a, start, d)) : ns;
+  const int32_t nb = sel_local_len<kFast>(a, P, d);
+  const int32_t ne = tree ? sel_local_len<kFast>(a, max(0, R.seq), d) : nb;
   return SelSpan{ns, nb - (lo - ns), ne - (lo - ns), lo - ns};
 }
 
@@ -89,12 +108,13 @@ __device__ __forceinline__ int32_t sel_tree_len(const DecodeArgs& a, const SelRo
 }
 
 // Row i's part of the prefix; len: its own length (chain or tree).
+template <bool kFast>
 __device__ __forceinline__ SelRow sel_row(const DecodeArgs& a, const SelRows& R, const SelSpan& S, int32_t i,
                                           int32_t len, int32_t d) {
   const int32_t P = a.sel.tree ? sel_prefix(R) : len;
   SelRow r;
-  r.vend = a.sel.tree ? S.vb : S.index_of(local_len(P, d, a.D, a.I));
-  r.vlo = a.sel.window > 0 ? S.index_of(local_len(min(max(0, len - a.sel.window), P), d, a.D, a.I)) : 0;
+  r.vend = a.sel.tree ? S.vb : S.index_of(sel_local_len<kFast>(a, P, d));
+  r.vlo = a.sel.window > 0 ? S.index_of(sel_local_len<kFast>(a, min(max(0, len - a.sel.window), P), d)) : 0;
   return r;
 }
 
@@ -182,14 +202,13 @@ __device__ __forceinline__ SelUnit sel_unit(const DecodeArgs& a, int32_t b, int3
 struct SelCoords {
   int32_t b, c, dd, s;
 };
-__device__ __forceinline__ SelCoords sel_coords(const DecodeArgs& a, int64_t u) {
+__device__ __forceinline__ SelCoords sel_coords(const DecodeArgs& a, int32_t u) {
   SelCoords k;
-  k.c = static_cast<int32_t>(u % a.sel.chunks);
-  u /= a.sel.chunks;
-  k.s = static_cast<int32_t>(u % a.plan.splits);
-  u /= a.plan.splits;
-  k.dd = static_cast<int32_t>(u % a.Dn);
-  k.b = static_cast<int32_t>(u / a.Dn);
+  const int32_t v = fast_div(u, a.sel.div_chunks), w = fast_div(v, a.sel.div_splits);
+  k.c = u - v * a.sel.chunks;
+  k.s = v - w * a.plan.splits;
+  k.b = fast_div(w, a.sel.div_Dn);
+  k.dd = w - k.b * a.Dn;
   return k;
 }
 #endif

@@ -124,6 +124,23 @@ def test_workspace_query(L):
             f(*bad)
 
 
+def test_workspace_query_covers_every_interleave(L):
+    """A workspace of the queried size is never refused (status 5), whatever
+    the interleave, shard range and window; without a device a call that gets
+    past its checks ends in a CUDA error."""
+    if torch.cuda.is_available():
+        pytest.skip("would launch on addresses that are not memory")
+    rng = np.random.default_rng(0)
+    for _ in range(3000):
+        B, H, D = int(rng.integers(1, 65)), int(rng.choice([1, 5, 16, 40, 64, 128])), int(rng.choice([1, 2, 5, 8, 32]))
+        q = int(rng.choice([1, 2, 4, 17, 64]))
+        msl, win, sinks = int(np.exp(rng.uniform(0, 12))), int(rng.choice([0, 1, 100, 5000])), int(rng.choice([0, 4, 900]))
+        n = dcp.dcp_decode_select_workspace_size(B, B * q, H, D, msl, q, win, sinks)
+        st = _call(L, "tree", B=B, T=B * q, H=H, D=D, dn=D, I=int(rng.choice([1, 3, 64, 10000])), mql=q, msl=msl, win=win,
+                   sinks=sinks, bs=64, w=4096, ws=4096, qs=H * 576, wk=0x9000 if n else None, wb=n, ms=4)
+        assert st == 6, (B, H, D, q, msl, win, sinks)
+
+
 def _args(**kw):
     a = dict(q=torch.zeros((2, 16, 576), dtype=torch.bfloat16), kv=torch.zeros((4, 16, 576), dtype=torch.bfloat16),
              tab=torch.zeros((2, 4), dtype=torch.int32), seq=torch.zeros(2, dtype=torch.int32),
