@@ -67,8 +67,7 @@ static SplitPlan cut(int64_t lmax, int64_t want) {
 // and many short ones not at all.
 constexpr double kTileUs = 0.68, kUnitUs = 14.0, kMergeUs = 4.0, kPartialUs = 0.06, kFill = 0.6;
 constexpr int64_t kMinSelectSplit = 128;
-static int64_t select_splits(int64_t units, int64_t lmax, int sm_count) {
-  const double clusters = std::max(1, sm_count / kTargetCtasPerUnit);
+static int64_t select_splits(int64_t units, int64_t lmax, int clusters) {
   const int64_t most = std::min<int64_t>(kMaxSplits, (lmax + kMinSelectSplit - 1) / kMinSelectSplit);
   int64_t best = 1;
   double least = 0;
@@ -83,9 +82,9 @@ static int64_t select_splits(int64_t units, int64_t lmax, int sm_count) {
   }
   return best;
 }
-static SplitPlan plan_select(int64_t units, int64_t lmax, int sm_count) {
+static SplitPlan plan_select(int64_t units, int64_t lmax, int clusters) {
   if (lmax <= 0 || units <= 0) return SplitPlan{1, kSplitRound};
-  return cut(lmax, select_splits(units, lmax, sm_count));
+  return cut(lmax, select_splits(units, lmax, clusters));
 }
 
 // Split-KV plan: pure function of its arguments (and the SM count).
@@ -125,6 +124,7 @@ struct DecodeLaunch {
   size_t obytes;     // launch order of the units (optional tail)
   bool simt;         // CUDA-core kernel instead of the tensor-core one
   bool use_order;    // units start longest first (order kernel launched)
+  int64_t units;     // windowed and tree decodes: units of the launch
 };
 
 DecodeLaunch decode_launch(int32_t T, int32_t H, int32_t D, int32_t interleave, int32_t d0, int32_t Dn,
@@ -147,6 +147,13 @@ DecodeLaunch decode_launch(int32_t T, int32_t H, int32_t D, int32_t interleave, 
   return L;
 }
 
+// Clusters of the windowed and tree decodes that run at once (without a device
+// to ask: a GB300's).
+int select_clusters() {
+  const int n = dcp::decode_select_clusters();
+  return n > 0 ? n : 72;
+}
+
 size_t order_bytes(int64_t units) { return (static_cast<size_t>(units) * sizeof(int32_t) + 255) / 256 * 256; }
 
 // The windowed and tree decodes.  A unit is a group of rows of one request
@@ -164,29 +171,22 @@ int64_t most_owned(int64_t n, int32_t D, int32_t I) {
 }
 
 DecodeLaunch select_launch(int32_t B, int32_t T, int32_t H, int32_t D, int32_t interleave, int32_t d0, int32_t Dn,
-                           int32_t max_seq_len, int32_t max_q_len, const dcp::SelectArgs& sel, bool have_workspace,
-                           size_t workspace_bytes) {
+                           int32_t max_seq_len, int32_t max_q_len, int64_t cache_rows, const dcp::SelectArgs& sel,
+                           bool have_workspace, size_t workspace_bytes) {
   DecodeLaunch L{};
-  const int sms = dcp::current_sm_count();
   int64_t lmax = dcp::local_len(max_seq_len, d0, D, interleave);
   if (sel.window > 0)  // the sinks, and a window for each row of the request
     lmax = std::min(lmax, most_owned(sel.sinks, D, interleave) +
                               most_owned(static_cast<int64_t>(sel.window) + max_q_len, D, interleave));
   const int64_t units = static_cast<int64_t>(B) * sel.chunks * Dn;
-  L.plan = dcp::plan_select(units, lmax, sms);
+  L.plan = dcp::plan_select(units, lmax, select_clusters());
   L.need = dcp::split_workspace_bytes(L.plan, T, H, Dn);
-  const int64_t all = (units + static_cast<int64_t>(sel.chunks) * Dn) * L.plan.splits;  // and the rows of no request
-  L.obytes = order_bytes(all);
-  dcp::DecodeArgs a{};
-  a.H = H;
-  a.plan = L.plan;
+  L.units = (units + static_cast<int64_t>(sel.chunks) * Dn) * L.plan.splits;  // and the rows of no request
+  L.obytes = order_bytes(L.units);
   const char* force = std::getenv("DCP_FORCE_SIMT");
-  // (the tensor-core kernel counts in 32 bits)
-  L.simt = (force && force[0] == '1') || !dcp::decode_tc_supported(a) ||
-           static_cast<int64_t>(D) * interleave > 0x7fffffffLL;
-  const int resident = dcp::decode_tc_resident_ctas();
-  L.use_order = !L.simt && resident > 0 && all > resident / 2 && all <= 0x3fffffff && have_workspace &&
-                workspace_bytes >= L.need + L.obytes;
+  L.simt = (force && force[0] == '1') ||
+           !dcp::decode_select_supported(H, cache_rows, static_cast<int64_t>(D) * interleave);
+  L.use_order = !L.simt && L.units > select_clusters() && have_workspace && workspace_bytes >= L.need + L.obytes;
   return L;
 }
 }  // namespace
@@ -273,12 +273,13 @@ static dcp_status_t decode_partial_impl(const void* q, int64_t q_stride_tok, con
     sel.chunks = (max_q_len - 1) / sel.group + 1;
   }
   const DecodeLaunch launch =
-      select ? select_launch(B, T, H, D, interleave, d0, Dn, max_seq_len, max_q_len, sel, workspace != nullptr,
-                             workspace_bytes)
+      select ? select_launch(B, T, H, D, interleave, d0, Dn, max_seq_len, max_q_len,
+                             static_cast<int64_t>(num_blocks) * block_size, sel, workspace != nullptr, workspace_bytes)
              : decode_launch(T, H, D, interleave, d0, Dn, max_seq_len, workspace != nullptr, workspace_bytes,
                              kv_dtype == DCP_KV_FP8_E4M3);
   const dcp::SplitPlan plan = launch.plan;
   const size_t need = launch.need;
+  if (select && launch.units > 0x3fffffff) return DCP_ERR_INVALID_ARG;  // (max_q_len far beyond any step's rows)
   if (need > 0 && (workspace_bytes < need || !workspace)) return DCP_ERR_WORKSPACE_TOO_SMALL;
   if (need > 0 && !aligned16(workspace)) return DCP_ERR_MISALIGNED;
 
@@ -343,14 +344,15 @@ static dcp_status_t decode_partial_impl(const void* q, int64_t q_stride_tok, con
     // more units than clusters that fit at once: start the long ones first
     // (the order lives in the workspace past the split partials; a workspace
     // without room for it keeps index order)
-    const int64_t units =
-        (select ? (static_cast<int64_t>(B) + 1) * sel.chunks : static_cast<int64_t>(T)) * Dn * plan.splits;
+    const int64_t units = select ? launch.units : static_cast<int64_t>(T) * Dn * plan.splits;
     int32_t* order = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + need);
-    e = dcp::launch_unit_order(a, static_cast<int32_t>(units), order, st);
+    e = select ? dcp::launch_select_order(a, static_cast<int32_t>(units), order, st)
+               : dcp::launch_unit_order(a, static_cast<int32_t>(units), order, st);
     if (e != cudaSuccess) return DCP_ERR_CUDA;
     a.unit_order = order;
   }
-  e = simt ? dcp::launch_decode_simt(a, st) : dcp::launch_decode_tc(a, st);
+  e = simt ? dcp::launch_decode_simt(a, st)
+           : (select ? dcp::launch_decode_select(a, static_cast<int32_t>(launch.units), st) : dcp::launch_decode_tc(a, st));
   if (e != cudaSuccess) return DCP_ERR_CUDA;
   if (plan.splits > 1) {
     const int64_t pairs = static_cast<int64_t>(Dn) * T * H;
@@ -473,7 +475,7 @@ size_t dcp_decode_select_workspace_size(int32_t B, int32_t T, int32_t H, int32_t
   if (window > 0) lmax = std::min(lmax, static_cast<int64_t>(window) + num_sinks + max_q_len);
   const int32_t group = select_group(H, max_q_len);
   const int64_t units = static_cast<int64_t>(B) * ((max_q_len - 1) / group + 1) * D;
-  const dcp::SplitPlan p{static_cast<int32_t>(dcp::select_splits(units, lmax, dcp::current_sm_count())), 0};
+  const dcp::SplitPlan p{static_cast<int32_t>(dcp::select_splits(units, lmax, select_clusters())), 0};
   return dcp::split_workspace_bytes(p, T, H, D) +
          order_bytes((units + static_cast<int64_t>((max_q_len - 1) / group + 1) * D) * p.splits);
 }

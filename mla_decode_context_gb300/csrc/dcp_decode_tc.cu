@@ -72,25 +72,7 @@
 //               value: bf16 cache: receive-ring producers (chunks 0-3 of
 //                      every tile)
 // Every wait is bounded (a timeout sets DCP_DEVERR_TIMEOUT and ends the unit).
-//
-// kSel (the windowed and tree decodes, dcp_select.cuh): a unit is a group of
-// rows of one request, as many as fill the 128 lanes (lane = row x heads), so
-// rows of few heads share their tiles and their MMAs.  Its tiles walk the
-// dense index of the tokens that any of the rows sees; tokens that none of
-// them sees are zero-filled like bad ids, and each lane masks the rest by its
-// own row (two bounds and a bit string, made once per unit).  Lanes may then
-// see nothing for many tiles, and sinks may outweigh everything after them, so
-// the value CTA keeps O in the scale of the largest running max so far and
-// scales a later tile's P down instead of O up (which could overflow; it
-// happens in the one or two tiles after a jump of the max, whose weights are
-// then rounded to bf16 a second time).  A weight of 0
-// does not keep a NaN or an infinity of V out of a product, and a token that
-// only some of the rows see may hold one: a non-finite latent shows in every
-// lane's score, so the lanes that mask it report it and the value CTA clears
-// such values from that tile before PV (rows that see the token have a NaN
-// weight there and stay NaN).
 #include "dcp_kernels.h"
-#include "dcp_select.cuh"
 #include "dcp_sm100.cuh"
 
 #include <cuda_fp16.h>
@@ -122,12 +104,6 @@ constexpr int kPBytes = 128 * kTile * 2;         // P tile: 128 rows x 32 bf16, 
 constexpr int kPWarpBytes = kPBytes / 4;         // one softmax warp's 32 rows
 constexpr int kPSlotBytes = 9216;                // P tile + running max per head (+ pad)
 constexpr uint32_t kPTx = kPBytes + 128 * 4;     // bytes that fill one P slot
-// kSel: a softmax warp's 32 maxima are followed by a word (16 bytes in the
-// copy) that says whether its lanes met a non-finite score of a token they do
-// not see
-constexpr int kMaxBytes = 128 + 16;
-constexpr uint32_t kPTxSel = kPBytes + 4 * kMaxBytes;
-static_assert(kPTxSel <= kPSlotBytes && kPTx <= kPSlotBytes, "P and the maxima must fit their slot");
 constexpr int kSmWarp1 = kProdWarp0 + kProdWarps;  // score: second softmax group (4 warps)
 constexpr int kThreads = 32 * (kSmWarp1 + 4);
 constexpr float kRescaleLog2 = 8.0f;
@@ -186,12 +162,6 @@ struct __align__(8) Bars {
   uint32_t mask[16];
   uint32_t tmem;
   int32_t abort;
-  // kSel: each row's part of the unit's prefix, the least vlo, and the rows'
-  // tree tokens in the unit's index (bit t: token vb + t) with their union
-  SelRow row[kMaxGroup];
-  int32_t vlo;
-  uint32_t tree[kMaxGroup][kMaxTree / 32];
-  uint32_t any[kMaxTree / 32];
 };
 
 constexpr int kOffStages = 0;                            // score: stage ring
@@ -308,22 +278,10 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes, uint64_t s2
   return *reinterpret_cast<uint32_t*>(&b);
 }
 
-// bits [0, n) of a word
-__device__ __forceinline__ uint32_t low_bits(int32_t n) {
-  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
-}
-// bits [t, t + 32) of a string of kMaxTree bits (zeros outside)
-__device__ __forceinline__ uint32_t bits_at(const uint32_t* words, int32_t t) {
-  const int32_t w = t >> 5;
-  const uint32_t lo = w >= 0 && w < kMaxTree / 32 ? words[w] : 0u;
-  const uint32_t hi = w >= -1 && w < kMaxTree / 32 - 1 ? words[w + 1] : 0u;
-  return __funnelshift_r(lo, hi, t & 31);
-}
-
 // kFp8: the cache holds FP8 E4M3 codes (576 bytes a row) with one fp32 scale
 // per slot; the producers widen them to bf16 on their way into shared
 // memory, so everything downstream is the same as for a bf16 cache.
-template <bool kFp8, bool kSel>
+template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   TR_ENTRY();
@@ -336,27 +294,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
   const uint32_t peer = cta ^ 1u;
 
   const int64_t unit = a.unit_order ? __ldg(a.unit_order + (blockIdx.x >> 1)) : (blockIdx.x >> 1);
-  int r, d, s;    // (first) row, shard (of D), split
-  int nl = a.H;   // lanes in use
-  SelUnit su{};
-  SelSpan span{};
-  if constexpr (kSel) {
-    const SelCoords k = sel_coords(a, static_cast<int32_t>(unit));
-    su = sel_unit(a, k.b, k.c);
-    r = su.R.r0;
-    d = a.d0 + k.dd;
-    s = k.s;
-    nl = su.R.n * a.H;
-    if (su.R.err && threadIdx.x == 0 && score && k.c == 0 && k.dd == 0 && s == 0) report(a.dev_error, su.R.err);
-    if (su.live) span = sel_span<true>(a, su.R, d);
-  } else {
-    const UnitCoords uc = unit_coords(a, unit);
-    r = uc.r;
-    d = a.d0 + uc.dd;
-    s = uc.s;
-  }
+  const UnitCoords uc = unit_coords(a, unit);
+  const int r = uc.r;
+  const int d = a.d0 + uc.dd;  // shard (of D)
+  const int s = uc.s;
 
-  if (score && warp < 8 && (!kSel || su.live)) {
+  if (score && warp < 8) {
     // Q load, issued first (it depends only on the row) so that its latency
     // overlaps the row lookup's loads and the set-up.  The 147 KB of Q (128
     // heads x 576 dims, the same for every unit of a row) come in with one
@@ -368,53 +311,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
     for (int p = threadIdx.x; p < 128 * 72; p += 256) {
       const int hh = p / 72, u = p - hh * 72;
       const int us = (u & ~7) | ((u & 7) ^ (hh & 7));
-      if constexpr (kSel) {  // lane hh: head hh % H of the group's row hh / H
-        const int i = hh < nl ? fast_div(hh, a.sel.div_H) : 0;
-        cp_async16_zfill(qs + hh * 1152 + us * 16,
-                         qb + 2 * i * a.q_stride_tok + (hh < nl ? hh - i * a.H : 0) * 1152 + u * 16, hh < nl ? 16u : 0u);
-      } else {
-        cp_async16_zfill(qs + hh * 1152 + us * 16, qb + (hh < a.H ? hh : 0) * 1152 + u * 16, hh < a.H ? 16u : 0u);
-      }
+      cp_async16_zfill(qs + hh * 1152 + us * 16, qb + (hh < a.H ? hh : 0) * 1152 + u * 16, hh < a.H ? 16u : 0u);
     }
     cp_async_commit();
   }
 
-  RowInfo ri{};
-  int32_t n_local;
-  if constexpr (kSel) {
-    ri.b = su.R.b;
-    n_local = su.live ? span.nv : 0;
-  } else {
-    ri = resolve_row(a.seq_lens, a.qsl, a.B, r, a.max_seq_len, a.max_q_len);
-    if (ri.err && threadIdx.x == 0 && cta == 0 && d == a.d0 && s == 0) report(a.dev_error, ri.err);
-    n_local = ri.padding ? 0 : local_len(ri.L, d, a.D, a.I);
-  }
+  const RowInfo ri = resolve_row(a.seq_lens, a.qsl, a.B, r, a.max_seq_len, a.max_q_len);
+  if (ri.err && threadIdx.x == 0 && cta == 0 && d == a.d0 && s == 0) report(a.dev_error, ri.err);
+  const int32_t n_local = ri.padding ? 0 : local_len(ri.L, d, a.D, a.I);
   const int32_t lo = s * a.plan.chunk;
   const int32_t hi = min(n_local, lo + a.plan.chunk);
   const int ntiles = lo < hi ? (hi - lo + kTile - 1) / kTile : 0;
   const int64_t pair0 = ((static_cast<int64_t>(s) * a.Dn + (d - a.d0)) * a.T + r) * a.H;
 
-  if constexpr (kSel) {
-    // rows without anything to see here, and rows that no unit computes
-    const int64_t row0 = (static_cast<int64_t>(s) * a.Dn + (d - a.d0)) * a.T;
-    const int64_t row_bytes = a.o_bf16 ? 2 * kLatent : 4 * kLatent;
-#pragma unroll 1
-    for (int part = 0; part < 2; ++part) {
-      const int64_t first = (row0 + (part ? su.extra0 : r)) * a.H;
-      const int64_t n = static_cast<int64_t>(part ? su.extra : (ntiles == 0 ? su.R.n : 0)) * a.H;
-      if (score) {
-        for (int64_t i = threadIdx.x; i < n; i += kThreads) a.lse_dst[first + i] = -INFINITY;
-      } else {
-        uint4* o = reinterpret_cast<uint4*>(static_cast<unsigned char*>(a.O_dst) + first * row_bytes);
-        for (int64_t i = threadIdx.x; i < n * (row_bytes / 16); i += kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-    if (ntiles == 0) {
-      if (score && warp < 8) cp_async_wait<0>();
-      TR_EXIT(unit);
-      return;
-    }
-  }
   if (ntiles == 0) {
     if (score && warp < 8) cp_async_wait<0>();  // the Q copies land before the CTA leaves
     // empty shard / split or padding row: masked at the source, no KV read
@@ -468,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
     fence_mbar_init();
     if (!score) {
       // every P slot starts free: expect the first P tile and max column
-      for (int i = 0; i < kPSlots; ++i) mbar_arrive_expect_tx(&bar.p_full[i], kSel ? kPTxSel : kPTx);
+      for (int i = 0; i < kPSlots; ++i) mbar_arrive_expect_tx(&bar.p_full[i], kPTx);
       if (kFp8)
         for (int i = 0; i < kRecv; ++i) mbar_arrive_expect_tx(&bar.v_full[i], kHalfBytes);
       mbar_arrive_expect_tx(&bar.fin_l, 128 * 4);
@@ -477,38 +386,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
   if (warp == 10) {
     tmem_alloc(&bar.tmem, kTmemCols);
     tmem_relinquish();
-  }
-  if constexpr (kSel) {
-    // what each row of the group sees (warps 19-22, idle here; both CTAs: the
-    // producers of each need the union, the score CTA's softmax the rows)
-    if (warp >= kSmWarp1) {
-      const bool tree = a.sel.tree != nullptr;
-      for (int i = warp - kSmWarp1; i < su.R.n; i += 4) {
-        const int32_t row = su.R.i0 + i;
-        const int32_t len = tree ? sel_tree_len(a, su.R, row) : sel_chain_len(su.R, row);
-        if (lane == 0) bar.row[i] = sel_row<true>(a, su.R, span, row, len, d);
-        // (words past the request's tree tokens of this shard are zero)
-        const int nw = tree ? min((span.nv - span.vb + 31) / 32, kMaxTree / 32) : 0;
-        if (lane >= nw && lane < kMaxTree / 32) bar.tree[i][lane] = 0;
-        for (int w = 0; w < nw; ++w) {
-          const int32_t t = 32 * w + lane;
-          const int32_t k = sel_position<true>(a, span.token_of(span.vb + t), d) - (su.R.seq - su.R.q_len);
-          const uint32_t m = __ballot_sync(0xffffffffu, span.vb + t < span.nv && sel_tree_bit(a, su.R, row, len, k));
-          if (lane == 0) bar.tree[i][w] = m;
-        }
-      }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (warp == kSmWarp1) {
-        int32_t vlo = 0x7fffffff;
-        uint32_t m = 0;
-        for (int i = 0; i < su.R.n; ++i) {
-          vlo = min(vlo, bar.row[i].vlo);
-          if (tree && lane < kMaxTree / 32) m |= bar.tree[i][lane];
-        }
-        if (lane == 0) bar.vlo = vlo;
-        if (lane < kMaxTree / 32) bar.any[lane] = m;
-      }
-    }
   }
   tc_fence_before();
   __syncthreads();
@@ -584,19 +461,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
     const int32_t DI = a.D * a.I, dI = d * a.I;
     bool in_n[2] = {false, false};
     int32_t off_n[2] = {0, 0}, blk_n[2] = {-1, -1};  // row within its block, block id
-    const int32_t vlo = kSel ? bar.vlo : 0;
     auto fetch = [&](int jj) {  // positions fit in 32 bits (seq_lens are int32)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        int32_t l = lo + jj * kTile + (e ? row1 : row0);
+        const int32_t l = lo + jj * kTile + (e ? row1 : row0);
         in_n[e] = l < hi;
-        if constexpr (kSel) {
-          // seen by some row of the group?  Then its token of the shard.
-          const int32_t t = l - span.vb;
-          if (t >= 0 && in_n[e]) in_n[e] = t < kMaxTree && ((bar.any[t >> 5] >> (t & 31)) & 1u);
-          else in_n[e] = in_n[e] && (l < span.vs || l >= vlo);
-          l = span.token_of(l);
-        }
         // the table index: the shard token's position, or (per-shard
         // layout) the local token index itself
         const int32_t lq = fast_div(l, a.div_I);
@@ -930,10 +799,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
     const float sl2 = a.scale * kLog2e;
     float m_used = -INFINITY, l_sum = 0.f;
     const int sw = (h >> 1) & 3;  // 64-byte swizzle of row h
-    // kSel: what this lane's row sees of the unit's index
-    const int row_i = kSel && h < nl ? fast_div(h, a.sel.div_H) : 0;
-    SelRow see{0, 0};
-    if (kSel && h < nl) see = bar.row[row_i];
     const uint32_t p_row = static_cast<uint32_t>((h >> 3) * 512 + (h & 7) * 64);
     bool ok = true;
     // failure-path test hook: a wait that runs out (nothing completes `never`)
@@ -956,15 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
       TR_LAP(4, 1);  // softmax: waiting for S
       if (!ok) break;
       tc_fence_after();
-      uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&bar.mask[j & 15]);
-      uint32_t hidden = 0;  // kSel: loaded for another row of the group, not for this one
-      if constexpr (kSel) {
-        const int32_t v0 = lo + j * kTile;
-        uint32_t mine = low_bits(see.vend - v0) & (low_bits(span.vs - v0) | ~low_bits(see.vlo - v0));
-        if (v0 + kTile > span.vb && span.nv > span.vb && h < nl) mine |= bits_at(bar.tree[row_i], v0 - span.vb);
-        hidden = h < nl ? mask & ~mine : 0u;
-        mask &= mine;
-      }
+      const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&bar.mask[j & 15]);
       uint32_t sr[32], sr2[32];
       tmem_ld32(lane_addr + kColS + 96 * b, sr);
       tmem_ld32(lane_addr + kColS + 96 * b + 32, sr2);
@@ -986,14 +843,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
         f2_unpack(f2_add(f2_pack(sc[2 * i], sc[2 * i + 1]),
                          f2_pack(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]))),
                   sc[2 * i], sc[2 * i + 1]);
-      bool foul = false;
-      if constexpr (kSel) {
-        if (__any_sync(0xffffffffu, hidden != 0)) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) foul |= ((hidden >> i) & 1u) && !(fabsf(sc[i]) < INFINITY);
-          foul = __any_sync(0xffffffffu, foul);
-        }
-      }
       // online softmax in base 2: x = s * scale * log2(e), scaled before the
       // mask and the max so that any finite scale (zero and negative too)
       // keeps masked tokens at -inf; masked tokens get weight 0 by selection
@@ -1056,12 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
       for (int c = 0; c < 4; ++c)
         *reinterpret_cast<uint4*>(stg + p_row + ((c ^ sw) << 4)) =
             make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-      if constexpr (kSel) {
-        *reinterpret_cast<float*>(stg + kPBytes + q4 * kMaxBytes + 4 * lane) = m_used;
-        if (lane == 0) *reinterpret_cast<uint32_t*>(stg + kPBytes + q4 * kMaxBytes + 128) = foul ? 1u : 0u;
-      } else {
-        *reinterpret_cast<float*>(stg + kPBytes + 4 * h) = m_used;
-      }
+      *reinterpret_cast<float*>(stg + kPBytes + 4 * h) = m_used;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -1069,8 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
         const uint32_t peer_slot = map_peer(smem_base + kOffP + slot * kPSlotBytes, peer);
         const uint32_t peer_full = map_peer(smem_u32(&bar.p_full[slot]), peer);
         bulk_copy_to_peer(peer_slot + q4 * kPWarpBytes, stg + q4 * kPWarpBytes, kPWarpBytes, peer_full);
-        constexpr int kMx = kSel ? kMaxBytes : 128;
-        bulk_copy_to_peer(peer_slot + kPBytes + q4 * kMx, stg + kPBytes + q4 * kMx, kMx, peer_full);
+        bulk_copy_to_peer(peer_slot + kPBytes + q4 * 128, stg + kPBytes + q4 * 128, 128, peer_full);
       }
       TR_LAP(4, 5);  // softmax: P out
     }
@@ -1092,16 +935,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
         // (a group's m is final after its last tile and never returns to
         // -inf): the group of tile ntiles - 1, else the other group
         const bool last0 = ((ntiles - 1) & 1) == 0;
-        // (kSel: of the largest m of any tile)
-        float mo = kSel ? fmaxf(m_used, m1) : (last0 ? m_used : m1);
-        if (!kSel && mo == -INFINITY) mo = last0 ? m1 : m_used;
+        float mo = last0 ? m_used : m1;
+        if (mo == -INFINITY) mo = last0 ? m1 : m_used;
         float l = 0.f;
         if (m_used != -INFINITY) l += l_sum * ex2_approx(m_used - mo);
         if (m1 != -INFINITY) l += l1 * ex2_approx(m1 - mo);
-        const bool live = kSel ? l != 0.f : l > 0.f;  // (kSel: a NaN weight gives NaN, not an empty row)
+        const bool live = l > 0.f;
         st_async_peer_b32(map_peer(smem_base + kOffFin + 4 * h, peer), __float_as_uint(live ? 1.f / l : 0.f),
                           map_peer(smem_u32(&bar.fin_l), peer));
-        if (h < nl) a.lse_dst[pair0 + h] = live ? (mo + log2f(l)) * kLn2 : -INFINITY;
+        if (h < a.H) a.lse_dst[pair0 + h] = live ? (mo + log2f(l)) * kLn2 : -INFINITY;
       }
     }
   } else if (!score && warp == 10) {
@@ -1163,37 +1005,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
         if (!ok) break;
         // the slot's next fill (tile j + kPSlots) cannot start before PV(j)
         // frees it, and PV(j) waits for this warp's p_ok below
-        if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&bar.p_full[slot], kSel ? kPTxSel : kPTx);
+        if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&bar.p_full[slot], kPTx);
         ++pdone;
-        const unsigned char* mx = smem + kOffP + slot * kPSlotBytes + kPBytes;
-        const float m_new = *reinterpret_cast<const volatile float*>(mx + (kSel ? q4 * kMaxBytes + 4 * lane : 4 * h));
-        if constexpr (kSel) {
-          const uint32_t foul = *reinterpret_cast<const volatile uint32_t*>(mx + (lane & 3) * kMaxBytes + 128);
-          if (__any_sync(0xffffffffu, foul != 0)) {
-            // clear the tile's NaNs and infinities, a quarter per warp (both
-            // rings' slots refill only after PV(j), which waits for this
-            // warp's p_ok)
-            const int vs = j % kRecv, os = j % kOwn;
-            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bar.v_full[vs], (j / kRecv) & 1) &&
-                                             mbar_wait(&bar.own_loaded[os], (j / kOwn) & 1));
-            if (!ok) break;
-            for (int i = h; i < 2 * kHalfBytes / 16; i += 128) {
-              uint4* p = reinterpret_cast<uint4*>(smem + (i < kHalfBytes / 16 ? kOffRecv + vs * kHalfBytes + 16 * i
-                                                                             : kOffOwn + os * kHalfBytes + 16 * i - kHalfBytes));
-              uint4 x = *p;
-              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u;
-                if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0x0000ffffu;
-              }
-              *p = x;
-            }
-            fence_proxy_async_smem();
-          }
-        }
+        const float m_new = *reinterpret_cast<const volatile float*>(smem + kOffP + slot * kPSlotBytes + kPBytes + 4 * h);
         // a tile computed with m = -inf has P = 0 and leaves O as it is
-        const bool need = (kSel ? m_new > m_prev : m_new != m_prev) && m_prev != -INFINITY && m_new != -INFINITY;
+        const bool need = m_new != m_prev && m_prev != -INFINITY && m_new != -INFINITY;
         if (__any_sync(0xffffffffu, need)) {
           // O holds PV(0..j-1): wait for PV(j-1), then scale this warp's rows.
           // PV(j - 1 - kPSlots) is complete (P(j) needed its slot), and PV(j)
@@ -1213,33 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
           }
           tmem_wait_st();
         }
-        if constexpr (kSel) {
-          // a tile in a smaller max's scale than O's: this lane's 32 weights
-          // of P(j) (64 bytes, in any order) come down to O's
-          const bool down = m_new < m_prev && m_new != -INFINITY;
-          if (__any_sync(0xffffffffu, down)) {
-            if (down) {
-              const float f = ex2_approx(m_new - m_prev);
-              uint4* row = reinterpret_cast<uint4*>(smem + kOffP + slot * kPSlotBytes + (h >> 3) * 512 + (h & 7) * 64);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint4 x = row[i];
-                uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(w[k] << 16) * f,
-                                                                 __uint_as_float(w[k] & 0xffff0000u) * f);
-                  w[k] = *reinterpret_cast<const uint32_t*>(&y);
-                }
-                row[i] = x;
-              }
-            }
-            fence_proxy_async_smem();
-          }
-          if (m_new > m_prev) m_prev = m_new;
-        } else if (m_new != -INFINITY) {
-          m_prev = m_new;
-        }
+        if (m_new != -INFINITY) m_prev = m_new;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_ok[slot]);
@@ -1264,42 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tc_kernel(DecodeArgs a) {
       // 32 rows x 32 fp32 per block, rows 144 B apart (16-byte aligned; a
       // warp's 16-byte writes and reads then hit 4 banks groups at most)
       float* scr = reinterpret_cast<float*>(smem + kOffStages) + warp * (32 * 36);
-      const int nrows = min(32, nl - q4 * 32);
-      if (kSel && a.o_bf16) {
-        // bf16, two 32-column blocks at a time: rounded (to nearest even) in
-        // registers, so the transpose moves half the bytes and each row's
-        // store is a whole 128-byte line (8 lanes of 16 bytes)
-        unsigned char* buf = smem + kOffStages + warp * (32 * 144);
-        __nv_bfloat16* orow0 = static_cast<__nv_bfloat16*>(a.O_dst) + (pair0 + q4 * 32) * kLatent;
-        for (int c = c0; c < c0 + 8; c += 2) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t o[32];
-            tmem_ld32(lane_addr + kColO + 32 * (c + half), o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * i]) * inv,
-                                                               __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
-                w[i] = *reinterpret_cast<const uint32_t*>(&b);
-              }
-              *reinterpret_cast<uint4*>(buf + lane * 144 + 64 * half + 16 * k) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          __syncwarp();
-#pragma unroll
-          for (int m = 0; m < 8; ++m) {
-            const int rr = 4 * m + (lane >> 3);
-            if (rr < nrows)
-              *reinterpret_cast<uint4*>(orow0 + rr * kLatent + 32 * c + 8 * (lane & 7)) =
-                  *reinterpret_cast<const uint4*>(buf + rr * 144 + 16 * (lane & 7));
-          }
-          __syncwarp();
-        }
-      } else
+      const int nrows = min(32, a.H - q4 * 32);
       for (int c = c0; c < c0 + 8; ++c) {
         uint32_t o[32];
         tmem_ld32(lane_addr + kColO + 32 * c, o);
@@ -1376,18 +1131,10 @@ __global__ void __launch_bounds__(1024) unit_order_kernel(DecodeArgs a, int32_t 
   __shared__ int32_t wcnt[32][33];
   const int t = threadIdx.x, w = t >> 5, lane = t & 31;
   auto key_of = [&](int32_t u) -> int {
-    int32_t n, s;
-    if (a.sel.on) {
-      const SelCoords k = sel_coords(a, u);
-      const SelUnit U = sel_unit(a, k.b, k.c);
-      n = U.live ? sel_span<true>(a, U.R, a.d0 + k.dd).nv : 0;
-      s = k.s;
-    } else {
-      const UnitCoords uc = unit_coords(a, u);
-      const RowInfo ri = resolve_row(a.seq_lens, a.qsl, a.B, uc.r, a.max_seq_len, a.max_q_len);
-      n = ri.padding ? 0 : local_len(ri.L, a.d0 + uc.dd, a.D, a.I);
-      s = uc.s;
-    }
+    const UnitCoords uc = unit_coords(a, u);
+    const int r = uc.r, d = a.d0 + uc.dd, s = uc.s;
+    const RowInfo ri = resolve_row(a.seq_lens, a.qsl, a.B, r, a.max_seq_len, a.max_q_len);
+    const int32_t n = ri.padding ? 0 : local_len(ri.L, d, a.D, a.I);
     const int32_t lo = s * a.plan.chunk, hi = min(n, lo + a.plan.chunk);
     const int32_t tiles = lo < hi ? (hi - lo + kTile - 1) / kTile : 0;
     return tiles == 0 ? 0 : 32 - __clz(tiles);  // 1 + floor(log2 tiles)
@@ -1458,17 +1205,14 @@ int setup_current_device() {
   if (dev < 0 || dev >= kMaxDevices) return 0;
   std::lock_guard<std::mutex> lock(g_setup_mu);
   if (g_resident[dev] > 0) return g_resident[dev];
-  void (*const kernels[])(DecodeArgs) = {decode_tc_kernel<false, false>, decode_tc_kernel<true, false>,
-                                         decode_tc_kernel<false, true>, decode_tc_kernel<true, true>};
-  for (auto k : kernels)
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) {
-      cudaGetLastError();
-      return 0;
-    }
+  if (cudaFuncSetAttribute(decode_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(decode_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
+          cudaSuccess) { cudaGetLastError(); return 0; }
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = launch_config(1, nullptr, attr);
   int clusters = 0;
-  if (cudaOccupancyMaxActiveClusters(&clusters, decode_tc_kernel<false, false>, &cfg) != cudaSuccess || clusters <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&clusters, decode_tc_kernel<false>, &cfg) != cudaSuccess || clusters <= 0) {
     cudaGetLastError();
     return 0;
   }
@@ -1525,16 +1269,11 @@ extern "C" int dcp_timeline_fetch(void* dst, size_t bytes) {
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t st) {
   if (!decode_tc_supported(a)) return cudaErrorInvalidValue;
   if (setup_current_device() <= 0) return cudaErrorInvalidDevice;
-  const int64_t units =
-      (a.sel.on ? (static_cast<int64_t>(a.B) + 1) * a.sel.chunks : static_cast<int64_t>(a.T)) * a.Dn * a.plan.splits;
+  const int64_t units = static_cast<int64_t>(a.T) * a.Dn * a.plan.splits;
   if (2 * units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = launch_config(units, st, attr);
-  if (a.sel.on)
-    return a.kv_fp8 ? cudaLaunchKernelEx(&cfg, decode_tc_kernel<true, true>, a)
-                    : cudaLaunchKernelEx(&cfg, decode_tc_kernel<false, true>, a);
-  return a.kv_fp8 ? cudaLaunchKernelEx(&cfg, decode_tc_kernel<true, false>, a)
-                  : cudaLaunchKernelEx(&cfg, decode_tc_kernel<false, false>, a);
+  return a.kv_fp8 ? cudaLaunchKernelEx(&cfg, decode_tc_kernel<true>, a) : cudaLaunchKernelEx(&cfg, decode_tc_kernel<false>, a);
 }
 
 }  // namespace dcp

@@ -187,6 +187,15 @@ cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t st);
 // start first when there are more units than clusters that fit at once.
 cudaError_t launch_unit_order(const DecodeArgs& a, int32_t units, int32_t* order, cudaStream_t st);
 
+// The windowed and tree decodes on the tensor cores (persistent clusters over
+// `units` units: (B + 1) x chunks x Dn x splits, the last request's standing
+// for the rows of no request), the order in which they take them, and how many
+// clusters fit on the current device (0 if unknown).
+bool decode_select_supported(int32_t H, int64_t cache_rows, int64_t period);
+int decode_select_clusters();
+cudaError_t launch_select_order(const DecodeArgs& a, int32_t units, int32_t* order, cudaStream_t st);
+cudaError_t launch_decode_select(const DecodeArgs& a, int32_t units, cudaStream_t st);
+
 bool decode_tc_supported(const DecodeArgs& a);
 // CTAs of the tensor-core decode resident at once on the current device
 // (0 if unknown); the split plan sizes one wave from it.

@@ -47,9 +47,9 @@ struct SelRow {
 
 #ifdef __CUDACC__
 // local_len and local_to_global with the launch's divisors: 64-bit divisions
-// by runtime values took half of a unit's set-up (8.5 us with them, 3.5 us
-// without).  kFast needs D x I < 2^31 (the tensor-core kernel); the CUDA-core
-// kernel takes any.
+// by runtime values took a quarter of a short unit's time (512 units of two
+// tiles: 134 us with them, 102 us without).  kFast needs D x I < 2^31 (the
+// tensor-core kernel); the CUDA-core kernel takes any.
 template <bool kFast>
 __device__ __forceinline__ int32_t sel_local_len(const DecodeArgs& a, int32_t L, int32_t d) {
   if constexpr (!kFast) return local_len(L, d, a.D, a.I);
