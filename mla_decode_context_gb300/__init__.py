@@ -357,43 +357,64 @@ def dcp_decode_select_workspace_size(B: int, T: int, H: int, D: int, max_seq_len
 def _decode_select(where, tree_mask, q, kv_cache, block_table, seq_lens, query_start_loc, O_part, lse_part, D,
                    interleave, scale, window, num_sinks, max_seq_len, max_q_len, kv_scale, shard_begin, shard_count,
                    workspace, dev_error, stream) -> None:
+    """The two selecting decodes' checks (as _decode_geometry's: what the
+    kernels index by, shapes before devices) and call."""
     if shard_count is None:
         shard_count = D - shard_begin
-    local = isinstance(block_table, torch.Tensor) and block_table.dim() == 3
-    extra = []
-    if where == "dcp_mla_decode_partial_tree":
-        if not isinstance(tree_mask, torch.Tensor) or tree_mask.dtype != torch.int64:
-            raise TypeError("tree_mask must be an int64 tensor (see pack_tree_mask)")
-        words = (max_q_len + 63) // 64
-        if tree_mask.dim() != 2 or tree_mask.shape[0] != q.shape[0] or tree_mask.shape[1] < words or \
-                (tree_mask.shape[1] > 1 and tree_mask.stride(1) != 1):
-            raise ValueError("tree_mask must be [T, >= %d] words with unit column stride" % words)
-        extra = [_ptr(tree_mask), tree_mask.stride(0) if tree_mask.shape[0] > 1 else words]
-    B, T, H = _decode_geometry(q, kv_cache, block_table, seq_lens, query_start_loc, O_part, lse_part, shard_count,
-                               local=local)
+    tree = where is _TREE
+    if not isinstance(O_part, torch.Tensor) or O_part.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("O_part must be a bfloat16 or float32 tensor")
     fp8 = _cache_format(kv_cache, kv_scale)
+    i32 = torch.int32
+    args = [("kv_cache", kv_cache, kv_cache.dtype, True), ("q", q, torch.bfloat16, False),
+            ("block_table", block_table, i32, False), ("seq_lens", seq_lens, i32, True),
+            ("query_start_loc", query_start_loc, i32, True), ("O_part", O_part, O_part.dtype, True),
+            ("lse_part", lse_part, torch.float32, True)]
+    if tree:
+        args.append(("tree_mask", tree_mask, torch.int64, False))
     if fp8:
-        _need(kv_scale, "kv_scale", torch.float32)
-    if extra:
-        _need(tree_mask, "tree_mask", torch.int64, contiguous=False)
-    _need_opt(workspace, "workspace", allow_empty=True)
-    if workspace is not None and workspace.numel() == 0:
-        workspace = None
-    _need_opt(dev_error, "dev_error", torch.int32)
-    guard = _same_device(kv_cache.device, q=q, block_table=block_table, seq_lens=seq_lens,
-                         query_start_loc=query_start_loc, O_part=O_part, lse_part=lse_part, kv_scale=kv_scale,
-                         tree_mask=tree_mask, workspace=workspace, dev_error=dev_error)
+        args.append(("kv_scale", kv_scale, torch.float32, True))
+    if workspace is not None:
+        args.append(("workspace", workspace, getattr(workspace, "dtype", None), True))
+    if dev_error is not None:
+        args.append(("dev_error", dev_error, i32, False))
+    _types(args)
+    if q.dim() != 3 or q.shape[2] != KV_DIM or q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != KV_DIM):
+        raise ValueError("q must be [T, H, 576] with contiguous heads")
+    T, H = q.shape[0], q.shape[1]
+    local = block_table.dim() == 3
+    if block_table.dim() not in (2, 3) or block_table.stride(-1) != 1 or (local and block_table.shape[0] != shard_count):
+        raise ValueError("block_table must be [B, W] or [shard_count, B, W] with unit column stride")
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    if tuple(query_start_loc.shape) != (B + 1,) or block_table.shape[-2] != B:
+        raise ValueError("seq_lens [B], query_start_loc [B + 1] and block_table [.., B, W] disagree on B")
+    if tuple(O_part.shape) != (shard_count, T, H, LATENT_DIM) or tuple(lse_part.shape) != (shard_count, T, H):
+        raise ValueError("O_part must be [D, T, H, 512] and lse_part [D, T, H]")
+    extra = ()
+    if tree:
+        words = (max_q_len + 63) // 64
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != T or tree_mask.shape[1] < words or \
+                (tree_mask.shape[1] > 1 and tree_mask.stride(1) != 1):
+            raise ValueError("tree_mask must be [T, >= %d] words with unit column stride (see pack_tree_mask)" % words)
+        extra = (tree_mask.data_ptr(), tree_mask.stride(0) if T > 1 else words)
+    if dev_error is not None and dev_error.numel() == 0:
+        raise ValueError("dev_error must not be empty")
+    device = _placed(args)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with guard, _Range(where):
+    with _on(device), _Range(where):
         st = getattr(lib(), where)(
-            _ptr(q), q.stride(0) if T > 1 else H * KV_DIM, _ptr(kv_cache), KV_FP8_E4M3 if fp8 else KV_BF16,
-            _ptr(kv_scale), kv_cache.shape[0], kv_cache.shape[1], _ptr(block_table), block_table.shape[-1],
-            block_table.stride(-2), 1 if local else 0, block_table.stride(0) if local else 0, shard_begin,
-            shard_count, _ptr(seq_lens), _ptr(query_start_loc), B, T, H, max_seq_len, max_q_len, D, interleave,
-            scale, *extra, window, num_sinks, _ptr(O_part),
-            DTYPE_BF16 if O_part.dtype == torch.bfloat16 else DTYPE_F32, _ptr(lse_part), _ptr(workspace), ws_bytes,
-            _ptr(dev_error), _stream(stream))
+            q.data_ptr(), q.stride(0) if T > 1 else H * KV_DIM, kv_cache.data_ptr(),
+            KV_FP8_E4M3 if fp8 else KV_BF16, _addr(kv_scale), kv_cache.shape[0], kv_cache.shape[1],
+            block_table.data_ptr(), block_table.shape[-1], block_table.stride(-2), 1 if local else 0,
+            block_table.stride(0) if local else 0, shard_begin, shard_count, seq_lens.data_ptr(),
+            query_start_loc.data_ptr(), B, T, H, max_seq_len, max_q_len, D, interleave, scale, *extra, window,
+            num_sinks, O_part.data_ptr(), DTYPE_BF16 if O_part.dtype == torch.bfloat16 else DTYPE_F32,
+            lse_part.data_ptr(), workspace.data_ptr() if ws_bytes else None, ws_bytes, _addr(dev_error),
+            _stream_of(stream, device))
     _check(st, where)
+
+
+_WINDOW, _TREE = "dcp_mla_decode_partial_window", "dcp_mla_decode_partial_tree"
 
 
 def dcp_mla_decode_partial_window(q, kv_cache, block_table, seq_lens, query_start_loc, O_part, lse_part, *,
@@ -405,7 +426,7 @@ def dcp_mla_decode_partial_window(q, kv_cache, block_table, seq_lens, query_star
     """The decode over a sliding window: each row sees the last ``window``
     tokens of its own context (0: all) and its first ``num_sinks``.  Other
     arguments as for dcp_mla_decode_partial_v2."""
-    _decode_select("dcp_mla_decode_partial_window", None, q, kv_cache, block_table, seq_lens, query_start_loc, O_part,
+    _decode_select(_WINDOW, None, q, kv_cache, block_table, seq_lens, query_start_loc, O_part,
                    lse_part, D, interleave, scale, window, num_sinks, max_seq_len, max_q_len, kv_scale, shard_begin,
                    shard_count, workspace, dev_error, stream)
 
@@ -422,7 +443,7 @@ def dcp_mla_decode_partial_tree(q, kv_cache, block_table, seq_lens, query_start_
     in its row of tree_mask (int64 words [T, >= max_q_len / 64], see
     pack_tree_mask).  window and num_sinks as for the window decode, over the
     row's own sequence.  Other arguments as for dcp_mla_decode_partial_v2."""
-    _decode_select("dcp_mla_decode_partial_tree", tree_mask, q, kv_cache, block_table, seq_lens, query_start_loc,
+    _decode_select(_TREE, tree_mask, q, kv_cache, block_table, seq_lens, query_start_loc,
                    O_part, lse_part, D, interleave, scale, window, num_sinks, max_seq_len, max_q_len, kv_scale,
                    shard_begin, shard_count, workspace, dev_error, stream)
 
@@ -539,15 +560,50 @@ def dcp_decode_concat_cache(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q_out, kv_c
     _check(st, "dcp_decode_concat_cache")
 
 
-def _same_device(device, **tensors):
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream() without the object: 0.1 of 3 us
+
+
+def _stream_of(stream, device: int):
+    if stream is None:
+        return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _types(args) -> None:
+    """args: (name, tensor, dtype, contiguous).  The first half of a call's
+    checks; _placed is the second, after the shapes."""
+    for name, t, dtype, _ in args:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+        if t.dtype != dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+
+
+def _placed(args) -> int:
+    """Every tensor on one CUDA device (its index is returned), contiguous
+    where it must be."""
+    device = args[0][1].get_device()
+    for name, t, _, contiguous in args:
+        if t.get_device() != device or device < 0:
+            if t.get_device() < 0:
+                raise ValueError("%s must be a CUDA tensor" % name)
+            raise ValueError("%s is on cuda:%d, %s on cuda:%d" % (name, t.get_device(), args[0][0], device))
+        if contiguous and not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+    return device
+
+
+def _on(device: int):
     """A context in which `device` is the current one (the library launches on
-    the current device); tensors elsewhere are refused."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError("%s is on %s, kv_cache on %s" % (name, t.device, device))
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    the current device)."""
+    return _HERE if device == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _cache_format(kv_cache, kv_scale):
@@ -576,13 +632,20 @@ def dcp_decode_concat_cache_v2(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q_out, k
     E4M3 codes with kv_scale fp32 [num_blocks, block_size] (each written row
     gets its own power-of-two scale).  ql_nope, q_pe and q_out may all be None
     to write the cache alone."""
+    bf16 = torch.bfloat16
     query = ql_nope is not None or q_pe is not None or q_out is not None
-    args = [("kv_c", kv_c, 2, LATENT_DIM), ("k_pe", k_pe, 2, ROPE_DIM)]
+    fp8 = _cache_format(kv_cache, kv_scale)
+    args = [("kv_cache", kv_cache, kv_cache.dtype, True), ("kv_c", kv_c, bf16, False), ("k_pe", k_pe, bf16, False)]
+    rows = [("kv_c", kv_c, 2, LATENT_DIM), ("k_pe", k_pe, 2, ROPE_DIM)]
     if query:
-        args += [("ql_nope", ql_nope, 3, LATENT_DIM), ("q_pe", q_pe, 3, ROPE_DIM), ("q_out", q_out, 3, KV_DIM)]
-    for name, t, dims, last in args:
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
-            raise TypeError("%s must be a %s tensor" % (name, torch.bfloat16))
+        args += [("ql_nope", ql_nope, bf16, False), ("q_pe", q_pe, bf16, False), ("q_out", q_out, bf16, False)]
+        rows += [("ql_nope", ql_nope, 3, LATENT_DIM), ("q_pe", q_pe, 3, ROPE_DIM), ("q_out", q_out, 3, KV_DIM)]
+    if fp8:
+        args.append(("kv_scale", kv_scale, torch.float32, True))
+    if dev_error is not None:
+        args.append(("dev_error", dev_error, torch.int32, False))
+    _types(args)
+    for name, t, dims, last in rows:
         if t.dim() != dims or t.shape[-1] != last or t.stride(-1) != 1:
             raise ValueError("%s must have %d dims, last of size %d with unit stride" % (name, dims, last))
     T = kv_c.shape[0]
@@ -594,28 +657,23 @@ def dcp_decode_concat_cache_v2(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q_out, k
     if not isinstance(slot_mapping, torch.Tensor) or slot_mapping.dtype != torch.int64 or \
             tuple(slot_mapping.shape) != (T,):
         raise ValueError("slot_mapping must be an int64 [T] tensor")
-    fp8 = _cache_format(kv_cache, kv_scale)
-    for name, t, _, _ in args:
-        _need(t, name, torch.bfloat16, contiguous=False)
-    _need(slot_mapping, "slot_mapping", torch.int64)
-    _need(kv_cache, "kv_cache", kv_cache.dtype)
-    if fp8:
-        _need(kv_scale, "kv_scale", torch.float32)
-    _need_opt(dev_error, "dev_error", torch.int32)
-    guard = _same_device(kv_cache.device, kv_c=kv_c, k_pe=k_pe, ql_nope=ql_nope, q_pe=q_pe, q_out=q_out,
-                         slot_mapping=slot_mapping, kv_scale=kv_scale, dev_error=dev_error)
+    args.append(("slot_mapping", slot_mapping, torch.int64, True))
+    if dev_error is not None and dev_error.numel() == 0:
+        raise ValueError("dev_error must not be empty")
+    device = _placed(args)
     if T == 0:
         return
-
-    def step(t, dim):  # the stride of a dimension of one element is never used
-        return t.stride(dim) if t is not None and t.shape[dim] > 1 else 0
-    q_step = H * KV_DIM if T == 1 else step(q_out, 0)
-    with guard, _Range("dcp_decode_concat_cache_v2"):
+    strides = [0] * 4
+    if query:  # (the stride of a dimension of one element is never used)
+        strides = [t.stride(d) if t.shape[d] > 1 else 0 for t in (ql_nope, q_pe) for d in (0, 1)]
+    many = T > 1
+    with _on(device), _Range("dcp_decode_concat_cache_v2"):
         st = lib().dcp_decode_concat_cache_v2(
-            _ptr(ql_nope), step(ql_nope, 0), step(ql_nope, 1), _ptr(q_pe), step(q_pe, 0), step(q_pe, 1), _ptr(kv_c),
-            step(kv_c, 0), _ptr(k_pe), step(k_pe, 0), _ptr(slot_mapping), T, H, _ptr(q_out), q_step,
-            _ptr(kv_cache), KV_FP8_E4M3 if fp8 else KV_BF16, _ptr(kv_scale),
-            kv_cache.shape[0] * kv_cache.shape[1], _ptr(dev_error), _stream(stream))
+            _addr(ql_nope), strides[0], strides[1], _addr(q_pe), strides[2], strides[3], kv_c.data_ptr(),
+            kv_c.stride(0) if many else 0, k_pe.data_ptr(), k_pe.stride(0) if many else 0, slot_mapping.data_ptr(), T,
+            H, _addr(q_out), q_out.stride(0) if query and many else H * KV_DIM, kv_cache.data_ptr(),
+            KV_FP8_E4M3 if fp8 else KV_BF16, _addr(kv_scale), kv_cache.shape[0] * kv_cache.shape[1],
+            _addr(dev_error), _stream_of(stream, device))
     _check(st, "dcp_decode_concat_cache_v2")
 
 
@@ -631,13 +689,17 @@ def dcp_latent_cache_read(kv_cache, block_table, cu_lens, out, *, seq_starts: Op
     if shard_count is None:
         shard_count = D - shard_begin
     fp8 = _cache_format(kv_cache, kv_scale)
-    ints = [("block_table", block_table), ("cu_lens", cu_lens)] + \
-        ([("seq_starts", seq_starts)] if seq_starts is not None else [])
-    for name, t in ints:
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
-            raise TypeError("%s must be an int32 tensor" % name)
     if not isinstance(out, torch.Tensor) or out.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out must be a bfloat16 or float32 tensor")
+    args = [("kv_cache", kv_cache, kv_cache.dtype, True), ("block_table", block_table, torch.int32, False),
+            ("cu_lens", cu_lens, torch.int32, True), ("out", out, out.dtype, False)]
+    if seq_starts is not None:
+        args.append(("seq_starts", seq_starts, torch.int32, True))
+    if fp8:
+        args.append(("kv_scale", kv_scale, torch.float32, True))
+    if dev_error is not None:
+        args.append(("dev_error", dev_error, torch.int32, False))
+    _types(args)
     if out.dim() != 2 or out.shape[1] != KV_DIM or out.stride(1) != 1:
         raise ValueError("out must be [N, 576] with unit column stride")
     if cu_lens.dim() != 1 or cu_lens.shape[0] < 1:
@@ -649,26 +711,21 @@ def dcp_latent_cache_read(kv_cache, block_table, cu_lens, out, *, seq_starts: Op
         raise ValueError("block_table must be [B, W] or [shard_count, B, W] with unit column stride")
     if seq_starts is not None and tuple(seq_starts.shape) != (B,):
         raise ValueError("seq_starts must be [B]")
+    if dev_error is not None and dev_error.numel() == 0:
+        raise ValueError("dev_error must not be empty")
     if D < 1 or D > MAX_SHARDS or shard_begin < 0 or shard_count < 1 or shard_begin + shard_count > D:
         raise ValueError("shards [shard_begin, shard_begin + shard_count) must lie in [0, D), D <= %d" % MAX_SHARDS)
-    _need(kv_cache, "kv_cache", kv_cache.dtype)
-    if fp8:
-        _need(kv_scale, "kv_scale", torch.float32)
-    for name, t in ints:
-        _need(t, name, torch.int32, contiguous=name != "block_table")
-    _need(out, "out", out.dtype, contiguous=False)
-    _need_opt(dev_error, "dev_error", torch.int32)
-    guard = _same_device(kv_cache.device, kv_scale=kv_scale, out=out, dev_error=dev_error, **dict(ints))
+    device = _placed(args)
     if B == 0 or N == 0:
         return
-    with guard, _Range("dcp_latent_cache_read"):
+    with _on(device), _Range("dcp_latent_cache_read"):
         st = lib().dcp_latent_cache_read(
-            _ptr(kv_cache), KV_FP8_E4M3 if fp8 else KV_BF16, _ptr(kv_scale), kv_cache.shape[0], kv_cache.shape[1],
-            _ptr(block_table), block_table.shape[-1], block_table.stride(-2), 1 if local else 0,
-            block_table.stride(0) if local else 0, D, interleave, shard_begin, shard_count, _ptr(seq_starts),
-            _ptr(cu_lens), B, N, _ptr(out), DTYPE_F32 if out.dtype == torch.float32 else DTYPE_BF16,
-            out.stride(0) if N > 1 else KV_DIM,
-            _ptr(dev_error), _stream(stream))
+            kv_cache.data_ptr(), KV_FP8_E4M3 if fp8 else KV_BF16, _addr(kv_scale), kv_cache.shape[0],
+            kv_cache.shape[1], block_table.data_ptr(), block_table.shape[-1], block_table.stride(-2),
+            1 if local else 0, block_table.stride(0) if local else 0, D, interleave, shard_begin, shard_count,
+            _addr(seq_starts), cu_lens.data_ptr(), B, N, out.data_ptr(),
+            DTYPE_F32 if out.dtype == torch.float32 else DTYPE_BF16, out.stride(0) if N > 1 else KV_DIM,
+            _addr(dev_error), _stream_of(stream, device))
     _check(st, "dcp_latent_cache_read")
 
 

@@ -174,11 +174,12 @@ struct __align__(8) Bars {
   uint64_t o_free;            // value: unit k's O has been read from TMEM (8 warps)
   uint64_t fin_l[kFinSlots];  // value: 1/l of unit k's lanes arrived
   uint64_t fin[1 + kSParts * kSBuf];  // each issuing warp's MMAs complete
-  uint64_t m_pub[8];          // score: running max after tile j posted (4 warps)
+  uint64_t m_pub[2];          // score: max after unit k's first tile posted (4 warps)
   uint64_t sm_fin;            // score: both softmax groups' l and m of unit k written (8 warps)
   uint64_t ud_full[kUnits], ud_free[kUnits];  // descriptor written / no longer needed (every other warp)
   uint64_t never;             // test hook only: initialised, never arrived on
   int32_t claimed[2];         // score: how many of its items producer group g has claimed a stage for
+  int32_t seen[2];            // score (fp8): tiles of S slot b whose kv_full its first issuer has seen, and it
   uint32_t mask[16];          // score: valid rows of tile j in mask[j % 16]
   uint32_t tmem;
   int32_t abort;
@@ -191,7 +192,7 @@ constexpr int kOffRecv = kOwn * kHalfBytes;              // value: receive ring
 constexpr int kOffP = kStages * kStageBytes;             // value: P slots; score: P staging
 constexpr int kOffMax = kOffP + kPSlots * kPBytes;       // the same for the maxima
 constexpr int kOffSm = kOffMax + kPSlots * 4 * kMaxBytes;
-constexpr int kSmBytes = (8 + 2 * 4) * 128 * 4;          // score: running max per tile (8), l and m of two units
+constexpr int kSmBytes = (2 + 2 * 4) * 128 * 4;          // score: first tile's max, l and m, of two units
 constexpr int kOffFin = kOffSm;                          // value: 1/l per lane, kFinSlots units
 constexpr int kOffBars = kOffSm + kSmBytes;
 constexpr int kSmemBytes = kOffBars + static_cast<int>(sizeof(Bars)) + 1024;  // + alignment slack
@@ -278,6 +279,27 @@ __device__ __forceinline__ void store32(unsigned char* p, const uint32_t (&w)[8]
   } else {
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// 4 x 4 transpose of 32-byte sectors over each four lanes: lane t comes with
+// the four sectors of its own row and leaves with sector t % 4 of the four rows
+// of its lanes (slot i: row t - t % 4 + i), so that four lanes store a row's
+// whole 128-byte line.
+__device__ __forceinline__ void transpose_sectors(uint32_t (&o)[32], int lane) {
+#pragma unroll
+  for (int x = 1; x < 4; x <<= 1) {
+    const bool up = lane & x;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      if (a & x) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t &lo = o[8 * a + i], &hi = o[8 * (a | x) + i];
+        const uint32_t got = __shfl_xor_sync(kFull, up ? lo : hi, x);
+        if (up) lo = got; else hi = got;
+      }
+    }
   }
 }
 
@@ -607,11 +629,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
     mbar_init(&bar.o_free, 8);
     for (int i = 0; i < kFinSlots; ++i) mbar_init(&bar.fin_l[i], 1);
     for (int i = 0; i < 1 + kSParts * kSBuf; ++i) mbar_init(&bar.fin[i], 1);
-    for (int i = 0; i < 8; ++i) mbar_init(&bar.m_pub[i], 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&bar.m_pub[i], 4);
     mbar_init(&bar.sm_fin, 8);
     for (int i = 0; i < kUnits; ++i) { mbar_init(&bar.ud_full[i], 1); mbar_init(&bar.ud_free[i], kThreads / 32 - 1); }
     mbar_init(&bar.never, 1);
     bar.claimed[0] = bar.claimed[1] = 0;
+    bar.seen[0] = bar.seen[1] = 0;
     bar.abort = 0;
     fence_mbar_init();
     if (!score) {
@@ -689,14 +712,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
   } else if (score && (group == 0 || group == 5)) {
     take_regs<Regs<kFp8>::softmax>();
     // ------------------------------------------------------------- softmax
-    // As in the plain decode: two groups take alternate tiles, each with its
-    // own running max and sum; before a unit's tile i a group adopts, if
-    // larger, the other group's max after tile i - 3 (tile 0 for tile 1), at a
-    // fixed lag, so results do not depend on timing.
+    // Two groups take alternate tiles, each with its own running max and sum.
+    // A unit's second tile starts from its first one's max, so that both
+    // groups keep to the same one until it has to grow by more than 2^8; what
+    // a group finds later stays its own (the value CTA brings tiles of
+    // different maxima together), so results do not depend on timing.  (The
+    // plain decode hands the max over at every tile: a barrier and a shared
+    // load that queue behind the copies, 530 of a group's 2,700 cycles.)
     const int sg = warp < 4 ? 0 : 1, q4 = warp & 3;
     const int h = q4 * 32 + lane;
     const uint32_t lane_addr = tbase + (static_cast<uint32_t>(q4 * 32) << 16);
-    float* m_ring = reinterpret_cast<float*>(smem + kOffSm);  // [tile % 8][128]: running max after the tile
+    float* m_first = reinterpret_cast<float*>(smem + kOffSm);  // [unit % 2][128]
     const float sl2 = a.scale * kLog2e;
     const int sw = (h >> 1) & 3;  // 64-byte swizzle of row h
     const uint32_t p_row = static_cast<uint32_t>((h >> 3) * 512 + (h & 7) * 64);
@@ -711,14 +737,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
       float m_used = -INFINITY, l_sum = 0.f;
       for (int j = j0 + ((j0 ^ sg) & 1); ok && j < j0 + ntiles; j += 2) {
         const int b = j % kSBuf, slot = j % kPSlots, i0 = j - j0;
-        // the other group's max after tile pm (waited for also where the unit
-        // has no such tile, so that no phase is skipped)
         float m_other = -INFINITY;
-        const int pm = i0 == 1 ? j - 1 : j - 3;
-        if (pm >= 0) {
-          ok = wait_all(&bar.m_pub[pm & 7], (pm >> 3) & 1);
+        if (i0 == 1) {
+          // (no phase of m_pub is skipped: unit k - 2's is over, since every
+          // warp has waited for that unit's sm_fin)
+          ok = wait_all(&bar.m_pub[k & 1], (k >> 1) & 1);
           if (!ok) break;
-          if (pm >= j0) m_other = *reinterpret_cast<volatile float*>(&m_ring[(pm & 7) * 128 + h]);
+          m_other = *reinterpret_cast<volatile float*>(&m_first[(k & 1) * 128 + h]);
         }
         ok = wait_all(&bar.s_full[b], (j / kSBuf) & 1);
         if (!ok) break;
@@ -777,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         for (int i = 0; i < 8; ++i) mx[i] = fmaxf(fmaxf(sc[4 * i], sc[4 * i + 1]), fmaxf(sc[4 * i + 2], sc[4 * i + 3]));
         const float tmax = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-        // adopt the other group's max if it is larger (it only grows)
+        // the unit's second tile: adopt the first one's max if it is larger
         if (m_other > m_used) {
           if (m_used != -INFINITY) l_sum *= ex2_approx(m_used - m_other);
           m_used = m_other;
@@ -789,9 +814,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
           if (m_used != -INFINITY) l_sum *= ex2_approx(m_used - tmax);
           m_used = tmax;
         }
-        m_ring[(j & 7) * 128 + h] = m_used;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.m_pub[j & 7]);
+        if (i0 == 0) {
+          m_first[(k & 1) * 128 + h] = m_used;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.m_pub[k & 1]);
+        }
         // p = 2^(x - m); masked (-inf) scores give exactly 0, and nothing is
         // live while m is still -inf
         const float nm = m_used == -INFINITY ? 0.f : -m_used;
@@ -836,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
       // phase, so one that has no tile in a short unit cannot run ahead.
       if (ok && k > 0) ok = wait_all(&bar.sm_fin, (k - 1) & 1);
       if (!ok) break;
-      float* fin_sh = m_ring + (8 + 4 * (k & 1)) * 128;  // [group][l, m][128]
+      float* fin_sh = m_first + (2 + 4 * (k & 1)) * 128;  // [group][l, m][128]
       fin_sh[(2 * sg) * 128 + h] = l_sum;
       fin_sh[(2 * sg + 1) * 128 + h] = m_used;
       __syncwarp();
@@ -966,40 +993,47 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
       if (!ok) break;
       tc_fence_after();
       const float inv = *reinterpret_cast<const volatile float*>(smem + kOffFin + fs * 512 + 4 * h);
-      const int c0 = (warp >> 2) * 8;
-      const bool live = h < nl;
-      unsigned char* orow = static_cast<unsigned char*>(a.O_dst) + (pair0 + (live ? h : 0)) * (a.o_bf16 ? 2 * kLatent : 4 * kLatent);
+      // blocks of 128 bytes a row (64 bf16 or 32 fp32 columns), transposed
+      // over four lanes to whole lines (each lane storing its own row took
+      // 4.2 us a bf16 unit and 7.4 us an fp32 one)
+      const int nblk = a.o_bf16 ? 4 : 8, row_bytes = a.o_bf16 ? 2 * kLatent : 4 * kLatent;
+      const uint32_t col0 = tbase + (static_cast<uint32_t>(q4 * 32) << 16) + kColO + 256 * (warp >> 2);
+      unsigned char* out = static_cast<unsigned char*>(a.O_dst) + (pair0 + q4 * 32 + (lane & ~3)) * row_bytes +
+                           (warp >> 2) * (row_bytes / 2) + 32 * (lane & 3);
 #pragma unroll 1
-      for (int c = c0; c < c0 + 8; ++c) {
+      for (int c = 0; c < nblk; ++c) {
         uint32_t o[32];
-        tmem_ld32(lane_addr + kColO + 32 * c, o);
-        tmem_wait_ld();
-        if (c == c0 + 7) {
+        if (a.o_bf16) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            uint32_t x[32];
+            tmem_ld32(col0 + 64 * c + 32 * n, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(x[2 * i]) * inv, __uint_as_float(x[2 * i + 1]) * inv);
+              o[16 * n + i] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+          }
+        } else {
+          tmem_ld32(col0 + 32 * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+        }
+        if (c == nblk - 1) {
           // O is read: the next unit's PV may overwrite it
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.o_free);
         }
-        if (live && a.o_bf16) {
+        transpose_sectors(o, lane);
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            uint32_t w[8];
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(o[16 * n + 2 * i]) * inv,
-                                                             __uint_as_float(o[16 * n + 2 * i + 1]) * inv);
-              w[i] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-            store32(orow + 64 * c + 32 * n, w, al32);
-          }
-        } else if (live) {
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(o[8 * n + i]) * inv);
-            store32(orow + 128 * c + 32 * n, w, al32);
-          }
+          for (int n = 0; n < 8; ++n) w[n] = o[8 * i + n];
+          if (q4 * 32 + (lane & ~3) + i < nl) store32(out + i * row_bytes + 128 * c, w, al32);
         }
         __syncwarp();
       }
@@ -1032,254 +1066,274 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
       }
       if (!ok) set_abort(bar, a.dev_error);
     } else if (score && warp == 10) {
-    // ------------------------------------------------- score CTA forwarder
-    // fence: once this CTA's rows of item gf have landed, fence them into the
-    //   async proxy and arrive on kv_full.
-    // copy (fp8): once tile item gc < gf is fenced and the value CTA's receive
-    //   slot is free, copy chunks 0-3 (16 KB) into it.
-    bool ok = true;
-    int gf = 0, gc = 0, jc = 0, base = 0;
-    for (;;) {
-      const Unit* U = it.get(bar, ok);
-      if (!U) break;
-      const int end = base + kQItems + U->ntiles;
-      uint32_t idle = 0;
-      while (ok && gc < end) {
-        bool moved = false;
-        if (!kFp8) {
-          ok = wait_all(&bar.kv_loaded[gf % kStages], (gf / kStages) & 1);
-          if (!ok) break;
-        }
-        if (gf < end && (!kFp8 || __all_sync(kFull, mbar_peek(&bar.kv_loaded[gf % kStages], (gf / kStages) & 1)))) {
-          fence_proxy_async_smem();  // the producers' writes -> S and the bulk copy
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.kv_full[gf % kStages]);
-          ++gf;
-          moved = true;
-        }
-        if (!kFp8) gc = gf;
-        if (kFp8 && gc < gf) {
-          if (gc - base < kQItems) {
-            ++gc;
-            moved = true;
-          } else if (__all_sync(kFull, mbar_peek_cluster(&bar.v_free[jc % kRecv], ((jc / kRecv) & 1) ^ 1))) {
-            const int st = gc % kStages, rs = jc % kRecv;
-            if (lane == 0)
-              bulk_copy_to_peer(map_peer(smem_base + kOffRecv + rs * kHalfBytes, peer), smem + stage_chunk_off(st, 0),
-                                kHalfBytes, map_peer(smem_u32(&bar.v_full[rs]), peer));
+      // ------------------------------------------------- score CTA forwarder
+      // fence: once this CTA's rows of item gf have landed, fence them into the
+      //   async proxy and arrive on kv_full.
+      // copy (fp8): once tile item gc < gf is fenced and the value CTA's receive
+      //   slot is free, copy chunks 0-3 (16 KB) into it.
+      bool ok = true;
+      int gf = 0, gc = 0, jc = 0, base = 0;
+      for (;;) {
+        const Unit* U = it.get(bar, ok);
+        if (!U) break;
+        const int end = base + kQItems + U->ntiles;
+        uint32_t idle = 0;
+        while (ok && gc < end) {
+          bool moved = false;
+          if (!kFp8) {
+            ok = wait_all(&bar.kv_loaded[gf % kStages], (gf / kStages) & 1);
+            if (!ok) break;
+          }
+          if (gf < end && (!kFp8 || __all_sync(kFull, mbar_peek(&bar.kv_loaded[gf % kStages], (gf / kStages) & 1)))) {
+            fence_proxy_async_smem();  // the producers' writes -> S and the bulk copy
             __syncwarp();
-            ++gc;
-            ++jc;
+            if (lane == 0) mbar_arrive(&bar.kv_full[gf % kStages]);
+            ++gf;
             moved = true;
           }
+          if (!kFp8) gc = gf;
+          if (kFp8 && gc < gf) {
+            if (gc - base < kQItems) {
+              ++gc;
+              moved = true;
+            } else if (__all_sync(kFull, mbar_peek_cluster(&bar.v_free[jc % kRecv], ((jc / kRecv) & 1) ^ 1))) {
+              const int st = gc % kStages, rs = jc % kRecv;
+              if (lane == 0)
+                bulk_copy_to_peer(map_peer(smem_base + kOffRecv + rs * kHalfBytes, peer), smem + stage_chunk_off(st, 0),
+                                  kHalfBytes, map_peer(smem_u32(&bar.v_full[rs]), peer));
+              __syncwarp();
+              ++gc;
+              ++jc;
+              moved = true;
+            }
+          }
+          idle = moved ? 0u : idle + 1u;
+          if (idle > kWaitLimit) ok = false;
         }
-        idle = moved ? 0u : idle + 1u;
-        if (idle > kWaitLimit) ok = false;
+        if (!ok) break;
+        base = end;
+        it.done(bar, lane);
       }
-      if (!ok) break;
-      base = end;
-      it.done(bar, lane);
-    }
-    if (!ok) set_abort(bar, a.dev_error);
+      if (!ok) set_abort(bar, a.dev_error);
     } else if (score) {
-    // --------------------------------------------- Q to TMEM, S MMA issuers
-    // warp 4 + 3b + part owns third `part` of S slot b for tiles j = b (mod 2)
-    const int b = (warp - 4) / kSParts, part = (warp - 4) % kSParts;
-    const uint32_t id_s = idesc_bf16(128, kTile, 0, 0);
-    const uint64_t dk = smem_desc(smem_base + kOffStages, 16, 1024, kSwizzle128B);
-    const uint32_t dS = tbase + kColS + 96 * b + 32 * part;
-    const uint32_t qa = tbase + kColQ + 96 * part;
-    const uint64_t dkp = dk + static_cast<uint64_t>((3 * part * kChunkBytes) >> 4);
-    bool ok = true;
-    int g0 = 0, j0 = 0;  // items and tiles before the unit
-    for (int k = 0;; ++k) {
-      const Unit* U = it.get(bar, ok);
-      if (!U) break;
-      const int ntiles = U->ntiles;
-      if (warp < 8) {
-        // item warp - 4 of the unit's Q, once no MMA reads the previous one
-        if (k > 0) ok = wait_all(&bar.s_end, (k - 1) & 1);
-        const int g = g0 + warp - 4, st = g % kStages;
-        ok = ok && wait_all_cluster(&bar.kv_full[st], (g / kStages) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t lane_addr = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-#pragma unroll 1
-        for (int c = 0; c < kNch; ++c) {
-          uint32_t v[32];
+      // --------------------------------------------- Q to TMEM, S MMA issuers
+      // warp 4 + 3b + part owns third `part` of S slot b for tiles j = b (mod 2)
+      const int b = (warp - 4) / kSParts, part = (warp - 4) % kSParts;
+      const uint32_t id_s = idesc_bf16(128, kTile, 0, 0);
+      const uint64_t dk = smem_desc(smem_base + kOffStages, 16, 1024, kSwizzle128B);
+      const uint32_t dS = tbase + kColS + 96 * b + 32 * part;
+      const uint32_t qa = tbase + kColQ + 96 * part;
+      const uint64_t dkp = dk + static_cast<uint64_t>((3 * part * kChunkBytes) >> 4);
+      bool ok = true;
+      int32_t other_seen = 0;
+      int g0 = 0, j0 = 0;  // items and tiles before the unit
+      for (int k = 0;; ++k) {
+        const Unit* U = it.get(bar, ok);
+        if (!U) break;
+        const int ntiles = U->ntiles;
+        if (warp < 8) {
+          // item warp - 4 of the unit's Q, once no MMA reads the previous one
+          if (k > 0) ok = wait_all(&bar.s_end, (k - 1) & 1);
+          const int g = g0 + warp - 4, st = g % kStages;
+          ok = ok && wait_all_cluster(&bar.kv_full[st], (g / kStages) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t lane_addr = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+          // (16 columns at a time, the next 16 read before these are stored)
+          uint32_t v[2][16];
+          auto read = [&](int n, uint32_t (&r)[16]) {  // dims 32 n ..: unit i of a chunk sits at position i ^ (lane & 7)
+            const unsigned char* row = smem + stage_chunk_off(st, 0) + (n >> 1) * kChunkBytes + lane * 128;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {  // unit i of the chunk sits at position i ^ (lane & 7)
-            const uint4 y = *reinterpret_cast<const uint4*>(smem + stage_chunk_off(st, c) + lane * 128 + ((i ^ (lane & 7)) << 4));
-            v[4 * i] = y.x; v[4 * i + 1] = y.y; v[4 * i + 2] = y.z; v[4 * i + 3] = y.w;
-          }
-          tmem_st32(lane_addr + kColQ + 32 * c, v);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          // the stage is free: as many arrivals as a tile's
-          for (int i = 0; i < (kFp8 ? kSParts + 1 : kSParts); ++i) mbar_arrive(&bar.s_done[st]);
-          mbar_arrive(&bar.q_ready);
-          if (kFp8) mbar_arrive_remote(map_peer(smem_u32(&bar.q_gone), peer));
-        }
-        __syncwarp();
-      }
-      ok = wait_all(&bar.q_ready, k & 1);
-      tc_fence_after();
-      for (int j = j0 + ((j0 ^ b) & 1); ok && j < j0 + ntiles; j += kSBuf) {
-        const int g = g0 + kQItems + j - j0, st = g % kStages, u = j / kSBuf;
-        ok = wait_all(&bar.s_free[b], (u & 1) ^ 1);
-        ok = ok && wait_all_cluster(&bar.kv_full[st], (g / kStages) & 1);
-        if (!ok) break;
-        // part 0's arrival passes on (release after the acquire of kv_full)
-        // the producers' write of the tile's mask, read after s_full
-        if (part == 0 && lane == 0) mbar_arrive(&bar.s_full[b]);
-        tc_fence_after();
-        if (lane == 0) {
-          uint64_t bc = dkp + static_cast<uint64_t>((st * kStageBytes) >> 4);
-          uint32_t ac = qa;
+            for (int i = 0; i < 4; ++i) {
+              const uint4 y = *reinterpret_cast<const uint4*>(row + (((4 * (n & 1) + i) ^ (lane & 7)) << 4));
+              r[4 * i] = y.x; r[4 * i + 1] = y.y; r[4 * i + 2] = y.z; r[4 * i + 3] = y.w;
+            }
+          };
+          read(0, v[0]);
 #pragma unroll 1
-          for (int c = 0; c < 3; ++c, bc += kChunkBytes >> 4, ac += 32) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mma_ts(dS, ac + 8 * i, bc + 2 * i, id_s, (c | i) != 0);
+          for (int n = 0; n < 2 * kNch; n += 2) {
+            read(n + 1, v[1]);
+            tmem_st16(lane_addr + kColQ + 16 * n, v[0]);
+            if (n + 2 < 2 * kNch) read(n + 2, v[0]);
+            tmem_st16(lane_addr + kColQ + 16 * n + 16, v[1]);
           }
-          mma_commit(&bar.s_full[b]);
-          if (kFp8) mma_commit_mc(&bar.s_done[st], 0x3);
-          else mma_commit(&bar.s_done[st]);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            // the stage is free: as many arrivals as a tile's
+            for (int i = 0; i < (kFp8 ? kSParts + 1 : kSParts); ++i) mbar_arrive(&bar.s_done[st]);
+            mbar_arrive(&bar.q_ready);
+            if (kFp8) mbar_arrive_remote(map_peer(smem_u32(&bar.q_gone), peer));
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        ok = wait_all(&bar.q_ready, k & 1);
+        tc_fence_after();
+        for (int j = j0 + ((j0 ^ b) & 1); ok && j < j0 + ntiles; j += kSBuf) {
+          const int g = g0 + kQItems + j - j0, st = g % kStages, u = j / kSBuf;
+          ok = wait_all(&bar.s_free[b], (u & 1) ^ 1);
+          // The stage's previous item has been full, so that the parity below
+          // can only mean this one: the forwarder arrives in order, so it has
+          // since S(j - 2) was issued; in the fp8 form the value CTA's halves
+          // might land out of order, so the other slot's issuers say so (a
+          // count that only grows, read again only when it falls short).
+          if constexpr (kFp8) {
+            for (uint32_t i = 0; other_seen < j - kStages + 1 && i < kWaitLimit; ++i)
+              other_seen = ld_relaxed_shared(&bar.seen[b ^ 1]);
+            ok = ok && __all_sync(kFull, other_seen >= j - kStages + 1);
+          }
+          ok = ok && wait_all_cluster(&bar.kv_full[st], (g / kStages) & 1);
+          if (kFp8 && part == 0 && lane == 0) st_relaxed_shared(&bar.seen[b], j + 1);
+          if (!ok) break;
+          // part 0's arrival passes on (release after the acquire of kv_full)
+          // the producers' write of the tile's mask, read after s_full
+          if (part == 0 && lane == 0) mbar_arrive(&bar.s_full[b]);
+          tc_fence_after();
+          if (lane == 0) {
+            uint64_t bc = dkp + static_cast<uint64_t>((st * kStageBytes) >> 4);
+            uint32_t ac = qa;
+#pragma unroll 1
+            for (int c = 0; c < 3; ++c, bc += kChunkBytes >> 4, ac += 32) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mma_ts(dS, ac + 8 * i, bc + 2 * i, id_s, (c | i) != 0);
+            }
+            mma_commit(&bar.s_full[b]);
+            if (kFp8) mma_commit_mc(&bar.s_done[st], 0x3);
+            else mma_commit(&bar.s_done[st]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (lane == 0) mma_commit(&bar.s_end);
+        g0 += kQItems + ntiles;
+        j0 += ntiles;
+        it.done(bar, lane);
       }
-      if (!ok) break;
-      if (lane == 0) mma_commit(&bar.s_end);
-      g0 += kQItems + ntiles;
-      j0 += ntiles;
-      it.done(bar, lane);
-    }
-    if (!ok) set_abort(bar, a.dev_error);
-    if (lane == 0) mma_commit(&bar.fin[1 + kSParts * b + part]);
-    __syncwarp();
-    mbar_wait(&bar.fin[1 + kSParts * b + part], 0);
+      if (!ok) set_abort(bar, a.dev_error);
+      if (lane == 0) mma_commit(&bar.fin[1 + kSParts * b + part]);
+      __syncwarp();
+      mbar_wait(&bar.fin[1 + kSParts * b + part], 0);
     } else if (warp == 10) {
-    // -------------------------------------------------------- PV MMA issuer
-    const uint32_t id_o = idesc_bf16(128, 256, 0, 1);
-    const uint64_t dv = smem_desc(smem_base, kChunkBytes, 1024, kSwizzle128B);
-    const uint64_t dp = smem_desc(smem_base + kOffP, 16, 512, kSwizzle64B);
-    // p_ok(j) stands for everything PV(j) needs: P(j) arrived and in O's
-    // scale (warps 0-3), V(j) landed and fenced (warp 9).  A unit's first PV
-    // overwrites O, once the previous unit's has been read.
-    bool ok = true;
-    int j0 = 0;
-    for (int k = 0;; ++k) {
-      const Unit* U = it.get(bar, ok);
-      if (!U) break;
-      const int ntiles = U->ntiles;
-      if (k > 0) ok = wait_all(&bar.o_free, (k - 1) & 1);
-      for (int j = j0; j < j0 + ntiles && ok; ++j) {
-        const int vs = j % kRecv, os = j % kOwn, slot = j % kPSlots;
-        ok = wait_all(&bar.p_ok[slot], (j / kPSlots) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t sv[2] = {static_cast<uint64_t>((kOffRecv + vs * kHalfBytes) >> 4),
-                                  static_cast<uint64_t>((kOffOwn + os * kHalfBytes) >> 4)};
-          const uint64_t po = static_cast<uint64_t>((slot * kPBytes) >> 4);
+      // -------------------------------------------------------- PV MMA issuer
+      const uint32_t id_o = idesc_bf16(128, 256, 0, 1);
+      const uint64_t dv = smem_desc(smem_base, kChunkBytes, 1024, kSwizzle128B);
+      const uint64_t dp = smem_desc(smem_base + kOffP, 16, 512, kSwizzle64B);
+      // p_ok(j) stands for everything PV(j) needs: P(j) arrived and in O's
+      // scale (warps 0-3), V(j) landed and fenced (warp 9).  A unit's first PV
+      // overwrites O, once the previous unit's has been read.
+      bool ok = true;
+      int j0 = 0;
+      for (int k = 0;; ++k) {
+        const Unit* U = it.get(bar, ok);
+        if (!U) break;
+        const int ntiles = U->ntiles;
+        if (k > 0) ok = wait_all(&bar.o_free, (k - 1) & 1);
+        for (int j = j0; j < j0 + ntiles && ok; ++j) {
+          const int vs = j % kRecv, os = j % kOwn, slot = j % kPSlots;
+          ok = wait_all(&bar.p_ok[slot], (j / kPSlots) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t sv[2] = {static_cast<uint64_t>((kOffRecv + vs * kHalfBytes) >> 4),
+                                    static_cast<uint64_t>((kOffOwn + os * kHalfBytes) >> 4)};
+            const uint64_t po = static_cast<uint64_t>((slot * kPBytes) >> 4);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-              mma_ss(tbase + kColO + 256 * n, dp + po + ((32 * i) >> 4), dv + sv[n] + ((2048 * i) >> 4), id_o,
-                     (j > j0 || i > 0) ? 1u : 0u);
-          mma_commit_mc(&bar.v_free[vs], 0x3);
-          mma_commit(&bar.own_free[os]);
-          mma_commit_mc(&bar.p_free[slot], 0x3);
-          mma_commit(&bar.pv_done[slot]);
-          if (j == j0 + ntiles - 1) mma_commit(&bar.o_final);
+              for (int n = 0; n < 2; ++n)
+                mma_ss(tbase + kColO + 256 * n, dp + po + ((32 * i) >> 4), dv + sv[n] + ((2048 * i) >> 4), id_o,
+                       (j > j0 || i > 0) ? 1u : 0u);
+            mma_commit_mc(&bar.v_free[vs], 0x3);
+            mma_commit(&bar.own_free[os]);
+            mma_commit_mc(&bar.p_free[slot], 0x3);
+            mma_commit(&bar.pv_done[slot]);
+            if (j == j0 + ntiles - 1) mma_commit(&bar.o_final);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (!ok) break;
+        j0 += ntiles;
+        it.done(bar, lane);
       }
-      if (!ok) break;
-      j0 += ntiles;
-      it.done(bar, lane);
-    }
-    if (!ok) set_abort(bar, a.dev_error);
-    if (lane == 0) mma_commit(&bar.fin[0]);
-    __syncwarp();
-    mbar_wait(&bar.fin[0], 0);
+      if (!ok) set_abort(bar, a.dev_error);
+      if (lane == 0) mma_commit(&bar.fin[0]);
+      __syncwarp();
+      mbar_wait(&bar.fin[0], 0);
     } else if (warp == 9) {
-    // ------------------------------------------------- receive-ring arrivals
-    bool ok = true;
-    int j = 0, g = 0;
-    for (;;) {
-      const Unit* U = it.get(bar, ok);
-      if (!U) break;
-      const int end = j + U->ntiles;
-      g += kQItems;
-      for (; j < end && ok; ++j, ++g) {
-        const int st = g % kStages, vs = j % kRecv, os = j % kOwn;
-        ok = wait_all_cluster(&bar.v_full[vs], (j / kRecv) & 1);
-        if (!ok) break;
-        if (kFp8 && lane == 0) {
-          mbar_arrive_expect_tx(&bar.v_full[vs], kHalfBytes);
-          mbar_arrive(&bar.s_done[st]);
-          mbar_arrive_remote_relaxed(map_peer(smem_u32(&bar.s_done[st]), peer));
+      // ------------------------------------------------- receive-ring arrivals
+      bool ok = true;
+      int j = 0, g = 0;
+      for (;;) {
+        const Unit* U = it.get(bar, ok);
+        if (!U) break;
+        const int end = j + U->ntiles;
+        g += kQItems;
+        for (; j < end && ok; ++j, ++g) {
+          const int st = g % kStages, vs = j % kRecv, os = j % kOwn;
+          ok = wait_all_cluster(&bar.v_full[vs], (j / kRecv) & 1);
+          if (!ok) break;
+          if (kFp8 && lane == 0) {
+            mbar_arrive_expect_tx(&bar.v_full[vs], kHalfBytes);
+            mbar_arrive(&bar.s_done[st]);
+            mbar_arrive_remote_relaxed(map_peer(smem_u32(&bar.s_done[st]), peer));
+          }
+          ok = wait_all(&bar.own_loaded[os], (j / kOwn) & 1);
+          if (!ok) break;
+          fence_proxy_async_smem();  // the own (bf16: and receive) slot's rows -> PV
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.p_ok[j % kPSlots]);
         }
-        ok = wait_all(&bar.own_loaded[os], (j / kOwn) & 1);
         if (!ok) break;
-        fence_proxy_async_smem();  // the own (bf16: and receive) slot's rows -> PV
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_ok[j % kPSlots]);
+        it.done(bar, lane);
       }
-      if (!ok) break;
-      it.done(bar, lane);
-    }
-    if (!ok) set_abort(bar, a.dev_error);
+      if (!ok) set_abort(bar, a.dev_error);
     } else if (kFp8) {
-    // ------------------------------------------------- value CTA forwarder
-    // fp8: own slot j % kOwn (chunks 4-7) -> the score CTA's stage of tile j,
-    // once item g - 5 has left it.  Of those items the tiles are waited for in
-    // order, each once (a stage's next tile needs this copy, so its barrier
-    // cannot get ahead); Q's by its own barrier.
-    bool ok = true;
-    int g = 0, j = 0;          // next item, next tile
-    int wg = 0;                // the next item whose release is to be waited for
-    uint32_t turn = 0;         // bit st: parity of stage st's tiles so far
-    int gp = 0;                // the previous unit's first item
-    for (int k = 0;; ++k) {
-      const Unit* U = it.get(bar, ok);
-      if (!U) break;
-      const int ntiles = U->ntiles, g0 = g;
-      g += kQItems;
-      for (int n = 0; n < ntiles && ok; ++n, ++g, ++j) {
-        const int st = g % kStages, os = j % kOwn;
-        ok = wait_all(&bar.own_loaded[os], (j / kOwn) & 1);
-        // (a unit of one tile waits too: its S, hence the next unit's Q, then
-        // comes after this phase, and no phase is skipped)
-        if (n == 1 || ntiles == 1) ok = ok && wait_all_cluster(&bar.q_gone, k & 1);
-        // (a unit has five items at least: only this one's and the last one's)
-        for (; ok && wg <= g - kStages; ++wg) {
-          if (wg - (wg < g0 ? gp : g0) < kQItems) continue;
-          const int ws = wg % kStages;
-          ok = wait_all_cluster(&bar.s_done[ws], (turn >> ws) & 1u);
-          turn ^= 1u << ws;
+      // ------------------------------------------------- value CTA forwarder
+      // fp8: own slot j % kOwn (chunks 4-7) -> the score CTA's stage of tile j,
+      // once item g - 5 has left it.  Of those items the tiles are waited for in
+      // order, each once (a stage's next tile needs this copy, so its barrier
+      // cannot get ahead); Q's by its own barrier.
+      bool ok = true;
+      int g = 0, j = 0;          // next item, next tile
+      int wg = 0;                // the next item whose release is to be waited for
+      uint32_t turn = 0;         // bit st: parity of stage st's tiles so far
+      int gp = 0;                // the previous unit's first item
+      for (int k = 0;; ++k) {
+        const Unit* U = it.get(bar, ok);
+        if (!U) break;
+        const int ntiles = U->ntiles, g0 = g;
+        g += kQItems;
+        for (int n = 0; n < ntiles && ok; ++n, ++g, ++j) {
+          const int st = g % kStages, os = j % kOwn;
+          ok = wait_all(&bar.own_loaded[os], (j / kOwn) & 1);
+          // (a unit of one tile waits too: its S, hence the next unit's Q, then
+          // comes after this phase, and no phase is skipped)
+          if (n == 1 || ntiles == 1) ok = ok && wait_all_cluster(&bar.q_gone, k & 1);
+          // (a unit has five items at least: only this one's and the last one's)
+          for (; ok && wg <= g - kStages; ++wg) {
+            if (wg - (wg < g0 ? gp : g0) < kQItems) continue;
+            const int ws = wg % kStages;
+            ok = wait_all_cluster(&bar.s_done[ws], (turn >> ws) & 1u);
+            turn ^= 1u << ws;
+          }
+          if (!ok) break;
+          fence_proxy_async_smem();
+          if (lane == 0)
+            bulk_copy_to_peer(map_peer(smem_base + stage_chunk_off(st, 4), peer), smem + kOffOwn + os * kHalfBytes,
+                              kHalfBytes, map_peer(smem_u32(&bar.kv_full[st]), peer));
+          __syncwarp();
         }
         if (!ok) break;
-        fence_proxy_async_smem();
-        if (lane == 0)
-          bulk_copy_to_peer(map_peer(smem_base + stage_chunk_off(st, 4), peer), smem + kOffOwn + os * kHalfBytes,
-                            kHalfBytes, map_peer(smem_u32(&bar.kv_full[st]), peer));
-        __syncwarp();
+        gp = g0;
+        it.done(bar, lane);
       }
-      if (!ok) break;
-      gp = g0;
-      it.done(bar, lane);
-    }
-    if (!ok) set_abort(bar, a.dev_error);
+      if (!ok) set_abort(bar, a.dev_error);
     } else {
-    // no role in this form: keep the descriptor ring moving
-    bool ok = true;
-    while (it.get(bar, ok)) it.done(bar, lane);
-    if (!ok) set_abort(bar, a.dev_error);
+      // no role in this form: keep the descriptor ring moving
+      bool ok = true;
+      while (it.get(bar, ok)) it.done(bar, lane);
+      if (!ok) set_abort(bar, a.dev_error);
     }
   } else {
     take_regs<Regs<kFp8>::producer>();

@@ -33,6 +33,7 @@ class Model(P.Model):
         self.j0 = [sum(self.sizes[:k]) for k in range(len(self.sizes) + 1)]
         self.g0 = [self.j0[k] + K_Q * k for k in range(len(self.sizes) + 1)]
         super().__init__(self.j0[-1], seed, rescale_prob=rescale_prob, mutation=mutation, decoupled=decoupled)
+        self.seen = [0, 0]
         self.q_tmem = [None] * K_Q       # the unit whose quarter is in TMEM
         self.s_running = 0               # S parts issued and not complete
         self.o_unit, self.o_pvs, self.o_read = None, set(), True
@@ -66,7 +67,7 @@ class Model(P.Model):
             mk(cta, "o_final", 1, 1)
             mk(cta, "o_free", 1, 2)          # two epilogue halves (the kernel: 8 warps)
             mk(cta, "fin_l", K_FIN, 1)
-            mk(cta, "m_pub", 8, 4)
+            mk(cta, "m_pub", 2, 4)
             mk(cta, "sm_fin", 1, 2)          # two groups (the kernel: 8 warps)
             mk(cta, "ud_full", K_UNITS, 1)
             mk(cta, "ud_free", K_UNITS, self.users[cta])
@@ -344,7 +345,13 @@ class Model(P.Model):
                 g = self.g0[k] + K_Q + j - j0
                 st = g % ST
                 yield self.W(0, "s_free", b, j // SB - 1)
+                if not self.decoupled and self.mut != "issuers_uncoupled":
+                    yield ("cond", lambda j=j: self.seen[1 - b] >= j - ST + 1)
                 yield self.W(0, "kv_full", st, g // ST)
+                if part == 0:
+                    def saw(j=j):
+                        self.seen[b] = j + 1
+                    yield ("do", saw)
 
                 def issue(j=j, g=g, st=st):
                     s = self.stage[st]
@@ -378,17 +385,12 @@ class Model(P.Model):
                 if j % 2 != grp:
                     continue
                 b, slot, i = j % SB, j % PS, j - j0
-                pm = j - 1 if i == 1 else j - 3
-                if self.mut == "max_wait_in_unit_only" and pm < j0:
-                    pm = -1
-                if pm >= 0:
-                    yield self.W(0, "m_pub", pm % 8, pm // 8)
+                if i == 1:
+                    yield self.W(0, "m_pub", k % 2, k // 2)
 
-                    def read_m(pm=pm, j=j):
-                        if pm < j0:
-                            return
-                        m = self.mring[pm % 8]
-                        self.check(m["tile"] == pm, "tile %s read tile %s's max, wanted %s", j, m["tile"], pm)
+                    def read_m(j=j):
+                        m = self.mring[k % 2]
+                        self.check(m["tile"] == j - 1, "tile %s read tile %s's max", j, m["tile"])
                         m["reads_left"] -= 1
                     yield ("do", read_m)
                 yield self.W(0, "s_full", b, j // SB)
@@ -405,14 +407,14 @@ class Model(P.Model):
                 for _ in range(4):
                     yield ("do", lambda b=b, j=j: self.b(0, "s_free", b).arrive(tag=j))
 
-                def post(j=j, i=i):
-                    m = self.mring[j % 8]
-                    self.check(m["reads_left"] <= 0, "max ring slot %s rewritten (tile %s) with tile %s unread", j % 8, j, m["tile"])
-                    readers = [r for r in (j + 3, j + 1 if i == 0 else None) if r is not None and r < self.j0[k + 1]]
-                    self.mring[j % 8] = dict(tile=j, reads_left=len(readers))
-                yield ("do", post)
-                for _ in range(4):
-                    yield ("do", lambda j=j: self.b(0, "m_pub", j % 8).arrive(tag=j))
+                if i == 0:
+                    def post(j=j):
+                        m = self.mring[k % 2]
+                        self.check(m["reads_left"] <= 0, "unit %s's first max overwritten by tile %s unread", k - 2, j)
+                        self.mring[k % 2] = dict(tile=j, reads_left=1 if self.sizes[k] > 1 else 0)
+                    yield ("do", post)
+                    for _ in range(4):
+                        yield ("do", lambda j=j: self.b(0, "m_pub", k % 2).arrive(tag=j))
                 yield self.W(0, "p_free", slot, j // PS - 1)
 
                 def send(j=j, slot=slot):
@@ -652,7 +654,8 @@ class Model(P.Model):
 # planted mistakes, and the protocol form each applies to (None: both)
 MUTATIONS = {"producers_uncoupled": None, "producers_skip_stage_free": None, "q_over_running_s": None, "q_waits_for_s_full": None, "epilogue_waits_for_pv_done": None,
              "sm_fin_without_wait": None, "two_fin_slots": None, "pv_over_unread_o": None,
-             "scheduler_skips_free": None, "value_forwarder_skips_q": False}
+             "scheduler_skips_free": None, "value_forwarder_skips_q": False,
+             "issuers_uncoupled": False}
 
 
 def run(sizes, seed, mutation=None, decoupled=True):
