@@ -56,25 +56,27 @@ static SplitPlan cut(int64_t lmax, int64_t want) {
   return p;
 }
 // Splits of the windowed and tree decodes: `units` units of at most `lmax`
-// tokens on `clusters` resident clusters.  A unit costs about kUnitUs besides
-// its tiles (measured: 64 requests x 8 shards on a 64-token window take 102 us
-// of 7.2 waves, and 0.68 us more per 32-token tile), a split adds a partial to
-// write and read, and lengths are only known to be at most lmax (kFill of it
-// on average).  While all units run at once, the time is a unit's; beyond
-// that, list scheduling's: the work per cluster and one unit at the end.  So
-// few long units are cut until they fill the GPU, ragged ones until the last
-// one no longer shows (16 requests of 1,000 to 16,384 tokens: 391 us uncut),
-// and many short ones not at all.
-constexpr double kTileUs = 0.68, kUnitUs = 14.0, kMergeUs = 4.0, kPartialUs = 0.06, kFill = 0.6;
+// tokens on `clusters` persistent clusters.  A 32-token tile takes kTileUs, a
+// cluster's further unit kUnitUs (its last output store and first tiles), the
+// merge kMergeUs and kPartialUs for each partial written and read; lengths are
+// only known to be at most lmax (kFill of it on average).  While all units run
+// at once, the time is a unit's; beyond that the work per cluster and half a
+// unit at the end.  So few long units are cut until they fill the GPU (one
+// request on a 1,028-token window: 39.6 us whole, 25.8 in eight), ragged ones
+// until the last one no longer shows (trees of 16 requests of up to 16,384
+// tokens: 356 us whole, 212-243 in two to eight), and many short ones not at
+// all (64 requests x 8 shards x 512 tokens: 123 us, 279 in two).
+constexpr double kTileUs = 0.6, kUnitUs = 6.0, kMergeUs = 4.0, kPartialUs = 0.1, kFill = 0.85;
 constexpr int64_t kMinSelectSplit = 128;
 static int64_t select_splits(int64_t units, int64_t lmax, int clusters) {
   const int64_t most = std::min<int64_t>(kMaxSplits, (lmax + kMinSelectSplit - 1) / kMinSelectSplit);
   int64_t best = 1;
   double least = 0;
   for (int64_t s = 1; s <= most; ++s) {
-    const double n = static_cast<double>(units) * s, unit = kTileUs * ((lmax + s * kSplitRound - 1) / (s * kSplitRound));
-    double t = unit + kUnitUs + (s > 1 ? kMergeUs + kPartialUs * n : 0.0);
-    if (n > clusters) t += n / clusters * (kFill * unit + kUnitUs);
+    const double n = static_cast<double>(units) * s;
+    const double unit = kTileUs * ((lmax + s * kSplitRound - 1) / (s * kSplitRound));
+    double t = n <= clusters ? unit : n / clusters * (kFill * unit + kUnitUs) + 0.5 * unit;
+    if (s > 1) t += kMergeUs + kPartialUs * n;
     if (s == 1 || t < least) {
       best = s;
       least = t;

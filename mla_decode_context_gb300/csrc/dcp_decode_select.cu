@@ -473,10 +473,10 @@ __device__ __forceinline__ void produce(const DecodeArgs& a, Bars& bar, uint32_t
     bool valid[2] = {false, false};
     int32_t crow[2] = {0, 0};
     bool bad = false;
+    const unsigned char* code_row[2] = {kvb, kvb};
     auto load_code = [&](int e, int i) {
       const int c = score ? (i < 4 ? i : 8) : 4 + i;
-      const unsigned char* src_row = kvb + static_cast<int64_t>(crow[e]) * kKDim + x * 8;
-      codes[e][i] = valid[e] ? __ldg(reinterpret_cast<const uint2*>(src_row + c * 64)) : make_uint2(0u, 0u);
+      codes[e][i] = valid[e] ? __ldg(reinterpret_cast<const uint2*>(code_row[e] + c * 64)) : make_uint2(0u, 0u);
     };
     auto load_scale = [&](int e) { return valid[e] ? __ldg(a.kv_scale + crow[e]) : 0.f; };
     const int j1 = (g - base) & (step - 1);  // the unit's first tile of this warp
@@ -487,6 +487,7 @@ __device__ __forceinline__ void produce(const DecodeArgs& a, Bars& bar, uint32_t
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           rscale[e] = load_scale(e);
+          code_row[e] = kvb + static_cast<int64_t>(crow[e]) * kKDim + x * 8;
 #pragma unroll
           for (int i = 0; i < 5; ++i) if (i < nch) load_code(e, i);
         }
@@ -542,7 +543,6 @@ __device__ __forceinline__ void produce(const DecodeArgs& a, Bars& bar, uint32_t
         cp_async_mbar_arrive_noinc(&slot_loaded[st]);
       } else {
         const bool next = kFp8 && j + step < ntiles;
-        if (next) rows_of(valid, crow, bad);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int row = e ? row1 : row0;
@@ -562,12 +562,21 @@ __device__ __forceinline__ void produce(const DecodeArgs& a, Bars& bar, uint32_t
                                          e4m3x2_to_bf16x2(w.y, sc), e4m3x2_to_bf16x2(w.y >> 16, sc));
               asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                            : "memory");
-              if (next) load_code(e, i);
             } else {
               cp_async16_zfill(dst, src_row + c * 128, src_bytes);
             }
           }
-          if (next) rscale[e] = load_scale(e);
+        }
+        if (next) rows_of(valid, crow, bad);
+        if (kFp8 && next) {  // (after the stores: in between, they held the stores up)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            rscale[e] = load_scale(e);
+            code_row[e] = kvb + static_cast<int64_t>(crow[e]) * kKDim + x * 8;
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+              if (i < nch) load_code(e, i);
+          }
         }
         if (next && j + 2 * step < ntiles) fetch(j + 2 * step);
         if constexpr (kFp8) mbar_arrive(&slot_loaded[st]);
@@ -660,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
     for (; dealt * clusters < units; ++dealt) {
       const int32_t at = dealt * clusters + ((dealt & 1) ? clusters - 1 - c : c);
       if (at >= units) continue;
-      const SelCoords k = sel_coords(a, a.unit_order ? __ldg(a.unit_order + at) : at);
+      const SelCoords k = sel_coords(a, a.unit_order ? *static_cast<const volatile int32_t*>(a.unit_order + at) : at);
       const SelUnit su = sel_unit(a, k.b, k.c);
       const int32_t d = a.d0 + k.dd;
       if (su.R.err && lane == 0 && score && k.c == 0 && k.dd == 0 && k.s == 0) report(a.dev_error, su.R.err);
@@ -694,7 +703,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
     return false;
   };
   bool more = false;
-  if (warp == kSchedWarp) more = next_unit(bar.unit[0]);  // alongside the set-up
+  if (warp == kSchedWarp) {  // alongside the set-up
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for the order; the inputs are older
+    more = next_unit(bar.unit[0]);
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // peer's barriers initialised and armed before any remote operation
@@ -1386,20 +1398,36 @@ __global__ void __launch_bounds__(1024) select_order_kernel(DecodeArgs a, int32_
     const int e = 31 - __clz(tiles4);
     return 4 * (e - 2) + static_cast<int>((tiles4 >> (e - 2)) & 3u) + 1;  // < 128
   };
+  // The decode's blocks may start on the other SMs: they set up and wait.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (t < kKeys) cnt[t] = 0;
+  const int mine = t < units ? key_of(t) : -1;  // (the first 1,024 keys are kept)
   __syncthreads();
-  for (int32_t u = t; u < units; u += 1024) atomicAdd(&cnt[key_of(u)], 1);
+  if (mine >= 0) atomicAdd(&cnt[mine], 1);
+  for (int32_t u = t + 1024; u < units; u += 1024) atomicAdd(&cnt[key_of(u)], 1);
   __syncthreads();
-  if (t == 0) {
-    int32_t acc = 0;
-    for (int k = kKeys - 1; k >= 0; --k) { off[k] = acc; acc += cnt[k]; }
+  if (w == 0) {  // off[k]: the units of larger keys; a lane takes 4 keys, the largest first
+    int c[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += c[i] = cnt[kKeys - 1 - (4 * lane + i)];
+    int acc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int x = __shfl_up_sync(kFull, acc, d);
+      if (lane >= d) acc += x;
+    }
+    acc -= sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      off[kKeys - 1 - (4 * lane + i)] = acc;
+      acc += c[i];
+    }
   }
-  __syncthreads();
   for (int32_t base = 0; base < units; base += 1024) {
     for (int i = t; i < 32 * kKeys; i += 1024) (&wcnt[0][0])[i] = 0;
     __syncthreads();
     const int32_t u = base + t;
-    const int k = u < units ? key_of(u) : -1;
+    const int k = base == 0 ? mine : u < units ? key_of(u) : -1;
     const unsigned same = __match_any_sync(kFull, k);
     const int rank = __popc(same & ((1u << lane) - 1u));
     if (k >= 0 && rank == 0) wcnt[w][k] = __popc(same);
@@ -1409,17 +1437,19 @@ __global__ void __launch_bounds__(1024) select_order_kernel(DecodeArgs a, int32_
       for (int v = 0; v < w; ++v) pos += wcnt[v][k];
       order[pos] = u;
     }
-    __syncthreads();
-    if (t < kKeys) {
-      int32_t add = 0;
-      for (int v = 0; v < 32; ++v) add += wcnt[v][t];
-      off[t] += add;
+    if (base + 1024 < units) {
+      __syncthreads();
+      if (t < kKeys) {
+        int32_t add = 0;
+        for (int v = 0; v < 32; ++v) add += wcnt[v][t];
+        off[t] += add;
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
-cudaLaunchConfig_t launch_config(int clusters, cudaStream_t st, cudaLaunchAttribute* attr) {
+cudaLaunchConfig_t launch_config(int clusters, bool ordered, cudaStream_t st, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));
   cfg.blockDim = dim3(kThreads);
@@ -1429,8 +1459,11 @@ cudaLaunchConfig_t launch_config(int clusters, cudaStream_t st, cudaLaunchAttrib
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  // (set up alongside the kernel that orders the units)
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ordered ? 2 : 1;
   return cfg;
 }
 
@@ -1454,8 +1487,8 @@ int decode_select_clusters() {
       cudaGetLastError();
       return 0;
     }
-  cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = launch_config(1, nullptr, attr);
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = launch_config(1, false, nullptr, attr);
   int clusters = 0;
   if (cudaOccupancyMaxActiveClusters(&clusters, decode_select_kernel<false>, &cfg) != cudaSuccess || clusters <= 0) {
     cudaGetLastError();
@@ -1479,8 +1512,8 @@ cudaError_t launch_decode_select(const DecodeArgs& a, int32_t units, cudaStream_
   const int resident = decode_select_clusters();
   if (resident <= 0) return cudaErrorInvalidDevice;
   if (units <= 0 || a.plan.chunk % kTile != 0) return cudaErrorInvalidValue;
-  cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = launch_config(units < resident ? units : resident, st, attr);
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = launch_config(units < resident ? units : resident, a.unit_order != nullptr, st, attr);
   return a.kv_fp8 ? cudaLaunchKernelEx(&cfg, decode_select_kernel<true>, a, units)
                   : cudaLaunchKernelEx(&cfg, decode_select_kernel<false>, a, units);
 }
