@@ -55,20 +55,33 @@ static SplitPlan cut(int64_t lmax, int64_t want) {
   if (p.splits < 1) p.splits = 1;
   return p;
 }
+// Clusters that share a unit's output: each computes the unit and writes its
+// own columns of it (`most` of them at most).  A cluster writes through one SM,
+// at 26-30 bytes per clock (7.4 us for 128 fp32 rows, as long as the rest of a
+// short unit), so clusters that would be idle take a part of that.
+static int32_t select_parts(int64_t units, int64_t others, int32_t most, int clusters) {
+  int32_t parts = 1;
+  while (parts < most && 2 * parts * units + others <= clusters) parts *= 2;
+  return parts;
+}
+constexpr int32_t kMostParts = 8, kMostPartsBf16 = 4;  // (128-byte blocks of a warp's half row)
+
 // Splits of the windowed and tree decodes: `units` units of at most `lmax`
-// tokens on `clusters` persistent clusters.  A 32-token tile takes kTileUs, a
-// cluster's further unit kUnitUs (its last output store and first tiles), the
-// merge kMergeUs and kPartialUs for each partial written and read; lengths are
-// only known to be at most lmax (kFill of it on average).  While all units run
-// at once, the time is a unit's; beyond that the work per cluster and half a
-// unit at the end.  So few long units are cut until they fill the GPU (one
-// request on a 1,028-token window: 39.6 us whole, 25.8 in eight), ragged ones
-// until the last one no longer shows (trees of 16 requests of up to 16,384
-// tokens: 356 us whole, 212-243 in two to eight), and many short ones not at
-// all (64 requests x 8 shards x 512 tokens: 123 us, 279 in two).
-constexpr double kTileUs = 0.6, kUnitUs = 6.0, kMergeUs = 4.0, kPartialUs = 0.1, kFill = 0.85;
+// tokens (and `others` for the rows of no request) on `clusters` persistent
+// clusters.  A 32-token tile takes kTileUs, a cluster's further unit kUnitUs
+// (its last output store and first tiles), the last output store kStoreUs over
+// the clusters that share it (twice that for fp32 partials), the merge kMergeUs
+// and kPartialUs for each partial written and read; lengths are only known to
+// be at most lmax (kFill of it on average).  While all units run at once, the
+// time is a unit's; beyond that the work per cluster and half a unit at the
+// end.  So few long units are cut until they fill the GPU (one request on a
+// 1,028-token window: 39.6 us whole, 25.8 in eight), ragged ones until the
+// last one no longer shows (trees of 16 requests of up to 16,384 tokens: 356
+// us whole, 212-243 in two to eight), and many short ones not at all (64
+// requests x 8 shards x 512 tokens: 123 us, 279 in two).
+constexpr double kTileUs = 0.6, kUnitUs = 6.0, kStoreUs = 3.7, kMergeUs = 4.0, kPartialUs = 0.1, kFill = 0.85;
 constexpr int64_t kMinSelectSplit = 128;
-static int64_t select_splits(int64_t units, int64_t lmax, int clusters) {
+static int64_t select_splits(int64_t units, int64_t others, int64_t lmax, int clusters) {
   const int64_t most = std::min<int64_t>(kMaxSplits, (lmax + kMinSelectSplit - 1) / kMinSelectSplit);
   int64_t best = 1;
   double least = 0;
@@ -76,6 +89,7 @@ static int64_t select_splits(int64_t units, int64_t lmax, int clusters) {
     const double n = static_cast<double>(units) * s;
     const double unit = kTileUs * ((lmax + s * kSplitRound - 1) / (s * kSplitRound));
     double t = n <= clusters ? unit : n / clusters * (kFill * unit + kUnitUs) + 0.5 * unit;
+    t += (s > 1 ? 2 : 1) * kStoreUs / select_parts(units * s, others * s, s > 1 ? kMostParts : kMostPartsBf16, clusters);
     if (s > 1) t += kMergeUs + kPartialUs * n;
     if (s == 1 || t < least) {
       best = s;
@@ -83,10 +97,6 @@ static int64_t select_splits(int64_t units, int64_t lmax, int clusters) {
     }
   }
   return best;
-}
-static SplitPlan plan_select(int64_t units, int64_t lmax, int clusters) {
-  if (lmax <= 0 || units <= 0) return SplitPlan{1, kSplitRound};
-  return cut(lmax, select_splits(units, lmax, clusters));
 }
 
 // Split-KV plan: pure function of its arguments (and the SM count).
@@ -126,7 +136,8 @@ struct DecodeLaunch {
   size_t obytes;     // launch order of the units (optional tail)
   bool simt;         // CUDA-core kernel instead of the tensor-core one
   bool use_order;    // units start longest first (order kernel launched)
-  int64_t units;     // windowed and tree decodes: units of the launch
+  int64_t units;     // windowed and tree decodes: units of the launch,
+  int32_t parts;     // and clusters that share one's output
 };
 
 DecodeLaunch decode_launch(int32_t T, int32_t H, int32_t D, int32_t interleave, int32_t d0, int32_t Dn,
@@ -172,18 +183,30 @@ int64_t most_owned(int64_t n, int32_t D, int32_t I) {
   return n / period * I + std::min<int64_t>(n % period, I);
 }
 
+// Most tokens that a request's rows see together, on any number of shards.
+int64_t select_visible(int32_t max_seq_len, int32_t max_q_len, int32_t window, int32_t sinks) {
+  return window > 0 ? std::min<int64_t>(max_seq_len, static_cast<int64_t>(window) + sinks + max_q_len) : max_seq_len;
+}
+
 DecodeLaunch select_launch(int32_t B, int32_t T, int32_t H, int32_t D, int32_t interleave, int32_t d0, int32_t Dn,
                            int32_t max_seq_len, int32_t max_q_len, int64_t cache_rows, const dcp::SelectArgs& sel,
-                           bool have_workspace, size_t workspace_bytes) {
+                           bool o_bf16, bool have_workspace, size_t workspace_bytes) {
   DecodeLaunch L{};
   int64_t lmax = dcp::local_len(max_seq_len, d0, D, interleave);
   if (sel.window > 0)  // the sinks, and a window for each row of the request
     lmax = std::min(lmax, most_owned(sel.sinks, D, interleave) +
                               most_owned(static_cast<int64_t>(sel.window) + max_q_len, D, interleave));
-  const int64_t units = static_cast<int64_t>(B) * sel.chunks * Dn;
-  L.plan = dcp::plan_select(units, lmax, select_clusters());
+  const int64_t units = static_cast<int64_t>(B) * sel.chunks * Dn, others = static_cast<int64_t>(sel.chunks) * Dn;
+  const int64_t visible = select_visible(max_seq_len, max_q_len, sel.window, sel.sinks);
+  const int clusters = select_clusters();
+  L.plan = dcp::SplitPlan{1, dcp::kSplitRound};
+  if (lmax > 0)  // (never more splits than the workspace's size allows for)
+    L.plan = dcp::cut(lmax, std::min(dcp::select_splits(units, others, lmax, clusters),
+                                     dcp::select_splits(units, others, visible, clusters)));
   L.need = dcp::split_workspace_bytes(L.plan, T, H, Dn);
-  L.units = (units + static_cast<int64_t>(sel.chunks) * Dn) * L.plan.splits;  // and the rows of no request
+  L.units = (units + others) * L.plan.splits;  // (others: the rows of no request)
+  L.parts = dcp::select_parts(units * L.plan.splits, others * L.plan.splits,
+                              o_bf16 && L.plan.splits == 1 ? dcp::kMostPartsBf16 : dcp::kMostParts, clusters);
   L.obytes = order_bytes(L.units);
   const char* force = std::getenv("DCP_FORCE_SIMT");
   L.simt = (force && force[0] == '1') ||
@@ -276,7 +299,8 @@ static dcp_status_t decode_partial_impl(const void* q, int64_t q_stride_tok, con
   }
   const DecodeLaunch launch =
       select ? select_launch(B, T, H, D, interleave, d0, Dn, max_seq_len, max_q_len,
-                             static_cast<int64_t>(num_blocks) * block_size, sel, workspace != nullptr, workspace_bytes)
+                             static_cast<int64_t>(num_blocks) * block_size, sel, o_dtype == DCP_DTYPE_BF16,
+                             workspace != nullptr, workspace_bytes)
              : decode_launch(T, H, D, interleave, d0, Dn, max_seq_len, workspace != nullptr, workspace_bytes,
                              kv_dtype == DCP_KV_FP8_E4M3);
   const dcp::SplitPlan plan = launch.plan;
@@ -302,6 +326,7 @@ static dcp_status_t decode_partial_impl(const void* q, int64_t q_stride_tok, con
     sel.div_period = dcp::make_fastdiv(static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(D) * interleave, 0x7fffffff)));
     sel.div_H = dcp::make_fastdiv(H);
   }
+  while (select && 1 << sel.parts_log2 < launch.parts) ++sel.parts_log2;
   a.sel = sel;
   a.num_blocks = num_blocks;
   a.block_size = block_size;
@@ -471,15 +496,17 @@ size_t dcp_decode_select_workspace_size(int32_t B, int32_t T, int32_t H, int32_t
       window < 0 || num_sinks < 0)
     return static_cast<size_t>(-1);
   if (B == 0 || T == 0) return 0;
-  // An upper bound over every interleave: a shard owns at most every visible
-  // token, and the split count grows with that bound.
-  int64_t lmax = max_seq_len;
-  if (window > 0) lmax = std::min(lmax, static_cast<int64_t>(window) + num_sinks + max_q_len);
-  const int32_t group = select_group(H, max_q_len);
-  const int64_t units = static_cast<int64_t>(B) * ((max_q_len - 1) / group + 1) * D;
-  const dcp::SplitPlan p{static_cast<int32_t>(dcp::select_splits(units, lmax, select_clusters())), 0};
-  return dcp::split_workspace_bytes(p, T, H, D) +
-         order_bytes((units + static_cast<int64_t>((max_q_len - 1) / group + 1) * D) * p.splits);
+  // Over every interleave and number of computed shards: no call cuts its
+  // units into more splits than it would if one shard owned everything.
+  const int64_t lmax = select_visible(max_seq_len, max_q_len, window, num_sinks);
+  const int32_t chunks = (max_q_len - 1) / select_group(H, max_q_len) + 1;
+  size_t most = 0;
+  for (int64_t Dn = 1; Dn <= D; ++Dn) {
+    const int64_t others = Dn * chunks, units = others * B;
+    const dcp::SplitPlan p{static_cast<int32_t>(dcp::select_splits(units, others, lmax, select_clusters())), 0};
+    most = std::max(most, dcp::split_workspace_bytes(p, T, H, static_cast<int32_t>(Dn)) + order_bytes((units + others) * p.splits));
+  }
+  return most;
 }
 
 int32_t dcp_decode_kernel_launches(int32_t B, int32_t T, int32_t H, int32_t D, int32_t interleave,

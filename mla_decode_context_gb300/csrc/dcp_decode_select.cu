@@ -139,6 +139,7 @@ struct Unit {
   // gap.  All but a few of a long unit's, so what the others need (the span,
   // the rows) is read from here for them and takes no registers.
   int32_t plain0, plain1;
+  int32_t c0, c1;                // 128-byte blocks of O's half rows to write (0: lse as well)
   int64_t pair0;                 // (row, head) pair of lane 0 in O_dst / lse_dst
   SelRow row[kMaxGroup];
   uint32_t tree[kMaxGroup][kMaxTree / 32];  // bit t: tree token vb + t
@@ -669,17 +670,26 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
     for (; dealt * clusters < units; ++dealt) {
       const int32_t at = dealt * clusters + ((dealt & 1) ? clusters - 1 - c : c);
       if (at >= units) continue;
-      const SelCoords k = sel_coords(a, a.unit_order ? *static_cast<const volatile int32_t*>(a.unit_order + at) : at);
+      // (units whose output several clusters share are all dealt in round 0)
+      int32_t u = at, part = 0;
+      if (a.unit_order) {
+        u = *static_cast<const volatile int32_t*>(a.unit_order + at);
+      } else if (a.sel.parts_log2 > 0) {
+        const int32_t parts = 1 << a.sel.parts_log2, mine = a.B * a.sel.chunks * a.Dn * a.plan.splits;
+        part = at < mine * parts ? at & (parts - 1) : 0;
+        u = at < mine * parts ? at >> a.sel.parts_log2 : at - mine * (parts - 1);
+      }
+      const SelCoords k = sel_coords(a, u);
       const SelUnit su = sel_unit(a, k.b, k.c);
       const int32_t d = a.d0 + k.dd;
-      if (su.R.err && lane == 0 && score && k.c == 0 && k.dd == 0 && k.s == 0) report(a.dev_error, su.R.err);
+      if (su.R.err && lane == 0 && score && part == 0 && k.c == 0 && k.dd == 0 && k.s == 0) report(a.dev_error, su.R.err);
       SelSpan S{0, 0, 0, 0};
       if (su.live) S = sel_span<true>(a, su.R, d);
       const int32_t lo = k.s * a.plan.chunk;
       const int32_t hi = min(S.nv, lo + a.plan.chunk);
-      write_empty(a, k.s, k.dd, su.extra0, su.extra, score, lane);
+      if (part == 0) write_empty(a, k.s, k.dd, su.extra0, su.extra, score, lane);
       if (lo >= hi) {
-        write_empty(a, k.s, k.dd, su.R.r0, su.R.n, score, lane);
+        if (part == 0) write_empty(a, k.s, k.dd, su.R.r0, su.R.n, score, lane);
         continue;
       }
       if (lane == 0) {
@@ -694,6 +704,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         U.vb = S.vb;
         U.vt = a.sel.tree ? S.vb : 0x7fffffff;
         U.gap = S.gap;
+        const int32_t blocks = a.o_bf16 ? 4 : 8;
+        U.c0 = (blocks * part) >> a.sel.parts_log2;
+        U.c1 = (blocks * (part + 1)) >> a.sel.parts_log2;
         U.pair0 = ((static_cast<int64_t>(k.s) * a.Dn + k.dd) * a.T + su.R.r0) * a.H;
       }
       describe_rows(a, su.R, S, d, lo, hi, U, lane);
@@ -894,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         const int fs = k % kFinSlots;
         st_async_peer_b32(map_peer(smem_base + kOffFin + fs * 512 + 4 * h, peer), __float_as_uint(some ? 1.f / l : 0.f),
                           map_peer(smem_u32(&bar.fin_l[fs]), peer));
-        if (h < U->nl) a.lse_dst[U->pair0 + h] = some ? (mo + log2f(l)) * kLn2 : -INFINITY;
+        if (h < U->nl && U->c0 == 0) a.lse_dst[U->pair0 + h] = some ? (mo + log2f(l)) * kLn2 : -INFINITY;
       }
       j0 += ntiles;
       it.done(bar, lane);
@@ -911,8 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
     for (int k = 0;; ++k) {
       const Unit* U = it.get(bar, ok);
       if (!U) break;
-      const int32_t ntiles = U->ntiles, nl = U->nl;
-      const int64_t pair0 = U->pair0;
+      const int32_t ntiles = U->ntiles;
       if (warp < 4) {
         // --------------------------------------------- max tracking, rescale
         float m_prev = -INFINITY;
@@ -1008,12 +1020,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
       // blocks of 128 bytes a row (64 bf16 or 32 fp32 columns), transposed
       // over four lanes to whole lines (each lane storing its own row took
       // 4.2 us a bf16 unit and 7.4 us an fp32 one)
-      const int nblk = a.o_bf16 ? 4 : 8, row_bytes = a.o_bf16 ? 2 * kLatent : 4 * kLatent;
+      const volatile Unit* V = U;
+      const int32_t nl = V->nl, c0 = V->c0, c1 = V->c1;
+      const int64_t pair0 = V->pair0;
+      const int row_bytes = a.o_bf16 ? 2 * kLatent : 4 * kLatent;
       const uint32_t col0 = tbase + (static_cast<uint32_t>(q4 * 32) << 16) + kColO + 256 * (warp >> 2);
       unsigned char* out = static_cast<unsigned char*>(a.O_dst) + (pair0 + q4 * 32 + (lane & ~3)) * row_bytes +
                            (warp >> 2) * (row_bytes / 2) + 32 * (lane & 3);
 #pragma unroll 1
-      for (int c = 0; c < nblk; ++c) {
+      for (int c = c0; c < c1; ++c) {
         uint32_t o[32];
         if (a.o_bf16) {
 #pragma unroll
@@ -1033,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
         }
-        if (c == nblk - 1) {
+        if (c == c1 - 1) {
           // O is read: the next unit's PV may overwrite it
           tc_fence_before();
           __syncwarp();
@@ -1511,7 +1526,12 @@ cudaError_t launch_select_order(const DecodeArgs& a, int32_t units, int32_t* ord
 cudaError_t launch_decode_select(const DecodeArgs& a, int32_t units, cudaStream_t st) {
   const int resident = decode_select_clusters();
   if (resident <= 0) return cudaErrorInvalidDevice;
-  if (units <= 0 || a.plan.chunk % kTile != 0) return cudaErrorInvalidValue;
+  const int32_t parts = 1 << a.sel.parts_log2;
+  if (units <= 0 || a.plan.chunk % kTile != 0 || parts > (a.o_bf16 ? 4 : 8)) return cudaErrorInvalidValue;
+  if (parts > 1) {
+    units += (parts - 1) * a.B * a.sel.chunks * a.Dn * a.plan.splits;
+    if (units > resident || a.unit_order) return cudaErrorInvalidValue;
+  }
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = launch_config(units < resident ? units : resident, a.unit_order != nullptr, st, attr);
   return a.kv_fp8 ? cudaLaunchKernelEx(&cfg, decode_select_kernel<true>, a, units)

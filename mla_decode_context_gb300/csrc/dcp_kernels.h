@@ -48,6 +48,9 @@ struct SelectArgs {
   // (tensor-core kernel) division by the unit index's factors, the interleave
   // period D x I (< 2^31 there) and H
   FastDiv div_chunks, div_splits, div_Dn, div_period, div_H;
+  // clusters (a power of two) that share a unit's output: each computes the
+  // unit and writes its own columns.  > 1 only where all run at once.
+  int32_t parts_log2;
 };
 
 // Everything one decode launch needs (validated by the C ABI).
