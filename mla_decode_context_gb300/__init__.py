@@ -11,7 +11,6 @@ The library is loaded on first use; if it has not been built the call raises
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -357,11 +356,80 @@ def dcp_decode_select_workspace_size(B: int, T: int, H: int, D: int, max_seq_len
 def _decode_select(where, tree_mask, q, kv_cache, block_table, seq_lens, query_start_loc, O_part, lse_part, D,
                    interleave, scale, window, num_sinks, max_seq_len, max_q_len, kv_scale, shard_begin, shard_count,
                    workspace, dev_error, stream) -> None:
-    """The two selecting decodes' checks (as _decode_geometry's: what the
-    kernels index by, shapes before devices) and call."""
+    """The two selecting decodes' checks and call.  One expression covers the
+    calls that are right; any other goes through _explain_select."""
     if shard_count is None:
         shard_count = D - shard_begin
     tree = where is _TREE
+    try:
+        T, H, dim = q.shape
+        blocks, block_size, row = kv_cache.shape
+        B, = seq_lens.shape
+        q0, q1, q2 = q.stride()
+        table, table_stride = block_table.shape, block_table.stride()
+        local = len(table) == 3
+        device = q.get_device()
+        o_dtype, fp8 = O_part.dtype, kv_cache.dtype is _U8
+        good = (
+            q.dtype is _BF16 and dim == row == KV_DIM and q1 == KV_DIM and q2 == 1 and device >= 0
+            and (fp8 or kv_cache.dtype is _BF16) and kv_cache.get_device() == device and kv_cache.is_contiguous()
+            and block_table.dtype is _I32T and block_table.get_device() == device and table_stride[-1] == 1
+            and (table[0] == shard_count if local else len(table) == 2) and table[-2] == B
+            and seq_lens.dtype is _I32T and seq_lens.get_device() == device and seq_lens.is_contiguous()
+            and query_start_loc.dtype is _I32T and query_start_loc.get_device() == device
+            and query_start_loc.shape == (B + 1,) and query_start_loc.is_contiguous()
+            and (o_dtype is _BF16 or o_dtype is _F32) and O_part.get_device() == device and O_part.is_contiguous()
+            and O_part.shape == (shard_count, T, H, LATENT_DIM)
+            and lse_part.dtype is _F32 and lse_part.get_device() == device and lse_part.is_contiguous()
+            and lse_part.shape == (shard_count, T, H)
+            and (_rows_scaled(kv_scale, blocks, block_size, device) if fp8 else kv_scale is None)
+            and (workspace is None or (workspace.get_device() == device and workspace.is_contiguous()))
+            and (dev_error is None or _flag_word(dev_error, device)))
+        if good and tree:
+            rows, words = tree_mask.shape
+            m0, m1 = tree_mask.stride()
+            good = (tree_mask.dtype is _I64T and tree_mask.get_device() == device and rows == T and m1 == 1
+                    and words * 64 >= max_q_len)
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        T, H, B, local, fp8, device = _explain_select(tree_mask if tree else None, q, kv_cache, block_table, seq_lens,
+                                                      query_start_loc, O_part, lse_part, max_q_len, kv_scale,
+                                                      shard_count, workspace, dev_error, tree)
+        q0, o_dtype = q.stride(0), O_part.dtype
+        blocks, block_size, _ = kv_cache.shape
+        table, table_stride = block_table.shape, block_table.stride()
+        m0 = tree_mask.stride(0) if tree else 0
+    extra = (tree_mask.data_ptr(), m0 if T > 1 else (max_q_len + 63) // 64) if tree else ()
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    call = getattr(_lib or lib(), where)
+    with _Call(where, device):
+        st = call(
+            q.data_ptr(), q0 if T > 1 else H * KV_DIM, kv_cache.data_ptr(),
+            KV_FP8_E4M3 if fp8 else KV_BF16, kv_scale.data_ptr() if fp8 else None, blocks, block_size,
+            block_table.data_ptr(), table[-1], table_stride[-2], 1 if local else 0,
+            table_stride[0] if local else 0, shard_begin, shard_count, seq_lens.data_ptr(),
+            query_start_loc.data_ptr(), B, T, H, max_seq_len, max_q_len, D, interleave, scale, *extra, window,
+            num_sinks, O_part.data_ptr(), DTYPE_BF16 if o_dtype is _BF16 else DTYPE_F32,
+            lse_part.data_ptr(), workspace.data_ptr() if ws_bytes else None, ws_bytes,
+            None if dev_error is None else dev_error.data_ptr(), _stream_of(stream, device))
+    if st:
+        _check(st, where)
+
+
+def _stream_context(stream, device):
+    """`stream` as the current one, for work on tensors of `device`."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
+    return torch.cuda.stream(stream)
+
+
+def _explain_select(tree_mask, q, kv_cache, block_table, seq_lens, query_start_loc, O_part, lse_part, max_q_len,
+                    kv_scale, shard_count, workspace, dev_error, tree):
+    """What is wrong with a selecting decode's tensors, shapes before devices
+    (as _decode_geometry), or (T, H, B, local, fp8, device) if nothing is."""
     if not isinstance(O_part, torch.Tensor) or O_part.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("O_part must be a bfloat16 or float32 tensor")
     fp8 = _cache_format(kv_cache, kv_scale)
@@ -390,28 +458,13 @@ def _decode_select(where, tree_mask, q, kv_cache, block_table, seq_lens, query_s
         raise ValueError("seq_lens [B], query_start_loc [B + 1] and block_table [.., B, W] disagree on B")
     if tuple(O_part.shape) != (shard_count, T, H, LATENT_DIM) or tuple(lse_part.shape) != (shard_count, T, H):
         raise ValueError("O_part must be [D, T, H, 512] and lse_part [D, T, H]")
-    extra = ()
-    if tree:
-        words = (max_q_len + 63) // 64
-        if tree_mask.dim() != 2 or tree_mask.shape[0] != T or tree_mask.shape[1] < words or \
-                (tree_mask.shape[1] > 1 and tree_mask.stride(1) != 1):
-            raise ValueError("tree_mask must be [T, >= %d] words with unit column stride (see pack_tree_mask)" % words)
-        extra = (tree_mask.data_ptr(), tree_mask.stride(0) if T > 1 else words)
+    words = (max_q_len + 63) // 64
+    if tree and (tree_mask.dim() != 2 or tree_mask.shape[0] != T or tree_mask.shape[1] < words or
+                 (tree_mask.shape[1] > 1 and tree_mask.stride(1) != 1)):
+        raise ValueError("tree_mask must be [T, >= %d] words with unit column stride (see pack_tree_mask)" % words)
     if dev_error is not None and dev_error.numel() == 0:
         raise ValueError("dev_error must not be empty")
-    device = _placed(args)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _on(device), _Range(where):
-        st = getattr(lib(), where)(
-            q.data_ptr(), q.stride(0) if T > 1 else H * KV_DIM, kv_cache.data_ptr(),
-            KV_FP8_E4M3 if fp8 else KV_BF16, _addr(kv_scale), kv_cache.shape[0], kv_cache.shape[1],
-            block_table.data_ptr(), block_table.shape[-1], block_table.stride(-2), 1 if local else 0,
-            block_table.stride(0) if local else 0, shard_begin, shard_count, seq_lens.data_ptr(),
-            query_start_loc.data_ptr(), B, T, H, max_seq_len, max_q_len, D, interleave, scale, *extra, window,
-            num_sinks, O_part.data_ptr(), DTYPE_BF16 if O_part.dtype == torch.bfloat16 else DTYPE_F32,
-            lse_part.data_ptr(), workspace.data_ptr() if ws_bytes else None, ws_bytes, _addr(dev_error),
-            _stream_of(stream, device))
-    _check(st, where)
+    return T, H, B, local, fp8, _placed(args)
 
 
 _WINDOW, _TREE = "dcp_mla_decode_partial_window", "dcp_mla_decode_partial_tree"
@@ -567,6 +620,51 @@ def _addr(t: Optional[torch.Tensor]):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream() without the object: 0.1 of 3 us
 
 
+_BF16, _F32, _U8, _I32T, _I64T = torch.bfloat16, torch.float32, torch.uint8, torch.int32, torch.int64
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _rows_scaled(kv_scale, blocks: int, block_size: int, device: int) -> bool:
+    return (kv_scale.dtype is _F32 and kv_scale.shape == (blocks, block_size) and kv_scale.get_device() == device
+            and kv_scale.is_contiguous())
+
+
+def _flag_word(dev_error, device: int) -> bool:
+    return dev_error.dtype is _I32T and dev_error.get_device() == device and dev_error.numel() > 0
+
+
+class _Call:
+    """The surroundings of a library call: `device` is the current one (the
+    library launches on the current device) and an NVTX range names it."""
+    __slots__ = ("name", "device", "before", "pushed")
+
+    def __init__(self, name: str, device: int):
+        self.name, self.device = name, device
+
+    def __enter__(self):
+        self.before = None
+        if _device_now() != self.device:
+            self.before = torch.cuda.device(self.device)
+            self.before.__enter__()
+        self.pushed = False
+        if _nvtx is not None:
+            try:
+                _nvtx.range_push(self.name)
+                self.pushed = True
+            except Exception:
+                pass
+
+    def __exit__(self, *exc):
+        if self.pushed:
+            try:
+                _nvtx.range_pop()
+            except Exception:
+                pass
+        if self.before is not None:
+            self.before.__exit__(*exc)
+        return False
+
+
 def _stream_of(stream, device: int):
     if stream is None:
         return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
@@ -597,15 +695,6 @@ def _placed(args) -> int:
     return device
 
 
-def _on(device: int):
-    """A context in which `device` is the current one (the library launches on
-    the current device)."""
-    return _HERE if device == torch.cuda.current_device() else torch.cuda.device(device)
-
-
-_HERE = contextlib.nullcontext()
-
-
 def _cache_format(kv_cache, kv_scale):
     """Check a paged cache [num_blocks, block_size, 576] (bf16, or uint8 FP8
     E4M3 codes with kv_scale fp32 [num_blocks, block_size]) and return
@@ -632,8 +721,68 @@ def dcp_decode_concat_cache_v2(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q_out, k
     E4M3 codes with kv_scale fp32 [num_blocks, block_size] (each written row
     gets its own power-of-two scale).  ql_nope, q_pe and q_out may all be None
     to write the cache alone."""
-    bf16 = torch.bfloat16
     query = ql_nope is not None or q_pe is not None or q_out is not None
+    H, strides, q_stride = 0, (0, 0, 0, 0), 0
+    try:
+        T, latent = kv_c.shape
+        blocks, block_size, row = kv_cache.shape
+        c0, c1 = kv_c.stride()
+        p0, p1 = k_pe.stride()
+        device = kv_cache.get_device()
+        fp8 = kv_cache.dtype is _U8
+        good = (
+            device >= 0 and (fp8 or kv_cache.dtype is _BF16) and row == KV_DIM and kv_cache.is_contiguous()
+            and kv_c.dtype is _BF16 and kv_c.get_device() == device and latent == LATENT_DIM and c1 == 1
+            and k_pe.dtype is _BF16 and k_pe.get_device() == device and k_pe.shape == (T, ROPE_DIM) and p1 == 1
+            and slot_mapping.dtype is _I64T and slot_mapping.get_device() == device
+            and slot_mapping.shape == (T,) and slot_mapping.is_contiguous()
+            and (_rows_scaled(kv_scale, blocks, block_size, device) if fp8 else kv_scale is None)
+            and (dev_error is None or _flag_word(dev_error, device)))
+        if good and query:
+            _, H, _ = ql_nope.shape
+            n0, n1, n2 = ql_nope.stride()
+            r0, r1, r2 = q_pe.stride()
+            q_stride, o1, o2 = q_out.stride()
+            strides = (n0, n1, r0, r1)
+            good = (
+                ql_nope.dtype is _BF16 and ql_nope.get_device() == device
+                and ql_nope.shape == (T, H, LATENT_DIM) and n2 == r2 == o2 == 1 and H >= 1 and T > 0
+                and q_pe.dtype is _BF16 and q_pe.get_device() == device and q_pe.shape == (T, H, ROPE_DIM)
+                and q_out.dtype is _BF16 and q_out.get_device() == device and q_out.shape == (T, H, KV_DIM)
+                and o1 == KV_DIM)
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        T, H, fp8, device = _explain_write(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q_out, kv_cache, kv_scale,
+                                           dev_error, query)
+        if query:
+            strides = [t.stride(d) for t in (ql_nope, q_pe) for d in (0, 1)]
+            q_stride = q_out.stride(0)
+        c0, p0 = kv_c.stride(0), k_pe.stride(0)
+        blocks, block_size, _ = kv_cache.shape
+    if T == 0:
+        return
+    if T == 1:  # (the stride of a dimension of one element is never used)
+        c0 = p0 = 0
+        q_stride = H * KV_DIM
+    if query and (T == 1 or H == 1):
+        many, heads = int(T > 1), int(H > 1)
+        strides = (strides[0] * many, strides[1] * heads, strides[2] * many, strides[3] * heads)
+    call = (_lib or lib()).dcp_decode_concat_cache_v2
+    with _Call("dcp_decode_concat_cache_v2", device):
+        st = call(
+            ql_nope.data_ptr() if query else None, strides[0], strides[1], q_pe.data_ptr() if query else None,
+            strides[2], strides[3], kv_c.data_ptr(), c0, k_pe.data_ptr(), p0, slot_mapping.data_ptr(), T, H,
+            q_out.data_ptr() if query else None, q_stride, kv_cache.data_ptr(),
+            KV_FP8_E4M3 if fp8 else KV_BF16, kv_scale.data_ptr() if fp8 else None, blocks * block_size,
+            None if dev_error is None else dev_error.data_ptr(), _stream_of(stream, device))
+    if st:
+        _check(st, "dcp_decode_concat_cache_v2")
+
+
+def _explain_write(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q_out, kv_cache, kv_scale, dev_error, query):
+    """What is wrong with a cache write's tensors, or (T, H, fp8, device)."""
+    bf16 = torch.bfloat16
     fp8 = _cache_format(kv_cache, kv_scale)
     args = [("kv_cache", kv_cache, kv_cache.dtype, True), ("kv_c", kv_c, bf16, False), ("k_pe", k_pe, bf16, False)]
     rows = [("kv_c", kv_c, 2, LATENT_DIM), ("k_pe", k_pe, 2, ROPE_DIM)]
@@ -660,21 +809,7 @@ def dcp_decode_concat_cache_v2(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q_out, k
     args.append(("slot_mapping", slot_mapping, torch.int64, True))
     if dev_error is not None and dev_error.numel() == 0:
         raise ValueError("dev_error must not be empty")
-    device = _placed(args)
-    if T == 0:
-        return
-    strides = [0] * 4
-    if query:  # (the stride of a dimension of one element is never used)
-        strides = [t.stride(d) if t.shape[d] > 1 else 0 for t in (ql_nope, q_pe) for d in (0, 1)]
-    many = T > 1
-    with _on(device), _Range("dcp_decode_concat_cache_v2"):
-        st = lib().dcp_decode_concat_cache_v2(
-            _addr(ql_nope), strides[0], strides[1], _addr(q_pe), strides[2], strides[3], kv_c.data_ptr(),
-            kv_c.stride(0) if many else 0, k_pe.data_ptr(), k_pe.stride(0) if many else 0, slot_mapping.data_ptr(), T,
-            H, _addr(q_out), q_out.stride(0) if query and many else H * KV_DIM, kv_cache.data_ptr(),
-            KV_FP8_E4M3 if fp8 else KV_BF16, _addr(kv_scale), kv_cache.shape[0] * kv_cache.shape[1],
-            _addr(dev_error), _stream_of(stream, device))
-    _check(st, "dcp_decode_concat_cache_v2")
+    return T, H, fp8, _placed(args)
 
 
 def dcp_latent_cache_read(kv_cache, block_table, cu_lens, out, *, seq_starts: Optional[torch.Tensor] = None,
@@ -688,6 +823,53 @@ def dcp_latent_cache_read(kv_cache, block_table, cu_lens, out, *, seq_starts: Op
     that other shards own are zeros, rows past cu_lens[B] are left alone."""
     if shard_count is None:
         shard_count = D - shard_begin
+    if D < 1 or D > MAX_SHARDS or shard_begin < 0 or shard_count < 1 or shard_begin + shard_count > D:
+        raise ValueError("shards [shard_begin, shard_begin + shard_count) must lie in [0, D), D <= %d" % MAX_SHARDS)
+    try:
+        N, dim = out.shape
+        out_stride, unit = out.stride()
+        blocks, block_size, row = kv_cache.shape
+        B = cu_lens.shape[0] - 1
+        table, table_stride = block_table.shape, block_table.stride()
+        local = len(table) == 3
+        device = kv_cache.get_device()
+        fp8, o_dtype = kv_cache.dtype is _U8, out.dtype
+        good = (
+            device >= 0 and (fp8 or kv_cache.dtype is _BF16) and row == dim == KV_DIM and kv_cache.is_contiguous()
+            and (o_dtype is _BF16 or o_dtype is _F32) and out.get_device() == device and unit == 1
+            and block_table.dtype is _I32T and block_table.get_device() == device and table_stride[-1] == 1
+            and (table[0] == shard_count if local else len(table) == 2) and table[-2] == B
+            and cu_lens.dtype is _I32T and cu_lens.get_device() == device and cu_lens.shape == (B + 1,)
+            and cu_lens.is_contiguous()
+            and (seq_starts is None or (seq_starts.dtype is _I32T and seq_starts.get_device() == device
+                                        and seq_starts.shape == (B,) and seq_starts.is_contiguous()))
+            and (_rows_scaled(kv_scale, blocks, block_size, device) if fp8 else kv_scale is None)
+            and (dev_error is None or _flag_word(dev_error, device)))
+    except (AttributeError, IndexError, TypeError, ValueError):
+        good = False
+    if not good:
+        B, N, local, fp8, device = _explain_read(kv_cache, block_table, cu_lens, out, seq_starts, kv_scale,
+                                                 shard_count, dev_error)
+        out_stride, o_dtype = out.stride(0), out.dtype
+        blocks, block_size, _ = kv_cache.shape
+        table, table_stride = block_table.shape, block_table.stride()
+    if B == 0 or N == 0:
+        return
+    call = (_lib or lib()).dcp_latent_cache_read
+    with _Call("dcp_latent_cache_read", device):
+        st = call(
+            kv_cache.data_ptr(), KV_FP8_E4M3 if fp8 else KV_BF16, kv_scale.data_ptr() if fp8 else None, blocks,
+            block_size, block_table.data_ptr(), table[-1], table_stride[-2], 1 if local else 0,
+            table_stride[0] if local else 0, D, interleave, shard_begin, shard_count,
+            None if seq_starts is None else seq_starts.data_ptr(), cu_lens.data_ptr(), B, N, out.data_ptr(),
+            DTYPE_F32 if o_dtype is _F32 else DTYPE_BF16, out_stride if N > 1 else KV_DIM,
+            None if dev_error is None else dev_error.data_ptr(), _stream_of(stream, device))
+    if st:
+        _check(st, "dcp_latent_cache_read")
+
+
+def _explain_read(kv_cache, block_table, cu_lens, out, seq_starts, kv_scale, shard_count, dev_error):
+    """What is wrong with a cache read's tensors, or (B, N, local, fp8, device)."""
     fp8 = _cache_format(kv_cache, kv_scale)
     if not isinstance(out, torch.Tensor) or out.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out must be a bfloat16 or float32 tensor")
@@ -713,20 +895,7 @@ def dcp_latent_cache_read(kv_cache, block_table, cu_lens, out, *, seq_starts: Op
         raise ValueError("seq_starts must be [B]")
     if dev_error is not None and dev_error.numel() == 0:
         raise ValueError("dev_error must not be empty")
-    if D < 1 or D > MAX_SHARDS or shard_begin < 0 or shard_count < 1 or shard_begin + shard_count > D:
-        raise ValueError("shards [shard_begin, shard_begin + shard_count) must lie in [0, D), D <= %d" % MAX_SHARDS)
-    device = _placed(args)
-    if B == 0 or N == 0:
-        return
-    with _on(device), _Range("dcp_latent_cache_read"):
-        st = lib().dcp_latent_cache_read(
-            kv_cache.data_ptr(), KV_FP8_E4M3 if fp8 else KV_BF16, _addr(kv_scale), kv_cache.shape[0],
-            kv_cache.shape[1], block_table.data_ptr(), block_table.shape[-1], block_table.stride(-2),
-            1 if local else 0, block_table.stride(0) if local else 0, D, interleave, shard_begin, shard_count,
-            _addr(seq_starts), cu_lens.data_ptr(), B, N, out.data_ptr(),
-            DTYPE_F32 if out.dtype == torch.float32 else DTYPE_BF16, out.stride(0) if N > 1 else KV_DIM,
-            _addr(dev_error), _stream_of(stream, device))
-    _check(st, "dcp_latent_cache_read")
+    return B, N, local, fp8, _placed(args)
 
 
 # ----------------------------------------------------------------------------
@@ -785,11 +954,15 @@ def decode_concat_cache(ql_nope, q_pe, kv_c, k_pe, slot_mapping, kv_cache, dev_e
     """Allocating form: returns the decode query q bf16 [T, H, 576]; writes
     the step's latent rows into kv_cache in place (bf16, or FP8 E4M3 codes and
     their scales with kv_scale)."""
+    if kv_scale is not None and stream is not None:  # (as in _decode_select_alloc)
+        with _stream_context(stream, ql_nope.device):
+            return decode_concat_cache(ql_nope, q_pe, kv_c, k_pe, slot_mapping, kv_cache, dev_error=dev_error,
+                                       kv_scale=kv_scale)
     T, H = ql_nope.shape[0], ql_nope.shape[1]
     q = torch.empty((T, H, KV_DIM), dtype=torch.bfloat16, device=ql_nope.device)
     if kv_scale is not None:
         dcp_decode_concat_cache_v2(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q, kv_cache, kv_scale=kv_scale,
-                                   dev_error=dev_error, stream=stream)
+                                   dev_error=dev_error)
         return q
     dcp_decode_concat_cache(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q, kv_cache, dev_error=dev_error,
                             stream=stream)
@@ -811,6 +984,11 @@ def latent_cache_read(kv_cache, block_table, cu_lens, num_rows: int, seq_starts:
                       stream=None):
     """Allocating form: returns out [num_rows, 576] of out_dtype, num_rows =
     cu_lens[B] (known on the host; rows past cu_lens[B] are undefined)."""
+    if stream is not None:  # (as in _decode_select_alloc)
+        with _stream_context(stream, kv_cache.device):
+            return latent_cache_read(kv_cache, block_table, cu_lens, num_rows, seq_starts=seq_starts,
+                                     kv_scale=kv_scale, out_dtype=out_dtype, D=D, interleave=interleave,
+                                     shard_begin=shard_begin, shard_count=shard_count, dev_error=dev_error)
     out = torch.empty((num_rows, KV_DIM), dtype=out_dtype, device=kv_cache.device)
     dcp_latent_cache_read(kv_cache, block_table, cu_lens, out, seq_starts=seq_starts, kv_scale=kv_scale, D=D,
                           interleave=interleave, shard_begin=shard_begin, shard_count=shard_count,
@@ -830,21 +1008,26 @@ def pack_tree_mask(visible: torch.Tensor) -> torch.Tensor:
     return (bits.view(T, words, 64) << torch.arange(64, device=visible.device)).sum(-1)
 
 
-def _decode_select_alloc(entry, masks, q, kv_cache, block_table, seq_lens, query_start_loc, D, interleave, scale,
+def _decode_select_alloc(where, tree_mask, q, kv_cache, block_table, seq_lens, query_start_loc, D, interleave, scale,
                          window, num_sinks, max_seq_len, max_q_len, kv_scale, out_dtype, workspace, dev_error, stream):
+    if stream is not None:  # memory for work on another stream comes from that stream's pool
+        with _stream_context(stream, q.device):
+            return _decode_select_alloc(where, tree_mask, q, kv_cache, block_table, seq_lens, query_start_loc, D,
+                                        interleave, scale, window, num_sinks, max_seq_len, max_q_len, kv_scale,
+                                        out_dtype, workspace, dev_error, None)
     T, H = q.shape[0], q.shape[1]
+    device = q.device
     if max_seq_len is None:
         max_seq_len = block_table.shape[-1] * kv_cache.shape[1] * (D if block_table.dim() == 3 else 1)
     if max_q_len is None:
         max_q_len = max(1, T)
-    O = torch.empty((D, T, H, LATENT_DIM), dtype=out_dtype, device=q.device)
-    lse = torch.empty((D, T, H), dtype=torch.float32, device=q.device)
+    O = torch.empty((D, T, H, LATENT_DIM), dtype=out_dtype, device=device)
+    lse = torch.empty((D, T, H), dtype=_F32, device=device)
     if workspace is None:
         n = dcp_decode_select_workspace_size(seq_lens.shape[0], T, H, D, max_seq_len, max_q_len, window, num_sinks)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
-    entry(q, kv_cache, block_table, seq_lens, query_start_loc, *masks, O, lse, D=D, interleave=interleave,
-          scale=scale, window=window, num_sinks=num_sinks, max_seq_len=max_seq_len, max_q_len=max_q_len,
-          kv_scale=kv_scale, workspace=workspace, dev_error=dev_error, stream=stream)
+        workspace = torch.empty(n, dtype=_U8, device=device) if n else None
+    _decode_select(where, tree_mask, q, kv_cache, block_table, seq_lens, query_start_loc, O, lse, D, interleave, scale,
+                   window, num_sinks, max_seq_len, max_q_len, kv_scale, 0, D, workspace, dev_error, None)
     return O, lse
 
 
@@ -856,7 +1039,7 @@ def decode_partial_window(q, kv_cache, block_table, seq_lens, query_start_loc, D
     """Allocating form of dcp_mla_decode_partial_window: returns (O_part
     [D, T, H, 512] of out_dtype, lse_part fp32 [D, T, H]); merge them with
     lse_combine."""
-    return _decode_select_alloc(dcp_mla_decode_partial_window, (), q, kv_cache, block_table, seq_lens,
+    return _decode_select_alloc(_WINDOW, None, q, kv_cache, block_table, seq_lens,
                                 query_start_loc, D, interleave, scale, window, num_sinks, max_seq_len, max_q_len,
                                 kv_scale, out_dtype, workspace, dev_error, stream)
 
@@ -869,6 +1052,6 @@ def decode_partial_tree(q, kv_cache, block_table, seq_lens, query_start_loc, tre
     """Allocating form of dcp_mla_decode_partial_tree: returns (O_part
     [D, T, H, 512] of out_dtype, lse_part fp32 [D, T, H]); merge them with
     lse_combine."""
-    return _decode_select_alloc(dcp_mla_decode_partial_tree, (tree_mask,), q, kv_cache, block_table, seq_lens,
+    return _decode_select_alloc(_TREE, tree_mask, q, kv_cache, block_table, seq_lens,
                                 query_start_loc, D, interleave, scale, window, num_sinks, max_seq_len, max_q_len,
                                 kv_scale, out_dtype, workspace, dev_error, stream)
