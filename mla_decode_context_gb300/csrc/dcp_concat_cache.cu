@@ -116,12 +116,12 @@ __device__ __forceinline__ uint2 to_codes8(const uint4& v, float pa, float pb) {
                     to_codes(v.z, pa, pb) | to_codes(v.w, pa, pb) << 16);
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kQuery>
 __global__ void __launch_bounds__(kThreadsV2) concat_cache_v2_kernel(ConcatCacheArgs a, int warps_per_token) {
   const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreadsV2 / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int64_t t = w / warps_per_token;
-  const int part = static_cast<int>(w - t * warps_per_token);
+  const int64_t t = kQuery ? w / warps_per_token : w;
+  const int part = kQuery ? static_cast<int>(w - t * warps_per_token) : 0;
   if (t >= a.T) return;
   if (part == 0) {
     // this token's cache row
@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kThreadsV2) concat_cache_v2_kernel(ConcatCache
     }
     return;
   }
+  if constexpr (!kQuery) return;
   const int h0 = (part - 1) * kHeadsPerWarp;
   const int n = min(kHeadsPerWarp, a.H - h0) * kUnitsRow;  // 16-byte units of this warp's heads
   const unsigned char* nope = static_cast<const unsigned char*>(a.ql_nope) + 2 * (t * a.ql_nope_stride_tok + h0 * a.ql_nope_stride_head);
@@ -181,8 +182,11 @@ cudaError_t launch_concat_cache_v2(const ConcatCacheArgs& a, cudaStream_t st) {
   const int64_t ctas = (static_cast<int64_t>(a.T) * per_token + kThreadsV2 / 32 - 1) / (kThreadsV2 / 32);
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>(ctas);
-  if (a.kv_scale) concat_cache_v2_kernel<true><<<grid, kThreadsV2, 0, st>>>(a, per_token);
-  else concat_cache_v2_kernel<false><<<grid, kThreadsV2, 0, st>>>(a, per_token);
+  // (without the query's nine loads a thread takes fewer registers: more rows
+  // in flight)
+  const auto kernel = a.kv_scale ? (a.H > 0 ? concat_cache_v2_kernel<true, true> : concat_cache_v2_kernel<true, false>)
+                                 : (a.H > 0 ? concat_cache_v2_kernel<false, true> : concat_cache_v2_kernel<false, false>);
+  kernel<<<grid, kThreadsV2, 0, st>>>(a, per_token);
   return cudaGetLastError();
 }
 
