@@ -44,7 +44,7 @@
  *     rope dims); values are the first DCP_LATENT_DIM = 512 dims.
  *   - LSEs are natural logarithms; -inf marks "no tokens".
  *   - Two environment variables, read on every call and unset in normal use,
- *     change what dcp_mla_decode_partial runs:
+ *     change what the decodes run (the windowed and tree ones included):
  *       DCP_FORCE_SIMT=1       the CUDA-core reference kernel instead of the
  *                              tensor-core one (A/B checks);
  *       DCP_TEST_STALL_WAIT=1  test hook for the failure path: one wait of
@@ -545,8 +545,8 @@ dcp_status_t dcp_mla_decode_partial_tree(
 
 /*
  * Bytes of device workspace the windowed and tree decodes need for these
- * sizes on the CURRENT device (D = shard_count), an upper bound over every
- * interleave.  Returns (size_t)-1 on invalid arguments.
+ * sizes on the CURRENT device: enough for every interleave and for every
+ * shard_count up to D.  Returns (size_t)-1 on invalid arguments.
  */
 size_t dcp_decode_select_workspace_size(int32_t B, int32_t T, int32_t H, int32_t D,
                                         int32_t max_seq_len, int32_t max_q_len,

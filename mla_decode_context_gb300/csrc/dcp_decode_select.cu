@@ -17,7 +17,9 @@
 // tiles, while setting a unit up, loading its Q, filling and draining the
 // pipeline and writing O took 14 us of a unit's 25 when each unit was its own
 // cluster launch.  So clusters are persistent: they walk the list of units,
-// and the rings run through the unit borders.
+// and the rings run through the unit borders (a further unit now takes 5-6 us
+// besides its tiles; 64 requests x 8 shards on that window: 175 -> 126 us, 120
+// now).
 //   - A scheduler warp per CTA resolves the next units (rows, spans, the
 //     lanes' masks) into a ring of descriptors while the current one runs; it
 //     also writes the rows that have nothing to see.
@@ -43,6 +45,13 @@
 // values from that tile before PV (rows that see the token have a NaN weight
 // there and stay NaN).
 //
+// What bounds it: the loop of a tile, 0.6 us (1,150-1,390 cycles; its MMAs alone
+// take ~600), in which the issue of S (three warps, ~120 cycles per MMA while
+// the copies land), the softmax's turn of an S slot and P's way to the value
+// CTA take nearly the same time.  4 trees of 32 rows at 128 heads over 8 shards
+// of 12,000-16,384 tokens: 587 us, 45 % of the measured bf16 rate; with an FP8
+// cache a tile takes 0.85 us, the producers' widening.
+//
 // Roundings: P and, for a bf16 output, O / l once, to bf16 (the MMA's operand
 // and the output type); fp8 codes x scale to bf16 (exact for power-of-two
 // scales).  Scores, maxima, sums, O and split partials are fp32.
@@ -62,8 +71,8 @@
 //   warps 20-23 score: softmax group 1 (odd tiles)
 //               value: bf16 cache: receive-ring producers
 // Twenty-four warps leave 80 registers a thread, of which softmax and producers
-// spilled (the fp8 producers the codes that they load ahead: 2.3 us a tile
-// instead of 0.95), so the warps of the issuers and the scheduler hand some of
+// spilled (the fp8 producers the codes that they load ahead: 2.3 us a tile, 0.95
+// without), so the warps of the issuers and the scheduler hand some of
 // theirs over, a group of four warps at a time (Regs).
 // Every wait is bounded (a timeout sets DCP_DEVERR_TIMEOUT and ends the
 // cluster's work).
