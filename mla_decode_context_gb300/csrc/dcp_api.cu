@@ -297,11 +297,14 @@ static dcp_status_t decode_partial_impl(const void* q, int64_t q_stride_tok, con
     sel.group = select_group(H, max_q_len);
     sel.chunks = (max_q_len - 1) / sel.group + 1;
   }
+  // (a workspace that holds no partials may be misaligned; it is then not used
+  // for the launch order either)
+  const bool usable = workspace != nullptr && aligned16(workspace);
   const DecodeLaunch launch =
       select ? select_launch(B, T, H, D, interleave, d0, Dn, max_seq_len, max_q_len,
                              static_cast<int64_t>(num_blocks) * block_size, sel, o_dtype == DCP_DTYPE_BF16,
-                             workspace != nullptr, workspace_bytes)
-             : decode_launch(T, H, D, interleave, d0, Dn, max_seq_len, workspace != nullptr, workspace_bytes,
+                             usable, workspace_bytes)
+             : decode_launch(T, H, D, interleave, d0, Dn, max_seq_len, usable, workspace_bytes,
                              kv_dtype == DCP_KV_FP8_E4M3);
   const dcp::SplitPlan plan = launch.plan;
   const size_t need = launch.need;

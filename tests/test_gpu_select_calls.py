@@ -109,6 +109,10 @@ def test_more_units_than_fit_with_and_without_room_for_their_order():
     check(inp, O, lse, oracle.decode_partial_select(inp, 0, 0), "ordered")
     O2, lse2, err = run(inp, t, 0, 0, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
     assert err == 0 and torch.equal(O, O2) and torch.equal(lse, lse2)
+    # a workspace at an odd address holds no order
+    odd = torch.empty(size + 16, dtype=torch.uint8, device="cuda")[1:]
+    O2, lse2, err = run(inp, t, 0, 0, workspace=odd)
+    assert err == 0 and torch.equal(O, O2) and torch.equal(lse, lse2)
 
 
 @pytest.mark.parametrize("B,extra", [(1, 1), (1, 300), (40, 77)])
