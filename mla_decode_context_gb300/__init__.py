@@ -407,7 +407,7 @@ def _decode_select(where, tree_mask, q, kv_cache, block_table, seq_lens, query_s
         st = call(
             q.data_ptr(), q0 if T > 1 else H * KV_DIM, kv_cache.data_ptr(),
             KV_FP8_E4M3 if fp8 else KV_BF16, kv_scale.data_ptr() if fp8 else None, blocks, block_size,
-            block_table.data_ptr(), table[-1], table_stride[-2], 1 if local else 0,
+            block_table.data_ptr(), table[-1], table_stride[-2] if B > 1 else table[-1], 1 if local else 0,
             table_stride[0] if local else 0, shard_begin, shard_count, seq_lens.data_ptr(),
             query_start_loc.data_ptr(), B, T, H, max_seq_len, max_q_len, D, interleave, scale, *extra, window,
             num_sinks, O_part.data_ptr(), DTYPE_BF16 if o_dtype is _BF16 else DTYPE_F32,
@@ -859,8 +859,8 @@ def dcp_latent_cache_read(kv_cache, block_table, cu_lens, out, *, seq_starts: Op
     with _Call("dcp_latent_cache_read", device):
         st = call(
             kv_cache.data_ptr(), KV_FP8_E4M3 if fp8 else KV_BF16, kv_scale.data_ptr() if fp8 else None, blocks,
-            block_size, block_table.data_ptr(), table[-1], table_stride[-2], 1 if local else 0,
-            table_stride[0] if local else 0, D, interleave, shard_begin, shard_count,
+            block_size, block_table.data_ptr(), table[-1], table_stride[-2] if B > 1 else table[-1],
+            1 if local else 0, table_stride[0] if local else 0, D, interleave, shard_begin, shard_count,
             None if seq_starts is None else seq_starts.data_ptr(), cu_lens.data_ptr(), B, N, out.data_ptr(),
             DTYPE_F32 if o_dtype is _F32 else DTYPE_BF16, out_stride if N > 1 else KV_DIM,
             None if dev_error is None else dev_error.data_ptr(), _stream_of(stream, device))
@@ -1021,6 +1021,8 @@ def _decode_select_alloc(where, tree_mask, q, kv_cache, block_table, seq_lens, q
         max_seq_len = block_table.shape[-1] * kv_cache.shape[1] * (D if block_table.dim() == 3 else 1)
     if max_q_len is None:
         max_q_len = max(1, T)
+        if where is _TREE:
+            max_q_len = max(1, min(T, 64 * tree_mask.shape[-1], MAX_TREE_ROWS))
     O = torch.empty((D, T, H, LATENT_DIM), dtype=out_dtype, device=device)
     lse = torch.empty((D, T, H), dtype=_F32, device=device)
     if workspace is None:
@@ -1038,7 +1040,9 @@ def decode_partial_window(q, kv_cache, block_table, seq_lens, query_start_loc, D
                           dev_error: Optional[torch.Tensor] = None, stream=None):
     """Allocating form of dcp_mla_decode_partial_window: returns (O_part
     [D, T, H, 512] of out_dtype, lse_part fp32 [D, T, H]); merge them with
-    lse_combine."""
+    lse_combine.  max_seq_len and max_q_len default to the bounds that the
+    table's width and the row count give; both size the launch, so pass the
+    step's own."""
     return _decode_select_alloc(_WINDOW, None, q, kv_cache, block_table, seq_lens,
                                 query_start_loc, D, interleave, scale, window, num_sinks, max_seq_len, max_q_len,
                                 kv_scale, out_dtype, workspace, dev_error, stream)
@@ -1051,7 +1055,8 @@ def decode_partial_tree(q, kv_cache, block_table, seq_lens, query_start_loc, tre
                         dev_error: Optional[torch.Tensor] = None, stream=None):
     """Allocating form of dcp_mla_decode_partial_tree: returns (O_part
     [D, T, H, 512] of out_dtype, lse_part fp32 [D, T, H]); merge them with
-    lse_combine."""
+    lse_combine.  Defaults as for decode_partial_window; max_q_len's is also
+    bounded by the bits of a mask row and by MAX_TREE_ROWS."""
     return _decode_select_alloc(_TREE, tree_mask, q, kv_cache, block_table, seq_lens,
                                 query_start_loc, D, interleave, scale, window, num_sinks, max_seq_len, max_q_len,
                                 kv_scale, out_dtype, workspace, dev_error, stream)

@@ -167,6 +167,8 @@ int select_clusters() {
   return n > 0 ? n : 72;
 }
 
+constexpr int64_t kMostUnits = 0x3fffffff;  // of one launch
+
 size_t order_bytes(int64_t units) { return (static_cast<size_t>(units) * sizeof(int32_t) + 255) / 256 * 256; }
 
 // The windowed and tree decodes.  A unit is a group of rows of one request
@@ -308,7 +310,7 @@ static dcp_status_t decode_partial_impl(const void* q, int64_t q_stride_tok, con
                              kv_dtype == DCP_KV_FP8_E4M3);
   const dcp::SplitPlan plan = launch.plan;
   const size_t need = launch.need;
-  if (select && launch.units > 0x3fffffff) return DCP_ERR_INVALID_ARG;  // (max_q_len far beyond any step's rows)
+  if (select && launch.units > kMostUnits) return DCP_ERR_INVALID_ARG;  // (max_q_len far beyond any step's rows)
   if (need > 0 && (workspace_bytes < need || !workspace)) return DCP_ERR_WORKSPACE_TOO_SMALL;
   if (need > 0 && !aligned16(workspace)) return DCP_ERR_MISALIGNED;
 
@@ -507,6 +509,7 @@ size_t dcp_decode_select_workspace_size(int32_t B, int32_t T, int32_t H, int32_t
   for (int64_t Dn = 1; Dn <= D; ++Dn) {
     const int64_t others = Dn * chunks, units = others * B;
     const dcp::SplitPlan p{static_cast<int32_t>(dcp::select_splits(units, others, lmax, select_clusters())), 0};
+    if ((units + others) * p.splits > kMostUnits) return static_cast<size_t>(-1);
     most = std::max(most, dcp::split_workspace_bytes(p, T, H, static_cast<int32_t>(Dn)) + order_bytes((units + others) * p.splits));
   }
   return most;

@@ -190,6 +190,9 @@ cudaError_t launch_batch(const InT* O_src, const float* lse_src, int64_t o_strid
 // Below this many pairs one warp per pair leaves most SMs idle (eight pairs
 // per 256-thread CTA), and the combine loads early instead.
 constexpr int64_t kFewPairs = 2048;
+// From this many on, a split merge of few splits has one warp per pair and all
+// the same fills the GPU more than once (152 SMs x 4 CTAs x 8 pairs = 4,864).
+constexpr int64_t kManyPairs = 8192;
 
 // The early way: all sources at once, two warps per pair up to 12 sources,
 // four up to 16; past 16 the batched way with four warps per pair.
@@ -210,7 +213,7 @@ cudaError_t launch_early(const InT* O_src, const float* lse_src, int64_t o_strid
                                                          seq_lens, qsl, B, out, out_lse, st);
 }
 
-// The split merge loads early, unless many pairs come in at most four splits:
+// The split merge loads early, unless very many pairs come in at most four splits:
 // those, and the combine of many pairs, take one warp per pair (four float4
 // columns per lane per source) and load two live sources at a time when there
 // are at most two, else four: fewer registers for small D leave room for more
@@ -220,7 +223,7 @@ cudaError_t launch(const InT* O_src, const float* lse_src, int64_t o_stride, int
                    int64_t npairs, int32_t H, const int32_t* seq_lens, const int32_t* qsl, int32_t B, OutT* out,
                    float* out_lse, cudaStream_t st) {
   if (npairs <= 0) return cudaSuccess;
-  if (npairs < kFewPairs || (!kRowMask && nsrc > 4))
+  if (npairs < (kRowMask ? kFewPairs : kManyPairs) || (!kRowMask && nsrc > 4))
     return launch_early<InT, OutT, kRowMask>(O_src, lse_src, o_stride, lse_stride, nsrc, npairs, H, seq_lens, qsl,
                                              B, out, out_lse, st);
   if (nsrc <= 2)
