@@ -191,8 +191,8 @@ cudaError_t launch_batch(const InT* O_src, const float* lse_src, int64_t o_strid
 // per 256-thread CTA), and the combine loads early instead.
 constexpr int64_t kFewPairs = 2048;
 // From this many on, a split merge of few splits has one warp per pair and all
-// the same fills the GPU more than once (152 SMs x 4 CTAs x 8 pairs = 4,864).
-constexpr int64_t kManyPairs = 8192;
+// the same fills the GPU (152 SMs x 4 CTAs x 8 pairs = 4,864).
+constexpr int64_t kManyPairs = 4865;
 
 // The early way: all sources at once, two warps per pair up to 12 sources,
 // four up to 16; past 16 the batched way with four warps per pair.
@@ -217,7 +217,7 @@ cudaError_t launch_early(const InT* O_src, const float* lse_src, int64_t o_strid
 // those, and the combine of many pairs, take one warp per pair (four float4
 // columns per lane per source) and load two live sources at a time when there
 // are at most two, else four: fewer registers for small D leave room for more
-// pairs per SM (15,616 pairs in three splits: 12.2 us instead of 16.4).
+// pairs per SM (7,648 pairs in three splits: 12.2 us instead of 16.4).
 template <typename InT, typename OutT, bool kRowMask>
 cudaError_t launch(const InT* O_src, const float* lse_src, int64_t o_stride, int64_t lse_stride, int nsrc,
                    int64_t npairs, int32_t H, const int32_t* seq_lens, const int32_t* qsl, int32_t B, OutT* out,

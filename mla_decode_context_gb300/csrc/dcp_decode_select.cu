@@ -403,9 +403,11 @@ __device__ __forceinline__ void describe_rows(const DecodeArgs& a, const SelRows
 // -------------------------------------------------------------- producers
 // As in the plain decode: warp gw of a group owns rows 8 gw .. 8 gw + 7 of
 // an item, four at a time, eight lanes per row (lane x: the x-th 16-byte
-// unit of every chunk it loads), each thread resolving its own two rows
-// one of its group's tiles ahead.  The first tile's block ids of a unit
-// are fetched ahead of its Q items.
+// unit of every chunk it loads).  The warp finds the cache rows of four of its
+// group's tiles at a time, a lane one row of one tile (resolved by the threads
+// that copy, two rows each, the arithmetic took as long as the copies of a
+// tile: 587 us for 4 trees of 32 rows, 560 so), and fetches their block ids four tiles ahead, the first
+// ones of a unit ahead of its Q items.
 // (The kind is a value, not a template argument: compiled for one kind, the
 // copies of a tile came in one burst per thread, which held up the other
 // warps' shared-memory accesses: 0.77 us a tile instead of 0.60.)
@@ -433,75 +435,80 @@ __device__ __forceinline__ void produce(const DecodeArgs& a, Bars& bar, uint32_t
   for (;;) {
     const Unit* U = it.get(bar, ok);
     if (!U) break;
-    const int32_t ntiles = U->ntiles, plain0 = U->plain0, plain1 = U->plain1, l0 = U->lo + U->gap + row0;
+    const int32_t ntiles = U->ntiles, plain0 = U->plain0, plain1 = U->plain1;
+    const int32_t l0 = U->lo + U->gap + 8 * gw + (lane & 7);
     const int32_t dI = U->d * a.I, DI = static_cast<int32_t>(a.sel.div_period.d);
     const int32_t* trow = a.block_table + static_cast<int64_t>(U->b) * a.bt_stride +
                           (a.local_tables ? static_cast<int64_t>(U->d - a.d0) * a.bt_shard_stride : 0);
-    bool in_n[2] = {false, false};
-    int32_t off_n[2] = {0, 0}, blk_n[2] = {-1, -1};  // row within its block, block id
-    auto fetch = [&](int jj) {
-      bool in[2] = {true, true};
-      int32_t tok[2] = {l0 + jj * kTile, l0 + jj * kTile + 4};
-      if (jj < plain0 || jj >= plain1) {
+    const int j1 = (g - base) & (step - 1);  // the unit's first tile of this warp
+    bool in_n = false;
+    int32_t off_n = 0, blk_n = -1;  // row within its block, block id
+    // of this lane's row (lane % 8) of the warp's tile n + lane / 8
+    auto fetch = [&](int n) {
+      const int jj = j1 + (n + (lane >> 3)) * step;
+      int32_t tok = l0 + jj * kTile;
+      in_n = jj < ntiles;
+      if (in_n && (jj < plain0 || jj >= plain1)) {
+        // seen by some row of the group?  Then its token of the shard.
         const volatile Unit* V = U;
-        const int32_t hi = V->hi, vs = V->vs, vb = V->vb, gap = V->gap, vlo = V->vlo;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // seen by some row of the group?  Then its token of the shard.
-          const int32_t l = tok[e] - gap, t = l - vb;
-          in[e] = l < hi;
-          if (in[e] && t >= 0) in[e] = t < kMaxTree && ((V->any[t >> 5] >> (t & 31)) & 1u);
-          else in[e] = in[e] && (l < vs || l >= vlo);
-          if (l < vs) tok[e] = l;
-        }
+        const int32_t vs = V->vs, l = tok - V->gap, t = l - V->vb;
+        in_n = l < V->hi;
+        if (in_n && t >= 0) in_n = t < kMaxTree && ((V->any[t >> 5] >> (t & 31)) & 1u);
+        else in_n = in_n && (l < vs || l >= V->vlo);
+        if (l < vs) tok = l;
       }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // the table index: the shard token's position, or (per-shard layout)
-        // the local token index itself
-        const int32_t lq = fast_div(tok[e], a.div_I);
-        const int32_t pos = in[e] ? (a.local_tables ? tok[e] : lq * DI + dI + (tok[e] - lq * a.I)) : 0;
-        const int32_t pb = fast_div(pos, a.div_bs);
-        in_n[e] = in[e];
-        off_n[e] = pos - pb * a.block_size;
-        blk_n[e] = in[e] ? __ldg(trow + pb) : -1;
-      }
+      // the table index: the shard token's position, or (per-shard layout)
+      // the local token index itself
+      const int32_t lq = fast_div(tok, a.div_I);
+      const int32_t pos = in_n ? (a.local_tables ? tok : lq * DI + dI + (tok - lq * a.I)) : 0;
+      const int32_t pb = fast_div(pos, a.div_bs);
+      off_n = pos - pb * a.block_size;
+      blk_n = in_n ? __ldg(trow + pb) : -1;
     };
-    auto rows_of = [&](bool (&valid)[2], int32_t (&crow)[2], bool& bad) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        valid[e] = in_n[e] && blk_n[e] >= 0 && blk_n[e] < a.num_blocks;
-        crow[e] = valid[e] ? blk_n[e] * a.block_size + off_n[e] : 0;
-      }
-      bad = (in_n[0] && !valid[0]) || (in_n[1] && !valid[1]);
+    // the cache rows of the four tiles that were fetched (-1: not seen)
+    int32_t crow_l = -1;
+    uint32_t seen_l = 0;
+    auto resolve = [&]() {
+      const bool there = blk_n >= 0 && blk_n < a.num_blocks;
+      crow_l = in_n && there ? blk_n * a.block_size + off_n : -1;
+      seen_l = __ballot_sync(kFull, crow_l >= 0);
+      if (__any_sync(kFull, in_n && !there) && score && lane == 0) report(a.dev_error, DCP_DEVERR_BAD_BLOCK);
+    };
+    // tile n: this thread's two rows, and the warp's eight bits of the mask
+    int32_t crow[2] = {-1, -1};
+    uint32_t m8 = 0;
+    auto take = [&](int n) {
+      const int from = 8 * (n & 3) + (lane >> 3);
+      crow[0] = __shfl_sync(kFull, crow_l, from);
+      crow[1] = __shfl_sync(kFull, crow_l, from + 4);
+      m8 = (seen_l >> (8 * (n & 3))) & 0xffu;
     };
     // FP8 cache: codes (8 per row and chunk) and row scales of the group's next
     // tile: a tile's are loaded into the registers that the one before leaves
     // as it is converted
     uint2 codes[2][5];
     float rscale[2] = {0.f, 0.f};
-    bool valid[2] = {false, false};
-    int32_t crow[2] = {0, 0};
-    bool bad = false;
-    const unsigned char* code_row[2] = {kvb, kvb};
-    auto load_code = [&](int e, int i) {
-      const int c = score ? (i < 4 ? i : 8) : 4 + i;
-      codes[e][i] = valid[e] ? __ldg(reinterpret_cast<const uint2*>(code_row[e] + c * 64)) : make_uint2(0u, 0u);
-    };
-    auto load_scale = [&](int e) { return valid[e] ? __ldg(a.kv_scale + crow[e]) : 0.f; };
-    const int j1 = (g - base) & (step - 1);  // the unit's first tile of this warp
-    if (j1 < ntiles) fetch(j1);
-    if constexpr (kFp8) {
-      if (j1 < ntiles) {
-        rows_of(valid, crow, bad);
+    auto load_codes = [&]() {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          rscale[e] = load_scale(e);
-          code_row[e] = kvb + static_cast<int64_t>(crow[e]) * kKDim + x * 8;
+      for (int e = 0; e < 2; ++e) {
+        const bool valid = crow[e] >= 0;
+        const unsigned char* code_row = kvb + static_cast<int64_t>(max(crow[e], 0)) * kKDim + x * 8 + (score ? 0 : 4 * 64);
+        rscale[e] = valid ? __ldg(a.kv_scale + crow[e]) : 0.f;
 #pragma unroll
-          for (int i = 0; i < 5; ++i) if (i < nch) load_code(e, i);
+        for (int i = 0; i < 5; ++i) {
+          const int c = i == 4 ? 8 : i;
+          if (i < nch) codes[e][i] = valid ? __ldg(reinterpret_cast<const uint2*>(code_row + c * 64)) : make_uint2(0u, 0u);
         }
-        if (j1 + step < ntiles) fetch(j1 + step);
+      }
+    };
+    int n = 0;  // the warp's tiles of this unit so far
+    if (j1 < ntiles) {
+      fetch(0);
+      if constexpr (kFp8) {
+        resolve();
+        if (j1 + 4 * step < ntiles) fetch(4);
+        take(0);
+        load_codes();
       }
     }
     for (; g < base + pre + ntiles; g += step) {
@@ -516,22 +523,20 @@ __device__ __forceinline__ void produce(const DecodeArgs& a, Bars& bar, uint32_t
       }
       if (!ok) break;
       if (!kFp8 && j >= 0) {
-        rows_of(valid, crow, bad);
-        if (j + step < ntiles) fetch(j + step);
+        if ((n & 3) == 0) {
+          resolve();
+          if (j + 4 * step < ntiles) fetch(n + 4);
+        }
+        take(n);
       }
       const bool ab = aborted(bar);
       ok = wait_all(&slot_free[st], (round & 1) ^ 1);
       if (!ok) break;
       if (score && gw == 0 && lane == 0) st_relaxed_shared(&bar.claimed[group], (g >> 1) + 1);
-      if (__any_sync(kFull, bad && j >= 0) && score && lane == 0) report(a.dev_error, DCP_DEVERR_BAD_BLOCK);
       if (score) {
         // this warp's 8 rows of the tile's mask, released by its arrival on
         // kv_full; fp8: warp 0 also arms kv_full for the value CTA's 16 KB
-        const unsigned v0 = __ballot_sync(kFull, valid[0]), v1 = __ballot_sync(kFull, valid[1]);
         if (lane == 0) {
-          uint32_t m8 = 0;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) m8 |= (((v0 >> (8 * q)) & 1u) << q) | (((v1 >> (8 * q)) & 1u) << (4 + q));
           if (j >= 0) reinterpret_cast<volatile uint8_t*>(&bar.mask[(jbase + j) & 15])[gw] = static_cast<uint8_t>(m8);
           if (kFp8 && gw == 0 && j >= 0) mbar_arrive_expect_tx(&bar.kv_full[st], kHalfBytes);
           else mbar_arrive(&bar.kv_full[st]);
@@ -552,20 +557,23 @@ __device__ __forceinline__ void produce(const DecodeArgs& a, Bars& bar, uint32_t
         }
         cp_async_mbar_arrive_noinc(&slot_loaded[st]);
       } else {
-        const bool next = kFp8 && j + step < ntiles;
+        // (the slot's first chunk and the row's first byte that this CTA loads:
+        // what follows is constant offsets)
+        const uint32_t slot0 = score ? smem_base + stage_chunk_off(st, 0)
+                                     : smem_base + (vrecv ? kOffRecv : kOffOwn) + st * kHalfBytes;
+        const int src_off = score || vrecv ? 0 : 4 * 128;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int row = e ? row1 : row0;
-          const unsigned char* src_row = kvb + static_cast<int64_t>(crow[e]) * (kKDim * 2) + x * 16;
-          const uint32_t src_bytes = valid[e] ? 16u : 0u;
-          const uint32_t swz = static_cast<uint32_t>(row * 128 + ((x ^ (row & 7)) << 4));
+          const unsigned char* src_row = kvb + static_cast<int64_t>(max(crow[e], 0)) * (kKDim * 2) + x * 16 + src_off;
+          const uint32_t src_bytes = crow[e] >= 0 ? 16u : 0u;
+          const uint32_t dst0 = slot0 + static_cast<uint32_t>(row * 128 + ((x ^ (row & 7)) << 4));
           const uint64_t sc = f2_pack(rscale[e], rscale[e]);
 #pragma unroll
-          for (int i = 0; i < (kFp8 ? 5 : nch); ++i) {
-            if (kFp8 && i >= nch) continue;
-            const int c = score ? (kFp8 ? (i < 4 ? i : 8) : i) : (vrecv ? i : 4 + i);
-            const uint32_t dst = score ? smem_base + stage_chunk_off(st, c) + swz
-                                       : smem_base + (vrecv ? kOffRecv : kOffOwn) + st * kHalfBytes + i * kChunkBytes + swz;
+          for (int i = 0; i < (kFp8 ? 5 : 9); ++i) {
+            if (i >= nch) continue;
+            const int c = kFp8 && i == 4 ? 8 : i;  // (the score CTA's fifth FP8 chunk is the rope's)
+            const uint32_t dst = dst0 + c * kChunkBytes;
             if constexpr (kFp8) {
               const uint2 w = codes[e][i];
               const uint4 v = make_uint4(e4m3x2_to_bf16x2(w.x, sc), e4m3x2_to_bf16x2(w.x >> 16, sc),
@@ -577,18 +585,15 @@ __device__ __forceinline__ void produce(const DecodeArgs& a, Bars& bar, uint32_t
             }
           }
         }
-        if (next) rows_of(valid, crow, bad);
-        if (kFp8 && next) {  // (after the stores: in between, they held the stores up)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            rscale[e] = load_scale(e);
-            code_row[e] = kvb + static_cast<int64_t>(crow[e]) * kKDim + x * 8;
-#pragma unroll
-            for (int i = 0; i < 5; ++i)
-              if (i < nch) load_code(e, i);
+        ++n;
+        if (kFp8 && j + step < ntiles) {  // (after the stores: in between, they held the stores up)
+          if ((n & 3) == 0) {
+            resolve();
+            if (j + 5 * step < ntiles) fetch(n + 4);
           }
+          take(n);
+          load_codes();
         }
-        if (next && j + 2 * step < ntiles) fetch(j + 2 * step);
         if constexpr (kFp8) mbar_arrive(&slot_loaded[st]);
         else cp_async_mbar_arrive_noinc(&slot_loaded[st]);
       }
