@@ -230,6 +230,14 @@ __device__ __forceinline__ void set_abort(Bars& bar, int32_t* dev_error) {
   report(dev_error, DCP_DEVERR_TIMEOUT);
   atomicExch(&bar.abort, 1);
 }
+// One lane of the warp, always the same.  Behind this (unlike behind a compare
+// of the lane index) values that all lanes share stay in uniform registers,
+// where the MMAs and commits take their operands.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
 __device__ __forceinline__ bool wait_all(uint64_t* b, uint32_t parity) { return __all_sync(kFull, mbar_wait(b, parity)); }
 __device__ __forceinline__ bool wait_all_cluster(uint64_t* b, uint32_t parity) {
   return __all_sync(kFull, mbar_wait_cluster(b, parity));
@@ -1159,7 +1167,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
     } else if (score) {
       // --------------------------------------------- Q to TMEM, S MMA issuers
       // warp 4 + 3b + part owns third `part` of S slot b for tiles j = b (mod 2)
-      const int b = (warp - 4) / kSParts, part = (warp - 4) % kSParts;
+      const int issuer = __shfl_sync(kFull, warp - 4, 0), b = issuer / kSParts, part = issuer % kSParts;
       const uint32_t id_s = idesc_bf16(128, kTile, 0, 0);
       const uint64_t dk = smem_desc(smem_base + kOffStages, 16, 1024, kSwizzle128B);
       const uint32_t dS = tbase + kColS + 96 * b + 32 * part;
@@ -1231,28 +1239,29 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
           // the producers' write of the tile's mask, read after s_full
           if (part == 0 && lane == 0) mbar_arrive(&bar.s_full[b]);
           tc_fence_after();
-          if (lane == 0) {
-            uint64_t bc = dkp + static_cast<uint64_t>((st * kStageBytes) >> 4);
+          const int stu = __shfl_sync(kFull, st, 0);
+          if (elect_one()) {
+            uint64_t bc = dkp + static_cast<uint64_t>((stu * kStageBytes) >> 4);
             uint32_t ac = qa;
-#pragma unroll 1
+#pragma unroll
             for (int c = 0; c < 3; ++c, bc += kChunkBytes >> 4, ac += 32) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) mma_ts(dS, ac + 8 * i, bc + 2 * i, id_s, (c | i) != 0);
             }
             mma_commit(&bar.s_full[b]);
-            if (kFp8) mma_commit_mc(&bar.s_done[st], 0x3);
-            else mma_commit(&bar.s_done[st]);
+            if (kFp8) mma_commit_mc(&bar.s_done[stu], 0x3);
+            else mma_commit(&bar.s_done[stu]);
           }
           __syncwarp();
         }
         if (!ok) break;
-        if (lane == 0) mma_commit(&bar.s_end);
+        if (elect_one()) mma_commit(&bar.s_end);
         g0 += kQItems + ntiles;
         j0 += ntiles;
         it.done(bar, lane);
       }
       if (!ok) set_abort(bar, a.dev_error);
-      if (lane == 0) mma_commit(&bar.fin[1 + kSParts * b + part]);
+      if (elect_one()) mma_commit(&bar.fin[1 + kSParts * b + part]);
       __syncwarp();
       mbar_wait(&bar.fin[1 + kSParts * b + part], 0);
     } else if (warp == 10) {
@@ -1271,11 +1280,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         const int ntiles = U->ntiles;
         if (k > 0) ok = wait_all(&bar.o_free, (k - 1) & 1);
         for (int j = j0; j < j0 + ntiles && ok; ++j) {
-          const int vs = j % kRecv, os = j % kOwn, slot = j % kPSlots;
+          const int slot = j % kPSlots;
           ok = wait_all(&bar.p_ok[slot], (j / kPSlots) & 1);
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
+          const int ju = __shfl_sync(kFull, j, 0);
+          if (elect_one()) {
+            const int vs = ju % kRecv, os = ju % kOwn, slot = ju % kPSlots;
             const uint64_t sv[2] = {static_cast<uint64_t>((kOffRecv + vs * kHalfBytes) >> 4),
                                     static_cast<uint64_t>((kOffOwn + os * kHalfBytes) >> 4)};
             const uint64_t po = static_cast<uint64_t>((slot * kPBytes) >> 4);
@@ -1298,7 +1309,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         it.done(bar, lane);
       }
       if (!ok) set_abort(bar, a.dev_error);
-      if (lane == 0) mma_commit(&bar.fin[0]);
+      if (elect_one()) mma_commit(&bar.fin[0]);
       __syncwarp();
       mbar_wait(&bar.fin[0], 0);
     } else if (warp == 9) {
