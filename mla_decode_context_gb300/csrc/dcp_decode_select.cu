@@ -103,8 +103,7 @@ constexpr int kGroupThreads = 32 * kProdWarps / 2;
 constexpr int kHalfBytes = 4 * kChunkBytes;      // 4 chunks
 constexpr int kOwn = 7;                          // value CTA: own ring slots (chunks 4-7)
 constexpr int kRecv = 4;                         // value CTA: receive ring slots (chunks 0-3)
-constexpr int kSBuf = 2;                         // S slots (three 32-column thirds each) in TMEM
-constexpr int kSParts = 3;                       // K-parts of S, one issuing warp each
+constexpr int kSBuf = 4;                         // S slots (32 columns) in TMEM, one issuing warp each
 constexpr int kPSlots = 4;                       // P slots in the value CTA
 constexpr int kPBytes = 128 * kTile * 2;         // P tile: 128 rows x 32 bf16, 64B-swizzled
 constexpr int kPWarpBytes = kPBytes / 4;         // one softmax warp's 32 rows
@@ -118,11 +117,11 @@ constexpr int kThreads = 32 * (kSmWarp1 + 4);
 constexpr int kRegsLaunch = 80;
 template <bool kFp8>
 struct Regs {
-  static constexpr int softmax = kFp8 ? 96 : 104, producer = kFp8 ? 80 : 72, issuer = 64, value = 88;
-  // (more than the launch's would wait forever; the value CTA's sixth group
-  // loads the receive ring, or is idle)
+  static constexpr int softmax = kFp8 ? 88 : 104, producer = kFp8 ? 88 : 72, issuer = 64, value = 88;
+  static constexpr int last = kFp8 ? issuer : producer;  // value CTA's sixth group: idle, or loads the receive ring
+  // (more than the launch's would wait forever)
   static_assert(2 * softmax + 2 * producer + 2 * issuer <= 6 * kRegsLaunch, "score CTA: more than was launched");
-  static_assert(2 * value + 3 * producer + issuer <= 6 * kRegsLaunch, "value CTA: more than was launched");
+  static_assert(2 * value + 2 * producer + last + issuer <= 6 * kRegsLaunch, "value CTA: more than was launched");
 };
 constexpr int kUnits = 3;                        // descriptor ring
 constexpr int kFinSlots = 8;                     // value CTA: 1/l of units whose O is not written yet
@@ -170,7 +169,7 @@ struct __align__(8) Bars {
   uint64_t own_free[kOwn];    // value: PV(j) done with own slot j % kOwn
   uint64_t v_full[kRecv];     // value: chunks 0-3 of tile j landed in receive slot j % kRecv
   uint64_t v_free[kRecv];     // both (multicast commit of PV(j)): receive slot j % kRecv may refill
-  uint64_t s_full[kSBuf];     // score: the three parts' commits + part 0's arrival
+  uint64_t s_full[kSBuf];     // score: S done (commit) + its issuer's arrival
   uint64_t s_free[kSBuf];     // score: the softmax has read the slot (4 warps)
   // score: unit k's Q is in TMEM (four of the S issuers; the others cannot fall
   // two phases behind: the next Q waits for their s_end too)
@@ -183,13 +182,13 @@ struct __align__(8) Bars {
   uint64_t o_final;           // value: unit k's last PV complete
   uint64_t o_free;            // value: unit k's O has been read from TMEM (8 warps)
   uint64_t fin_l[kFinSlots];  // value: 1/l of unit k's lanes arrived
-  uint64_t fin[1 + kSParts * kSBuf];  // each issuing warp's MMAs complete
+  uint64_t fin[1 + kSBuf];    // each issuing warp's MMAs complete
   uint64_t m_pub[2];          // score: max after unit k's first tile posted (4 warps)
   uint64_t sm_fin;            // score: both softmax groups' l and m of unit k written (8 warps)
   uint64_t ud_full[kUnits], ud_free[kUnits];  // descriptor written / no longer needed (every other warp)
   uint64_t never;             // test hook only: initialised, never arrived on
   int32_t claimed[2];         // score: how many of its items producer group g has claimed a stage for
-  int32_t seen[2];            // score (fp8): tiles of S slot b whose kv_full its first issuer has seen, and it
+  int32_t seen[kSBuf];        // score (fp8): tiles up to the last one whose kv_full the issuer of slot b has seen
   uint32_t mask[16];          // score: valid rows of tile j in mask[j % 16]
   uint32_t tmem;
   int32_t abort;
@@ -643,14 +642,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar.kv_loaded[i], kGroupThreads);
       mbar_init(&bar.kv_full[i], 5);  // 4 producer warps of the item's group + the forwarder
-      mbar_init(&bar.s_done[i], kFp8 ? kSParts + 1 : kSParts);
+      mbar_init(&bar.s_done[i], kFp8 ? 2 : 1);
     }
     for (int i = 0; i < kOwn; ++i) { mbar_init(&bar.own_loaded[i], kGroupThreads); mbar_init(&bar.own_free[i], 1); }
     mbar_init(&bar.q_gone, 4);
     for (int i = 0; i < kRecv; ++i) { mbar_init(&bar.v_full[i], kFp8 ? 1 : kGroupThreads); mbar_init(&bar.v_free[i], 1); }
-    for (int i = 0; i < kSBuf; ++i) { mbar_init(&bar.s_full[i], kSParts + 1); mbar_init(&bar.s_free[i], 4); }
+    for (int i = 0; i < kSBuf; ++i) { mbar_init(&bar.s_full[i], 2); mbar_init(&bar.s_free[i], 4); }
     mbar_init(&bar.q_ready, 4);
-    mbar_init(&bar.s_end, kSParts * kSBuf);
+    mbar_init(&bar.s_end, kSBuf);
     for (int i = 0; i < kPSlots; ++i) {
       mbar_init(&bar.p_full[i], 1);
       mbar_init(&bar.p_free[i], 1);
@@ -660,13 +659,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
     mbar_init(&bar.o_final, 1);
     mbar_init(&bar.o_free, 8);
     for (int i = 0; i < kFinSlots; ++i) mbar_init(&bar.fin_l[i], 1);
-    for (int i = 0; i < 1 + kSParts * kSBuf; ++i) mbar_init(&bar.fin[i], 1);
+    for (int i = 0; i < 1 + kSBuf; ++i) mbar_init(&bar.fin[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&bar.m_pub[i], 4);
     mbar_init(&bar.sm_fin, 8);
     for (int i = 0; i < kUnits; ++i) { mbar_init(&bar.ud_full[i], 1); mbar_init(&bar.ud_free[i], kThreads / 32 - 1); }
     mbar_init(&bar.never, 1);
     bar.claimed[0] = bar.claimed[1] = 0;
-    bar.seen[0] = bar.seen[1] = 0;
+    for (int i = 0; i < kSBuf; ++i) bar.seen[i] = 0;
     bar.abort = 0;
     fence_mbar_init();
     if (!score) {
@@ -796,18 +795,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         if (!ok) break;
         tc_fence_after();
         uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&bar.mask[j & 15]);
-        uint32_t sr[32], sr2[32];
-        tmem_ld32(lane_addr + kColS + 96 * b, sr);
-        tmem_ld32(lane_addr + kColS + 96 * b + 32, sr2);
-        tmem_wait_ld();
-        float sc[32];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)  // the K-parts of S, pairwise
-          f2_unpack(f2_add(f2_pack(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
-                           f2_pack(__uint_as_float(sr2[2 * i]), __uint_as_float(sr2[2 * i + 1]))),
-                    sc[2 * i], sc[2 * i + 1]);
-        tmem_ld32(lane_addr + kColS + 96 * b + 64, sr);
-        // what this lane sees of the tile, while the third part arrives
+        uint32_t sr[32];
+        tmem_ld32(lane_addr + kColS + 32 * b, sr);
+        // what this lane sees of the tile, while S arrives
         uint32_t hidden = 0;  // loaded for another row of the group only
         if (i0 < plain0 || i0 >= plain1) {
           const volatile Unit* V = U;
@@ -823,11 +813,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.s_free[b]);
+        float sc[32];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          f2_unpack(f2_add(f2_pack(sc[2 * i], sc[2 * i + 1]),
-                           f2_pack(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]))),
-                    sc[2 * i], sc[2 * i + 1]);
+        for (int i = 0; i < 32; ++i) sc[i] = __uint_as_float(sr[i]);
         bool foul = false;
         if (__any_sync(kFull, hidden != 0)) {
 #pragma unroll
@@ -1164,15 +1152,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         it.done(bar, lane);
       }
       if (!ok) set_abort(bar, a.dev_error);
-    } else if (score) {
+    } else if (score && group == 1) {
       // --------------------------------------------- Q to TMEM, S MMA issuers
-      // warp 4 + 3b + part owns third `part` of S slot b for tiles j = b (mod 2)
-      const int issuer = __shfl_sync(kFull, warp - 4, 0), b = issuer / kSParts, part = issuer % kSParts;
+      // warp 4 + b owns S slot b, for tiles j = b (mod 4)
+      const int b = __shfl_sync(kFull, warp - 4, 0);
       const uint32_t id_s = idesc_bf16(128, kTile, 0, 0);
       const uint64_t dk = smem_desc(smem_base + kOffStages, 16, 1024, kSwizzle128B);
-      const uint32_t dS = tbase + kColS + 96 * b + 32 * part;
-      const uint32_t qa = tbase + kColQ + 96 * part;
-      const uint64_t dkp = dk + static_cast<uint64_t>((3 * part * kChunkBytes) >> 4);
+      const uint32_t dS = tbase + kColS + 32 * b, qa = tbase + kColQ;
       bool ok = true;
       int32_t other_seen = 0;
       int g0 = 0, j0 = 0;  // items and tiles before the unit
@@ -1180,7 +1166,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         const Unit* U = it.get(bar, ok);
         if (!U) break;
         const int ntiles = U->ntiles;
-        if (warp < 8) {
+        {
           // item warp - 4 of the unit's Q, once no MMA reads the previous one
           if (k > 0) ok = wait_all(&bar.s_end, (k - 1) & 1);
           const int g = g0 + warp - 4, st = g % kStages;
@@ -1211,7 +1197,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
           __syncwarp();
           if (lane == 0) {
             // the stage is free: as many arrivals as a tile's
-            for (int i = 0; i < (kFp8 ? kSParts + 1 : kSParts); ++i) mbar_arrive(&bar.s_done[st]);
+            for (int i = 0; i < (kFp8 ? 2 : 1); ++i) mbar_arrive(&bar.s_done[st]);
             mbar_arrive(&bar.q_ready);
             if (kFp8) mbar_arrive_remote(map_peer(smem_u32(&bar.q_gone), peer));
           }
@@ -1219,35 +1205,34 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         }
         ok = wait_all(&bar.q_ready, k & 1);
         tc_fence_after();
-        for (int j = j0 + ((j0 ^ b) & 1); ok && j < j0 + ntiles; j += kSBuf) {
+        for (int j = j0 + ((b - j0) & (kSBuf - 1)); ok && j < j0 + ntiles; j += kSBuf) {
           const int g = g0 + kQItems + j - j0, st = g % kStages, u = j / kSBuf;
           ok = wait_all(&bar.s_free[b], (u & 1) ^ 1);
           // The stage's previous item has been full, so that the parity below
           // can only mean this one: the forwarder arrives in order, so it has
-          // since S(j - 2) was issued; in the fp8 form the value CTA's halves
-          // might land out of order, so the other slot's issuers say so (a
-          // count that only grows, read again only when it falls short).
+          // since S(j - 4) was issued; in the fp8 form the value CTA's halves
+          // might land out of order, so that tile's issuer says so (a count
+          // that only grows, read again only when it falls short).
           if constexpr (kFp8) {
             for (uint32_t i = 0; other_seen < j - kStages + 1 && i < kWaitLimit; ++i)
-              other_seen = ld_relaxed_shared(&bar.seen[b ^ 1]);
+              other_seen = ld_relaxed_shared(&bar.seen[(j + kSBuf * kStages - kStages) % kSBuf]);
             ok = ok && __all_sync(kFull, other_seen >= j - kStages + 1);
           }
           ok = ok && wait_all_cluster(&bar.kv_full[st], (g / kStages) & 1);
-          if (kFp8 && part == 0 && lane == 0) st_relaxed_shared(&bar.seen[b], j + 1);
+          if (kFp8 && lane == 0) st_relaxed_shared(&bar.seen[b], j + 1);
           if (!ok) break;
-          // part 0's arrival passes on (release after the acquire of kv_full)
+          // this arrival passes on (release after the acquire of kv_full)
           // the producers' write of the tile's mask, read after s_full
-          if (part == 0 && lane == 0) mbar_arrive(&bar.s_full[b]);
+          if (lane == 0) mbar_arrive(&bar.s_full[b]);
           tc_fence_after();
           const int stu = __shfl_sync(kFull, st, 0);
           if (elect_one()) {
-            uint64_t bc = dkp + static_cast<uint64_t>((stu * kStageBytes) >> 4);
-            uint32_t ac = qa;
+            const uint64_t bd = dk + static_cast<uint64_t>((stu * kStageBytes) >> 4);
 #pragma unroll
-            for (int c = 0; c < 3; ++c, bc += kChunkBytes >> 4, ac += 32) {
+            for (int c = 0; c < kNch; ++c)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mma_ts(dS, ac + 8 * i, bc + 2 * i, id_s, (c | i) != 0);
-            }
+              for (int i = 0; i < 4; ++i)
+                mma_ts(dS, qa + 32 * c + 8 * i, bd + ((c * kChunkBytes) >> 4) + 2 * i, id_s, (c | i) != 0);
             mma_commit(&bar.s_full[b]);
             if (kFp8) mma_commit_mc(&bar.s_done[stu], 0x3);
             else mma_commit(&bar.s_done[stu]);
@@ -1261,10 +1246,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         it.done(bar, lane);
       }
       if (!ok) set_abort(bar, a.dev_error);
-      if (elect_one()) mma_commit(&bar.fin[1 + kSParts * b + part]);
+      if (elect_one()) mma_commit(&bar.fin[1 + b]);
       __syncwarp();
-      mbar_wait(&bar.fin[1 + kSParts * b + part], 0);
-    } else if (warp == 10) {
+      mbar_wait(&bar.fin[1 + b], 0);
+    } else if (!score && warp == 10) {
       // -------------------------------------------------------- PV MMA issuer
       const uint32_t id_o = idesc_bf16(128, 256, 0, 1);
       const uint64_t dv = smem_desc(smem_base, kChunkBytes, 1024, kSwizzle128B);
@@ -1312,7 +1297,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
       if (elect_one()) mma_commit(&bar.fin[0]);
       __syncwarp();
       mbar_wait(&bar.fin[0], 0);
-    } else if (warp == 9) {
+    } else if (!score && warp == 9) {
       // ------------------------------------------------- receive-ring arrivals
       bool ok = true;
       int j = 0, g = 0;
@@ -1340,7 +1325,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         it.done(bar, lane);
       }
       if (!ok) set_abort(bar, a.dev_error);
-    } else if (kFp8) {
+    } else if (kFp8 && !score) {
       // ------------------------------------------------- value CTA forwarder
       // fp8: own slot j % kOwn (chunks 4-7) -> the score CTA's stage of tile j,
       // once item g - 5 has left it.  Of those items the tiles are waited for in
@@ -1388,7 +1373,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
       if (!ok) set_abort(bar, a.dev_error);
     }
   } else {
-    take_regs<Regs<kFp8>::producer>();
+    take_regs<Regs<kFp8>::last>();
     // no role in this form: keep the descriptor ring moving
     bool ok = true;
     while (it.get(bar, ok)) it.done(bar, lane);

@@ -24,7 +24,9 @@ ProtocolError = P.ProtocolError
 K_Q, K_UNITS, K_FIN = 4, 3, 8
 PTX = 128 * 32 * 2 + 4 * 144
 HALF = P.HALF
-ST, OWN, RECV, SB, SP, PS = P.K_STAGES, P.K_OWN, P.K_RECV, P.K_SBUF, P.K_SPARTS, P.K_PSLOTS
+ST, OWN, RECV, PS = P.K_STAGES, P.K_OWN, P.K_RECV, P.K_PSLOTS
+SB = 4                               # S slots, one issuing warp each
+DONE = set(range(P.K_SPARTS))        # what the plain decode's model calls a finished S
 
 
 class Model(P.Model):
@@ -33,9 +35,10 @@ class Model(P.Model):
         self.j0 = [sum(self.sizes[:k]) for k in range(len(self.sizes) + 1)]
         self.g0 = [self.j0[k] + K_Q * k for k in range(len(self.sizes) + 1)]
         super().__init__(self.j0[-1], seed, rescale_prob=rescale_prob, mutation=mutation, decoupled=decoupled)
-        self.seen = [0, 0]
+        self.seen = [0] * SB
+        self.sslot = [dict(tile=None, parts_done=0, read=True) for _ in range(SB)]
         self.q_tmem = [None] * K_Q       # the unit whose quarter is in TMEM
-        self.s_running = 0               # S parts issued and not complete
+        self.s_running = 0               # tiles whose S is issued and not complete
         self.o_unit, self.o_pvs, self.o_read = None, set(), True
         self.fin_slot = [None] * K_FIN
         self.fin_sh = [dict(unit=None, groups=set(), read=True) for _ in range(2)]
@@ -46,20 +49,20 @@ class Model(P.Model):
             for i in range(n):
                 self.bars[(cta, name, i)] = P.Bar("%s[%d]@%d" % (name, i, cta), count)
         # roles per CTA that use a descriptor, counted as the kernel counts warps
-        self.users = {0: 2 + 1 + 6 + 2, 1: (3 if self.decoupled else 2) + (0 if self.decoupled else 1) + 1 + 1 + 1 + 1}
+        self.users = {0: 2 + 1 + SB + 2, 1: (3 if self.decoupled else 2) + (0 if self.decoupled else 1) + 1 + 1 + 1 + 1}
         for cta in (0, 1):
             mk(cta, "kv_loaded", ST, 128)
             mk(cta, "kv_full", ST, 5)
-            mk(cta, "s_done", ST, SP if self.decoupled else SP + 1)
+            mk(cta, "s_done", ST, 1 if self.decoupled else 2)
             mk(cta, "own_loaded", OWN, 128)
             mk(cta, "own_free", OWN, 1)
             mk(cta, "q_gone", 1, 4)
             mk(cta, "v_full", RECV, 128 if self.decoupled else 1)
             mk(cta, "v_free", RECV, 1)
-            mk(cta, "s_full", SB, SP + 1)
+            mk(cta, "s_full", SB, 2)
             mk(cta, "s_free", SB, 4)
             mk(cta, "q_ready", 1, 4)
-            mk(cta, "s_end", 1, 6)
+            mk(cta, "s_end", 1, SB)
             mk(cta, "p_full", PS, 1)
             mk(cta, "p_free", PS, 1)
             mk(cta, "p_ok", PS, 5)
@@ -310,34 +313,31 @@ class Model(P.Model):
                 yield ("do", lambda j=j: self.b(1, "p_ok", j % PS).arrive(tag=j))
         yield from self._units(1, inner)
 
-    def s_issuer(self, b, part):
-        w = SP * b + part
-
+    def s_issuer(self, b):
         def inner(k):
             j0 = self.j0[k]
-            if w < K_Q:
-                if k > 0 and self.mut == "q_waits_for_s_full":
-                    for p in range(1, SB + 1):
-                        if j0 >= p:
-                            yield self.W(0, "s_full", (j0 - p) % SB, (j0 - p) // SB)
-                elif k > 0 and self.mut != "q_over_running_s":
-                    yield self.W(0, "s_end", 0, k - 1)
-                g = self.g0[k] + w
-                st = g % ST
-                yield self.W(0, "kv_full", st, g // ST)
+            if k > 0 and self.mut == "q_waits_for_s_full":
+                for p in range(1, SB + 1):
+                    if j0 >= p:
+                        yield self.W(0, "s_full", (j0 - p) % SB, (j0 - p) // SB)
+            elif k > 0 and self.mut != "q_over_running_s":
+                yield self.W(0, "s_end", 0, k - 1)
+            g = self.g0[k] + b
+            st = g % ST
+            yield self.W(0, "kv_full", st, g // ST)
 
-                def move(st=st, g=g):
-                    s = self.stage[st]
-                    self.check(s["tile"] == g and s["own"], "Q quarter of item %s read from a stage holding %s", g, s["tile"])
-                    self.check(self.s_running == 0, "Q of unit %s overwrites TMEM while S runs", k)
-                    self.q_tmem[w] = k
-                    s["s_done"] = set(range(SP))
-                    n = SP if self.decoupled else SP + 1
-                    self.b(0, "s_done", st).arrive(n, tag=g)
-                yield ("do", move)
-                yield ("do", lambda: self.b(0, "q_ready", 0).arrive(tag=k))
-                if not self.decoupled:
-                    yield ("do", lambda: self.later(lambda: self.b(1, "q_gone", 0).arrive(tag=k)))
+            def move(st=st, g=g):
+                s = self.stage[st]
+                self.check(s["tile"] == g and s["own"], "Q quarter of item %s read from a stage holding %s", g, s["tile"])
+                self.check(self.s_running == 0, "Q of unit %s overwrites TMEM while S runs", k)
+                self.q_tmem[b] = k
+                s["s_done"] = DONE
+                n = 1 if self.decoupled else 2
+                self.b(0, "s_done", st).arrive(n, tag=g)
+            yield ("do", move)
+            yield ("do", lambda: self.b(0, "q_ready", 0).arrive(tag=k))
+            if not self.decoupled:
+                yield ("do", lambda: self.later(lambda: self.b(1, "q_gone", 0).arrive(tag=k)))
             yield self.W(0, "q_ready", 0, k)
             for j in range(j0, self.j0[k + 1]):
                 if j % SB != b:
@@ -346,36 +346,35 @@ class Model(P.Model):
                 st = g % ST
                 yield self.W(0, "s_free", b, j // SB - 1)
                 if not self.decoupled and self.mut != "issuers_uncoupled":
-                    yield ("cond", lambda j=j: self.seen[1 - b] >= j - ST + 1)
+                    yield ("cond", lambda j=j: self.seen[(j - ST) % SB] >= j - ST + 1)
                 yield self.W(0, "kv_full", st, g // ST)
-                if part == 0:
-                    def saw(j=j):
-                        self.seen[b] = j + 1
-                    yield ("do", saw)
+
+                def saw(j=j):
+                    self.seen[b] = j + 1
+                yield ("do", saw)
 
                 def issue(j=j, g=g, st=st):
                     s = self.stage[st]
-                    self.check(s["tile"] == g and s["own"] and s["fwd"], "S(%s) part %s issued on stage %s holding item %s", j, part, st, s["tile"])
+                    self.check(s["tile"] == g and s["own"] and s["fwd"], "S(%s) issued on stage %s holding item %s", j, st, s["tile"])
                     self.check(all(q == k for q in self.q_tmem), "S(%s) of unit %s issued with Q of %s", j, k, self.q_tmem)
                     sl = self.sslot[b]
                     if sl["tile"] != j:
                         self.check(sl["read"], "S slot %s rewritten (tile %s) before the softmax read tile %s", b, j, sl["tile"])
                         self.sslot[b] = dict(tile=j, parts_done=0, read=False)
-                    if part == 0:
-                        self.b(0, "s_full", b).arrive(tag=j)
+                    self.b(0, "s_full", b).arrive(tag=j)
                     self.s_running += 1
 
                     def done():
                         self.s_running -= 1
                         self.sslot[b]["parts_done"] += 1
-                        self.stage[st]["s_done"].add(part)
+                        self.stage[st]["s_done"] = DONE
                         self.b(0, "s_full", b).arrive(tag=j)
                         self.b(0, "s_done", st).arrive(tag=g)
                         if not self.decoupled:
                             self.b(1, "s_done", st).arrive(tag=g)
-                    self.later(done, fifo=("S", b, part))
+                    self.later(done, fifo=("S", b))
                 yield ("do", issue)
-            yield ("do", lambda: self.later(lambda: self.b(0, "s_end", 0).arrive(tag=k), fifo=("S", b, part)))
+            yield ("do", lambda: self.later(lambda: self.b(0, "s_end", 0).arrive(tag=k), fifo=("S", b)))
         yield from self._units(0, inner)
 
     def softmax(self, grp):
@@ -397,7 +396,7 @@ class Model(P.Model):
 
                 def read_s(j=j, b=b):
                     sl = self.sslot[b]
-                    self.check(sl["tile"] == j and sl["parts_done"] == SP, "softmax read S slot %s for tile %s: holds %s (%s parts)",
+                    self.check(sl["tile"] == j and sl["parts_done"] == 1, "softmax read S slot %s for tile %s: holds %s (%s parts)",
                                b, j, sl["tile"], sl["parts_done"])
                     m = self.mask[j % 16]
                     self.check(m["tile"] == j, "mask slot %s holds tile %s, wanted %s", j % 16, m["tile"], j)
@@ -569,10 +568,9 @@ class Model(P.Model):
             r["vp%d" % g] = self.value_producers(g)
             r["sm%d" % g] = self.softmax(g)
         for b in range(SB):
-            for p in range(SP):
-                r["s%d%d" % (b, p)] = self.s_issuer(b, p)
+            r["s%d" % b] = self.s_issuer(b)
         # every role uses each descriptor of its CTA once
-        n0 = sum(x.startswith(("sp", "sm", "s0", "s1", "fwd0")) for x in r)
+        n0 = sum(x.startswith(("sp", "sm", "s0", "s1", "s2", "s3", "fwd0")) for x in r)
         n1 = len(r) - 2 - n0
         assert (n0, n1) == (self.users[0], self.users[1]), (n0, n1, self.users)
         return r
@@ -645,7 +643,7 @@ class Model(P.Model):
     @property
     def slow(self):
         if not hasattr(self, "_slow"):
-            names = ["sp0", "sp1", "vp0", "vp1", "vp2", "sm0", "sm1", "s00", "s01", "s02", "s10", "s11", "s12", "pv", "epi",
+            names = ["sp0", "sp1", "vp0", "vp1", "vp2", "sm0", "sm1", "s0", "s1", "s2", "s3", "pv", "epi",
                      "vmax", "recv", "fwd0", "fwd1", "sched0", "sched1"]
             self._slow = set(self.rng.sample(names, self.rng.randint(0, 3)))
         return self._slow
