@@ -75,11 +75,11 @@ constexpr int32_t kMostParts = 8, kMostPartsBf16 = 4;  // (128-byte blocks of a 
 // be at most lmax (kFill of it on average).  While all units run at once, the
 // time is a unit's; beyond that the work per cluster and half a unit at the
 // end.  So few long units are cut until they fill the GPU (one request on a
-// 1,028-token window: 39.6 us whole, 25.8 in eight), ragged ones until the
-// last one no longer shows (trees of 16 requests of up to 16,384 tokens: 356
-// us whole, 212-243 in two to eight), and many short ones not at all (64
-// requests x 8 shards x 512 tokens: 123 us, 279 in two).
-constexpr double kTileUs = 0.6, kUnitUs = 6.0, kStoreUs = 3.7, kMergeUs = 4.0, kPartialUs = 0.1, kFill = 0.85;
+// 1,028-token window: 31.9 us whole, 21.6 in four), ragged ones until the last
+// one no longer shows (trees of 16 requests of up to 16,384 tokens: 271 us
+// whole, 163 in two, 200 in eight), and many short ones not at all (64 requests
+// x 8 shards x 512 tokens: 103 us, 220 in two).
+constexpr double kTileUs = 0.5, kUnitUs = 6.0, kStoreUs = 3.7, kMergeUs = 4.0, kPartialUs = 0.1, kFill = 0.85;
 constexpr int64_t kMinSelectSplit = 128;
 static int64_t select_splits(int64_t units, int64_t others, int64_t lmax, int clusters) {
   const int64_t most = std::min<int64_t>(kMaxSplits, (lmax + kMinSelectSplit - 1) / kMinSelectSplit);

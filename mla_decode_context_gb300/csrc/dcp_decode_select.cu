@@ -7,8 +7,8 @@
 // A unit runs on a cluster of two CTAs with the division of work of the plain
 // decode (dcp_decode_tc.cu, which also gives the measurements behind it):
 //   score CTA (rank 0)  holds Q in TMEM (288 columns), computes S(j) = Q K(j)^T
-//                       in three K-parts over two slots, runs the online
-//                       softmax and ships P(j) and each lane's running max;
+//                       into one of four slots, runs the online softmax and
+//                       ships P(j) and each lane's running max;
 //   value CTA (rank 1)  holds O (all 512 TMEM columns), rescales it when a
 //                       running max moves, accumulates O += P(j) V(j) and
 //                       writes O / l.
@@ -45,12 +45,13 @@
 // values from that tile before PV (rows that see the token have a NaN weight
 // there and stay NaN).
 //
-// What bounds it: the loop of a tile, 0.6 us (1,150-1,390 cycles; its MMAs alone
-// take ~600), in which the issue of S (three warps, ~120 cycles per MMA while
-// the copies land), the softmax's turn of an S slot and P's way to the value
-// CTA take nearly the same time.  4 trees of 32 rows at 128 heads over 8 shards
-// of 12,000-16,384 tokens: 587 us, 45 % of the measured bf16 rate; with an FP8
-// cache a tile takes 0.85 us, the producers' widening.
+// What bounds it: the loop of a tile, 0.5 us (~1,090 cycles; its MMAs alone take
+// ~600).  The softmax groups are busy all of it (S read 240 of a group's 2,180
+// cycles, arithmetic 770, P staged and sent 530, polls of barriers 500); the
+// copies into both CTAs are 85 % of it behind.  4 trees of 32 rows at 128 heads
+// over 8 shards of 12,000-16,384 tokens: 456 us, 58 % of the measured bf16 rate;
+// 64 requests x 8 shards on a 4,096-token window: 101.5 us, 53 % of the measured
+// bandwidth.  With an FP8 cache a tile takes 0.75 us, the producers' widening.
 //
 // Roundings: P and, for a bf16 output, O / l once, to bf16 (the MMA's operand
 // and the output type); fp8 codes x scale to bf16 (exact for power-of-two
@@ -60,10 +61,11 @@
 //   warps 0-3   score: softmax group 0 (thread = lane of the unit = TMEM lane;
 //                      even tiles)
 //               value: max tracking and O rescale; epilogue columns 0-255
-//   warps 4-9   score: S issuers (warp 4 + 3i + k: third k of S for tiles
-//                      j = i mod 2); 4-7 also move Q to TMEM
-//               value: 4-7 epilogue columns 256-511; 8 forwarder (fp8); 9
-//                      receive-ring arrivals and the proxy fence for PV
+//   warps 4-7   score: Q to TMEM; S issuers (warp 4 + b: slot b, tiles j = b mod 4)
+//               value: epilogue columns 256-511
+//   warps 8-9   score: none
+//               value: 8 forwarder (fp8); 9 receive-ring arrivals and the
+//                      proxy fence for PV
 //   warp 10     both:  TMEM allocation; score: proxy fence of the stage's
 //                      rows, forwarder (fp8); value: PV issuer
 //   warp 11     both:  scheduler
@@ -71,9 +73,9 @@
 //   warps 20-23 score: softmax group 1 (odd tiles)
 //               value: bf16 cache: receive-ring producers
 // Twenty-four warps leave 80 registers a thread, of which softmax and producers
-// spilled (the fp8 producers the codes that they load ahead: 2.3 us a tile, 0.95
-// without), so the warps of the issuers and the scheduler hand some of
-// theirs over, a group of four warps at a time (Regs).
+// spill (8 FP8 trees of 16 rows: 150 us with 80 for the producers, 137 with 88),
+// so the warps of the issuers and the scheduler hand some of theirs over, a
+// group of four warps at a time (Regs).
 // Every wait is bounded (a timeout sets DCP_DEVERR_TIMEOUT and ends the
 // cluster's work).
 #include "dcp_kernels.h"
@@ -103,7 +105,11 @@ constexpr int kGroupThreads = 32 * kProdWarps / 2;
 constexpr int kHalfBytes = 4 * kChunkBytes;      // 4 chunks
 constexpr int kOwn = 7;                          // value CTA: own ring slots (chunks 4-7)
 constexpr int kRecv = 4;                         // value CTA: receive ring slots (chunks 0-3)
-constexpr int kSBuf = 4;                         // S slots (32 columns) in TMEM, one issuing warp each
+// S slots (32 columns) in TMEM, one issuing warp each.  (The plain decode has
+// three K-parts of S per tile, so that three warps share its 36 MMAs; behind
+// elect_one one warp keeps up, and the parts only cost the softmax their sum:
+// 4 trees of 32 rows 510 us, 460 so.)
+constexpr int kSBuf = 4;
 constexpr int kPSlots = 4;                       // P slots in the value CTA
 constexpr int kPBytes = 128 * kTile * 2;         // P tile: 128 rows x 32 bf16, 64B-swizzled
 constexpr int kPWarpBytes = kPBytes / 4;         // one softmax warp's 32 rows
@@ -131,7 +137,7 @@ constexpr float kRescaleLog2 = 8.0f;
 
 // TMEM columns
 constexpr uint32_t kColQ = 0;    // score: 288 columns of Q, 2 bf16 per column
-constexpr uint32_t kColS = 288;  // score: 2 slots x 3 thirds x 32 columns of S
+constexpr uint32_t kColS = 288;  // score: 4 slots x 32 columns of S
 constexpr uint32_t kColO = 0;    // value: 512 columns of O
 constexpr uint32_t kTmemCols = 512;
 
@@ -160,7 +166,7 @@ struct __align__(8) Bars {
   // their bytes of the row mask, the forwarder fenced the rows into the async
   // proxy, and (fp8 tiles) the value CTA's 16 KB landed (armed by a producer)
   uint64_t kv_full[kStages];
-  // s_done (score): item g's stage is free again: all three parts of S done
+  // s_done (score): item g's stage is free again: S done
   // (fp8: and chunks 0-3 landed in the value CTA), or Q moved to TMEM.
   // (value, fp8): the same for tiles only
   uint64_t s_done[kStages];
@@ -231,7 +237,8 @@ __device__ __forceinline__ void set_abort(Bars& bar, int32_t* dev_error) {
 }
 // One lane of the warp, always the same.  Behind this (unlike behind a compare
 // of the lane index) values that all lanes share stay in uniform registers,
-// where the MMAs and commits take their operands.
+// where MMAs, commits and bulk copies take their operands: ~65 cycles per MMA
+// of an issuing warp instead of ~120 (4 trees of 32 rows: 548 -> 511 us).
 __device__ __forceinline__ bool elect_one() {
   uint32_t yes;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
@@ -413,8 +420,8 @@ __device__ __forceinline__ void describe_rows(const DecodeArgs& a, const SelRows
 // unit of every chunk it loads).  The warp finds the cache rows of four of its
 // group's tiles at a time, a lane one row of one tile (resolved by the threads
 // that copy, two rows each, the arithmetic took as long as the copies of a
-// tile: 587 us for 4 trees of 32 rows, 560 so), and fetches their block ids four tiles ahead, the first
-// ones of a unit ahead of its Q items.
+// tile: 4 trees of 32 rows 587 us, 560 so), and fetches their block ids four
+// tiles ahead, the first ones of a unit ahead of its Q items.
 // (The kind is a value, not a template argument: compiled for one kind, the
 // copies of a tile came in one burst per thread, which held up the other
 // warps' shared-memory accesses: 0.77 us a tile instead of 0.60.)
@@ -769,6 +776,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
     const int h = q4 * 32 + lane;
     const uint32_t lane_addr = tbase + (static_cast<uint32_t>(q4 * 32) << 16);
     float* m_first = reinterpret_cast<float*>(smem + kOffSm);  // [unit % 2][128]
+    // (as of elect_one, the same for the warp)
+    const int qu = __shfl_sync(kFull, q4, 0);
+    const uint32_t peer_base = map_peer(smem_base, peer), peer_p_full = map_peer(smem_u32(&bar.p_full[0]), peer);
     const float sl2 = a.scale * kLog2e;
     const int sw = (h >> 1) & 3;  // 64-byte swizzle of row h
     const uint32_t p_row = static_cast<uint32_t>((h >> 3) * 512 + (h & 7) * 64);
@@ -782,7 +792,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
       const int32_t ntiles = U->ntiles, plain0 = U->plain0, plain1 = U->plain1;
       float m_used = -INFINITY, l_sum = 0.f;
       for (int j = j0 + ((j0 ^ sg) & 1); ok && j < j0 + ntiles; j += 2) {
-        const int b = j % kSBuf, slot = j % kPSlots, i0 = j - j0;
+        const uint32_t uj = static_cast<uint32_t>(j);
+        const uint32_t b = uj % kSBuf, slot = uj % kPSlots, turn = (uj / kPSlots) & 1;
+        static_assert(kSBuf == kPSlots, "one turn for both");
+        const int i0 = j - j0;
         float m_other = -INFINITY;
         if (i0 == 1) {
           // (no phase of m_pub is skipped: unit k - 2's is over, since every
@@ -791,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
           if (!ok) break;
           m_other = *reinterpret_cast<volatile float*>(&m_first[(k & 1) * 128 + h]);
         }
-        ok = wait_all(&bar.s_full[b], (j / kSBuf) & 1);
+        ok = wait_all(&bar.s_full[b], turn);
         if (!ok) break;
         tc_fence_after();
         uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&bar.mask[j & 15]);
@@ -874,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         f2_unpack(ps[1], q2, q3);
         l_sum += (q0 + q1) + (q2 + q3);
         // the slot (and this CTA's staging copy of it) is free once PV(j - kPSlots) is done
-        ok = wait_all_cluster(&bar.p_free[slot], ((j / kPSlots) & 1) ^ 1);
+        ok = wait_all_cluster(&bar.p_free[slot], turn ^ 1);
         if (!ok) break;
         unsigned char* stg = smem + kOffP + slot * kPBytes;
         unsigned char* smx = smem + kOffMax + (4 * slot + q4) * kMaxBytes;
@@ -886,11 +899,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         if (lane == 0) *reinterpret_cast<uint32_t*>(smx + 128) = foul ? 1u : 0u;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
+        const int su = __shfl_sync(kFull, slot, 0);
+        if (elect_one()) {
           // this warp's 32 rows of P, then its 32 maxima and flag: two bulk copies
-          const uint32_t peer_full = map_peer(smem_u32(&bar.p_full[slot]), peer);
-          bulk_copy_to_peer(map_peer(smem_u32(stg) + q4 * kPWarpBytes, peer), stg + q4 * kPWarpBytes, kPWarpBytes, peer_full);
-          bulk_copy_to_peer(map_peer(smem_u32(smx), peer), smx, kMaxBytes, peer_full);
+          const uint32_t full = peer_p_full + 8 * su;
+          const uint32_t rows = kOffP + su * kPBytes + qu * kPWarpBytes, maxima = kOffMax + (4 * su + qu) * kMaxBytes;
+          bulk_copy_to_peer(peer_base + rows, smem + rows, kPWarpBytes, full);
+          bulk_copy_to_peer(peer_base + maxima, smem + maxima, kMaxBytes, full);
         }
       }
       // both groups' sums meet here (two units' worth of space); group 0
