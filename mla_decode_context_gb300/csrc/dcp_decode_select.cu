@@ -45,13 +45,15 @@
 // values from that tile before PV (rows that see the token have a NaN weight
 // there and stay NaN).
 //
-// What bounds it: the loop of a tile, 0.5 us (~1,090 cycles; its MMAs alone take
-// ~600).  The softmax groups are busy all of it (S read 240 of a group's 2,180
-// cycles, arithmetic 770, P staged and sent 530, polls of barriers 500); the
-// copies into both CTAs are 85 % of it behind.  4 trees of 32 rows at 128 heads
-// over 8 shards of 12,000-16,384 tokens: 456 us, 58 % of the measured bf16 rate;
-// 64 requests x 8 shards on a 4,096-token window: 101.5 us, 53 % of the measured
-// bandwidth.  With an FP8 cache a tile takes 0.75 us, the producers' widening.
+// What bounds it: the chain of barriers, polls, fences and copies from S to P to
+// PV, ~970 cycles a tile (its MMAs alone take ~600; without any KV byte loaded,
+// or without the softmax's arithmetic, the time stays), and the way of a unit's
+// O out through one SM (26-30 bytes per clock), for which the next unit's PV
+// waits ~5,000 cycles (9 % of units of 51 tiles, 30 % of units of 16).  4 trees
+// of 32 rows at 128 heads over 8 shards of 12,000-16,384 tokens: 454 us, 58 % of
+// the measured bf16 rate; 64 requests x 8 shards on a 4,096-token window: 100
+// us, 54 % of the measured bandwidth.  With an FP8 cache a tile takes ~0.75 us,
+// the producers' widening.
 //
 // Roundings: P and, for a bf16 output, O / l once, to bf16 (the MMA's operand
 // and the output type); fp8 codes x scale to bf16 (exact for power-of-two
@@ -964,7 +966,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
           const unsigned char* mx = smem + kOffMax + 4 * slot * kMaxBytes;
           const float m_new = *reinterpret_cast<const volatile float*>(mx + q4 * kMaxBytes + 4 * lane);
           const uint32_t foul = *reinterpret_cast<const volatile uint32_t*>(mx + (lane & 3) * kMaxBytes + 128);
-          if (__any_sync(kFull, foul != 0)) {
+          // a tile computed with m = -inf has P = 0 and leaves O as it is
+          const bool up = m_new > m_prev && m_prev != -INFINITY;
+          // a tile in a smaller max's scale than O's: this lane's 32 weights
+          // of P(j) (64 bytes, in any order) come down to O's
+          const bool down = m_new < m_prev && m_new != -INFINITY;
+          const bool rare = __any_sync(kFull, foul != 0 || up || down);  // (one vote in the common case)
+          if (rare && __any_sync(kFull, foul != 0)) {
             // clear the tile's NaNs and infinities, a quarter per warp (both
             // rings' slots refill only after PV(j), which waits for this
             // warp's p_ok)
@@ -985,9 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
             }
             fence_proxy_async_smem();
           }
-          // a tile computed with m = -inf has P = 0 and leaves O as it is
-          const bool up = m_new > m_prev && m_prev != -INFINITY;
-          if (__any_sync(kFull, up)) {
+          if (rare && __any_sync(kFull, up)) {
             // O holds this unit's PVs up to j - 1: wait for them, then scale
             // this warp's rows
             const int jp = j - 1;
@@ -1005,10 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
             }
             tmem_wait_st();
           }
-          // a tile in a smaller max's scale than O's: this lane's 32 weights
-          // of P(j) (64 bytes, in any order) come down to O's
-          const bool down = m_new < m_prev && m_new != -INFINITY;
-          if (__any_sync(kFull, down)) {
+          if (rare && __any_sync(kFull, down)) {
             if (down) {
               const float f = ex2_approx(m_new - m_prev);
               uint4* row = reinterpret_cast<uint4*>(smem + kOffP + slot * kPBytes + (h >> 3) * 512 + (h & 7) * 64);
@@ -1296,9 +1299,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
               for (int n = 0; n < 2; ++n)
                 mma_ss(tbase + kColO + 256 * n, dp + po + ((32 * i) >> 4), dv + sv[n] + ((2048 * i) >> 4), id_o,
                        (j > j0 || i > 0) ? 1u : 0u);
+            mma_commit_mc(&bar.p_free[slot], 0x3);
             mma_commit_mc(&bar.v_free[vs], 0x3);
             mma_commit(&bar.own_free[os]);
-            mma_commit_mc(&bar.p_free[slot], 0x3);
             mma_commit(&bar.pv_done[slot]);
             if (j == j0 + ntiles - 1) mma_commit(&bar.o_final);
           }
