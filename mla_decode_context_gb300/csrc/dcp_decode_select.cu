@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
     for (; dealt * clusters < units; ++dealt) {
       const int32_t at = dealt * clusters + ((dealt & 1) ? clusters - 1 - c : c);
       if (at >= units) continue;
-      // (units whose output several clusters share are all dealt in round 0)
+      // (units whose output several clusters share are all in the first turn of the deal)
       int32_t u = at, part = 0;
       if (a.unit_order) {
         u = *static_cast<const volatile int32_t*>(a.unit_order + at);

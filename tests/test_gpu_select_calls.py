@@ -226,3 +226,20 @@ def test_a_wait_that_runs_out_is_reported(monkeypatch):
         O, lse, err = run(inp, t, 100, 2)
         assert err == 0
         check(inp, O, lse, oracle.decode_partial_select(inp, 100, 2), "after")
+
+
+def test_many_pairs_in_few_splits_are_the_plain_decode():
+    """320 rows of 32 heads (10,240 pairs, merged a warp each) over 9,000
+    tokens in two to four splits, on a chain: the partials of the decode without
+    selection, within twice the attention tolerances."""
+    inp = wl.make_decode_inputs(S("merge", seed=91, B=2, seq_lens=(9000, 8000), q_len=160, H=32, D=1, block_size=64))
+    t = G.to_device(inp)
+    size = dcp.dcp_decode_select_workspace_size(2, 320, 32, 1, 9000, 160, 0, 0)
+    assert 2 <= size // (320 * 32 * 2052) <= 4
+    want, want_lse = G.run_decode(inp, t)[:2]
+    for dt in (torch.float32, torch.bfloat16):
+        O, lse, err = run(inp, t, 0, 0, out_dtype=dt)
+        assert err == 0
+        step = 0.0 if dt == torch.float32 else 2.0 ** -8
+        assert ((O.float() - want).abs() <= 2 * G.ATT_OUT_ABS + step * want.abs()).all()
+        assert (lse - want_lse).abs().max().item() <= 2 * G.ATT_LSE_ABS
