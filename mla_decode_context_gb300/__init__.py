@@ -403,8 +403,7 @@ def _decode_select(where, tree_mask, q, kv_cache, block_table, seq_lens, query_s
     extra = (tree_mask.data_ptr(), m0 if T > 1 else (max_q_len + 63) // 64) if tree else ()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     call = getattr(_lib or lib(), where)
-    with _Call(where, device):
-        st = call(
+    _launch(where, device, call,
             q.data_ptr(), q0 if T > 1 else H * KV_DIM, kv_cache.data_ptr(),
             KV_FP8_E4M3 if fp8 else KV_BF16, kv_scale.data_ptr() if fp8 else None, blocks, block_size,
             block_table.data_ptr(), table[-1], table_stride[-2] if B > 1 else table[-1], 1 if local else 0,
@@ -413,8 +412,6 @@ def _decode_select(where, tree_mask, q, kv_cache, block_table, seq_lens, query_s
             num_sinks, O_part.data_ptr(), DTYPE_BF16 if o_dtype is _BF16 else DTYPE_F32,
             lse_part.data_ptr(), workspace.data_ptr() if ws_bytes else None, ws_bytes,
             None if dev_error is None else dev_error.data_ptr(), _stream_of(stream, device))
-    if st:
-        _check(st, where)
 
 
 def _stream_context(stream, device):
@@ -633,36 +630,29 @@ def _flag_word(dev_error, device: int) -> bool:
     return dev_error.dtype is _I32T and dev_error.get_device() == device and dev_error.numel() > 0
 
 
-class _Call:
-    """The surroundings of a library call: `device` is the current one (the
-    library launches on the current device) and an NVTX range names it."""
-    __slots__ = ("name", "device", "before", "pushed")
+try:  # the calls under torch.cuda.nvtx, without its wrappers
+    from torch._C import _nvtx as _raw_nvtx
+    _push, _pop = _raw_nvtx.rangePushA, _raw_nvtx.rangePop
+except Exception:  # pragma: no cover
+    _push = _pop = None
 
-    def __init__(self, name: str, device: int):
-        self.name, self.device = name, device
 
-    def __enter__(self):
-        self.before = None
-        if _device_now() != self.device:
-            self.before = torch.cuda.device(self.device)
-            self.before.__enter__()
-        self.pushed = False
-        if _nvtx is not None:
-            try:
-                _nvtx.range_push(self.name)
-                self.pushed = True
-            except Exception:
-                pass
-
-    def __exit__(self, *exc):
-        if self.pushed:
-            try:
-                _nvtx.range_pop()
-            except Exception:
-                pass
-        if self.before is not None:
-            self.before.__exit__(*exc)
-        return False
+def _launch(name: str, device: int, call, *args) -> None:
+    """A library call with `device` as the current one (the library launches
+    there), named by an NVTX range."""
+    if _device_now() != device:
+        with torch.cuda.device(device):
+            _launch(name, device, call, *args)
+        return
+    if _push is not None:
+        _push(name)
+    try:
+        st = call(*args)
+    finally:
+        if _pop is not None:
+            _pop()
+    if st:
+        _check(st, name)
 
 
 def _stream_of(stream, device: int):
@@ -769,15 +759,12 @@ def dcp_decode_concat_cache_v2(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q_out, k
         many, heads = int(T > 1), int(H > 1)
         strides = (strides[0] * many, strides[1] * heads, strides[2] * many, strides[3] * heads)
     call = (_lib or lib()).dcp_decode_concat_cache_v2
-    with _Call("dcp_decode_concat_cache_v2", device):
-        st = call(
+    _launch("dcp_decode_concat_cache_v2", device, call,
             ql_nope.data_ptr() if query else None, strides[0], strides[1], q_pe.data_ptr() if query else None,
             strides[2], strides[3], kv_c.data_ptr(), c0, k_pe.data_ptr(), p0, slot_mapping.data_ptr(), T, H,
             q_out.data_ptr() if query else None, q_stride, kv_cache.data_ptr(),
             KV_FP8_E4M3 if fp8 else KV_BF16, kv_scale.data_ptr() if fp8 else None, blocks * block_size,
             None if dev_error is None else dev_error.data_ptr(), _stream_of(stream, device))
-    if st:
-        _check(st, "dcp_decode_concat_cache_v2")
 
 
 def _explain_write(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q_out, kv_cache, kv_scale, dev_error, query):
@@ -856,16 +843,13 @@ def dcp_latent_cache_read(kv_cache, block_table, cu_lens, out, *, seq_starts: Op
     if B == 0 or N == 0:
         return
     call = (_lib or lib()).dcp_latent_cache_read
-    with _Call("dcp_latent_cache_read", device):
-        st = call(
+    _launch("dcp_latent_cache_read", device, call,
             kv_cache.data_ptr(), KV_FP8_E4M3 if fp8 else KV_BF16, kv_scale.data_ptr() if fp8 else None, blocks,
             block_size, block_table.data_ptr(), table[-1], table_stride[-2] if B > 1 else table[-1],
             1 if local else 0, table_stride[0] if local else 0, D, interleave, shard_begin, shard_count,
             None if seq_starts is None else seq_starts.data_ptr(), cu_lens.data_ptr(), B, N, out.data_ptr(),
             DTYPE_F32 if o_dtype is _F32 else DTYPE_BF16, out_stride if N > 1 else KV_DIM,
             None if dev_error is None else dev_error.data_ptr(), _stream_of(stream, device))
-    if st:
-        _check(st, "dcp_latent_cache_read")
 
 
 def _explain_read(kv_cache, block_table, cu_lens, out, seq_starts, kv_scale, shard_count, dev_error):
