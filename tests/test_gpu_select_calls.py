@@ -243,3 +243,35 @@ def test_many_pairs_in_few_splits_are_the_plain_decode():
         step = 0.0 if dt == torch.float32 else 2.0 ** -8
         assert ((O.float() - want).abs() <= 2 * G.ATT_OUT_ABS + step * want.abs()).all()
         assert (lse - want_lse).abs().max().item() <= 2 * G.ATT_LSE_ABS
+
+
+def test_captured_call_of_ordered_units_replays():
+    """The kernel that orders the units and the decode that sets up alongside
+    it, captured once and replayed on other lengths: as a fresh call, bit for
+    bit, also when replays follow one another without a pause."""
+    inp = wl.make_decode_inputs(S("ordered", seed=92, B=60, seq_lens=(200,) * 60, q_len=1, H=128, D=8))
+    t = G.to_device(inp)
+    rng = np.random.default_rng(92)
+    size = dcp.dcp_decode_select_workspace_size(60, 60, 128, 8, 200, 1, 90, 3)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def call():
+        return dcp.decode_partial_window(t["q"], t["kv_cache"], t["block_table"], t["seq_lens"], t["query_start_loc"],
+                                         D=8, interleave=1, scale=inp["scale"], window=90, num_sinks=3,
+                                         max_seq_len=200, max_q_len=1, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        O, lse = call()
+    for _ in range(4):
+        seq = rng.integers(0, 201, 60).astype(np.int32)
+        t["seq_lens"].copy_(torch.from_numpy(seq))
+        O.fill_(float("nan"))
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+        O2, lse2 = call()
+        torch.cuda.synchronize()
+        assert torch.equal(O, O2) and torch.equal(lse, lse2)
+    check(inp, O, lse, oracle.decode_partial_select(dict(inp, seq_lens=seq), 90, 3), "ordered")
