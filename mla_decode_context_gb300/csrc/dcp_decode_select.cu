@@ -237,10 +237,10 @@ __device__ __forceinline__ void set_abort(Bars& bar, int32_t* dev_error) {
   report(dev_error, DCP_DEVERR_TIMEOUT);
   atomicExch(&bar.abort, 1);
 }
-// One lane of the warp, always the same.  Behind this (unlike behind a compare
-// of the lane index) values that all lanes share stay in uniform registers,
-// where MMAs, commits and bulk copies take their operands: ~65 cycles per MMA
-// of an issuing warp instead of ~120 (4 trees of 32 rows: 548 -> 511 us).
+// One lane of the warp, always the same.  MMAs, commits and bulk copies take
+// operands that all lanes share; behind this, unlike behind a compare of the
+// lane index, they can be kept as such: ~65 cycles per MMA of an issuing warp
+// instead of ~120 (4 trees of 32 rows: 548 -> 511 us).
 __device__ __forceinline__ bool elect_one() {
   uint32_t yes;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
