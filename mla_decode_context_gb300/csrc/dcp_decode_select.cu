@@ -927,9 +927,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_select_kernel(DecodeArgs a
         const float m1 = *reinterpret_cast<volatile float*>(&fin_sh[3 * 128 + h]);
         // O is in the scale of the largest m of any tile
         const float mo = fmaxf(m_used, m1);
-        float l = 0.f;
-        if (m_used != -INFINITY) l += l_sum * ex2_approx(m_used - mo);
-        if (m1 != -INFINITY) l += l1 * ex2_approx(m1 - mo);
+        // (a group whose m is -inf has a sum of 0, or of NaN where all it saw
+        // were NaN scores, which a maximum passes over: NaN stays)
+        const float l = (m_used != -INFINITY ? l_sum * ex2_approx(m_used - mo) : l_sum) +
+                        (m1 != -INFINITY ? l1 * ex2_approx(m1 - mo) : l1);
         const bool some = l != 0.f;  // (a NaN weight gives NaN, not an empty row)
         const int fs = k % kFinSlots;
         st_async_peer_b32(map_peer(smem_base + kOffFin + fs * 512 + 4 * h, peer), __float_as_uint(some ? 1.f / l : 0.f),
