@@ -481,7 +481,7 @@ dcp_status_t dcp_mla_decode_partial_tree(
     size_t workspace_bytes, int32_t* dev_error, void* stream) {
   if (max_q_len > DCP_MAX_TREE_ROWS) return DCP_ERR_INVALID_ARG;
   if (B > 0 && T > 0) {
-    if (!tree_mask || (T > 1 && mask_stride < (max_q_len + 63) / 64)) return DCP_ERR_INVALID_ARG;
+    if (!tree_mask || mask_stride < (max_q_len + 63) / 64) return DCP_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(tree_mask) % 8 != 0) return DCP_ERR_MISALIGNED;
   }
   dcp::SelectArgs sel{};
