@@ -1010,7 +1010,13 @@ def _decode_select_alloc(where, tree_mask, q, kv_cache, block_table, seq_lens, q
     O = torch.empty((D, T, H, LATENT_DIM), dtype=out_dtype, device=device)
     lse = torch.empty((D, T, H), dtype=_F32, device=device)
     if workspace is None:
-        n = dcp_decode_select_workspace_size(seq_lens.shape[0], T, H, D, max_seq_len, max_q_len, window, num_sinks)
+        sizes = seq_lens.shape[0], T, H, D, max_seq_len, max_q_len, window, num_sinks
+        index = q.get_device()
+        if index < 0 or _device_now() == index:
+            n = dcp_decode_select_workspace_size(*sizes)
+        else:  # (it goes by the clusters of the device that the call runs on)
+            with torch.cuda.device(index):
+                n = dcp_decode_select_workspace_size(*sizes)
         workspace = torch.empty(n, dtype=_U8, device=device) if n else None
     _decode_select(where, tree_mask, q, kv_cache, block_table, seq_lens, query_start_loc, O, lse, D, interleave, scale,
                    window, num_sinks, max_seq_len, max_q_len, kv_scale, 0, D, workspace, dev_error, None)
