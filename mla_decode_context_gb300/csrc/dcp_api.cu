@@ -299,9 +299,9 @@ static dcp_status_t decode_partial_impl(const void* q, int64_t q_stride_tok, con
     sel.group = select_group(H, max_q_len);
     sel.chunks = (max_q_len - 1) / sel.group + 1;
   }
-  // (a workspace that holds no partials may be misaligned; it is then not used
-  // for the launch order either)
-  const bool usable = workspace != nullptr && aligned16(workspace);
+  // (a workspace that holds no partials may be misaligned; the launch order,
+  // int32 words, goes into it at any multiple of 4)
+  const bool usable = workspace != nullptr && reinterpret_cast<uintptr_t>(workspace) % alignof(int32_t) == 0;
   const DecodeLaunch launch =
       select ? select_launch(B, T, H, D, interleave, d0, Dn, max_seq_len, max_q_len,
                              static_cast<int64_t>(num_blocks) * block_size, sel, o_dtype == DCP_DTYPE_BF16,
