@@ -345,8 +345,17 @@ def dcp_mla_decode_partial_v2(q, kv_cache, block_table, seq_lens, query_start_lo
     _check(st, "dcp_mla_decode_partial_v2")
 
 
+def _fits32(bits: int, where: str) -> None:
+    """`bits`: a call's whole numbers, ORed.  ctypes cuts a number to its
+    parameter's 32 bits.  (One that does not fit may hide behind a negative
+    one, which the library refuses.)"""
+    if bits >> 31 not in (0, -1):
+        raise ValueError("%s: a number does not fit 32 bits" % where)
+
+
 def dcp_decode_select_workspace_size(B: int, T: int, H: int, D: int, max_seq_len: int, max_q_len: int,
                                      window: int = 0, num_sinks: int = 0) -> int:
+    _fits32(B | T | H | D | max_seq_len | max_q_len | window | num_sinks, "dcp_decode_select_workspace_size")
     n = lib().dcp_decode_select_workspace_size(B, T, H, D, max_seq_len, max_q_len, window, num_sinks)
     if n == ctypes.c_size_t(-1).value:
         raise DCPError(1, "dcp_decode_select_workspace_size")
@@ -360,6 +369,7 @@ def _decode_select(where, tree_mask, q, kv_cache, block_table, seq_lens, query_s
     calls that are right; any other goes through _explain_select."""
     if shard_count is None:
         shard_count = D - shard_begin
+    _fits32(D | interleave | window | num_sinks | max_seq_len | max_q_len | shard_begin, where)
     tree = where is _TREE
     try:
         T, H, dim = q.shape
@@ -812,6 +822,7 @@ def dcp_latent_cache_read(kv_cache, block_table, cu_lens, out, *, seq_starts: Op
         shard_count = D - shard_begin
     if D < 1 or D > MAX_SHARDS or shard_begin < 0 or shard_count < 1 or shard_begin + shard_count > D:
         raise ValueError("shards [shard_begin, shard_begin + shard_count) must lie in [0, D), D <= %d" % MAX_SHARDS)
+    _fits32(interleave, "dcp_latent_cache_read")
     try:
         N, dim = out.shape
         out_stride, unit = out.stride()
@@ -1002,7 +1013,7 @@ def _decode_select_alloc(where, tree_mask, q, kv_cache, block_table, seq_lens, q
     T, H = q.shape[0], q.shape[1]
     device = q.device
     if max_seq_len is None:
-        max_seq_len = block_table.shape[-1] * kv_cache.shape[1] * (D if block_table.dim() == 3 else 1)
+        max_seq_len = min(block_table.shape[-1] * kv_cache.shape[1] * (D if block_table.dim() == 3 else 1), 0x7fffffff)
     if max_q_len is None:
         max_q_len = max(1, T)
         if where is _TREE:
