@@ -14,11 +14,12 @@
 //   batched (kEarly = false): after the weights, the live sources only,
 //     kBatch at a time.  A masked source's partial is never read.  The
 //     combine takes this way with one warp per pair when there are many
-//     pairs, so that many pairs per SM keep enough bytes in flight.
+//     pairs, so that many pairs per SM keep enough bytes in flight, and the
+//     split merge when there are very many in at most four splits.
 //   early (kEarly = true): every source's partial is loaded before the
 //     weights are known (one memory round trip in all) and the sum takes the
 //     live ones only, so the bytes of a masked source (NaN or anything) are
-//     read but never used.  The split merge (up to 16 splits) and the
+//     read but never used.  The other split merges (up to 16 splits) and the
 //     combine of few pairs take this way: two warps per pair up to 8 or 12
 //     sources, four warps up to 16; a thread holds at most 96 loaded
 //     registers and two 256-thread CTAs fit on an SM.
@@ -190,8 +191,15 @@ cudaError_t launch_batch(const InT* O_src, const float* lse_src, int64_t o_strid
 // Below this many pairs one warp per pair leaves most SMs idle (eight pairs
 // per 256-thread CTA), and the combine loads early instead.
 constexpr int64_t kFewPairs = 2048;
-// From this many on, a split merge of few splits has one warp per pair and all
-// the same fills the GPU (152 SMs x 4 CTAs x 8 pairs = 4,864).
+// From this many on, a split merge of at most four splits takes one warp per
+// pair.  Measured with both ways on fp32 partials and a bf16 output (early / one
+// warp, us, L2 cold; the partials in L2): two splits of 2,048 pairs 6.4 / 5.2;
+// 3.5 / 2.6, of 7,648 pairs 14.3 / 9.8; 9.4 / 6.5; three of 7,648 15.5 / 13.4;
+// 10.9 / 10.2; four of 7,648 16.7 / 15.8; 11.2 / 12.0, of 9,728 20.4 / 18.5;
+// 15.1 / 14.9.  So two and three splits would gain from 2,048 pairs on; the
+// threshold is past what the tensor-core plain decode ever splits on 152 SMs (a
+// quarter as many rows, of up to 128 heads), so that its merges keep their
+// kernel.
 constexpr int64_t kManyPairs = 4865;
 
 // The early way: all sources at once, two warps per pair up to 12 sources,
@@ -217,7 +225,7 @@ cudaError_t launch_early(const InT* O_src, const float* lse_src, int64_t o_strid
 // those, and the combine of many pairs, take one warp per pair (four float4
 // columns per lane per source) and load two live sources at a time when there
 // are at most two, else four: fewer registers for small D leave room for more
-// pairs per SM (7,648 pairs in three splits: 12.2 us instead of 16.4).
+// pairs per SM.
 template <typename InT, typename OutT, bool kRowMask>
 cudaError_t launch(const InT* O_src, const float* lse_src, int64_t o_stride, int64_t lse_stride, int nsrc,
                    int64_t npairs, int32_t H, const int32_t* seq_lens, const int32_t* qsl, int32_t B, OutT* out,

@@ -18,7 +18,7 @@
 // pipeline and writing O took 14 us of a unit's 25 when each unit was its own
 // cluster launch.  So clusters are persistent: they walk the list of units,
 // and the rings run through the unit borders (a further unit now takes 5-6 us
-// besides its tiles; 64 requests x 8 shards on that window: 175 -> 126 us, 120
+// besides its tiles; 64 requests x 8 shards on that window: 175 -> 126 us, 101
 // now).
 //   - A scheduler warp per CTA resolves the next units (rows, spans, the
 //     lanes' masks) into a ring of descriptors while the current one runs; it
@@ -42,23 +42,24 @@
 // and every second tile be scaled down.  The maxima of a lane are therefore
 // whole steps of 2 apart (the first tile's max, or 1, times powers of 2): the
 // scaling moves the weights' exponents, and each is rounded to bf16 once.  It
-// costs time, not digits (4 trees of 32 rows over 16,000 tokens: 507 us with
-// level scores, 592 with one 14 bits above the rest in the fifth tile, 841 with
+// costs time, not digits (4 trees of 32 rows over 16,000 tokens: 504 us with
+// level scores, 591 with one 14 bits above the rest in the fifth tile, 838 with
 // scores that rise by 20 bits through the context).
 // A weight of 0 does not keep a NaN or an infinity of V out of a product, and a
 // token that only some of the rows see may hold one: a non-finite latent shows
 // in every lane's score, so the lanes that mask it report it and the value CTA
-// clears such values from that tile before PV (rows that see the token have a
-// NaN weight there and stay NaN).
+// clears such values from that tile before PV.  Rows that see the token have a
+// NaN weight there and stay NaN, or score it -inf: a weight of 0, with which it
+// then counts for nothing, as in the CUDA-core kernel.
 //
 // What bounds it: the chain of barriers, polls, fences and copies from S to P to
 // PV, ~970 cycles a tile (its MMAs alone take ~600; without any KV byte loaded,
 // or without the softmax's arithmetic, the time stays), and the way of a unit's
 // O out through one SM (26-30 bytes per clock), for which the next unit's PV
 // waits ~5,000 cycles (9 % of units of 51 tiles, 30 % of units of 16).  4 trees
-// of 32 rows at 128 heads over 8 shards of 12,000-16,384 tokens: 454 us, 58 % of
-// the measured bf16 rate; 64 requests x 8 shards on a 4,096-token window: 100
-// us, 54 % of the measured bandwidth.  With an FP8 cache a tile takes ~0.75 us,
+// of 32 rows at 128 heads over 8 shards of 12,000-16,384 tokens: 456 us, 58 % of
+// the measured bf16 rate; 64 requests x 8 shards on a 4,096-token window: 101
+// us, 53 % of the measured bandwidth.  With an FP8 cache a tile takes ~0.75 us,
 // the producers' widening.
 //
 // Roundings: P and, for a bf16 output, O / l once, to bf16 (the MMA's operand
