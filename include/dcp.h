@@ -75,6 +75,8 @@ extern "C" {
 #define DCP_DEVERR_SEQ_TOO_LONG 2 /* seq_len > max_seq_len (clamped to max_seq_len) */
 #define DCP_DEVERR_BAD_ROWS 4     /* query_start_loc decreasing, or q_len > max_q_len */
 #define DCP_DEVERR_TIMEOUT 8      /* a bounded on-device wait gave up */
+#define DCP_DEVERR_NO_BLOCKS 16   /* the free list ran out (dcp_cache_extend) */
+#define DCP_DEVERR_BAD_POSITION 32 /* a position past the cos/sin table (dcp_norm_rope_cache) */
 
 typedef enum {
   DCP_OK = 0,
@@ -563,6 +565,90 @@ dcp_status_t dcp_mla_decode_partial_tree(
 size_t dcp_decode_select_workspace_size(int32_t B, int32_t T, int32_t H, int32_t D,
                                         int32_t max_seq_len, int32_t max_q_len,
                                         int32_t window, int32_t num_sinks);
+
+/*
+ * Block tables and slot maps of a step, built on the GPU from the requests'
+ * lengths: takes the blocks that the step's new tokens need from a free list,
+ * enters them in the requests' tables and gives every query row its position
+ * and cache slot.  (The pages take tables and slot_mapping as given; each DCP
+ * rank's holds its own tokens, [PRHUB] implementation step 3.)
+ *
+ * Request b has seq_lens[b] tokens after the step, the last q_len = qsl[b+1] -
+ * qsl[b] of them new.  Its table (per_shard_tables: each of its shards' tables,
+ * over the shard's local tokens, dcp_local_len) holds the blocks of the others
+ * and gets columns [ceil(len(old) / block_size), ceil(len(seq) / block_size)),
+ * old = max(0, seq_lens[b] - q_len).  New entry k, counted from 0 over
+ * requests, then shards, then columns, is free_blocks[free_count - 1 - k].  All
+ * other entries are left as they are.  A request of no tokens takes nothing.
+ *   - Out of free blocks: the entries are -1 and DCP_DEVERR_NO_BLOCKS is set.
+ *   - Columns at or past bt_width are not taken (DCP_DEVERR_SEQ_TOO_LONG).
+ * Row i of a request is the token at position p = seq_lens[b] - q_len + i:
+ *   positions[r] = p, slot_mapping[r] = entry(p) * block_size + offset(p)
+ * slot_mapping -1 where the entry is negative or missing, or a shard outside
+ * [shard_begin, shard_begin + shard_count) owns the token; both -1 for rows of
+ * no request, of a request of no tokens, and before position 0.
+ *
+ *   block_table  in/out, as for dcp_mla_decode_partial_v2; a width of 2^20 at
+ *                most.
+ *   seq_lens, query_start_loc, B, T, D, interleave, shard_begin, shard_count
+ *                as for dcp_mla_decode_partial_v2.
+ *   free_blocks  int32 [num_free], a stack of block ids; free_count int32 [1],
+ *                how many of them are left (clamped to [0, num_free]).  Blocks
+ *                of finished requests go back by writing their ids from
+ *                free_blocks[count] on and raising the count.
+ *   free_left    int32 [1], how many are left afterwards; may be free_count.
+ *   positions    int32 [T]; slot_mapping int64 [T].
+ */
+dcp_status_t dcp_cache_extend(
+    int32_t* block_table, int32_t bt_width, int64_t bt_stride,
+    int32_t per_shard_tables, int64_t bt_shard_stride,
+    const int32_t* seq_lens, const int32_t* query_start_loc, int32_t B, int32_t T, int32_t block_size,
+    int32_t D, int32_t interleave, int32_t shard_begin, int32_t shard_count,
+    const int32_t* free_blocks, int32_t num_free, const int32_t* free_count, int32_t* free_left,
+    int32_t* positions, int64_t* slot_mapping,
+    int32_t* dev_error, void* stream);
+
+/*
+ * dcp_decode_concat_cache_v2 from the projections' outputs: the latent's norm
+ * and the rotation of the rope parts by their positions in the same launch
+ * ([PRHUB], key snippet "Decode: latent multi-query attention":
+ * _decode_concat_cache with rope_positions).
+ *
+ *   c    = kv_c * norm_weight / sqrt(mean(kv_c^2) + eps)   (512 dims; norm_weight
+ *          NULL: kv_c as it is)
+ *   rot  turns pairs (x, y) of a rope part by its token's angles:
+ *          (x cos_i - y sin_i, y cos_i + x sin_i), i < 32; pairs are dims
+ *          (2i, 2i + 1) if interleaved, else (i, i + 32).
+ *   cache row of slot_mapping[t] = [c | rot(k_pe)], q_out = [ql_nope | rot(q_pe)].
+ * Computed in fp32 and rounded once: to bf16 (nearest even), or for an FP8
+ * cache to the codes of dcp_decode_concat_cache_v2 (scale 2^e with e >= -126)
+ * straight from the fp32 values.  (Squares that overflow fp32 give a norm of
+ * infinity: a row of zeros and NaN.)
+ *
+ *   ql_nope      bf16 [T, H, 512], or NULL: q_out gets the rotated rope parts
+ *                alone (a chunk's queries, whose other part stays where it is).
+ *   q_pe, q_out  bf16 [T, H, 64] and [T, H, 576] (64 without ql_nope); token and
+ *                head strides of any order, outputs not overlapping.  Without
+ *                ql_nope q_out may be q_pe itself, with the same strides.
+ *   H            0: no query; ql_nope, q_pe and q_out NULL.
+ *   positions    int32 [T].  Negative: rope parts are not turned (padding
+ *                rows).  max_pos or more: likewise, and
+ *                DCP_DEVERR_BAD_POSITION is set.
+ *   cos_sin      fp32 [max_pos, 64]: a position's 32 cosines, then its 32 sines.
+ * Everything else as for dcp_decode_concat_cache_v2 (16-byte alignment,
+ * norm_weight bf16 [512] and cos_sin included).
+ */
+dcp_status_t dcp_norm_rope_cache(
+    const void* ql_nope, int64_t ql_nope_stride_tok, int64_t ql_nope_stride_head,
+    const void* q_pe, int64_t q_pe_stride_tok, int64_t q_pe_stride_head,
+    void* q_out, int64_t q_out_stride_tok, int64_t q_out_stride_head,
+    const void* kv_c, int64_t kv_c_stride_tok,
+    const void* k_pe, int64_t k_pe_stride_tok,
+    const void* norm_weight, float eps,
+    const int32_t* positions, const float* cos_sin, int32_t max_pos, int32_t interleaved,
+    const int64_t* slot_mapping, int32_t T, int32_t H,
+    void* kv_cache, dcp_kv_dtype_t kv_dtype, float* kv_scale, int64_t num_slots,
+    int32_t* dev_error, void* stream);
 
 #ifdef __cplusplus
 }

@@ -29,6 +29,8 @@ DEVERR_BAD_BLOCK = 1
 DEVERR_SEQ_TOO_LONG = 2
 DEVERR_BAD_ROWS = 4
 DEVERR_TIMEOUT = 8
+DEVERR_NO_BLOCKS = 16
+DEVERR_BAD_POSITION = 32
 
 def compute_dtype() -> str:
     """Arithmetic type of the decode contraction: bf16 tensor-core MMAs with
@@ -84,6 +86,11 @@ EXPORTS = [
      [_P, _I64, _P, ctypes.c_int, _P, _I32, _I32, _P, _I32, _I64, _I32, _I64, _I32, _I32, _P, _P, _I32, _I32, _I32,
       _I32, _I32, _I32, _I32, _F, _P, _I64, _I32, _I32, _P, ctypes.c_int, _P, _P, _SZ, _P, _P]),
     ("dcp_decode_select_workspace_size", _SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32]),
+    ("dcp_cache_extend", ctypes.c_int,
+     [_P, _I32, _I64, _I32, _I64, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _P]),
+    ("dcp_norm_rope_cache", ctypes.c_int,
+     [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _F, _P, _P, _I32, _I32, _P, _I32, _I32,
+      _P, ctypes.c_int, _P, _I64, _P, _P]),
 ]
 
 _lib = None
@@ -893,6 +900,195 @@ def _explain_read(kv_cache, block_table, cu_lens, out, seq_starts, kv_scale, sha
     return B, N, local, fp8, _placed(args)
 
 
+def dcp_cache_extend(block_table, seq_lens, query_start_loc, free_blocks, free_count, free_left, positions,
+                     slot_mapping, *, block_size: int, D: int = 1, interleave: int = 1, shard_begin: int = 0,
+                     shard_count: Optional[int] = None, dev_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Build a step's block tables and slot map: block_table int32 [B, W] or
+    per-shard [shard_count, B, W] (extended in place), free_blocks int32 [F],
+    free_count and free_left int32 [1] (may be the same), positions int32 [T]
+    and slot_mapping int64 [T] (written)."""
+    if shard_count is None:
+        shard_count = D - shard_begin
+    _fits32(D | interleave | block_size | shard_begin, "dcp_cache_extend")
+    try:
+        B, = seq_lens.shape
+        T, = positions.shape
+        num_free, = free_blocks.shape
+        table, table_stride = block_table.shape, block_table.stride()
+        local = len(table) == 3
+        device = block_table.get_device()
+        good = (
+            device >= 0 and block_table.dtype is _I32T and (table_stride[-1] == 1 or table[-1] == 1)
+            and (table[0] == shard_count if local else len(table) == 2) and table[-2] == B
+            and seq_lens.dtype is _I32T and seq_lens.get_device() == device and seq_lens.is_contiguous()
+            and query_start_loc.dtype is _I32T and query_start_loc.get_device() == device
+            and query_start_loc.shape == (B + 1,) and query_start_loc.is_contiguous()
+            and free_blocks.dtype is _I32T and free_blocks.get_device() == device and free_blocks.is_contiguous()
+            and free_count.dtype is _I32T and free_count.get_device() == device and free_count.numel() == 1
+            and free_left.dtype is _I32T and free_left.get_device() == device and free_left.numel() == 1
+            and positions.dtype is _I32T and positions.get_device() == device and positions.is_contiguous()
+            and slot_mapping.dtype is _I64T and slot_mapping.get_device() == device and slot_mapping.shape == (T,)
+            and slot_mapping.is_contiguous() and (dev_error is None or _flag_word(dev_error, device)))
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        B, T, local, device = _explain_extend(block_table, seq_lens, query_start_loc, free_blocks, free_count,
+                                              free_left, positions, slot_mapping, shard_count, dev_error)
+        num_free = free_blocks.shape[0]
+        table, table_stride = block_table.shape, block_table.stride()
+    call = (_lib or lib()).dcp_cache_extend
+    _launch("dcp_cache_extend", device, call,
+            block_table.data_ptr(), table[-1], table_stride[-2] if B > 1 else table[-1], 1 if local else 0,
+            table_stride[0] if local else 0, seq_lens.data_ptr(), query_start_loc.data_ptr(), B, T, block_size, D,
+            interleave, shard_begin, shard_count, free_blocks.data_ptr(), num_free, free_count.data_ptr(),
+            free_left.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(),
+            None if dev_error is None else dev_error.data_ptr(), _stream_of(stream, device))
+
+
+def _explain_extend(block_table, seq_lens, query_start_loc, free_blocks, free_count, free_left, positions,
+                    slot_mapping, shard_count, dev_error):
+    """What is wrong with a table extension's tensors, or (B, T, local, device)."""
+    i32 = torch.int32
+    args = [("block_table", block_table, i32, False), ("seq_lens", seq_lens, i32, True),
+            ("query_start_loc", query_start_loc, i32, True), ("free_blocks", free_blocks, i32, True),
+            ("free_count", free_count, i32, False), ("free_left", free_left, i32, False),
+            ("positions", positions, i32, True), ("slot_mapping", slot_mapping, torch.int64, True)]
+    if dev_error is not None:
+        args.append(("dev_error", dev_error, i32, False))
+    _types(args)
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    local = block_table.dim() == 3
+    if block_table.dim() not in (2, 3) or block_table.shape[-2] != B or \
+            (block_table.shape[-1] > 1 and block_table.stride(-1) != 1) or (local and block_table.shape[0] != shard_count):
+        raise ValueError("block_table must be [B, W] or [shard_count, B, W] with unit column stride")
+    if tuple(query_start_loc.shape) != (B + 1,):
+        raise ValueError("seq_lens [B] and query_start_loc [B + 1] disagree on B")
+    if free_blocks.dim() != 1 or free_count.numel() != 1 or free_left.numel() != 1:
+        raise ValueError("free_blocks must be [F], free_count and free_left [1]")
+    if positions.dim() != 1 or tuple(slot_mapping.shape) != tuple(positions.shape):
+        raise ValueError("positions and slot_mapping must be [T]")
+    if dev_error is not None and dev_error.numel() == 0:
+        raise ValueError("dev_error must not be empty")
+    return B, positions.shape[0], local, _placed(args)
+
+
+def dcp_norm_rope_cache(ql_nope, q_pe, q_out, kv_c, k_pe, norm_weight, positions, cos_sin, slot_mapping, kv_cache, *,
+                        eps: float = 1e-6, interleaved: bool = True, kv_scale: Optional[torch.Tensor] = None,
+                        dev_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Norm of the latents, rotation of the rope parts and the cache write in
+    one launch: kv_c bf16 [T, 512], k_pe bf16 [T, 64] (rows may be strided),
+    norm_weight bf16 [512] or None, positions int32 [T], cos_sin fp32
+    [max_pos, 64], slot_mapping int64 [T], kv_cache bf16 or FP8 with kv_scale.
+    With ql_nope bf16 [T, H, 512] and q_pe [T, H, 64] the decode query goes to
+    q_out [T, H, 576]; with q_pe alone its rotated form to q_out [T, H, 64]
+    (any token and head strides; q_out may be q_pe)."""
+    query, absorbed = q_pe is not None or q_out is not None or ql_nope is not None, ql_nope is not None
+    H, strides = 0, (0, 0, 0, 0, 0, 0)
+    try:
+        T, latent = kv_c.shape
+        blocks, block_size, row = kv_cache.shape
+        max_pos, angles = cos_sin.shape
+        c0, c1 = kv_c.stride()
+        p0, p1 = k_pe.stride()
+        device = kv_cache.get_device()
+        fp8 = kv_cache.dtype is _U8
+        good = (
+            device >= 0 and (fp8 or kv_cache.dtype is _BF16) and row == KV_DIM and kv_cache.is_contiguous()
+            and kv_c.dtype is _BF16 and kv_c.get_device() == device and latent == LATENT_DIM and c1 == 1
+            and k_pe.dtype is _BF16 and k_pe.get_device() == device and k_pe.shape == (T, ROPE_DIM) and p1 == 1
+            and slot_mapping.dtype is _I64T and slot_mapping.get_device() == device
+            and slot_mapping.shape == (T,) and slot_mapping.is_contiguous()
+            and positions.dtype is _I32T and positions.get_device() == device and positions.shape == (T,)
+            and positions.is_contiguous() and cos_sin.dtype is _F32 and cos_sin.get_device() == device
+            and angles == ROPE_DIM and cos_sin.is_contiguous()
+            and (norm_weight is None or (norm_weight.dtype is _BF16 and norm_weight.get_device() == device
+                                         and norm_weight.shape == (LATENT_DIM,) and norm_weight.is_contiguous()))
+            and (_rows_scaled(kv_scale, blocks, block_size, device) if fp8 else kv_scale is None)
+            and (dev_error is None or _flag_word(dev_error, device)))
+        if good and query:
+            _, H, _ = q_pe.shape
+            r0, r1, r2 = q_pe.stride()
+            o0, o1, o2 = q_out.stride()
+            n0 = n1 = 0
+            good = (
+                q_pe.dtype is _BF16 and q_pe.get_device() == device and q_pe.shape == (T, H, ROPE_DIM) and r2 == o2 == 1
+                and q_out.dtype is _BF16 and q_out.get_device() == device and H >= 1 and T > 0
+                and q_out.shape == (T, H, KV_DIM if absorbed else ROPE_DIM))
+            if good and absorbed:
+                n0, n1, n2 = ql_nope.stride()
+                good = (ql_nope.dtype is _BF16 and ql_nope.get_device() == device and n2 == 1
+                        and ql_nope.shape == (T, H, LATENT_DIM))
+            strides = (n0, n1, r0, r1, o0, o1)
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        T, H, fp8, device = _explain_norm_rope(ql_nope, q_pe, q_out, kv_c, k_pe, norm_weight, positions, cos_sin,
+                                               slot_mapping, kv_cache, kv_scale, dev_error)
+        if query:
+            strides = [t.stride(d) if t is not None else 0 for t in (ql_nope, q_pe, q_out) for d in (0, 1)]
+        c0, p0 = kv_c.stride(0), k_pe.stride(0)
+        blocks, block_size, _ = kv_cache.shape
+        max_pos = cos_sin.shape[0]
+    _fits32(max_pos, "dcp_norm_rope_cache")
+    if T == 0:
+        return
+    if T == 1:  # (the stride of a dimension of one element is never used)
+        c0 = p0 = 0
+    if query and (T == 1 or H == 1):
+        many, heads = int(T > 1), int(H > 1)
+        strides = [s * (heads if i % 2 else many) for i, s in enumerate(strides)]
+    call = (_lib or lib()).dcp_norm_rope_cache
+    _launch("dcp_norm_rope_cache", device, call,
+            ql_nope.data_ptr() if absorbed else None, strides[0], strides[1], q_pe.data_ptr() if query else None,
+            strides[2], strides[3], q_out.data_ptr() if query else None, strides[4], strides[5], kv_c.data_ptr(), c0,
+            k_pe.data_ptr(), p0, None if norm_weight is None else norm_weight.data_ptr(), eps, positions.data_ptr(),
+            cos_sin.data_ptr(), max_pos, 1 if interleaved else 0, slot_mapping.data_ptr(), T, H, kv_cache.data_ptr(),
+            KV_FP8_E4M3 if fp8 else KV_BF16, kv_scale.data_ptr() if fp8 else None, blocks * block_size,
+            None if dev_error is None else dev_error.data_ptr(), _stream_of(stream, device))
+
+
+def _explain_norm_rope(ql_nope, q_pe, q_out, kv_c, k_pe, norm_weight, positions, cos_sin, slot_mapping, kv_cache,
+                       kv_scale, dev_error):
+    """What is wrong with a norm and rotation's tensors, or (T, H, fp8, device)."""
+    bf16 = torch.bfloat16
+    fp8 = _cache_format(kv_cache, kv_scale)
+    args = [("kv_cache", kv_cache, kv_cache.dtype, True), ("kv_c", kv_c, bf16, False), ("k_pe", k_pe, bf16, False),
+            ("positions", positions, torch.int32, True), ("cos_sin", cos_sin, torch.float32, True),
+            ("slot_mapping", slot_mapping, torch.int64, True)]
+    rows = [("kv_c", kv_c, 2, LATENT_DIM), ("k_pe", k_pe, 2, ROPE_DIM)]
+    query = q_pe is not None or q_out is not None or ql_nope is not None
+    if query:
+        args += [("q_pe", q_pe, bf16, False), ("q_out", q_out, bf16, False)]
+        rows += [("q_pe", q_pe, 3, ROPE_DIM), ("q_out", q_out, 3, ROPE_DIM if ql_nope is None else KV_DIM)]
+        if ql_nope is not None:
+            args.append(("ql_nope", ql_nope, bf16, False))
+            rows.append(("ql_nope", ql_nope, 3, LATENT_DIM))
+    if norm_weight is not None:
+        args.append(("norm_weight", norm_weight, bf16, True))
+    if fp8:
+        args.append(("kv_scale", kv_scale, torch.float32, True))
+    if dev_error is not None:
+        args.append(("dev_error", dev_error, torch.int32, False))
+    _types(args)
+    for name, t, dims, last in rows:
+        if t.dim() != dims or t.shape[-1] != last or t.stride(-1) != 1:
+            raise ValueError("%s must have %d dims, last of size %d with unit stride" % (name, dims, last))
+    T = kv_c.shape[0]
+    H = q_pe.shape[1] if query else 0
+    if k_pe.shape[0] != T or tuple(positions.shape) != (T,) or tuple(slot_mapping.shape) != (T,):
+        raise ValueError("kv_c, k_pe, positions and slot_mapping disagree on T")
+    if query and (H < 1 or tuple(q_pe.shape[:2]) != (T, H) or tuple(q_out.shape[:2]) != (T, H) or
+                  (ql_nope is not None and tuple(ql_nope.shape[:2]) != (T, H))):
+        raise ValueError("ql_nope, q_pe and q_out must be [T, H, ..] with H >= 1")
+    if norm_weight is not None and tuple(norm_weight.shape) != (LATENT_DIM,):
+        raise ValueError("norm_weight must be [512]")
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != ROPE_DIM or cos_sin.shape[0] < 1:
+        raise ValueError("cos_sin must be [max_pos, 64]")
+    if dev_error is not None and dev_error.numel() == 0:
+        raise ValueError("dev_error must not be empty")
+    return T, H, fp8, _placed(args)
+
+
 # ----------------------------------------------------------------------------
 # allocating conveniences
 # ----------------------------------------------------------------------------
@@ -1061,3 +1257,45 @@ def decode_partial_tree(q, kv_cache, block_table, seq_lens, query_start_loc, tre
     return _decode_select_alloc(_TREE, tree_mask, q, kv_cache, block_table, seq_lens,
                                 query_start_loc, D, interleave, scale, window, num_sinks, max_seq_len, max_q_len,
                                 kv_scale, out_dtype, workspace, dev_error, stream)
+
+
+def cache_extend(block_table, seq_lens, query_start_loc, free_blocks, free_count, num_tokens: int, block_size: int,
+                 free_left: Optional[torch.Tensor] = None, D: int = 1, interleave: int = 1, shard_begin: int = 0,
+                 shard_count: Optional[int] = None, dev_error: Optional[torch.Tensor] = None, stream=None):
+    """Allocating form of dcp_cache_extend: extends block_table in place, writes
+    what is left of the free list into free_left (free_count itself by
+    default) and returns (positions int32, slot_mapping int64) of the step's
+    num_tokens rows."""
+    if stream is not None:  # (as in _decode_select_alloc)
+        with _stream_context(stream, block_table.device):
+            return cache_extend(block_table, seq_lens, query_start_loc, free_blocks, free_count, num_tokens,
+                                block_size, free_left=free_left, D=D, interleave=interleave, shard_begin=shard_begin,
+                                shard_count=shard_count, dev_error=dev_error)
+    positions = torch.empty(num_tokens, dtype=_I32T, device=block_table.device)
+    slots = torch.empty(num_tokens, dtype=_I64T, device=block_table.device)
+    dcp_cache_extend(block_table, seq_lens, query_start_loc, free_blocks, free_count,
+                     free_count if free_left is None else free_left, positions, slots, block_size=block_size, D=D,
+                     interleave=interleave, shard_begin=shard_begin, shard_count=shard_count, dev_error=dev_error)
+    return positions, slots
+
+
+def norm_rope_cache(kv_c, k_pe, slot_mapping, kv_cache, positions, cos_sin,
+                    norm_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                    ql_nope: Optional[torch.Tensor] = None, q_pe: Optional[torch.Tensor] = None,
+                    q_out: Optional[torch.Tensor] = None, interleaved: bool = True,
+                    kv_scale: Optional[torch.Tensor] = None, dev_error: Optional[torch.Tensor] = None, stream=None):
+    """Allocating form of dcp_norm_rope_cache: writes the normed and rotated
+    latent rows into kv_cache in place and returns the query: the decode's
+    [T, H, 576] with ql_nope and q_pe, the rotated rope parts [T, H, 64] with
+    q_pe alone (in q_out where it is given), None without."""
+    if stream is not None:  # (as in _decode_select_alloc)
+        with _stream_context(stream, kv_cache.device):
+            return norm_rope_cache(kv_c, k_pe, slot_mapping, kv_cache, positions, cos_sin, norm_weight=norm_weight,
+                                   eps=eps, ql_nope=ql_nope, q_pe=q_pe, q_out=q_out, interleaved=interleaved,
+                                   kv_scale=kv_scale, dev_error=dev_error)
+    if q_out is None and q_pe is not None:
+        q_out = torch.empty((q_pe.shape[0], q_pe.shape[1], ROPE_DIM if ql_nope is None else KV_DIM), dtype=_BF16,
+                            device=q_pe.device)
+    dcp_norm_rope_cache(ql_nope, q_pe, q_out, kv_c, k_pe, norm_weight, positions, cos_sin, slot_mapping, kv_cache,
+                        eps=eps, interleaved=interleaved, kv_scale=kv_scale, dev_error=dev_error)
+    return q_out

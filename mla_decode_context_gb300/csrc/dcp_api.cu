@@ -676,4 +676,94 @@ dcp_status_t dcp_latent_cache_read(const void* kv_cache, dcp_kv_dtype_t kv_dtype
   return dcp::launch_cache_read(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DCP_OK : DCP_ERR_CUDA;
 }
 
+dcp_status_t dcp_norm_rope_cache(const void* ql_nope, int64_t ql_nope_stride_tok, int64_t ql_nope_stride_head,
+                                 const void* q_pe, int64_t q_pe_stride_tok, int64_t q_pe_stride_head, void* q_out,
+                                 int64_t q_out_stride_tok, int64_t q_out_stride_head, const void* kv_c,
+                                 int64_t kv_c_stride_tok, const void* k_pe, int64_t k_pe_stride_tok,
+                                 const void* norm_weight, float eps, const int32_t* positions, const float* cos_sin,
+                                 int32_t max_pos, int32_t interleaved, const int64_t* slot_mapping, int32_t T,
+                                 int32_t H, void* kv_cache, dcp_kv_dtype_t kv_dtype, float* kv_scale,
+                                 int64_t num_slots, int32_t* dev_error, void* stream) {
+  if (T < 0 || H < 0 || num_slots < 1 || max_pos < 1) return DCP_ERR_INVALID_ARG;
+  if (kv_dtype != DCP_KV_BF16 && kv_dtype != DCP_KV_FP8_E4M3) return DCP_ERR_UNSUPPORTED_DTYPE;
+  if (T == 0) return DCP_OK;
+  const bool fp8 = kv_dtype == DCP_KV_FP8_E4M3, query = H > 0;
+  if (!kv_c || !k_pe || !slot_mapping || !kv_cache || !positions || !cos_sin || (fp8 && !kv_scale)) return DCP_ERR_INVALID_ARG;
+  if (query ? (!q_pe || !q_out) : (ql_nope || q_pe || q_out)) return DCP_ERR_INVALID_ARG;
+  if (norm_weight && !(eps >= 0.f && std::isfinite(eps))) return DCP_ERR_INVALID_ARG;
+  if (kv_c_stride_tok < 0 || k_pe_stride_tok < 0) return DCP_ERR_INVALID_ARG;
+  if (kv_c_stride_tok % 8 != 0 || k_pe_stride_tok % 8 != 0) return DCP_ERR_MISALIGNED;  // 16-byte units
+  if (!aligned16(kv_c) || !aligned16(k_pe) || !aligned16(kv_cache) || !aligned16(norm_weight) || !aligned16(cos_sin) ||
+      (fp8 && reinterpret_cast<uintptr_t>(kv_scale) % 4 != 0))
+    return DCP_ERR_MISALIGNED;
+  if (query) {
+    if (!ql_nope) ql_nope_stride_tok = ql_nope_stride_head = 0;
+    const int64_t width = ql_nope ? DCP_KV_DIM : DCP_ROPE_DIM;
+    if (ql_nope_stride_tok < 0 || ql_nope_stride_head < 0 || q_pe_stride_tok < 0 || q_pe_stride_head < 0 ||
+        (H > 1 && q_out_stride_head < width) || (T > 1 && q_out_stride_tok < width))
+      return DCP_ERR_INVALID_ARG;
+    // one (token, head)'s output must not be another's: heads within tokens, or tokens within heads
+    if (T > 1 && H > 1 && q_out_stride_tok < (H - 1) * q_out_stride_head + width &&
+        q_out_stride_head < (T - 1) * q_out_stride_tok + width)
+      return DCP_ERR_INVALID_ARG;
+    const int64_t strides[] = {ql_nope_stride_tok, ql_nope_stride_head, q_pe_stride_tok, q_pe_stride_head,
+                               q_out_stride_tok, q_out_stride_head};
+    for (int64_t st : strides)
+      if (st % 8 != 0) return DCP_ERR_MISALIGNED;
+    if (!aligned16(ql_nope) || !aligned16(q_pe) || !aligned16(q_out)) return DCP_ERR_MISALIGNED;
+  }
+  dcp::NormRopeArgs a{};
+  a.ql_nope = static_cast<const __nv_bfloat16*>(ql_nope);
+  a.ql_nope_stride_tok = ql_nope_stride_tok; a.ql_nope_stride_head = ql_nope_stride_head;
+  a.q_pe = static_cast<const __nv_bfloat16*>(q_pe);
+  a.q_pe_stride_tok = q_pe_stride_tok; a.q_pe_stride_head = q_pe_stride_head;
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.q_out_stride_tok = q_out_stride_tok; a.q_out_stride_head = q_out_stride_head;
+  a.kv_c = static_cast<const __nv_bfloat16*>(kv_c); a.kv_c_stride_tok = kv_c_stride_tok;
+  a.k_pe = static_cast<const __nv_bfloat16*>(k_pe); a.k_pe_stride_tok = k_pe_stride_tok;
+  a.norm_weight = static_cast<const __nv_bfloat16*>(norm_weight);
+  a.eps = eps;
+  a.positions = positions; a.cos_sin = cos_sin; a.max_pos = max_pos; a.pairs = interleaved != 0;
+  a.slot_mapping = slot_mapping;
+  a.T = T; a.H = H;
+  a.kv_cache = kv_cache; a.kv_scale = fp8 ? kv_scale : nullptr; a.num_slots = num_slots;
+  a.dev_error = dev_error;
+  return dcp::launch_norm_rope(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DCP_OK : DCP_ERR_CUDA;
+}
+
+dcp_status_t dcp_cache_extend(int32_t* block_table, int32_t bt_width, int64_t bt_stride, int32_t per_shard_tables,
+                              int64_t bt_shard_stride, const int32_t* seq_lens, const int32_t* query_start_loc,
+                              int32_t B, int32_t T, int32_t block_size, int32_t D, int32_t interleave,
+                              int32_t shard_begin, int32_t shard_count, const int32_t* free_blocks, int32_t num_free,
+                              const int32_t* free_count, int32_t* free_left, int32_t* positions,
+                              int64_t* slot_mapping, int32_t* dev_error, void* stream) {
+  if (B < 0 || T < 0 || D < 1 || D > DCP_MAX_SHARDS || interleave < 1 || block_size < 1 || num_free < 0)
+    return DCP_ERR_INVALID_ARG;
+  if (shard_begin < 0 || shard_count < 1 || shard_begin + static_cast<int64_t>(shard_count) > D) return DCP_ERR_INVALID_ARG;
+  if (!free_count || !free_left || (num_free > 0 && !free_blocks)) return DCP_ERR_INVALID_ARG;
+  if (T > 0 && (!positions || !slot_mapping)) return DCP_ERR_INVALID_ARG;
+  if (B > 0) {
+    if (!block_table || !seq_lens || !query_start_loc || bt_width < 1 || bt_width > (1 << 20) || bt_stride < bt_width)
+      return DCP_ERR_INVALID_ARG;
+    if (per_shard_tables && shard_count > 1 && bt_shard_stride < static_cast<int64_t>(B - 1) * bt_stride + bt_width)
+      return DCP_ERR_INVALID_ARG;  // shards' tables would overlap
+  }
+  dcp::CacheExtendArgs a{};
+  a.block_table = block_table; a.bt_width = bt_width; a.bt_stride = bt_stride;
+  a.local_tables = per_shard_tables ? 1 : 0;
+  a.bt_shard_stride = per_shard_tables ? bt_shard_stride : 0;
+  a.seq_lens = seq_lens; a.qsl = query_start_loc; a.B = B; a.T = T; a.block_size = block_size;
+  a.D = D; a.I = interleave; a.d0 = shard_begin; a.Dn = shard_count;
+  a.S = a.local_tables ? shard_count : 1;
+  a.period = static_cast<int64_t>(D) * interleave;
+  if (a.period <= 0x7fffffff) a.div_period = dcp::make_fastdiv(static_cast<int32_t>(a.period));
+  a.div_I = dcp::make_fastdiv(interleave);
+  a.div_D = dcp::make_fastdiv(D);
+  a.div_bs = dcp::make_fastdiv(block_size);
+  a.free_blocks = free_blocks; a.num_free = num_free; a.free_count = free_count; a.free_left = free_left;
+  a.positions = positions; a.slot_mapping = slot_mapping;
+  a.dev_error = dev_error;
+  return dcp::launch_cache_extend(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DCP_OK : DCP_ERR_CUDA;
+}
+
 }  // extern "C"

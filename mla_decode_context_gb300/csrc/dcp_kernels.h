@@ -181,6 +181,59 @@ struct CacheReadArgs {
 };
 cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t st);
 
+// Norm, rotation, query concat and cache write (validated by the C ABI;
+// strides in elements, whole 16-byte units).
+struct NormRopeArgs {
+  const __nv_bfloat16* ql_nope;  // [T, H, 512], or nullptr: the queries' rope parts alone
+  int64_t ql_nope_stride_tok, ql_nope_stride_head;
+  const __nv_bfloat16* q_pe;     // [T, H, 64]
+  int64_t q_pe_stride_tok, q_pe_stride_head;
+  __nv_bfloat16* q_out;          // [T, H, 576], or [T, H, 64] without ql_nope
+  int64_t q_out_stride_tok, q_out_stride_head;
+  const __nv_bfloat16* kv_c;     // [T, 512]
+  int64_t kv_c_stride_tok;
+  const __nv_bfloat16* k_pe;     // [T, 64]
+  int64_t k_pe_stride_tok;
+  const __nv_bfloat16* norm_weight;  // [512], or nullptr: kv_c as it is
+  float eps;
+  const int32_t* positions;      // [T]
+  const float* cos_sin;          // [max_pos, 64]
+  int32_t max_pos;
+  int32_t pairs;                 // pairs (2 i, 2 i + 1); else (i, i + 32)
+  const int64_t* slot_mapping;   // [T]
+  int32_t T, H;                  // H 0: no query
+  void* kv_cache;
+  float* kv_scale;               // FP8 cache, else nullptr
+  int64_t num_slots;
+  int32_t* dev_error;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t st);
+
+// Block tables and slot maps of a step (validated by the C ABI).
+struct CacheExtendArgs {
+  int32_t* block_table;
+  int32_t bt_width;
+  int64_t bt_stride;
+  int32_t local_tables;
+  int64_t bt_shard_stride;
+  const int32_t* seq_lens;
+  const int32_t* qsl;
+  int32_t B, T, block_size;
+  int32_t D, I, d0, Dn;
+  int32_t S;              // tables per request: Dn, or 1
+  int64_t period;         // D * I
+  FastDiv div_period;     // d = 0: the period is 2^31 or more
+  FastDiv div_I, div_D, div_bs;
+  const int32_t* free_blocks;
+  int32_t num_free;
+  const int32_t* free_count;
+  int32_t* free_left;
+  int32_t* positions;     // [T]
+  int64_t* slot_mapping;  // [T]
+  int32_t* dev_error;
+};
+cudaError_t launch_cache_extend(const CacheExtendArgs& a, cudaStream_t st);
+
 // Tensor-core decode (tcgen05/TMEM/TMA, 2-CTA clusters).  Supported when
 // H <= 128 and the shard layout tiles into whole TMA boxes: block_size a
 // multiple of D * interleave (runs inside blocks) or interleave a multiple
