@@ -69,6 +69,8 @@ extern "C" {
 #define DCP_KV_DIM 576
 #define DCP_MAX_SHARDS 32
 #define DCP_MAX_TREE_ROWS 256 /* rows of a request under a tree mask */
+#define DCP_NOPE_DIM 128      /* a head's key dims projected up from the latent (chunk attention) */
+#define DCP_VALUE_DIM 128     /* and its value dims */
 
 /* Device-side error bits ORed into *dev_error. */
 #define DCP_DEVERR_BAD_BLOCK 1    /* a referenced block id is outside [0, num_blocks) */
@@ -649,6 +651,77 @@ dcp_status_t dcp_norm_rope_cache(
     const int64_t* slot_mapping, int32_t T, int32_t H,
     void* kv_cache, dcp_kv_dtype_t kv_dtype, float* kv_scale, int64_t num_slots,
     int32_t* dev_error, void* stream);
+
+/*
+ * The up projection's weight in the order in which dcp_mla_chunk_attention
+ * reads it, laid out once per layer.
+ *   w_kv_b  bf16 [H * 256, 512], a head's 128 key rows before its 128 value rows.
+ *   packed  the same number of bytes; must not overlap w_kv_b.
+ */
+dcp_status_t dcp_pack_kv_b(const void* w_kv_b, int32_t H, void* packed, void* stream);
+
+/*
+ * Causal attention of chunks of new tokens over the paged latent cache (a
+ * prefill over a cached prefix, a prompt's chunks, decoding rows among them),
+ * with each head's own keys and values projected up from the latents (the
+ * pages' prefill side; the decodes work on the latents themselves and return
+ * 512 latent dims).
+ *
+ * Row i of request b sees L = max(0, seq_lens[b] - (q_len - 1 - i)) tokens, as
+ * in dcp_mla_decode_partial (the new tokens are already in the cache):
+ *   k_h(p) = [W_h[0:128] c(p) | kv(p)[512:576]],  v_h(p) = W_h[128:256] c(p),
+ *   c(p) = kv(p)[0:512],  s_p = scale * sum_{k<192} q[r,h,k] * k_h(p)[k]
+ *   lse[r,h] = ln sum_{p<L} exp(s_p),  out[r,h,:] = sum_{p<L} exp(s_p - lse[r,h]) v_h(p)
+ * A row with nothing to see, of no request or of a request of no tokens: 0 and
+ * -inf.  Whole contexts: per-shard tables hold all D shards.
+ *
+ *   q            bf16 [T, H, 192], 128 dims for W_h's keys, then 64 rope dims
+ *                (rotated, dcp_norm_rope_cache); token and head strides in
+ *                multiples of 8 elements.
+ *   kv_cache .. query_start_loc, B, T, scale
+ *                as for dcp_mla_decode_partial_v2 (D and interleave matter for
+ *                per-shard tables only).  A token without a table column or with
+ *                a block id outside the cache is skipped (DCP_DEVERR_BAD_BLOCK).
+ *   H            1 .. 1024.
+ *   total_len    host-known bound of the sum of seq_lens (sizes the workspace).
+ *                Requests past it see nothing (DCP_DEVERR_SEQ_TOO_LONG).
+ *   packed_kv_b  from dcp_pack_kv_b.
+ *   out          bf16 (round to nearest even) or fp32 [T, H, 128], dense,
+ *                16-byte aligned; lse fp32 [T, H].
+ *   workspace    16-byte aligned; its contents on entry are ignored.
+ *                dcp_chunk_attention_workspace_size(...) bytes for the fewest
+ *                passes over the heads (4 GiB at most, or what one head takes);
+ *                with less, down to one head's part, more passes are made.
+ *                Calls that may overlap need one each.
+ *
+ * Numbers: keys and values are rounded to bf16 once and the softmax weights
+ * (relative to a running maximum) once, everything else is fp32.  An FP8 code
+ * times a scale that is no power of two is rounded to bf16 too.  A NaN score,
+ * or a value with an element that is not finite, makes the rows that see its
+ * token NaN, and no others.
+ *
+ * Cost: 640 operations per row, token and head and 262,144 per token and head,
+ * against 2,176 per row, token and head of the decodes: below ~170 rows of a
+ * request a decode with absorbed queries does less work.
+ */
+dcp_status_t dcp_mla_chunk_attention(
+    const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+    const void* kv_cache, dcp_kv_dtype_t kv_dtype, const float* kv_scale,
+    int32_t num_blocks, int32_t block_size,
+    const int32_t* block_table, int32_t bt_width, int64_t bt_stride,
+    int32_t per_shard_tables, int64_t bt_shard_stride, int32_t D, int32_t interleave,
+    const int32_t* seq_lens, const int32_t* query_start_loc,
+    int32_t B, int32_t T, int32_t H, int64_t total_len, float scale,
+    const void* packed_kv_b,
+    void* out, dcp_dtype_t out_dtype, float* lse,
+    void* workspace, size_t workspace_bytes,
+    int32_t* dev_error, void* stream);
+
+/*
+ * Bytes of workspace for dcp_mla_chunk_attention; (size_t)-1 on invalid
+ * arguments.
+ */
+size_t dcp_chunk_attention_workspace_size(int32_t B, int32_t T, int32_t H, int64_t total_len);
 
 #ifdef __cplusplus
 }

@@ -24,6 +24,8 @@ ROPE_DIM = 64
 KV_DIM = 576
 MAX_SHARDS = 32
 MAX_TREE_ROWS = 256
+NOPE_DIM = 128
+VALUE_DIM = 128
 
 DEVERR_BAD_BLOCK = 1
 DEVERR_SEQ_TOO_LONG = 2
@@ -91,6 +93,11 @@ EXPORTS = [
     ("dcp_norm_rope_cache", ctypes.c_int,
      [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _F, _P, _P, _I32, _I32, _P, _I32, _I32,
       _P, ctypes.c_int, _P, _I64, _P, _P]),
+    ("dcp_pack_kv_b", ctypes.c_int, [_P, _I32, _P, _P]),
+    ("dcp_mla_chunk_attention", ctypes.c_int,
+     [_P, _I64, _I64, _P, ctypes.c_int, _P, _I32, _I32, _P, _I32, _I64, _I32, _I64, _I32, _I32, _P, _P, _I32, _I32,
+      _I32, _I64, _F, _P, _P, ctypes.c_int, _P, _P, _SZ, _P, _P]),
+    ("dcp_chunk_attention_workspace_size", _SZ, [_I32, _I32, _I32, _I64]),
 ]
 
 _lib = None
@@ -1089,6 +1096,122 @@ def _explain_norm_rope(ql_nope, q_pe, q_out, kv_c, k_pe, norm_weight, positions,
     return T, H, fp8, _placed(args)
 
 
+def dcp_pack_kv_b(w_kv_b, packed, *, stream=None) -> None:
+    """Lay out the up projection's weight bf16 [H * 256, 512] (a head's 128 key
+    rows before its 128 value rows) for chunk attention: packed bf16
+    [H, 8, 256, 64]."""
+    _types([("w_kv_b", w_kv_b, torch.bfloat16, True), ("packed", packed, torch.bfloat16, True)])
+    if w_kv_b.dim() != 2 or w_kv_b.shape[1] != LATENT_DIM or w_kv_b.shape[0] % (NOPE_DIM + VALUE_DIM) or not w_kv_b.shape[0]:
+        raise ValueError("w_kv_b must be [H * 256, 512]")
+    H = w_kv_b.shape[0] // (NOPE_DIM + VALUE_DIM)
+    if tuple(packed.shape) != (H, 8, NOPE_DIM + VALUE_DIM, 64):
+        raise ValueError("packed must be [H, 8, 256, 64]")
+    device = _placed([("w_kv_b", w_kv_b, torch.bfloat16, True), ("packed", packed, torch.bfloat16, True)])
+    _launch("dcp_pack_kv_b", device, lib().dcp_pack_kv_b, w_kv_b.data_ptr(), H, packed.data_ptr(),
+            _stream_of(stream, device))
+
+
+def dcp_chunk_attention_workspace_size(B: int, T: int, H: int, total_len: int) -> int:
+    _fits32(B | T | H, "dcp_chunk_attention_workspace_size")
+    n = (_lib or lib()).dcp_chunk_attention_workspace_size(B, T, H, min(max(total_len, -1), 1 << 62))
+    if n == ctypes.c_size_t(-1).value:
+        raise DCPError(1, "dcp_chunk_attention_workspace_size")
+    return n
+
+
+def dcp_mla_chunk_attention(q, kv_cache, block_table, seq_lens, query_start_loc, packed_kv_b, out, lse, workspace, *,
+                            scale: float, total_len: int, kv_scale: Optional[torch.Tensor] = None, D: int = 1,
+                            interleave: int = 1, dev_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Causal attention of chunks of new tokens over the paged latent cache:
+    q bf16 [T, H, 192] (any token and head strides), kv_cache bf16 or FP8 with
+    kv_scale, block_table int32 [B, W] or per-shard [D, B, W], packed_kv_b from
+    dcp_pack_kv_b; writes out bf16 or fp32 [T, H, 128] and lse fp32 [T, H].
+    total_len bounds the sum of seq_lens; workspace has
+    dcp_chunk_attention_workspace_size bytes (fewer: more passes)."""
+    _fits32(D | interleave, "dcp_mla_chunk_attention")
+    try:
+        T, H, dim = q.shape
+        blocks, block_size, row = kv_cache.shape
+        B, = seq_lens.shape
+        q0, q1, q2 = q.stride()
+        table, table_stride = block_table.shape, block_table.stride()
+        local = len(table) == 3
+        device = q.get_device()
+        o_dtype, fp8 = out.dtype, kv_cache.dtype is _U8
+        good = (
+            q.dtype is _BF16 and dim == NOPE_DIM + ROPE_DIM and q2 == 1 and device >= 0
+            and (fp8 or kv_cache.dtype is _BF16) and row == KV_DIM and kv_cache.get_device() == device
+            and kv_cache.is_contiguous()
+            and block_table.dtype is _I32T and block_table.get_device() == device and table_stride[-1] == 1
+            and (table[0] == D if local else len(table) == 2) and table[-2] == B
+            and seq_lens.dtype is _I32T and seq_lens.get_device() == device and seq_lens.is_contiguous()
+            and query_start_loc.dtype is _I32T and query_start_loc.get_device() == device
+            and query_start_loc.shape == (B + 1,) and query_start_loc.is_contiguous()
+            and packed_kv_b.dtype is _BF16 and packed_kv_b.get_device() == device and packed_kv_b.is_contiguous()
+            and packed_kv_b.shape == (H, 8, NOPE_DIM + VALUE_DIM, 64)
+            and (o_dtype is _BF16 or o_dtype is _F32) and out.get_device() == device and out.is_contiguous()
+            and out.shape == (T, H, VALUE_DIM)
+            and lse.dtype is _F32 and lse.get_device() == device and lse.is_contiguous() and lse.shape == (T, H)
+            and (_rows_scaled(kv_scale, blocks, block_size, device) if fp8 else kv_scale is None)
+            and (workspace is None or (workspace.get_device() == device and workspace.is_contiguous()))
+            and (dev_error is None or _flag_word(dev_error, device)))
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        T, H, B, local, fp8, device = _explain_chunk(q, kv_cache, block_table, seq_lens, query_start_loc, packed_kv_b,
+                                                     out, lse, workspace, kv_scale, D, dev_error)
+        q0, q1, o_dtype = q.stride(0), q.stride(1), out.dtype
+        blocks, block_size, _ = kv_cache.shape
+        table, table_stride = block_table.shape, block_table.stride()
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    call = (_lib or lib()).dcp_mla_chunk_attention
+    _launch("dcp_mla_chunk_attention", device, call,
+            q.data_ptr(), q0 if T > 1 else 0, q1 if H > 1 else 0, kv_cache.data_ptr(),
+            KV_FP8_E4M3 if fp8 else KV_BF16, kv_scale.data_ptr() if fp8 else None, blocks, block_size,
+            block_table.data_ptr(), table[-1], table_stride[-2] if B > 1 else table[-1], 1 if local else 0,
+            table_stride[0] if local else 0, D, interleave, seq_lens.data_ptr(), query_start_loc.data_ptr(), B, T, H,
+            min(max(total_len, -1), 1 << 62), scale, packed_kv_b.data_ptr(), out.data_ptr(),
+            DTYPE_BF16 if o_dtype is _BF16 else DTYPE_F32, lse.data_ptr(),
+            workspace.data_ptr() if ws_bytes else None, ws_bytes,
+            None if dev_error is None else dev_error.data_ptr(), _stream_of(stream, device))
+
+
+def _explain_chunk(q, kv_cache, block_table, seq_lens, query_start_loc, packed_kv_b, out, lse, workspace, kv_scale, D,
+                   dev_error):
+    """What is wrong with a chunk attention's tensors, or (T, H, B, local, fp8, device)."""
+    if not isinstance(out, torch.Tensor) or out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out must be a bfloat16 or float32 tensor")
+    fp8 = _cache_format(kv_cache, kv_scale)
+    i32, bf16 = torch.int32, torch.bfloat16
+    args = [("kv_cache", kv_cache, kv_cache.dtype, True), ("q", q, bf16, False),
+            ("block_table", block_table, i32, False), ("seq_lens", seq_lens, i32, True),
+            ("query_start_loc", query_start_loc, i32, True), ("packed_kv_b", packed_kv_b, bf16, True),
+            ("out", out, out.dtype, True), ("lse", lse, torch.float32, True)]
+    if fp8:
+        args.append(("kv_scale", kv_scale, torch.float32, True))
+    if workspace is not None:
+        args.append(("workspace", workspace, getattr(workspace, "dtype", None), True))
+    if dev_error is not None:
+        args.append(("dev_error", dev_error, i32, False))
+    _types(args)
+    if q.dim() != 3 or q.shape[2] != NOPE_DIM + ROPE_DIM or q.stride(2) != 1:
+        raise ValueError("q must be [T, H, 192] with unit stride in the last dim")
+    T, H = q.shape[0], q.shape[1]
+    local = block_table.dim() == 3
+    if block_table.dim() not in (2, 3) or block_table.stride(-1) != 1 or (local and block_table.shape[0] != D):
+        raise ValueError("block_table must be [B, W] or [D, B, W] with unit column stride")
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    if tuple(query_start_loc.shape) != (B + 1,) or block_table.shape[-2] != B:
+        raise ValueError("seq_lens [B], query_start_loc [B + 1] and block_table [.., B, W] disagree on B")
+    if tuple(packed_kv_b.shape) != (H, 8, NOPE_DIM + VALUE_DIM, 64):
+        raise ValueError("packed_kv_b must be [H, 8, 256, 64] (see pack_kv_b)")
+    if tuple(out.shape) != (T, H, VALUE_DIM) or tuple(lse.shape) != (T, H):
+        raise ValueError("out must be [T, H, 128] and lse [T, H]")
+    if dev_error is not None and dev_error.numel() == 0:
+        raise ValueError("dev_error must not be empty")
+    return T, H, B, local, fp8, _placed(args)
+
+
 # ----------------------------------------------------------------------------
 # allocating conveniences
 # ----------------------------------------------------------------------------
@@ -1299,3 +1422,40 @@ def norm_rope_cache(kv_c, k_pe, slot_mapping, kv_cache, positions, cos_sin,
     dcp_norm_rope_cache(ql_nope, q_pe, q_out, kv_c, k_pe, norm_weight, positions, cos_sin, slot_mapping, kv_cache,
                         eps=eps, interleaved=interleaved, kv_scale=kv_scale, dev_error=dev_error)
     return q_out
+
+
+def pack_kv_b(w_kv_b, num_heads: Optional[int] = None, stream=None):
+    """Allocating form of dcp_pack_kv_b: the up projection's weight bf16
+    [H * 256, 512] as chunk_attention takes it, laid out once per layer."""
+    if stream is not None:  # (as in _decode_select_alloc)
+        with _stream_context(stream, w_kv_b.device):
+            return pack_kv_b(w_kv_b, num_heads)
+    H = w_kv_b.shape[0] // (NOPE_DIM + VALUE_DIM)
+    if num_heads is not None and num_heads * (NOPE_DIM + VALUE_DIM) != w_kv_b.shape[0]:
+        raise ValueError("w_kv_b has %d rows, not 256 for each of %d heads" % (w_kv_b.shape[0], num_heads))
+    packed = torch.empty((H, 8, NOPE_DIM + VALUE_DIM, 64), dtype=torch.bfloat16, device=w_kv_b.device)
+    dcp_pack_kv_b(w_kv_b, packed)
+    return packed
+
+
+def chunk_attention(q, kv_cache, block_table, seq_lens, query_start_loc, packed_kv_b, scale: float, total_len: int,
+                    kv_scale: Optional[torch.Tensor] = None, D: int = 1, interleave: int = 1,
+                    out_dtype=torch.bfloat16, workspace: Optional[torch.Tensor] = None,
+                    dev_error: Optional[torch.Tensor] = None, stream=None):
+    """Allocating form of dcp_mla_chunk_attention: returns (out [T, H, 128] of
+    out_dtype, lse fp32 [T, H])."""
+    if stream is not None:  # (as in _decode_select_alloc)
+        with _stream_context(stream, q.device):
+            return chunk_attention(q, kv_cache, block_table, seq_lens, query_start_loc, packed_kv_b, scale, total_len,
+                                   kv_scale=kv_scale, D=D, interleave=interleave, out_dtype=out_dtype,
+                                   workspace=workspace, dev_error=dev_error)
+    T, H = q.shape[0], q.shape[1]
+    out = torch.empty((T, H, VALUE_DIM), dtype=out_dtype, device=q.device)
+    lse = torch.empty((T, H), dtype=_F32, device=q.device)
+    if workspace is None:
+        n = dcp_chunk_attention_workspace_size(seq_lens.shape[0], T, H, total_len)
+        workspace = torch.empty(n, dtype=_U8, device=q.device) if n else None
+    dcp_mla_chunk_attention(q, kv_cache, block_table, seq_lens, query_start_loc, packed_kv_b, out, lse, workspace,
+                            scale=scale, total_len=total_len, kv_scale=kv_scale, D=D, interleave=interleave,
+                            dev_error=dev_error)
+    return out, lse

@@ -1,5 +1,6 @@
 // C ABI of the DCP MLA hot path: host-side validation, the split-KV plan and
 // kernel launches.  No allocation, no synchronisation, no global state.
+#include "dcp_chunk.cuh"
 #include "dcp_kernels.h"
 
 #include <algorithm>
@@ -764,6 +765,125 @@ dcp_status_t dcp_cache_extend(int32_t* block_table, int32_t bt_width, int64_t bt
   a.positions = positions; a.slot_mapping = slot_mapping;
   a.dev_error = dev_error;
   return dcp::launch_cache_extend(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DCP_OK : DCP_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Workspace of chunk attention: requests' first images and units, the heads'
+// shared parts (token masks and rope images), then keys, values and masks of as
+// many heads as there is room for.
+struct ChunkPlan {
+  int64_t tiles, units;
+  size_t starts, valid, rope, per_head;  // offsets of the parts, bytes of a head's
+  size_t fixed;                          // bytes of all but the heads'
+};
+constexpr size_t kChunkRecommended = size_t{4} << 30;
+
+size_t round256(size_t n) { return (n + 255) & ~size_t{255}; }
+
+bool chunk_plan(int32_t B, int32_t T, int32_t H, int64_t total_len, ChunkPlan* p) {
+  if (B < 0 || T < 0 || H < 1 || H > 1024 || total_len < 0 || total_len > (int64_t{1} << 36)) return false;
+  p->tiles = total_len / dcp::kChunkTile + B;
+  p->units = T / dcp::kChunkRows + static_cast<int64_t>(B) + 2;
+  if (p->tiles * H > 0x7fffffff || p->units * H > 0x7fffffff) return false;
+  const size_t n = static_cast<size_t>(p->tiles);
+  p->starts = 0;
+  p->valid = round256(2 * (static_cast<size_t>(B) + 1) * 4);
+  p->rope = round256(p->valid + n * 16);
+  p->fixed = p->rope + n * dcp::kImage;
+  p->per_head = n * (4 * dcp::kImage + 16);
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dcp_chunk_attention_workspace_size(int32_t B, int32_t T, int32_t H, int64_t total_len) {
+  ChunkPlan p{};
+  if (!chunk_plan(B, T, H, total_len, &p)) return static_cast<size_t>(-1);
+  if (B == 0 || T == 0) return 0;
+  size_t heads = p.per_head > 0 ? kChunkRecommended / p.per_head : 1;
+  heads = heads < 1 ? 1 : (heads > static_cast<size_t>(H) ? static_cast<size_t>(H) : heads);
+  return p.fixed + heads * p.per_head;
+}
+
+dcp_status_t dcp_pack_kv_b(const void* w_kv_b, int32_t H, void* packed, void* stream) {
+  if (H < 1 || H > 1024 || !w_kv_b || !packed) return DCP_ERR_INVALID_ARG;
+  if (!aligned16(w_kv_b) || !aligned16(packed)) return DCP_ERR_MISALIGNED;
+  return dcp::launch_pack_kv_b(w_kv_b, H, packed, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DCP_OK : DCP_ERR_CUDA;
+}
+
+dcp_status_t dcp_mla_chunk_attention(const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+                                     const void* kv_cache, dcp_kv_dtype_t kv_dtype, const float* kv_scale,
+                                     int32_t num_blocks, int32_t block_size, const int32_t* block_table,
+                                     int32_t bt_width, int64_t bt_stride, int32_t per_shard_tables,
+                                     int64_t bt_shard_stride, int32_t D, int32_t interleave, const int32_t* seq_lens,
+                                     const int32_t* query_start_loc, int32_t B, int32_t T, int32_t H,
+                                     int64_t total_len, float scale, const void* packed_kv_b, void* out,
+                                     dcp_dtype_t out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                                     int32_t* dev_error, void* stream) {
+  ChunkPlan p{};
+  if (!chunk_plan(B, T, H, total_len, &p) || D < 1 || D > DCP_MAX_SHARDS || interleave < 1 || !std::isfinite(scale))
+    return DCP_ERR_INVALID_ARG;
+  if ((kv_dtype != DCP_KV_BF16 && kv_dtype != DCP_KV_FP8_E4M3) ||
+      (out_dtype != DCP_DTYPE_F32 && out_dtype != DCP_DTYPE_BF16))
+    return DCP_ERR_UNSUPPORTED_DTYPE;
+  if (B == 0 || T == 0) return DCP_OK;
+  const bool fp8 = kv_dtype == DCP_KV_FP8_E4M3;
+  if (!q || !kv_cache || !block_table || !seq_lens || !query_start_loc || !packed_kv_b || !out || !lse || (fp8 && !kv_scale))
+    return DCP_ERR_INVALID_ARG;
+  if (num_blocks < 1 || block_size < 1 || bt_width < 1 || bt_stride < bt_width || q_stride_tok < 0 || q_stride_head < 0)
+    return DCP_ERR_INVALID_ARG;
+  if (per_shard_tables && D > 1 && bt_shard_stride < static_cast<int64_t>(B - 1) * bt_stride + bt_width)
+    return DCP_ERR_INVALID_ARG;  // shards' tables would overlap
+  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(packed_kv_b) || !aligned16(out) || !aligned16(workspace) ||
+      q_stride_tok % 8 != 0 || q_stride_head % 8 != 0)
+    return DCP_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < p.fixed + p.per_head) return DCP_ERR_WORKSPACE_TOO_SMALL;
+  // heads per pass: as many as fit, in passes of nearly equal size
+  const size_t fit = (workspace_bytes - p.fixed) / p.per_head;
+  int32_t heads = fit < static_cast<size_t>(H) ? static_cast<int32_t>(fit) : H;
+  const int32_t passes = (H + heads - 1) / heads;
+  heads = (H + passes - 1) / passes;
+  dcp::ChunkArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_stride_tok = q_stride_tok; a.q_stride_head = q_stride_head;
+  a.kv = kv_cache; a.kv_scale = fp8 ? kv_scale : nullptr;
+  a.num_blocks = num_blocks; a.block_size = block_size;
+  a.block_table = block_table; a.bt_width = bt_width; a.bt_stride = bt_stride;
+  a.local_tables = per_shard_tables ? 1 : 0;
+  a.bt_shard_stride = per_shard_tables ? bt_shard_stride : 0;
+  a.D = D; a.I = interleave;
+  a.div_I = dcp::make_fastdiv(interleave);
+  a.div_D = dcp::make_fastdiv(D);
+  a.div_bs = dcp::make_fastdiv(block_size);
+  a.seq_lens = seq_lens; a.qsl = query_start_loc; a.B = B; a.T = T; a.H = H;
+  // (a scale of 0 as a positive one that makes every score 0: 0 x -inf would be NaN)
+  a.scale_log2 = scale == 0.f ? 0x1p-120f : std::fabs(scale) * dcp::kLog2e;
+  a.q_sign = scale < 0.f ? 0x80008000u : 0u;
+  a.weight = packed_kv_b;
+  a.out = out; a.out_f32 = out_dtype == DCP_DTYPE_F32; a.lse = lse;
+  a.dev_error = dev_error;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.tiles = static_cast<int32_t>(p.tiles);
+  a.tile_start = reinterpret_cast<int32_t*>(ws + p.starts);
+  a.block_start = a.tile_start + B + 1;
+  a.valid = reinterpret_cast<uint4*>(ws + p.valid);
+  a.rope = ws + p.rope;
+  a.keys = ws + p.fixed;
+  a.values = a.keys + static_cast<size_t>(heads) * p.tiles * (2 * dcp::kImage);
+  a.bad = reinterpret_cast<uint4*>(a.values + static_cast<size_t>(heads) * p.tiles * (2 * dcp::kImage));
+  a.units = static_cast<int32_t>(p.units);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dcp::launch_chunk_plan(a, st) != cudaSuccess) return DCP_ERR_CUDA;
+  for (a.h0 = 0; a.h0 < H; a.h0 += heads) {
+    a.heads = std::min(heads, H - a.h0);
+    if (dcp::launch_chunk_expand(a, st) != cudaSuccess || dcp::launch_chunk_attention(a, st) != cudaSuccess) return DCP_ERR_CUDA;
+  }
+  return DCP_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,485 @@
+// Chunk attention, second half: causal attention of a chunk's query rows over
+// the keys and values that dcp_chunk_expand.cu left as tile images.
+//
+//   s = scale (q_nope . k_h(p) + q_rope . k_pe(p)),  p < L_r = seq - (q_len - 1 - i)
+//   out = sum_p exp(s - lse) v_h(p),  lse = ln sum_p exp(s)
+//
+// 2 x (192 + 128) operations per (row, token, head): bound by the tensor pipe.
+// Unit: 256 rows of one request at one head, as two MMA tiles of 128 rows that
+// share each tile of 128 keys and values in shared memory and take turns on the
+// tensor pipe: while one's scores go through the softmax, the other's products
+// run.  TMEM holds both tiles' scores (128 columns each; the weights P replace
+// them as bf16) and both outputs (128 columns each): all 512 columns.
+//
+// Warp roles (384 threads):
+//   warps 0-3, 4-7  softmax of tile 0, 1 (thread = row = TMEM lane): Q into shared
+//                   memory, running maximum and sum, P, the rare rescale of O,
+//                   and the output
+//   warp 8          MMA issuer: per tile j and group: PV(j - 1), then S(j)
+//   warp 9          loads: bulk copies of 16 KB images into a ring of 8 slots (a
+//                   tile takes three for K, two for V)
+//   warp 10         TMEM allocation
+// The running maximum moves only when a row's scores grow past it by 2^8 (P is
+// at most 256 then, and bf16 has the same relative step there), so O is
+// rescaled a few times per unit at most.
+//
+// Roundings: keys and values to bf16 once (they are MMA operands), P to bf16
+// once, the output once.  Scores, maxima, sums and O are fp32.
+#include "dcp_chunk.cuh"
+
+#include <cmath>
+#include <mutex>
+
+namespace dcp {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 384;
+constexpr int kGroup = 128;       // threads of a softmax group
+constexpr int kSlots = 8;         // ring of images
+constexpr int kQChunks = 3, kVChunks = 2;
+constexpr int kPerTile = kQChunks + kVChunks;
+constexpr int kMaskSlots = 4;     // ring of the tiles' token masks
+constexpr int kOffQ = 0;          // two query tiles of 3 images
+constexpr int kOffRing = 2 * kQChunks * kImage;
+constexpr int kOffMask = kOffRing + kSlots * kImage;  // kMaskSlots x (valid, bad)
+constexpr int kOffBars = kOffMask + kMaskSlots * 32;
+constexpr float kRescaleLog2 = 8.0f;
+
+struct Bars {
+  uint64_t q_full[2];                  // a group's Q is in shared memory (128)
+  uint64_t full[kSlots], free_[kSlots];
+  uint64_t mask_full[kMaskSlots];
+  uint64_t s_full[2];                  // S_g(j) is in TMEM
+  uint64_t p_full[2];                  // P_g(j) is in TMEM and O_g in its scale (4 warps)
+  uint64_t pv_done[2];                 // PV_g(j) is complete
+  uint64_t fin;
+  uint32_t tmem;
+  int32_t abort;
+  int32_t b, q0, q1, seq, r0, block;   // the unit
+};
+constexpr int kSmemBytes = kOffBars + static_cast<int>(sizeof(Bars)) + 1024;
+static_assert(kSmemBytes <= 232448, "exceeds the 227 KB of shared memory per CTA");
+
+// registers per thread: eight softmax warps take what the other four leave
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
+static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch, "more than was launched");
+
+constexpr uint32_t kColS = 0, kColO = 256;  // group g: + 128 g
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The rows of this group's tile that exist, and the images that they need.
+struct Tile {
+  int32_t first, rows;  // row of the request, number of rows
+  int32_t tiles;        // key tiles
+};
+__device__ __forceinline__ Tile tile_of(const Bars& bar, int g, int32_t have) {
+  Tile t;
+  const int32_t q_len = bar.q1 - bar.q0;
+  t.first = bar.block * kChunkRows + 128 * g;
+  t.rows = bar.b < 0 ? 0 : max(0, min(128, q_len - t.first));
+  // what the last row sees
+  const int64_t end = static_cast<int64_t>(bar.seq) - (q_len - 1) + (t.first + t.rows - 1);
+  t.tiles = t.rows > 0 && end > 0 ? static_cast<int32_t>((end + kChunkTile - 1) / kChunkTile) : 0;
+  if (t.tiles > have) t.tiles = 0;  // (its images did not fit the workspace)
+  return t;
+}
+
+// Rows of no request: zeros and -inf.
+__device__ void pad_rows(const ChunkArgs& a, int64_t r0, int64_t r1, int32_t h) {
+  for (int64_t i = threadIdx.x; i < (r1 - r0) * (kVDim / 4); i += kThreads) {
+    const int64_t at = ((r0 + i / (kVDim / 4)) * a.H + h) * kVDim + 4 * (i % (kVDim / 4));
+    if (a.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(0.f, 0.f, 0.f, 0.f);
+    else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) = make_uint2(0u, 0u);
+  }
+  for (int64_t r = r0 + threadIdx.x; r < r1; r += kThreads) a.lse[r * a.H + h] = -INFINITY;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ ChunkArgs a) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars& bar = *reinterpret_cast<Bars*>(smem + kOffBars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  launch_dependents();
+  const int32_t hp = static_cast<int32_t>(blockIdx.x / static_cast<uint32_t>(a.units));
+  const int32_t h = a.h0 + hp;
+  const int32_t u = static_cast<int32_t>(blockIdx.x - static_cast<uint32_t>(hp) * a.units);
+  wait_dependency();
+  // ---- the unit
+  if (warp == 0) {
+    const int32_t blocks = a.block_start[a.B];
+    int32_t b = -1, block = u - blocks;
+    if (u < blocks) {
+      b = find_range(a.block_start, a.B, u);
+      block = u - a.block_start[b];
+    }
+    if (lane == 0) {
+      bar.b = b;
+      bar.block = block;
+      if (b >= 0) bar.q0 = a.qsl[b], bar.q1 = a.qsl[b + 1], bar.seq = max(0, a.seq_lens[b]);
+      bar.abort = 0;
+    }
+  }
+  if (threadIdx.x == 32) {
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&bar.q_full[g], kGroup);
+      mbar_init(&bar.s_full[g], 1);
+      mbar_init(&bar.p_full[g], 4);
+      mbar_init(&bar.pv_done[g], 1);
+    }
+    for (int i = 0; i < kSlots; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.free_[i], 1);
+    for (int i = 0; i < kMaskSlots; ++i) mbar_init(&bar.mask_full[i], 1);
+    mbar_init(&bar.fin, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (bar.b < 0) {  // rows before the first request's and from the last one's end on, 256 to a unit
+    const int64_t lead = max(0, min(a.qsl[0], a.T)), tail = max(0, min(a.qsl[a.B], a.T));
+    const int64_t n = lead + (a.T - max(tail, lead));
+    int64_t i0 = static_cast<int64_t>(bar.block) * kChunkRows, i1 = min(n, i0 + kChunkRows);
+    const int64_t skip = max(tail, lead) - lead;  // rows of requests between the two
+    if (i0 < i1) {
+      const int64_t cut = min(max(lead, i0), i1);
+      pad_rows(a, i0, cut, h);
+      pad_rows(a, cut + skip, i1 + skip, h);
+    }
+    return;
+  }
+  if (warp == 10) {
+    tmem_alloc(&bar.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem;
+  const int32_t image0 = a.tile_start[bar.b];
+  const int32_t have = a.tile_start[bar.b + 1] - image0;
+  const int32_t all = static_cast<int32_t>((static_cast<int64_t>(bar.seq) + kChunkTile - 1) / kChunkTile);
+  const Tile t0 = tile_of(bar, 0, have < all ? 0 : have), t1 = tile_of(bar, 1, have < all ? 0 : have);
+  const int32_t n0 = t0.tiles, n1 = t1.tiles, n = max(n0, n1);
+  volatile int32_t* stop = &bar.abort;
+  auto failed = [&]() {
+    if (a.dev_error) atomicOr(a.dev_error, DCP_DEVERR_TIMEOUT);
+    *stop = 1;
+  };
+
+  if (warp < 8) {
+    // -------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int g = warp >> 2, row = threadIdx.x & 127;
+    const int32_t tiles = g ? n1 : n0, rows = g ? t1.rows : t0.rows, first = g ? t1.first : t0.first;
+    const int64_t r = static_cast<int64_t>(bar.q0) + first + row;  // this thread's query row
+    unsigned char* qs = smem + kOffQ + g * (kQChunks * kImage);
+    // ---- Q: 24 16-byte units a row, eight lanes per 128-byte line
+    if (tiles > 0) {
+#pragma unroll 2
+      for (int i = 0; i < 32; i += 4) {
+        const int qr = 32 * (warp & 3) + i + (lane >> 3), un = lane & 7;
+        const bool in = qr < rows && static_cast<int64_t>(bar.q0) + first + qr < a.T;
+        const __nv_bfloat16* src = a.q + (static_cast<int64_t>(bar.q0) + first + qr) * a.q_stride_tok + h * a.q_stride_head + 8 * un;
+#pragma unroll
+        for (int c = 0; c < kQChunks; ++c) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (in) v = __ldg(reinterpret_cast<const uint4*>(src + 64 * c));
+          v.x ^= a.q_sign, v.y ^= a.q_sign, v.z ^= a.q_sign, v.w ^= a.q_sign;
+          *reinterpret_cast<uint4*>(qs + c * kImage + image_unit(qr, un)) = v;
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&bar.q_full[g]);
+    }
+    const int32_t L = static_cast<int32_t>(max(static_cast<int64_t>(0), static_cast<int64_t>(bar.seq) - (bar.q1 - bar.q0 - 1) + first + row));
+    const int32_t L_first = __shfl_sync(0xffffffffu, L, 0);  // the least of the warp's
+    const uint32_t ts = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kColS + 128u * g;
+    const uint32_t to = ts - kColS + kColO;
+    float m = -INFINITY, l = 0.f;  // running maximum (log2, scaled) and sum
+    bool ok = true, nan_row = false;
+    const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2);
+    for (int32_t j = 0; j < tiles; ++j) {
+      ok = mbar_wait_warp(&bar.s_full[g], j & 1) && !*stop;
+      ok = ok && mbar_wait_warp(&bar.mask_full[j % kMaskSlots], (j / kMaskSlots) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      float s[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t(&)[32]>(s[32 * c]));
+      const uint4* masks = reinterpret_cast<const uint4*>(smem + kOffMask + (j % kMaskSlots) * 32);
+      const uint4 valid = masks[0], bad = masks[1];
+      tmem_wait_ld();
+      const int32_t p0 = j * kChunkTile;
+      const bool plain = (valid.x & valid.y & valid.z & valid.w) == 0xffffffffu && (bad.x | bad.y | bad.z | bad.w) == 0u &&
+                         p0 + kChunkTile <= L_first;
+      if (!plain) {
+        const uint32_t vw[4] = {valid.x, valid.y, valid.z, valid.w}, bw[4] = {bad.x, bad.y, bad.z, bad.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int32_t left = L - p0 - 32 * w;
+          const uint32_t see = (left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u) & vw[w];
+          nan_row = nan_row || (see & bw[w]) != 0u;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) s[32 * w + k] = (see >> k) & 1u ? s[32 * w + k] : -INFINITY;
+        }
+      }
+      float mx[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx[k] = max3(s[k], s[k + 4], s[k + 8]);
+#pragma unroll
+      for (int i = 12; i < 124; i += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[i + k], s[i + k + 4]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[124 + k]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+      // (a scale of 0 times an infinite score is NaN: such a row is NaN through its sum)
+      if (__any_sync(0xffffffffu, top > m + kRescaleLog2 || (m == -INFINITY && top > m))) {
+        const bool grow = top > m + kRescaleLog2 || (m == -INFINITY && top > m);
+        const float to_m = grow ? top : m;
+        const float f = grow ? ex2_approx(m - to_m) : 1.f;
+        m = to_m;
+        l *= f;
+        if (j > 0) {
+          ok = mbar_wait_warp(&bar.pv_done[g], (j - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld16(to + 16 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st16(to + 16 * c, o);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+      const uint64_t nb = f2_pack(-base, -base);
+      uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t p[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          float x, y;
+          f2_unpack(f2_fma(f2_pack(s[64 * half + 2 * k], s[64 * half + 2 * k + 1]), c2, nb), x, y);
+          x = ex2_approx(x);
+          y = ex2_approx(y);
+          sum[k & 1] = f2_add(sum[k & 1], f2_pack(x, y));
+          const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+          p[k] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        tmem_st32(ts + 32 * half, p);
+      }
+      float x, y;
+      f2_unpack(f2_add(sum[0], sum[1]), x, y);
+      l += x + y;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.p_full[g]);
+    }
+    // ---- output: O / l through shared memory (Q's, which no MMA reads any more)
+    if (tiles > 0 && ok) ok = mbar_wait_warp(&bar.pv_done[g], (tiles - 1) & 1);
+    if (!ok) failed();
+    tc_fence_after();
+    if (nan_row) l = __int_as_float(0x7fc00000);
+    const float inv = tiles > 0 && l != 0.f ? 1.0f / l : 0.f;
+    if (row < rows && r < a.T) a.lse[r * a.H + h] = tiles > 0 && l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    const int wr = 32 * (warp & 3);  // this warp's rows
+    const int live = min(32, static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(rows), a.T - static_cast<int64_t>(bar.q0) - first) - wr)));
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {  // 32 dims at a time; a warp's rows are its own
+      uint32_t o[32];
+      if (tiles > 0) {
+        tmem_ld32(to + 32 * c, o);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = tiles > 0 && l != 0.f ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
+      unsigned char* stage = qs + wr * 128;
+      const int64_t out0 = (static_cast<int64_t>(bar.q0) + first + wr) * a.H + h;
+      __syncwarp();
+      if (a.out_f32) {  // 128 bytes a row: eight lanes each
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(stage + image_unit(lane, k)) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int q = 4 * k + (lane >> 3);
+          if (q < live)
+            *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + (out0 + static_cast<int64_t>(q) * a.H) * kVDim + 32 * c + 4 * (lane & 7)) =
+                *reinterpret_cast<const uint4*>(stage + image_unit(q, lane & 7));
+        }
+      } else {  // 64 bytes a row: four lanes each
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]), __uint_as_float(o[8 * k + 2 * e + 1]));
+            w[e] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          *reinterpret_cast<uint4*>(stage + image_unit(lane, k)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int q = 8 * k + (lane >> 2);
+          if (q < live)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (out0 + static_cast<int64_t>(q) * a.H) * kVDim + 32 * c + 8 * (lane & 3)) =
+                *reinterpret_cast<const uint4*>(stage + image_unit(q, lane & 3));
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 8) {
+      // -------------------------------------------------- MMAs
+      const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, 128, 0, 1);
+      const uint64_t dq = smem_desc(smem_u32(smem + kOffQ), 16, 1024, kSwizzle128B);
+      const uint64_t dk = smem_desc(smem_u32(smem + kOffRing), 16, 1024, kSwizzle128B);
+      bool ok = true;
+      for (int32_t j = 0; j <= n && ok; ++j) {
+        for (int g = 0; g < 2 && ok; ++g) {
+          const int32_t tiles = g ? n1 : n0;
+          if (j >= 1 && j - 1 < tiles) {  // O_g += P_g(j - 1) V(j - 1)
+            ok = mbar_wait_warp(&bar.p_full[g], (j - 1) & 1);
+            const int32_t v0 = (j - 1) * kPerTile + kQChunks;
+            for (int c = 0; c < kVChunks && ok; ++c) ok = mbar_wait_warp(&bar.full[(v0 + c) % kSlots], ((v0 + c) / kSlots) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elected()) {
+              // (64 dims to a slot, so two MMAs of N = 64 where the second slot is not the next one)
+              const uint32_t a0 = v0 % kSlots, a1 = (v0 + 1) % kSlots;
+              const uint64_t dv = smem_desc(smem_u32(smem + kOffRing + a0 * kImage), kImage, 1024, kSwizzle128B);
+              if (a1 == a0 + 1) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  mma_ts(tmem + kColO + 128 * g, tmem + kColS + 128 * g + 8 * k, dv + ((2048 * k) >> 4), id_o, j > 1 || k > 0);
+              } else {
+                const uint32_t id_h = idesc_bf16(128, 64, 0, 1);
+                const uint64_t dv1 = smem_desc(smem_u32(smem + kOffRing + a1 * kImage), kImage, 1024, kSwizzle128B);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  mma_ts(tmem + kColO + 128 * g, tmem + kColS + 128 * g + 8 * k, dv + ((2048 * k) >> 4), id_h, j > 1 || k > 0);
+                  mma_ts(tmem + kColO + 128 * g + 64, tmem + kColS + 128 * g + 8 * k, dv1 + ((2048 * k) >> 4), id_h, j > 1 || k > 0);
+                }
+              }
+              mma_commit(&bar.pv_done[g]);
+            }
+            __syncwarp();
+          }
+          if (g == 1 && j >= 1 && elected()) {
+            const int32_t v0 = (j - 1) * kPerTile + kQChunks;
+            for (int c = 0; c < kVChunks; ++c) mma_commit(&bar.free_[(v0 + c) % kSlots]);
+          }
+          __syncwarp();
+          if (j < tiles) {  // S_g(j) = Q_g K(j)^T
+            if (j == 0) ok = mbar_wait_warp(&bar.q_full[g], 0);
+            for (int c = 0; c < kQChunks && ok; ++c) {
+              const int32_t k0 = j * kPerTile + c;
+              ok = mbar_wait_warp(&bar.full[k0 % kSlots], (k0 / kSlots) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              if (elected()) {
+                const uint64_t ac = dq + (((g * kQChunks + c) * kImage) >> 4), bc = dk + (((k0 % kSlots) * kImage) >> 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mma_ss(tmem + kColS + 128 * g, ac + 2 * k, bc + 2 * k, id_s, (c | k) != 0);
+              }
+              __syncwarp();
+            }
+            if (ok && elected()) mma_commit(&bar.s_full[g]);
+            __syncwarp();
+          }
+          if (g == 1 && j < n && elected()) {
+            for (int c = 0; c < kQChunks; ++c) mma_commit(&bar.free_[(j * kPerTile + c) % kSlots]);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) failed();
+      if (elected()) mma_commit(&bar.fin);  // the MMAs are complete before TMEM goes
+      __syncwarp();
+      mbar_wait_warp(&bar.fin, 0);
+    } else if (warp == 9) {
+      // -------------------------------------------------- loads
+      if (elected()) {
+        const unsigned char* keys = a.keys + (static_cast<int64_t>(hp) * a.tiles + image0) * (2 * kImage);
+        const unsigned char* values = a.values + (static_cast<int64_t>(hp) * a.tiles + image0) * (2 * kImage);
+        const unsigned char* rope = a.rope + static_cast<int64_t>(image0) * kImage;
+        const uint4* valid = a.valid + image0;
+        const uint4* bad = a.bad + static_cast<int64_t>(hp) * a.tiles + image0;
+        int32_t it = 0, masks = 0;
+        for (int32_t j = 0; j < n && !*stop; ++j) {
+          for (int c = 0; c < kPerTile; ++c, ++it) {
+            const int s = it % kSlots;
+            if (!mbar_wait(&bar.free_[s], ((it / kSlots) & 1) ^ 1)) { failed(); break; }
+            if (c == 0) {
+              uint64_t* mb = &bar.mask_full[j % kMaskSlots];
+              unsigned char* dst = smem + kOffMask + (j % kMaskSlots) * 32;
+              mbar_arrive_expect_tx(mb, 32);
+              bulk_load(dst, valid + j, 16, mb);
+              bulk_load(dst + 16, bad + j, 16, mb);
+              ++masks;
+            }
+            mbar_arrive_expect_tx(&bar.full[s], kImage);
+            const unsigned char* src = c < 2 ? keys + static_cast<int64_t>(j) * (2 * kImage) + c * kImage
+                                     : c == 2 ? rope + static_cast<int64_t>(j) * kImage
+                                              : values + static_cast<int64_t>(j) * (2 * kImage) + (c - 3) * kImage;
+            bulk_load(smem + kOffRing + s * kImage, src, kImage, &bar.full[s]);
+          }
+        }
+        // nothing lands after the CTA is gone
+        for (int32_t k = max(0, it - kSlots); k < it; ++k) mbar_wait(&bar.full[k % kSlots], (k / kSlots) & 1);
+        for (int32_t k = max(0, masks - kMaskSlots); k < masks; ++k) mbar_wait(&bar.mask_full[k % kMaskSlots], (k / kMaskSlots) & 1);
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 10) tmem_dealloc(tmem, 512);
+}
+
+std::mutex g_mutex;
+bool g_ready[64];
+
+cudaError_t set_up() {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (dev < 64 && g_ready[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e == cudaSuccess && dev < 64) g_ready[dev] = true;
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t st) {
+  const cudaError_t e = set_up();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.units) * a.heads));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_kernel, a);
+}
+
+}  // namespace dcp

@@ -1,0 +1,426 @@
+// Chunk attention, first half: the latents of the requests' contexts, gathered
+// from the paged cache, times the up projection's weight.
+//
+//   keys_h(p) = W_h[0:128] c(p),  values_h(p) = W_h[128:256] c(p)   (c: 512 dims)
+//
+// A matrix product of tokens x 512 by 512 x 256 per head on the tensor cores:
+// 2 x 512 x 256 operations per token and head, 512 bytes out.  Unit of work:
+// (tile of 128 tokens of a request, head), token-major, in equal shares of a
+// persistent grid, so that a CTA gathers a tile's latents once (128 KB of
+// shared memory, all 512 dims) and streams the weights of head after head past
+// them.
+//
+// Warp roles (384 threads):
+//   warps 0-3   epilogue: accumulator -> bf16 -> images in shared memory -> bulk
+//               stores; thread = token = TMEM lane
+//   warp 4      weights: 32 KB bulk copies (64 latent dims of a head's 256 rows)
+//   warp 5      MMA issuer (M = 128 tokens, N = 256, K = 16); two accumulators
+//   warp 6      TMEM allocation
+//   warps 8-11  gather of the latents (8 lanes per 128-byte line)
+// Every wait is bounded (DCP_DEVERR_TIMEOUT).
+//
+// A value that is not finite would reach query rows that do not see its token
+// (0 x NaN in the product with the weights of a tile), so a token with one gets
+// a row of zeros and a bit in `bad`: rows that see it become NaN.
+#include "dcp_chunk.cuh"
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <mutex>
+
+namespace dcp {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 384;
+constexpr int kEpiThreads = 128, kLoadThreads = 128;
+constexpr int kChunks = kLatent / 64;  // 8 chunks of 64 latent dims
+constexpr int kWStages = 2;
+constexpr int kOffA = 0;
+constexpr int kOffW = kChunks * kImage;
+constexpr int kOffOut = kOffW + kWStages * kWeightStage;
+constexpr int kOffBars = kOffOut + 2 * kImage;
+
+struct Bars {
+  uint64_t a_full, a_free;
+  uint64_t w_full[kWStages], w_free[kWStages];
+  uint64_t acc_full[2], acc_free[2];
+  uint64_t fin;  // the issuer's MMAs are complete
+  uint32_t tmem;
+  int32_t abort;
+};
+constexpr int kSmemBytes = kOffBars + static_cast<int>(sizeof(Bars)) + 1024;
+static_assert(kSmemBytes <= 232448, "exceeds the 227 KB of shared memory per CTA");
+
+__device__ __forceinline__ uint32_t widen2(uint32_t codes, float s) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xffffu), __NV_E4M3);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));  // exact
+  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Cache row of position p of request b, -1 for none (flagged).
+__device__ __forceinline__ int64_t cache_row(const ChunkArgs& a, int32_t b, int32_t p) {
+  int32_t j = p;
+  int64_t table = static_cast<int64_t>(b) * a.bt_stride;
+  if (a.local_tables) {
+    const int32_t run = fast_div(p, a.div_I), turn = fast_div(run, a.div_D);
+    table += (run - turn * a.D) * a.bt_shard_stride;
+    j = turn * a.I + (p - run * a.I);
+  }
+  const int32_t col = fast_div(j, a.div_bs);
+  if (col < a.bt_width) {
+    const int32_t blk = __ldg(a.block_table + table + col);
+    if (blk >= 0 && blk < a.num_blocks) return static_cast<int64_t>(blk) * a.block_size + (j - col * a.block_size);
+  }
+  if (a.dev_error) atomicOr(a.dev_error, DCP_DEVERR_BAD_BLOCK);
+  return -1;
+}
+
+struct Work {
+  int32_t i0, i1;  // items [i0, i1): tile i / heads, head i % heads
+};
+__device__ __forceinline__ Work my_items(const ChunkArgs& a, int32_t tiles) {
+  const int64_t n = static_cast<int64_t>(tiles) * a.heads;
+  Work w;
+  w.i0 = static_cast<int32_t>(n * blockIdx.x / gridDim.x);
+  w.i1 = static_cast<int32_t>(n * (blockIdx.x + 1) / gridDim.x);
+  return w;
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_constant__ ChunkArgs a) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars& bar = *reinterpret_cast<Bars*>(smem + kOffBars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  launch_dependents();
+  if (threadIdx.x == 0) {
+    mbar_init(&bar.a_full, kLoadThreads);
+    mbar_init(&bar.a_free, 1);
+    for (int i = 0; i < kWStages; ++i) mbar_init(&bar.w_full[i], 1), mbar_init(&bar.w_free[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bar.acc_full[i], 1), mbar_init(&bar.acc_free[i], 4);
+    mbar_init(&bar.fin, 1);
+    bar.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 6) {
+    tmem_alloc(&bar.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem;
+  wait_dependency();
+  const int32_t tiles = min(a.tile_start[a.B], a.tiles);
+  const Work work = my_items(a, tiles);
+  volatile int32_t* stop = &bar.abort;
+  auto failed = [&]() {
+    if (a.dev_error) atomicOr(a.dev_error, DCP_DEVERR_TIMEOUT);
+    *stop = 1;
+  };
+
+  if (warp < 4) {
+    // -------------------------------------------------- epilogue
+    const int row = threadIdx.x;
+    for (int32_t i = work.i0, n = 0; i < work.i1; ++i, ++n) {
+      const int acc = n & 1;
+      const bool ok = mbar_wait(&bar.acc_full[acc], (n >> 1) & 1) && !*stop;
+      if (!named_barrier_and(1, kEpiThreads, ok)) { failed(); break; }  // (one answer: barriers follow)
+      tc_fence_after();
+      const int32_t tile = i / a.heads, h = i - tile * a.heads;
+      const int64_t slot = static_cast<int64_t>(h) * a.tiles + tile;
+      const uint32_t col = tmem + (static_cast<uint32_t>(warp) << 21) + 256u * acc;
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {  // keys, values
+        uint32_t v[64];  // 128 dims as bf16 pairs
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          tmem_ld32(col + 128 * part + 32 * c, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+            v[16 * c + k] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+        }
+        if (part == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.acc_free[acc]);
+          bool fin = true;
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            fin = fin && (v[k] & 0x7f80u) != 0x7f80u && (v[k] & 0x7f800000u) != 0x7f800000u;
+          const uint32_t nan_rows = __ballot_sync(0xffffffffu, !fin);
+          if (!fin) {
+#pragma unroll
+            for (int k = 0; k < 64; ++k) v[k] = 0;
+          }
+          if (lane == 0) reinterpret_cast<uint32_t*>(a.bad + slot)[warp] = nan_rows;
+        }
+        // the images' last bulk stores (two parts ago) have read them
+        if (threadIdx.x == 0) bulk_wait_read<0>();
+        named_barrier(1, kEpiThreads);
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+          *reinterpret_cast<uint4*>(smem + kOffOut + (u >> 3) * kImage + image_unit(row, u & 7)) =
+              make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+        fence_proxy_async_smem();
+        named_barrier(1, kEpiThreads);
+        if (threadIdx.x == 0) {
+          bulk_store((part ? a.values : a.keys) + slot * (2 * kImage), smem + kOffOut, 2 * kImage);
+          bulk_commit();
+        }
+      }
+    }
+    if (threadIdx.x == 0) bulk_wait<0>();
+  } else if (warp == 4) {
+    // -------------------------------------------------- weights
+    if (elected()) {
+      uint32_t it = 0;
+      for (int32_t i = work.i0; i < work.i1 && !*stop; ++i) {
+        const int32_t h = a.h0 + i % a.heads;
+        const unsigned char* w = static_cast<const unsigned char*>(a.weight) + static_cast<int64_t>(h) * (kChunks * kWeightStage);
+        for (int c = 0; c < kChunks; ++c, ++it) {
+          const uint32_t s = it % kWStages, ph = (it / kWStages) & 1;
+          if (!mbar_wait(&bar.w_free[s], ph ^ 1)) { failed(); break; }
+          mbar_arrive_expect_tx(&bar.w_full[s], kWeightStage);
+          bulk_load(smem + kOffW + s * kWeightStage, w + c * kWeightStage, kWeightStage, &bar.w_full[s]);
+        }
+      }
+      // nothing lands after the CTA is gone
+      for (uint32_t k = it > kWStages ? it - kWStages : 0; k < it; ++k) mbar_wait(&bar.w_full[k % kWStages], (k / kWStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // -------------------------------------------------- MMAs
+    const uint32_t id = idesc_bf16(128, 256, 0, 0);
+    const uint64_t da = smem_desc(smem_u32(smem + kOffA), 16, 1024, kSwizzle128B);
+    const uint64_t dw = smem_desc(smem_u32(smem + kOffW), 16, 1024, kSwizzle128B);
+    uint32_t it = 0, loads = 0;
+    int32_t last = -1;
+    bool ok = true;
+    for (int32_t i = work.i0, n = 0; i < work.i1 && ok; ++i, ++n) {
+      const int acc = n & 1;
+      const int32_t tile = i / a.heads;
+      if (tile != last) {
+        ok = mbar_wait_warp(&bar.a_full, loads & 1);
+        ++loads;
+        last = tile;
+      }
+      ok = ok && mbar_wait_warp(&bar.acc_free[acc], ((n >> 1) & 1) ^ 1);
+      tc_fence_after();
+      for (int c = 0; c < kChunks && ok; ++c, ++it) {
+        const uint32_t s = it % kWStages;
+        ok = mbar_wait_warp(&bar.w_full[s], (it / kWStages) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elected()) {
+          const uint64_t ac = da + ((c * kImage) >> 4), wc = dw + ((s * kWeightStage) >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_ss(tmem + 256 * acc, ac + 2 * k, wc + 2 * k, id, (c | k) != 0);
+          mma_commit(&bar.w_free[s]);
+        }
+        __syncwarp();
+      }
+      if (ok && elected()) {
+        mma_commit(&bar.acc_full[acc]);
+        if (i + 1 == work.i1 || (i + 1) / a.heads != tile) mma_commit(&bar.a_free);
+      }
+      __syncwarp();
+    }
+    if (!ok) failed();
+    // the MMAs are complete before TMEM goes
+    if (elected()) mma_commit(&bar.fin);
+    __syncwarp();
+    mbar_wait_warp(&bar.fin, 0);
+  } else if (warp >= 8) {
+    // -------------------------------------------------- latents
+    const int lw = warp - 8;
+    int32_t last = -1;
+    uint32_t loads = 0;
+    for (int32_t i = work.i0; i < work.i1; i = (last + 1) * a.heads) {
+      const int32_t tile = i / a.heads;
+      last = tile;
+      // this thread's token
+      const int32_t b = find_range(a.tile_start, a.B, tile);
+      const int32_t seq = a.seq_lens[b];
+      const int64_t p = static_cast<int64_t>(tile - a.tile_start[b]) * kChunkTile + 32 * lw + lane;
+      int64_t src = -1;
+      if (p < seq) src = cache_row(a, b, static_cast<int32_t>(p));
+      const float scale = kFp8 && src >= 0 ? __ldg(a.kv_scale + src) : 0.f;
+      // what the heads share is written with the first head
+      const bool shared_too = a.h0 == 0 && i == tile * a.heads;
+      const uint32_t live = __ballot_sync(0xffffffffu, src >= 0);
+      if (shared_too && lane == 0) reinterpret_cast<uint32_t*>(a.valid + tile)[lw] = live;
+      if (loads > 0 && !mbar_wait_warp(&bar.a_free, (loads - 1) & 1)) { failed(); break; }
+      ++loads;
+      const int u = lane & 7;
+#pragma unroll 2
+      for (int g = 0; g < 8; ++g) {
+        const int r = 4 * g + (lane >> 3);
+        const int64_t from = __shfl_sync(0xffffffffu, src, r);
+        const float s = kFp8 ? __shfl_sync(0xffffffffu, scale, r) : 0.f;
+        const uint32_t at = image_unit(32 * lw + r, u);
+        uint4 rope = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (kFp8) {
+          const uint2* row = reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(a.kv) + from * kKDim) + u;
+          uint2 v[kChunks + 1];
+#pragma unroll
+          for (int c = 0; c <= kChunks; ++c) v[c] = from >= 0 ? __ldg(row + 8 * c) : make_uint2(0u, 0u);
+#pragma unroll
+          for (int c = 0; c <= kChunks; ++c) {
+            const uint4 w = make_uint4(widen2(v[c].x, s), widen2(v[c].x >> 16, s), widen2(v[c].y, s), widen2(v[c].y >> 16, s));
+            if (c < kChunks) *reinterpret_cast<uint4*>(smem + kOffA + c * kImage + at) = w;
+            else rope = w;
+          }
+        } else {
+          const unsigned char* row = static_cast<const unsigned char*>(a.kv) + (from >= 0 ? from : 0) * (2 * kKDim) + 16 * u;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            cp_async16_zfill(smem_u32(smem + kOffA + c * kImage + at), row + 128 * c, from >= 0 ? 16u : 0u);
+          if (shared_too && from >= 0) rope = __ldg(reinterpret_cast<const uint4*>(row + 128 * kChunks));
+        }
+        if (shared_too) *reinterpret_cast<uint4*>(a.rope + static_cast<int64_t>(tile) * kImage + at) = rope;
+      }
+      if constexpr (!kFp8) {
+        cp_async_commit();
+        cp_async_wait<0>();
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&bar.a_full);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 6) tmem_dealloc(tmem, 512);
+}
+
+// packed[h][c] = rows 256 h .. 256 h + 255 of w [H x 256, 512], latent dims
+// 64 c .. 64 c + 63, as the MMAs read them
+__global__ void __launch_bounds__(256) pack_kernel(const uint4* __restrict__ w, unsigned char* __restrict__ packed, int64_t units) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;  // 16-byte unit of w
+  if (i >= units) return;
+  const int64_t row = i >> 6;
+  const int u = static_cast<int>(i & 63), r = static_cast<int>(row & (kUp - 1));
+  *reinterpret_cast<uint4*>(packed + (row / kUp) * (kChunks * kWeightStage) + (u >> 3) * kWeightStage + image_unit(r, u & 7)) = __ldg(w + i);
+}
+
+constexpr int kPlanThreads = 1024;
+
+// First images and first units of the requests: two scans.  Requests whose
+// images do not all fit get none (and their rows nothing to see).
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ ChunkArgs a) {
+  __shared__ int64_t sums[2][32];
+  launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t base[2] = {0, 0};
+  for (int32_t b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int32_t b = b0 + tid;
+    int64_t x[2] = {0, 0};
+    int64_t own[2] = {0, 0};
+    if (b < a.B) {
+      const int32_t q0 = __ldg(a.qsl + b), q1 = __ldg(a.qsl + b + 1), seq = __ldg(a.seq_lens + b);
+      const bool rows = q0 >= 0 && q1 > q0;
+      if ((q1 < q0 || q0 < 0) && a.dev_error) atomicOr(a.dev_error, DCP_DEVERR_BAD_ROWS);
+      // (tokens that no row sees are not needed)
+      own[0] = rows && seq > 0 ? (static_cast<int64_t>(seq) + kChunkTile - 1) / kChunkTile : 0;
+      own[1] = rows ? (static_cast<int64_t>(q1) - q0 + kChunkRows - 1) / kChunkRows : 0;
+      x[0] = own[0], x[1] = own[1];
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x[k], o);
+        if (lane >= o) x[k] += y;
+      }
+      if (lane == 31) sums[k][warp] = x[k];
+    }
+    __syncthreads();
+    if (warp < 2) {
+      int64_t s = sums[warp][lane];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+      }
+      sums[warp][lane] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      x[k] += base[k] + (warp > 0 ? sums[k][warp - 1] : 0);
+      base[k] += sums[k][31];
+    }
+    if (b < a.B) {
+      // ends, cut at what the workspace holds; a request past it has none
+      const int64_t end = x[0] < a.tiles ? x[0] : a.tiles;
+      if (x[0] > a.tiles && own[0] > 0 && a.dev_error) atomicOr(a.dev_error, DCP_DEVERR_SEQ_TOO_LONG);
+      a.tile_start[b + 1] = static_cast<int32_t>(end);
+      a.block_start[b + 1] = static_cast<int32_t>(x[1] < 0x7fffffff ? x[1] : 0x7fffffff);
+    }
+    __syncthreads();
+  }
+  if (tid == 0) a.tile_start[0] = a.block_start[0] = 0;
+}
+
+std::mutex g_mutex;
+bool g_ready[2][64];
+
+template <bool kFp8>
+cudaError_t set_up() {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (dev < 64 && g_ready[kFp8][dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(expand_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e == cudaSuccess && dev < 64) g_ready[kFp8][dev] = true;
+  return e;
+}
+
+cudaError_t launch_pdl(void (*kernel)(ChunkArgs), const ChunkArgs& a, int grid, int threads, int smem, cudaStream_t st) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace
+
+cudaError_t launch_pack_kv_b(const void* w, int32_t H, void* packed, cudaStream_t st) {
+  const int64_t units = static_cast<int64_t>(H) * kUp * (kLatent / 8);
+  pack_kernel<<<static_cast<unsigned>((units + 255) / 256), 256, 0, st>>>(static_cast<const uint4*>(w),
+                                                                          static_cast<unsigned char*>(packed), units);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t st) {
+  plan_kernel<<<1, kPlanThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_chunk_expand(const ChunkArgs& a, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = a.kv_scale ? set_up<true>() : set_up<false>();
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t items = static_cast<int64_t>(a.tiles) * a.heads;
+  const int grid = static_cast<int>(items < sms ? items : sms);
+  return launch_pdl(a.kv_scale ? expand_kernel<true> : expand_kernel<false>, a, grid, kThreads, kSmemBytes, st);
+}
+
+}  // namespace dcp
