@@ -91,6 +91,72 @@ __device__ __forceinline__ Tile tile_of(const Bars& bar, int g, int32_t have) {
   return t;
 }
 
+// The issuing lane's work on tile j for group g: PV(j - 1), then S(j).
+struct Issue {
+  Bars& bar;
+  const uint64_t dq, dk, dv;
+  const int32_t n0, n1;
+  bool ok;
+
+  template <int g>
+  __device__ __forceinline__ void step(int32_t j, uint32_t k0) {
+    const int32_t tiles = g ? n1 : n0, n = n0 > n1 ? n0 : n1;
+    // (images that the other group has waited for are there)
+    const bool first_v = g == 0 || j - 1 >= n0, first_k = g == 0 || j >= n0;
+    const uint32_t v0 = (k0 - kVChunks) % kSlots, v1 = (v0 + 1) % kSlots;
+    if (j >= 1 && j - 1 < tiles && ok) {  // O_g += P_g(j - 1) V(j - 1)
+      if (first_v) {
+        ok = mbar_wait(&bar.full[v0], ((k0 - kVChunks) / kSlots) & 1);
+        ok = ok && mbar_wait(&bar.full[v1], ((k0 - kVChunks + 1) / kSlots) & 1);
+      }
+      ok = ok && mbar_wait(&bar.p_full[g], (j - 1) & 1);
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t d = dv + ((v0 * kImage) >> 4);
+      constexpr uint32_t o = kColO + 128 * g, p = kColS + 128 * g;
+      if (v1 == v0 + 1) {
+        constexpr uint32_t id = idesc_bf16(128, 128, 0, 1);
+        mma_ts(o, p, d, id, j > 1);
+#pragma unroll
+        for (int k = 1; k < 8; ++k) mma_ts(o, p + 8 * k, d + ((2048 * k) >> 4), id, 1);
+      } else {  // (64 dims each from the ring's last and first slot)
+        constexpr uint32_t id = idesc_bf16(128, 64, 0, 1);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          mma_ts(o, p + 8 * k, d + ((2048 * k) >> 4), id, j > 1 || k > 0);
+          mma_ts(o + 64, p + 8 * k, dv + ((2048 * k) >> 4), id, j > 1 || k > 0);
+        }
+      }
+      mma_commit(&bar.pv_done[g]);
+    }
+    if (g == 1 && j >= 1) {
+      mma_commit(&bar.free_[v0]);
+      mma_commit(&bar.free_[v1]);
+    }
+    if (j < tiles && ok) {  // S_g(j) = Q_g K(j)^T
+      if (j == 0) ok = mbar_wait(&bar.q_full[g], 0);
+#pragma unroll
+      for (int c = 0; c < kQChunks; ++c) {
+        const uint32_t s = (k0 + c) % kSlots;
+        if (first_k) {
+          ok = ok && mbar_wait(&bar.full[s], ((k0 + c) / kSlots) & 1);
+          if (!ok) return;
+          tc_fence_after();
+        }
+        const uint64_t q = dq + (((g * kQChunks + c) * kImage) >> 4), k = dk + ((s * kImage) >> 4);
+        constexpr uint32_t id = idesc_bf16(128, 128, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mma_ss(kColS + 128 * g, q + 2 * i, k + 2 * i, id, (c | i) != 0);
+      }
+      mma_commit(&bar.s_full[g]);
+    }
+    if (g == 1 && j < n) {
+#pragma unroll
+      for (int c = 0; c < kQChunks; ++c) mma_commit(&bar.free_[(k0 + c) % kSlots]);
+    }
+  }
+};
+
 // Rows of no request: zeros and -inf.
 __device__ void pad_rows(const ChunkArgs& a, int64_t r0, int64_t r1, int32_t h) {
   for (int64_t i = threadIdx.x; i < (r1 - r0) * (kVDim / 4); i += kThreads) {
@@ -158,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bar.tmem;
+  const uint32_t tmem = 0;  // (all 512 columns: the allocation starts at the first)
   const int32_t image0 = a.tile_start[bar.b];
   const int32_t have = a.tile_start[bar.b + 1] - image0;
   const int32_t all = static_cast<int32_t>((static_cast<int64_t>(bar.seq) + kChunkTile - 1) / kChunkTile);
@@ -343,72 +409,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 8) {
       // -------------------------------------------------- MMAs
-      const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, 128, 0, 1);
-      const uint64_t dq = smem_desc(smem_u32(smem + kOffQ), 16, 1024, kSwizzle128B);
-      const uint64_t dk = smem_desc(smem_u32(smem + kOffRing), 16, 1024, kSwizzle128B);
-      bool ok = true;
-      for (int32_t j = 0; j <= n && ok; ++j) {
-        for (int g = 0; g < 2 && ok; ++g) {
-          const int32_t tiles = g ? n1 : n0;
-          if (j >= 1 && j - 1 < tiles) {  // O_g += P_g(j - 1) V(j - 1)
-            ok = mbar_wait_warp(&bar.p_full[g], (j - 1) & 1);
-            const int32_t v0 = (j - 1) * kPerTile + kQChunks;
-            for (int c = 0; c < kVChunks && ok; ++c) ok = mbar_wait_warp(&bar.full[(v0 + c) % kSlots], ((v0 + c) / kSlots) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (elected()) {
-              // (64 dims to a slot, so two MMAs of N = 64 where the second slot is not the next one)
-              const uint32_t a0 = v0 % kSlots, a1 = (v0 + 1) % kSlots;
-              const uint64_t dv = smem_desc(smem_u32(smem + kOffRing + a0 * kImage), kImage, 1024, kSwizzle128B);
-              if (a1 == a0 + 1) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  mma_ts(tmem + kColO + 128 * g, tmem + kColS + 128 * g + 8 * k, dv + ((2048 * k) >> 4), id_o, j > 1 || k > 0);
-              } else {
-                const uint32_t id_h = idesc_bf16(128, 64, 0, 1);
-                const uint64_t dv1 = smem_desc(smem_u32(smem + kOffRing + a1 * kImage), kImage, 1024, kSwizzle128B);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  mma_ts(tmem + kColO + 128 * g, tmem + kColS + 128 * g + 8 * k, dv + ((2048 * k) >> 4), id_h, j > 1 || k > 0);
-                  mma_ts(tmem + kColO + 128 * g + 64, tmem + kColS + 128 * g + 8 * k, dv1 + ((2048 * k) >> 4), id_h, j > 1 || k > 0);
-                }
-              }
-              mma_commit(&bar.pv_done[g]);
-            }
-            __syncwarp();
-          }
-          if (g == 1 && j >= 1 && elected()) {
-            const int32_t v0 = (j - 1) * kPerTile + kQChunks;
-            for (int c = 0; c < kVChunks; ++c) mma_commit(&bar.free_[(v0 + c) % kSlots]);
-          }
-          __syncwarp();
-          if (j < tiles) {  // S_g(j) = Q_g K(j)^T
-            if (j == 0) ok = mbar_wait_warp(&bar.q_full[g], 0);
-            for (int c = 0; c < kQChunks && ok; ++c) {
-              const int32_t k0 = j * kPerTile + c;
-              ok = mbar_wait_warp(&bar.full[k0 % kSlots], (k0 / kSlots) & 1);
-              if (!ok) break;
-              tc_fence_after();
-              if (elected()) {
-                const uint64_t ac = dq + (((g * kQChunks + c) * kImage) >> 4), bc = dk + (((k0 % kSlots) * kImage) >> 4);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mma_ss(tmem + kColS + 128 * g, ac + 2 * k, bc + 2 * k, id_s, (c | k) != 0);
-              }
-              __syncwarp();
-            }
-            if (ok && elected()) mma_commit(&bar.s_full[g]);
-            __syncwarp();
-          }
-          if (g == 1 && j < n && elected()) {
-            for (int c = 0; c < kQChunks; ++c) mma_commit(&bar.free_[(j * kPerTile + c) % kSlots]);
-          }
-          __syncwarp();
+      // (one lane, every operand a base plus constants: an issuing thread that
+      // computes what its next MMA needs falls behind the tensor pipe)
+      if (elected()) {
+        const uint64_t dq = smem_desc(smem_u32(smem + kOffQ), 16, 1024, kSwizzle128B);
+        const uint64_t dk = smem_desc(smem_u32(smem + kOffRing), 16, 1024, kSwizzle128B);
+        const uint64_t dv = smem_desc(smem_u32(smem + kOffRing), kImage, 1024, kSwizzle128B);
+        Issue is{bar, dq, dk, dv, n0, n1, true};
+        uint32_t k0 = 0;  // K(j)'s first image
+        for (int32_t j = 0; j <= n && is.ok; ++j, k0 += kPerTile) {
+          is.step<0>(j, k0);
+          is.step<1>(j, k0);
         }
+        if (!is.ok) failed();
+        mma_commit(&bar.fin);  // the MMAs are complete before TMEM goes
+        mbar_wait(&bar.fin, 0);
       }
-      if (!ok) failed();
-      if (elected()) mma_commit(&bar.fin);  // the MMAs are complete before TMEM goes
       __syncwarp();
-      mbar_wait_warp(&bar.fin, 0);
     } else if (warp == 9) {
       // -------------------------------------------------- loads
       if (elected()) {
@@ -447,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 10) tmem_dealloc(tmem, 512);
+  if (warp == 10) tmem_dealloc(bar.tmem, 512);
 }
 
 std::mutex g_mutex;
