@@ -37,7 +37,7 @@ using namespace sm100;
 
 constexpr int kThreads = 384;
 constexpr int kGroup = 128;       // threads of a softmax group
-constexpr int kSlots = 8;         // ring of images
+constexpr uint32_t kSlots = 8;         // ring of images
 constexpr int kQChunks = 3, kVChunks = 2;
 constexpr int kPerTile = kQChunks + kVChunks;
 constexpr int kMaskSlots = 4;     // ring of the tiles' token masks
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       mbar_init(&bar.p_full[g], 4);
       mbar_init(&bar.pv_done[g], 1);
     }
-    for (int i = 0; i < kSlots; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.free_[i], 1);
+    for (uint32_t i = 0; i < kSlots; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.free_[i], 1);
     for (int i = 0; i < kMaskSlots; ++i) mbar_init(&bar.mask_full[i], 1);
     mbar_init(&bar.fin, 1);
     fence_mbar_init();
@@ -428,35 +428,41 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       __syncwarp();
     } else if (warp == 9) {
       // -------------------------------------------------- loads
+      // (running pointers and slots: a copy whose operands are computed anew
+      // takes its thread ~600 cycles)
       if (elected()) {
         const unsigned char* keys = a.keys + (static_cast<int64_t>(hp) * a.tiles + image0) * (2 * kImage);
         const unsigned char* values = a.values + (static_cast<int64_t>(hp) * a.tiles + image0) * (2 * kImage);
         const unsigned char* rope = a.rope + static_cast<int64_t>(image0) * kImage;
         const uint4* valid = a.valid + image0;
         const uint4* bad = a.bad + static_cast<int64_t>(hp) * a.tiles + image0;
-        int32_t it = 0, masks = 0;
-        for (int32_t j = 0; j < n && !*stop; ++j) {
+        unsigned char* ring = smem + kOffRing;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int32_t j = 0; j < n && ok; ++j) {
+#pragma unroll
           for (int c = 0; c < kPerTile; ++c, ++it) {
-            const int s = it % kSlots;
-            if (!mbar_wait(&bar.free_[s], ((it / kSlots) & 1) ^ 1)) { failed(); break; }
+            const uint32_t s = it % kSlots;
+            ok = ok && mbar_wait(&bar.free_[s], ((it / kSlots) & 1) ^ 1);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&bar.full[s], kImage);
+            bulk_load(ring + s * kImage, c < 2 ? keys + c * kImage : c == 2 ? rope : values + (c - 3) * kImage, kImage, &bar.full[s]);
             if (c == 0) {
               uint64_t* mb = &bar.mask_full[j % kMaskSlots];
               unsigned char* dst = smem + kOffMask + (j % kMaskSlots) * 32;
               mbar_arrive_expect_tx(mb, 32);
-              bulk_load(dst, valid + j, 16, mb);
-              bulk_load(dst + 16, bad + j, 16, mb);
-              ++masks;
+              bulk_load(dst, valid, 16, mb);
+              bulk_load(dst + 16, bad, 16, mb);
             }
-            mbar_arrive_expect_tx(&bar.full[s], kImage);
-            const unsigned char* src = c < 2 ? keys + static_cast<int64_t>(j) * (2 * kImage) + c * kImage
-                                     : c == 2 ? rope + static_cast<int64_t>(j) * kImage
-                                              : values + static_cast<int64_t>(j) * (2 * kImage) + (c - 3) * kImage;
-            bulk_load(smem + kOffRing + s * kImage, src, kImage, &bar.full[s]);
           }
+          keys += 2 * kImage, values += 2 * kImage, rope += kImage, ++valid, ++bad;
         }
+        if (!ok) failed();
         // nothing lands after the CTA is gone
-        for (int32_t k = max(0, it - kSlots); k < it; ++k) mbar_wait(&bar.full[k % kSlots], (k / kSlots) & 1);
-        for (int32_t k = max(0, masks - kMaskSlots); k < masks; ++k) mbar_wait(&bar.mask_full[k % kMaskSlots], (k / kMaskSlots) & 1);
+        for (uint32_t k = it > kSlots ? it - kSlots : 0; k < it; ++k) mbar_wait(&bar.full[k % kSlots], (k / kSlots) & 1);
+        const uint32_t masks = (it + kPerTile - 1) / kPerTile;
+        for (uint32_t k = masks > kMaskSlots ? masks - kMaskSlots : 0; k < masks; ++k)
+          mbar_wait(&bar.mask_full[k % kMaskSlots], (k / kMaskSlots) & 1);
       }
       __syncwarp();
     }

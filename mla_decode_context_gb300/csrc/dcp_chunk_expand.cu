@@ -5,16 +5,21 @@
 //
 // A matrix product of tokens x 512 by 512 x 256 per head on the tensor cores:
 // 2 x 512 x 256 operations per token and head, 512 bytes out.  Unit of work:
-// (tile of 128 tokens of a request, head), token-major, in equal shares of a
-// persistent grid, so that a CTA gathers a tile's latents once (128 KB of
-// shared memory, all 512 dims) and streams the weights of head after head past
-// them.
+// (two tiles of 128 tokens, head), token-major, in equal shares of a persistent
+// grid, so that latents are gathered once per tile (128 KB of a CTA's shared
+// memory, all 512 dims) and the weights of head after head stream past them.
+// Two CTAs share the weights: one MMA (M = 256, N = 256) reads each CTA's 128
+// tokens and half of a head's rows from either's shared memory, so that each
+// streams 32 bytes of weights a clock instead of 64.  (A CTA by itself, with a
+// ring of two 32 KB stages, waited for its weights: 24,000 tokens at 128 heads
+// 851 us.)
 //
-// Warp roles (384 threads):
+// Warp roles (384 threads in each CTA of the pair):
 //   warps 0-3   epilogue: accumulator -> bf16 -> images in shared memory -> bulk
 //               stores; thread = token = TMEM lane
-//   warp 4      weights: 32 KB bulk copies (64 latent dims of a head's 256 rows)
-//   warp 5      MMA issuer (M = 128 tokens, N = 256, K = 16); two accumulators
+//   warp 4      weights: 16 KB bulk copies (64 latent dims of half a head's rows)
+//   warp 5      CTA 0: MMA issuer, two accumulators; CTA 1: tells CTA 0 of its
+//               weights
 //   warp 6      TMEM allocation
 //   warps 8-11  gather of the latents (8 lanes per 128-byte line)
 // Every wait is bounded (DCP_DEVERR_TIMEOUT).
@@ -28,6 +33,7 @@
 #include <cuda_fp8.h>
 
 #include <mutex>
+#include <type_traits>
 
 namespace dcp {
 namespace {
@@ -37,17 +43,22 @@ using namespace sm100;
 constexpr int kThreads = 384;
 constexpr int kEpiThreads = 128, kLoadThreads = 128;
 constexpr int kChunks = kLatent / 64;  // 8 chunks of 64 latent dims
-constexpr int kWStages = 2;
+constexpr int kWStages = 4;
+constexpr int kWHalf = kWeightStage / 2;  // a CTA's rows of a weight stage
 constexpr int kOffA = 0;
 constexpr int kOffW = kChunks * kImage;
-constexpr int kOffOut = kOffW + kWStages * kWeightStage;
+constexpr int kOffOut = kOffW + kWStages * kWHalf;
 constexpr int kOffBars = kOffOut + 2 * kImage;
 
 struct Bars {
-  uint64_t a_full, a_free;
-  uint64_t w_full[kWStages], w_free[kWStages];
-  uint64_t acc_full[2], acc_free[2];
-  uint64_t fin;  // the issuer's MMAs are complete
+  uint64_t a_full;            // CTA 0: both CTAs' latents are in shared memory (every loader)
+  uint64_t a_free;            // both: the tiles' MMAs are complete
+  uint64_t w_full[kWStages];  // both: this CTA's half of a weight stage landed
+  uint64_t w_peer[kWStages];  // CTA 0: CTA 1's half landed
+  uint64_t w_free[kWStages];  // both
+  uint64_t acc_full[2];       // both: an accumulator is complete
+  uint64_t acc_free[2];       // CTA 0: both CTAs' epilogues have read it (4 warps each)
+  uint64_t fin;               // both: the issuer's MMAs are complete
   uint32_t tmem;
   int32_t abort;
 };
@@ -80,13 +91,14 @@ __device__ __forceinline__ int64_t cache_row(const ChunkArgs& a, int32_t b, int3
 }
 
 struct Work {
-  int32_t i0, i1;  // items [i0, i1): tile i / heads, head i % heads
+  int32_t i0, i1;  // items [i0, i1): tiles 2 (i / heads) and the next, head i % heads
 };
 __device__ __forceinline__ Work my_items(const ChunkArgs& a, int32_t tiles) {
-  const int64_t n = static_cast<int64_t>(tiles) * a.heads;
+  const int64_t n = static_cast<int64_t>((tiles + 1) / 2) * a.heads;
+  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   Work w;
-  w.i0 = static_cast<int32_t>(n * blockIdx.x / gridDim.x);
-  w.i1 = static_cast<int32_t>(n * (blockIdx.x + 1) / gridDim.x);
+  w.i0 = static_cast<int32_t>(n * pair / pairs);
+  w.i1 = static_cast<int32_t>(n * (pair + 1) / pairs);
   return w;
 }
 
@@ -98,22 +110,24 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();
   if (threadIdx.x == 0) {
-    mbar_init(&bar.a_full, kLoadThreads);
+    mbar_init(&bar.a_full, 2 * kLoadThreads);
     mbar_init(&bar.a_free, 1);
-    for (int i = 0; i < kWStages; ++i) mbar_init(&bar.w_full[i], 1), mbar_init(&bar.w_free[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&bar.acc_full[i], 1), mbar_init(&bar.acc_free[i], 4);
+    for (int i = 0; i < kWStages; ++i) mbar_init(&bar.w_full[i], 1), mbar_init(&bar.w_peer[i], 1), mbar_init(&bar.w_free[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bar.acc_full[i], 1), mbar_init(&bar.acc_free[i], 8);
     mbar_init(&bar.fin, 1);
     bar.abort = 0;
     fence_mbar_init();
   }
   if (warp == 6) {
-    tmem_alloc(&bar.tmem, 512);
-    tmem_relinquish();
+    tmem_alloc_pair(&bar.tmem, 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // (the peer's barriers are set up)
   tc_fence_after();
-  const uint32_t tmem = bar.tmem;
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t tmem = 0;  // (all 512 columns: the allocation starts at the first)
   wait_dependency();
   const int32_t tiles = min(a.tile_start[a.B], a.tiles);
   const Work work = my_items(a, tiles);
@@ -131,7 +145,14 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       const bool ok = mbar_wait(&bar.acc_full[acc], (n >> 1) & 1) && !*stop;
       if (!named_barrier_and(1, kEpiThreads, ok)) { failed(); break; }  // (one answer: barriers follow)
       tc_fence_after();
-      const int32_t tile = i / a.heads, h = i - tile * a.heads;
+      const int32_t pair = i / a.heads, h = i - pair * a.heads;
+      const int32_t tile = 2 * pair + static_cast<int32_t>(rank);
+      if (tile >= tiles) {  // (the last tile has no second one)
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_relaxed(map_peer(smem_u32(&bar.acc_free[acc]), 0));
+        continue;
+      }
       const int64_t slot = static_cast<int64_t>(h) * a.tiles + tile;
       const uint32_t col = tmem + (static_cast<uint32_t>(warp) << 21) + 256u * acc;
 #pragma unroll 1
@@ -151,7 +172,9 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
         if (part == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.acc_free[acc]);
+          // (relaxed: the accumulator has been read, and no write of this warp
+          // concerns the issuer; a release waited ~3,000 cycles for them)
+          if (lane == 0) mbar_arrive_remote_relaxed(map_peer(smem_u32(&bar.acc_free[acc]), 0));
           bool fin = true;
 #pragma unroll
           for (int k = 0; k < 64; ++k)
@@ -163,99 +186,127 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
           }
           if (lane == 0) reinterpret_cast<uint32_t*>(a.bad + slot)[warp] = nan_rows;
         }
-        // the images' last bulk stores (two parts ago) have read them
-        if (threadIdx.x == 0) bulk_wait_read<0>();
-        named_barrier(1, kEpiThreads);
+        named_barrier(1, kEpiThreads);  // (everyone has read the last images)
 #pragma unroll
         for (int u = 0; u < 16; ++u)
           *reinterpret_cast<uint4*>(smem + kOffOut + (u >> 3) * kImage + image_unit(row, u & 7)) =
               make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-        fence_proxy_async_smem();
         named_barrier(1, kEpiThreads);
-        if (threadIdx.x == 0) {
-          bulk_store((part ? a.values : a.keys) + slot * (2 * kImage), smem + kOffOut, 2 * kImage);
-          bulk_commit();
-        }
+        uint4* dst = reinterpret_cast<uint4*>((part ? a.values : a.keys) + slot * (2 * kImage));
+        const uint4* src = reinterpret_cast<const uint4*>(smem + kOffOut);
+#pragma unroll
+        for (int k = 0; k < 2 * kImage / 16 / kEpiThreads; ++k) dst[k * kEpiThreads + threadIdx.x] = src[k * kEpiThreads + threadIdx.x];
       }
     }
-    if (threadIdx.x == 0) bulk_wait<0>();
   } else if (warp == 4) {
     // -------------------------------------------------- weights
+    // (unrolled: with slots and phases computed from a counter a copy took this
+    // thread ~600 cycles, and eight of them more than an item's MMAs)
     if (elected()) {
-      uint32_t it = 0;
-      for (int32_t i = work.i0; i < work.i1 && !*stop; ++i) {
-        const int32_t h = a.h0 + i % a.heads;
-        const unsigned char* w = static_cast<const unsigned char*>(a.weight) + static_cast<int64_t>(h) * (kChunks * kWeightStage);
-        for (int c = 0; c < kChunks; ++c, ++it) {
-          const uint32_t s = it % kWStages, ph = (it / kWStages) & 1;
-          if (!mbar_wait(&bar.w_free[s], ph ^ 1)) { failed(); break; }
-          mbar_arrive_expect_tx(&bar.w_full[s], kWeightStage);
-          bulk_load(smem + kOffW + s * kWeightStage, w + c * kWeightStage, kWeightStage, &bar.w_full[s]);
+      bool ok = true;
+      int32_t h = work.i0 % a.heads;
+      const unsigned char* weight = static_cast<const unsigned char*>(a.weight) + static_cast<int64_t>(a.h0) * (kChunks * kWeightStage) + rank * kWHalf;
+      for (int32_t i = work.i0; i < work.i1 && ok; ++i) {
+        const unsigned char* w = weight + static_cast<int64_t>(h) * (kChunks * kWeightStage);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          constexpr int kS = kWStages;
+          const int s = c % kS;
+          ok = ok && mbar_wait(&bar.w_free[s], ((c / kS) & 1) ^ 1);
+          if (ok) {
+            mbar_arrive_expect_tx(&bar.w_full[s], kWHalf);
+            bulk_load(smem + kOffW + s * kWHalf, w + c * kWeightStage, kWHalf, &bar.w_full[s]);
+          }
         }
+        h = h + 1 == a.heads ? 0 : h + 1;
       }
-      // nothing lands after the CTA is gone
-      for (uint32_t k = it > kWStages ? it - kWStages : 0; k < it; ++k) mbar_wait(&bar.w_full[k % kWStages], (k / kWStages) & 1);
+      if (!ok) failed();
+      // nothing lands after the CTA is gone (each slot's last phase is odd)
+      if (work.i1 > work.i0)
+        for (int s = 0; s < kWStages; ++s) mbar_wait(&bar.w_full[s], 1);
     }
     __syncwarp();
   } else if (warp == 5) {
     // -------------------------------------------------- MMAs
-    const uint32_t id = idesc_bf16(128, 256, 0, 0);
-    const uint64_t da = smem_desc(smem_u32(smem + kOffA), 16, 1024, kSwizzle128B);
-    const uint64_t dw = smem_desc(smem_u32(smem + kOffW), 16, 1024, kSwizzle128B);
-    uint32_t it = 0, loads = 0;
-    int32_t last = -1;
-    bool ok = true;
-    for (int32_t i = work.i0, n = 0; i < work.i1 && ok; ++i, ++n) {
-      const int acc = n & 1;
-      const int32_t tile = i / a.heads;
-      if (tile != last) {
-        ok = mbar_wait_warp(&bar.a_full, loads & 1);
-        ++loads;
-        last = tile;
-      }
-      ok = ok && mbar_wait_warp(&bar.acc_free[acc], ((n >> 1) & 1) ^ 1);
-      tc_fence_after();
-      for (int c = 0; c < kChunks && ok; ++c, ++it) {
-        const uint32_t s = it % kWStages;
-        ok = mbar_wait_warp(&bar.w_full[s], (it / kWStages) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (elected()) {
-          const uint64_t ac = da + ((c * kImage) >> 4), wc = dw + ((s * kWeightStage) >> 4);
+    // (one lane, every operand a base plus constants: an issuing thread that
+    // computes what its next MMA needs falls behind the tensor pipe)
+    if (rank == 1) {
+      if (elected()) {
+        bool ok = true;
+        const uint32_t to = map_peer(smem_u32(&bar.w_peer[0]), 0);
+        for (int32_t i = work.i0; i < work.i1 && ok; ++i) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_ss(tmem + 256 * acc, ac + 2 * k, wc + 2 * k, id, (c | k) != 0);
-          mma_commit(&bar.w_free[s]);
+          for (int c = 0; c < kChunks; ++c) {
+            constexpr int kS = kWStages;
+            ok = ok && mbar_wait(&bar.w_full[c % kS], (c / kS) & 1);
+            if (ok) mbar_arrive_remote_relaxed(to + 8 * (c % kS));
+          }
         }
-        __syncwarp();
+        if (!ok) failed();
+        mbar_wait(&bar.fin, 0);
       }
-      if (ok && elected()) {
-        mma_commit(&bar.acc_full[acc]);
-        if (i + 1 == work.i1 || (i + 1) / a.heads != tile) mma_commit(&bar.a_free);
+    } else if (elected()) {
+      constexpr uint32_t id = idesc_bf16(256, 256, 0, 0);
+      const uint64_t da = smem_desc(smem_u32(smem + kOffA), 16, 1024, kSwizzle128B);
+      const uint64_t dw = smem_desc(smem_u32(smem + kOffW), 16, 1024, kSwizzle128B);
+      uint32_t loads = 0, acc_phase = 1;
+      int32_t left = 0;  // items of the tile at hand
+      bool ok = true;
+      int32_t tile_end = (work.i0 / a.heads) * a.heads;  // first item of the next tiles
+      // item n of this CTA, into accumulator `acc`
+      auto item = [&](auto acc_c, int32_t i) {
+        constexpr uint32_t acc = decltype(acc_c)::value;
+        if (left == 0) {
+          ok = ok && mbar_wait_cluster(&bar.a_full, loads & 1);
+          ++loads;
+          tile_end += a.heads;
+          left = min(tile_end, work.i1) - i;
+        }
+        ok = ok && mbar_wait_cluster(&bar.acc_free[acc], acc_phase);
+        if (!ok) return;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          constexpr int kS = kWStages;
+          const int st = c % kS;
+          ok = ok && mbar_wait(&bar.w_full[st], (c / kS) & 1) && mbar_wait_cluster(&bar.w_peer[st], (c / kS) & 1);
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss_pair(256 * acc, da + ((c * kImage) >> 4) + 2 * k, dw + ((st * kWHalf) >> 4) + 2 * k, id, (c | k) != 0);
+          mma_commit_pair(&bar.w_free[st]);
+        }
+        static_assert(kChunks % (2 * kWStages) == 0, "the ring's phase is the same for every item");
+        mma_commit_pair(&bar.acc_full[acc]);
+        if (--left == 0) mma_commit_pair(&bar.a_free);
+      };
+      for (int32_t i = work.i0; i < work.i1 && ok; i += 2, acc_phase ^= 1) {
+        item(std::integral_constant<uint32_t, 0>{}, i);
+        if (i + 1 < work.i1 && ok) item(std::integral_constant<uint32_t, 1>{}, i + 1);
       }
-      __syncwarp();
+      if (!ok) failed();
+      mma_commit_pair(&bar.fin);  // the MMAs are complete before TMEM goes
+      mbar_wait(&bar.fin, 0);
     }
-    if (!ok) failed();
-    // the MMAs are complete before TMEM goes
-    if (elected()) mma_commit(&bar.fin);
     __syncwarp();
-    mbar_wait_warp(&bar.fin, 0);
   } else if (warp >= 8) {
     // -------------------------------------------------- latents
     const int lw = warp - 8;
     int32_t last = -1;
     uint32_t loads = 0;
     for (int32_t i = work.i0; i < work.i1; i = (last + 1) * a.heads) {
-      const int32_t tile = i / a.heads;
-      last = tile;
-      // this thread's token
-      const int32_t b = find_range(a.tile_start, a.B, tile);
-      const int32_t seq = a.seq_lens[b];
-      const int64_t p = static_cast<int64_t>(tile - a.tile_start[b]) * kChunkTile + 32 * lw + lane;
+      last = i / a.heads;
+      const int32_t tile = 2 * last + static_cast<int32_t>(rank);
+      // this thread's token (a tile past the last is all zeros)
       int64_t src = -1;
-      if (p < seq) src = cache_row(a, b, static_cast<int32_t>(p));
+      if (tile < tiles) {
+        const int32_t b = find_range(a.tile_start, a.B, tile);
+        const int64_t p = static_cast<int64_t>(tile - a.tile_start[b]) * kChunkTile + 32 * lw + lane;
+        if (p < a.seq_lens[b]) src = cache_row(a, b, static_cast<int32_t>(p));
+      }
       const float scale = kFp8 && src >= 0 ? __ldg(a.kv_scale + src) : 0.f;
       // what the heads share is written with the first head
-      const bool shared_too = a.h0 == 0 && i == tile * a.heads;
+      const bool shared_too = a.h0 == 0 && i == last * a.heads && tile < tiles;
       const uint32_t live = __ballot_sync(0xffffffffu, src >= 0);
       if (shared_too && lane == 0) reinterpret_cast<uint32_t*>(a.valid + tile)[lw] = live;
       if (loads > 0 && !mbar_wait_warp(&bar.a_free, (loads - 1) & 1)) { failed(); break; }
@@ -293,13 +344,14 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
         cp_async_wait<0>();
       }
       fence_proxy_async_smem();
-      mbar_arrive(&bar.a_full);
+      mbar_arrive_remote(map_peer(smem_u32(&bar.a_full), 0));
     }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // (neither CTA goes while the other's MMAs or arrivals need it)
   tc_fence_after();
-  if (warp == 6) tmem_dealloc(tmem, 512);
+  if (warp == 6) tmem_dealloc_pair(bar.tmem, 512);
 }
 
 // packed[h][c] = rows 256 h .. 256 h + 255 of w [H x 256, 512], latent dims
@@ -384,17 +436,20 @@ cudaError_t set_up() {
   return e;
 }
 
-cudaError_t launch_pdl(void (*kernel)(ChunkArgs), const ChunkArgs& a, int grid, int threads, int smem, cudaStream_t st) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+cudaError_t launch_pairs(void (*kernel)(ChunkArgs), const ChunkArgs& a, int grid, int threads, int smem, cudaStream_t st) {
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
@@ -418,9 +473,9 @@ cudaError_t launch_chunk_expand(const ChunkArgs& a, cudaStream_t st) {
   if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int64_t items = static_cast<int64_t>(a.tiles) * a.heads;
-  const int grid = static_cast<int>(items < sms ? items : sms);
-  return launch_pdl(a.kv_scale ? expand_kernel<true> : expand_kernel<false>, a, grid, kThreads, kSmemBytes, st);
+  const int64_t items = static_cast<int64_t>((a.tiles + 1) / 2) * a.heads;
+  const int grid = 2 * static_cast<int>(items < sms / 2 ? items : sms / 2);
+  return launch_pairs(a.kv_scale ? expand_kernel<true> : expand_kernel<false>, a, grid, kThreads, kSmemBytes, st);
 }
 
 }  // namespace dcp
