@@ -14,9 +14,11 @@
 // ring of two 32 KB stages, waited for its weights: 24,000 tokens at 128 heads
 // 851 us.)
 //
-// Warp roles (384 threads in each CTA of the pair):
-//   warps 0-3   epilogue: accumulator -> bf16 -> images in shared memory -> bulk
-//               stores; thread = token = TMEM lane
+// Warp roles (512 threads in each CTA of the pair):
+//   warps 0-3, 12-15  epilogue of the keys and of the values: accumulator -> bf16
+//               -> images in shared memory -> bulk stores; thread = token = TMEM
+//               lane.  (By four warps for both ~3,400 cycles an item; with plain
+//               stores ~4,500, more than its MMAs' 4,096.)
 //   warp 4      weights: 16 KB bulk copies (64 latent dims of half a head's rows)
 //   warp 5      CTA 0: MMA issuer, two accumulators; CTA 1: tells CTA 0 of its
 //               weights
@@ -40,24 +42,24 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 384;
-constexpr int kEpiThreads = 128, kLoadThreads = 128;
+constexpr int kThreads = 512;
+constexpr int kLoadThreads = 128;
 constexpr int kChunks = kLatent / 64;  // 8 chunks of 64 latent dims
-constexpr int kWStages = 4;
+constexpr uint32_t kWStages = 4;
 constexpr int kWHalf = kWeightStage / 2;  // a CTA's rows of a weight stage
 constexpr int kOffA = 0;
 constexpr int kOffW = kChunks * kImage;
 constexpr int kOffOut = kOffW + kWStages * kWHalf;
-constexpr int kOffBars = kOffOut + 2 * kImage;
+constexpr int kOutWarp = 32 * 128;        // an epilogue warp's 32 rows of an image
+constexpr int kOffBars = kOffOut + 8 * kOutWarp;
 
 struct Bars {
   uint64_t a_full;            // CTA 0: both CTAs' latents are in shared memory (every loader)
   uint64_t a_free;            // both: the tiles' MMAs are complete
-  uint64_t w_full[kWStages];  // both: this CTA's half of a weight stage landed
-  uint64_t w_peer[kWStages];  // CTA 0: CTA 1's half landed
+  uint64_t w_full[kWStages];  // a weight stage landed: CTA 1 its half, CTA 0 both (CTA 1 tells it)
   uint64_t w_free[kWStages];  // both
   uint64_t acc_full[2];       // both: an accumulator is complete
-  uint64_t acc_free[2];       // CTA 0: both CTAs' epilogues have read it (4 warps each)
+  uint64_t acc_free[2];       // CTA 0: both CTAs' epilogues have read it (8 warps each)
   uint64_t fin;               // both: the issuer's MMAs are complete
   uint32_t tmem;
   int32_t abort;
@@ -109,11 +111,12 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
   Bars& bar = *reinterpret_cast<Bars*>(smem + kOffBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();
+  const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
     mbar_init(&bar.a_full, 2 * kLoadThreads);
     mbar_init(&bar.a_free, 1);
-    for (int i = 0; i < kWStages; ++i) mbar_init(&bar.w_full[i], 1), mbar_init(&bar.w_peer[i], 1), mbar_init(&bar.w_free[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&bar.acc_full[i], 1), mbar_init(&bar.acc_free[i], 8);
+    for (uint32_t i = 0; i < kWStages; ++i) mbar_init(&bar.w_full[i], rank == 0 ? 2 : 1), mbar_init(&bar.w_free[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bar.acc_full[i], 1), mbar_init(&bar.acc_free[i], 16);
     mbar_init(&bar.fin, 1);
     bar.abort = 0;
     fence_mbar_init();
@@ -126,7 +129,6 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
   __syncthreads();
   cluster_sync();  // (the peer's barriers are set up)
   tc_fence_after();
-  const uint32_t rank = cluster_ctarank();
   const uint32_t tmem = 0;  // (all 512 columns: the allocation starts at the first)
   wait_dependency();
   const int32_t tiles = min(a.tile_start[a.B], a.tiles);
@@ -137,93 +139,97 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     *stop = 1;
   };
 
-  if (warp < 4) {
+  if (warp < 4 || warp >= 12) {
     // -------------------------------------------------- epilogue
-    const int row = threadIdx.x;
+    const int part = warp >= 12, quad = warp & 3;  // keys or values; the warp's TMEM lanes
+    unsigned char* stage = smem + kOffOut + (4 * part + quad) * kOutWarp;
+    const uint32_t free0 = map_peer(smem_u32(&bar.acc_free[0]), 0);
+    unsigned char* images = part ? a.values : a.keys;
+    int32_t pair = work.i0 / a.heads, h = work.i0 - pair * a.heads;
     for (int32_t i = work.i0, n = 0; i < work.i1; ++i, ++n) {
       const int acc = n & 1;
-      const bool ok = mbar_wait(&bar.acc_full[acc], (n >> 1) & 1) && !*stop;
-      if (!named_barrier_and(1, kEpiThreads, ok)) { failed(); break; }  // (one answer: barriers follow)
+      if (!mbar_wait_warp(&bar.acc_full[acc], (n >> 1) & 1)) { failed(); break; }
       tc_fence_after();
-      const int32_t pair = i / a.heads, h = i - pair * a.heads;
       const int32_t tile = 2 * pair + static_cast<int32_t>(rank);
-      if (tile >= tiles) {  // (the last tile has no second one)
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote_relaxed(map_peer(smem_u32(&bar.acc_free[acc]), 0));
-        continue;
-      }
       const int64_t slot = static_cast<int64_t>(h) * a.tiles + tile;
-      const uint32_t col = tmem + (static_cast<uint32_t>(warp) << 21) + 256u * acc;
-#pragma unroll 1
-      for (int part = 0; part < 2; ++part) {  // keys, values
-        uint32_t v[64];  // 128 dims as bf16 pairs
+      const uint32_t col = tmem + (static_cast<uint32_t>(quad) << 21) + 256u * acc + 128u * part;
+      uint32_t v[64];  // 128 dims as bf16 pairs
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          tmem_ld32(col + 128 * part + 32 * c, r);
-          tmem_wait_ld();
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        tmem_ld32(col + 32 * c, r);
+        tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
-            v[16 * c + k] = *reinterpret_cast<const uint32_t*>(&b);
-          }
+        for (int k = 0; k < 16; ++k) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+          v[16 * c + k] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        if (part == 1) {
-          tc_fence_before();
-          __syncwarp();
-          // (relaxed: the accumulator has been read, and no write of this warp
-          // concerns the issuer; a release waited ~3,000 cycles for them)
-          if (lane == 0) mbar_arrive_remote_relaxed(map_peer(smem_u32(&bar.acc_free[acc]), 0));
+      }
+      tc_fence_before();
+      __syncwarp();
+      // (relaxed: the accumulator has been read, and no write of this warp
+      // concerns the issuer; a release waited ~3,000 cycles for them)
+      if (lane == 0) mbar_arrive_remote_relaxed(free0 + 8 * acc);
+      if (tile < tiles) {  // (the last tile may have no second one)
+        if (part) {
           bool fin = true;
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
-            fin = fin && (v[k] & 0x7f80u) != 0x7f80u && (v[k] & 0x7f800000u) != 0x7f800000u;
+          for (int k = 0; k < 64; ++k) fin = fin && (v[k] & 0x7f80u) != 0x7f80u && (v[k] & 0x7f800000u) != 0x7f800000u;
           const uint32_t nan_rows = __ballot_sync(0xffffffffu, !fin);
           if (!fin) {
 #pragma unroll
             for (int k = 0; k < 64; ++k) v[k] = 0;
           }
-          if (lane == 0) reinterpret_cast<uint32_t*>(a.bad + slot)[warp] = nan_rows;
+          if (lane == 0) reinterpret_cast<uint32_t*>(a.bad + slot)[quad] = nan_rows;
         }
-        named_barrier(1, kEpiThreads);  // (everyone has read the last images)
+        unsigned char* dst = images + slot * (2 * kImage) + quad * kOutWarp;
 #pragma unroll
-        for (int u = 0; u < 16; ++u)
-          *reinterpret_cast<uint4*>(smem + kOffOut + (u >> 3) * kImage + image_unit(row, u & 7)) =
-              make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-        named_barrier(1, kEpiThreads);
-        uint4* dst = reinterpret_cast<uint4*>((part ? a.values : a.keys) + slot * (2 * kImage));
-        const uint4* src = reinterpret_cast<const uint4*>(smem + kOffOut);
+        for (int c = 0; c < 2; ++c) {  // an image's 64 dims
+          if (elected()) bulk_wait_read<0>();  // (the last store has read its source)
+          __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 2 * kImage / 16 / kEpiThreads; ++k) dst[k * kEpiThreads + threadIdx.x] = src[k * kEpiThreads + threadIdx.x];
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<uint4*>(stage + image_unit(lane, u)) =
+                make_uint4(v[32 * c + 4 * u], v[32 * c + 4 * u + 1], v[32 * c + 4 * u + 2], v[32 * c + 4 * u + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (elected()) {
+            bulk_store(dst + c * kImage, stage, kOutWarp);
+            bulk_commit();
+          }
+        }
       }
+      if (++h == a.heads) h = 0, ++pair;
     }
+    if (elected()) bulk_wait<0>();
+    __syncwarp();
   } else if (warp == 4) {
     // -------------------------------------------------- weights
-    // (unrolled: with slots and phases computed from a counter a copy took this
-    // thread ~600 cycles, and eight of them more than an item's MMAs)
+    // (running slots and phases: with ones computed from a counter a copy took
+    // this thread ~600 cycles, and eight of them more than an item's MMAs)
     if (elected()) {
       bool ok = true;
       int32_t h = work.i0 % a.heads;
+      uint32_t s = 0, phase = 0, used = 0;
+      const uint64_t keep = l2_keep();  // (the images that stream out would push the weights out)
       const unsigned char* weight = static_cast<const unsigned char*>(a.weight) + static_cast<int64_t>(a.h0) * (kChunks * kWeightStage) + rank * kWHalf;
       for (int32_t i = work.i0; i < work.i1 && ok; ++i) {
         const unsigned char* w = weight + static_cast<int64_t>(h) * (kChunks * kWeightStage);
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          constexpr int kS = kWStages;
-          const int s = c % kS;
-          ok = ok && mbar_wait(&bar.w_free[s], ((c / kS) & 1) ^ 1);
+          ok = ok && mbar_wait(&bar.w_free[s], phase ^ 1);
           if (ok) {
             mbar_arrive_expect_tx(&bar.w_full[s], kWHalf);
-            bulk_load(smem + kOffW + s * kWHalf, w + c * kWeightStage, kWHalf, &bar.w_full[s]);
+            bulk_load_hint(smem + kOffW + s * kWHalf, w + c * kWeightStage, kWHalf, &bar.w_full[s], keep);
+            ++used;
           }
+          if (++s == kWStages) s = 0, phase ^= 1;
         }
         h = h + 1 == a.heads ? 0 : h + 1;
       }
       if (!ok) failed();
-      // nothing lands after the CTA is gone (each slot's last phase is odd)
-      if (work.i1 > work.i0)
-        for (int s = 0; s < kWStages; ++s) mbar_wait(&bar.w_full[s], 1);
+      // nothing lands after the CTA is gone
+      for (uint32_t k = used > kWStages ? used - kWStages : 0; k < used; ++k) mbar_wait(&bar.w_full[k % kWStages], (k / kWStages) & 1);
     }
     __syncwarp();
   } else if (warp == 5) {
@@ -233,13 +239,16 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     if (rank == 1) {
       if (elected()) {
         bool ok = true;
-        const uint32_t to = map_peer(smem_u32(&bar.w_peer[0]), 0);
+        const uint32_t to = map_peer(smem_u32(&bar.w_full[0]), 0);
+        uint32_t s = 0, phase = 0;
         for (int32_t i = work.i0; i < work.i1 && ok; ++i) {
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
-            constexpr int kS = kWStages;
-            ok = ok && mbar_wait(&bar.w_full[c % kS], (c / kS) & 1);
-            if (ok) mbar_arrive_remote_relaxed(to + 8 * (c % kS));
+            ok = ok && mbar_wait(&bar.w_full[s], phase);
+            // (relaxed: this thread has written nothing, and the copy is in
+            // shared memory once its barrier says so; a release took ~1,500 cycles)
+            if (ok) mbar_arrive_remote_relaxed(to + 8 * s);
+            if (++s == kWStages) s = 0, phase ^= 1;
           }
         }
         if (!ok) failed();
@@ -249,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       constexpr uint32_t id = idesc_bf16(256, 256, 0, 0);
       const uint64_t da = smem_desc(smem_u32(smem + kOffA), 16, 1024, kSwizzle128B);
       const uint64_t dw = smem_desc(smem_u32(smem + kOffW), 16, 1024, kSwizzle128B);
-      uint32_t loads = 0, acc_phase = 1;
+      uint32_t loads = 0, acc_phase = 1, st = 0, phase = 0;
       int32_t left = 0;  // items of the tile at hand
       bool ok = true;
       int32_t tile_end = (work.i0 / a.heads) * a.heads;  // first item of the next tiles
@@ -266,17 +275,17 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
         if (!ok) return;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          constexpr int kS = kWStages;
-          const int st = c % kS;
-          ok = ok && mbar_wait(&bar.w_full[st], (c / kS) & 1) && mbar_wait_cluster(&bar.w_peer[st], (c / kS) & 1);
+          // (one barrier for both halves: a wait takes ~200 cycles even when
+          // nothing is left to wait for)
+          ok = ok && mbar_wait_cluster(&bar.w_full[st], phase);
           if (!ok) return;
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_ss_pair(256 * acc, da + ((c * kImage) >> 4) + 2 * k, dw + ((st * kWHalf) >> 4) + 2 * k, id, (c | k) != 0);
           mma_commit_pair(&bar.w_free[st]);
+          if (++st == kWStages) st = 0, phase ^= 1;
         }
-        static_assert(kChunks % (2 * kWStages) == 0, "the ring's phase is the same for every item");
         mma_commit_pair(&bar.acc_full[acc]);
         if (--left == 0) mma_commit_pair(&bar.a_free);
       };
@@ -289,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       mbar_wait(&bar.fin, 0);
     }
     __syncwarp();
-  } else if (warp >= 8) {
+  } else if (warp >= 8) {  // (to 11)
     // -------------------------------------------------- latents
     const int lw = warp - 8;
     int32_t last = -1;
