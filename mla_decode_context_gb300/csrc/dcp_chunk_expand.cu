@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     unsigned char* stage = smem + kOffOut + (4 * part + quad) * kOutWarp;
     const uint32_t free0 = map_peer(smem_u32(&bar.acc_free[0]), 0);
     unsigned char* images = part ? a.values : a.keys;
+    const uint64_t stream = l2_stream();
     int32_t pair = work.i0 / a.heads, h = work.i0 - pair * a.heads;
     for (int32_t i = work.i0, n = 0; i < work.i1; ++i, ++n) {
       const int acc = n & 1;
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
           fence_proxy_async_smem();
           __syncwarp();
           if (elected()) {
-            bulk_store(dst + c * kImage, stage, kOutWarp);
+            bulk_store_hint(dst + c * kImage, stage, kOutWarp, stream);
             bulk_commit();
           }
         }
