@@ -19,6 +19,9 @@
 //   warp 9          loads: bulk copies of 16 KB images into a ring of 8 slots (a
 //                   tile takes three for K, two for V)
 //   warp 10         TMEM allocation
+//   warp 11         gate: waits for V(j) and adds its arrival to the softmax's,
+//                   so that the issuer has one barrier to wait for (a wait takes
+//                   ~200 cycles even when nothing is left to wait for)
 // The running maximum moves only when a row's scores grow past it by 2^8 (P is
 // at most 256 then, and bf16 has the same relative step there), so O is
 // rescaled a few times per unit at most.
@@ -49,11 +52,11 @@ constexpr float kRescaleLog2 = 8.0f;
 
 struct Bars {
   uint64_t q_full[2];                  // a group's Q is in shared memory (128)
-  uint64_t full[kSlots], free_[kSlots];
+  uint64_t k_full[2], v_full[2];       // K(j), V(j) are in the ring (barrier j mod 2)
+  uint64_t k_free[2], v_free[2];       // both groups are done with them
   uint64_t mask_full[kMaskSlots];
-  uint64_t s_full[2];                  // S_g(j) is in TMEM
-  uint64_t p_full[2];                  // P_g(j) is in TMEM and O_g in its scale (4 warps)
-  uint64_t pv_done[2];                 // PV_g(j) is complete
+  uint64_t s_full[2];                  // S_g(j) is in TMEM and PV_g(j - 1) complete; last, PV_g of the last tile
+  uint64_t p_full[2];                  // P_g(j) is in TMEM and O_g in its scale (4 warps); V(j) is there (gate)
   uint64_t fin;
   uint32_t tmem;
   int32_t abort;
@@ -94,25 +97,19 @@ __device__ __forceinline__ Tile tile_of(const Bars& bar, int g, int32_t have) {
 // The issuing lane's work on tile j for group g: PV(j - 1), then S(j).
 struct Issue {
   Bars& bar;
-  const uint64_t dq, dk, dv;
+  const uint64_t dq, dring;
   const int32_t n0, n1;
   bool ok;
 
   template <int g>
-  __device__ __forceinline__ void step(int32_t j, uint32_t k0) {
+  __device__ __forceinline__ void step(int32_t j, uint32_t k0) {  // k0: K(j)'s first image
     const int32_t tiles = g ? n1 : n0, n = n0 > n1 ? n0 : n1;
-    // (images that the other group has waited for are there)
-    const bool first_v = g == 0 || j - 1 >= n0, first_k = g == 0 || j >= n0;
-    const uint32_t v0 = (k0 - kVChunks) % kSlots, v1 = (v0 + 1) % kSlots;
     if (j >= 1 && j - 1 < tiles && ok) {  // O_g += P_g(j - 1) V(j - 1)
-      if (first_v) {
-        ok = mbar_wait(&bar.full[v0], ((k0 - kVChunks) / kSlots) & 1);
-        ok = ok && mbar_wait(&bar.full[v1], ((k0 - kVChunks + 1) / kSlots) & 1);
-      }
-      ok = ok && mbar_wait(&bar.p_full[g], (j - 1) & 1);
+      const uint32_t v0 = (k0 - kVChunks) % kSlots, v1 = (v0 + 1) % kSlots;
+      ok = mbar_wait(&bar.p_full[g], (j - 1) & 1);
       if (!ok) return;
       tc_fence_after();
-      const uint64_t d = dv + ((v0 * kImage) >> 4);
+      const uint64_t d = dring + ((v0 * kImage) >> 4);
       constexpr uint32_t o = kColO + 128 * g, p = kColS + 128 * g;
       if (v1 == v0 + 1) {
         constexpr uint32_t id = idesc_bf16(128, 128, 0, 1);
@@ -124,36 +121,27 @@ struct Issue {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           mma_ts(o, p + 8 * k, d + ((2048 * k) >> 4), id, j > 1 || k > 0);
-          mma_ts(o + 64, p + 8 * k, dv + ((2048 * k) >> 4), id, j > 1 || k > 0);
+          mma_ts(o + 64, p + 8 * k, dring + ((2048 * k) >> 4), id, j > 1 || k > 0);
         }
       }
-      mma_commit(&bar.pv_done[g]);
+      if (j == tiles) mma_commit(&bar.s_full[g]);
     }
-    if (g == 1 && j >= 1) {
-      mma_commit(&bar.free_[v0]);
-      mma_commit(&bar.free_[v1]);
-    }
+    if (g == 1 && j >= 1) mma_commit(&bar.v_free[(j - 1) & 1]);
     if (j < tiles && ok) {  // S_g(j) = Q_g K(j)^T
       if (j == 0) ok = mbar_wait(&bar.q_full[g], 0);
+      if (g == 0 || j >= n0) ok = ok && mbar_wait(&bar.k_full[j & 1], (j >> 1) & 1);  // (else group 0 has waited)
+      if (!ok) return;
+      tc_fence_after();
 #pragma unroll
       for (int c = 0; c < kQChunks; ++c) {
-        const uint32_t s = (k0 + c) % kSlots;
-        if (first_k) {
-          ok = ok && mbar_wait(&bar.full[s], ((k0 + c) / kSlots) & 1);
-          if (!ok) return;
-          tc_fence_after();
-        }
-        const uint64_t q = dq + (((g * kQChunks + c) * kImage) >> 4), k = dk + ((s * kImage) >> 4);
+        const uint64_t q = dq + (((g * kQChunks + c) * kImage) >> 4), k = dring + ((((k0 + c) % kSlots) * kImage) >> 4);
         constexpr uint32_t id = idesc_bf16(128, 128, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) mma_ss(kColS + 128 * g, q + 2 * i, k + 2 * i, id, (c | i) != 0);
       }
       mma_commit(&bar.s_full[g]);
     }
-    if (g == 1 && j < n) {
-#pragma unroll
-      for (int c = 0; c < kQChunks; ++c) mma_commit(&bar.free_[(k0 + c) % kSlots]);
-    }
+    if (g == 1 && j < n) mma_commit(&bar.k_free[j & 1]);
   }
 };
 
@@ -196,10 +184,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     for (int g = 0; g < 2; ++g) {
       mbar_init(&bar.q_full[g], kGroup);
       mbar_init(&bar.s_full[g], 1);
-      mbar_init(&bar.p_full[g], 4);
-      mbar_init(&bar.pv_done[g], 1);
+      mbar_init(&bar.p_full[g], 5);
+      mbar_init(&bar.k_full[g], 1), mbar_init(&bar.v_full[g], 1);
+      mbar_init(&bar.k_free[g], 1), mbar_init(&bar.v_free[g], 1);
     }
-    for (uint32_t i = 0; i < kSlots; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.free_[i], 1);
     for (int i = 0; i < kMaskSlots; ++i) mbar_init(&bar.mask_full[i], 1);
     mbar_init(&bar.fin, 1);
     fence_mbar_init();
@@ -239,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   if (warp < 8) {
     // -------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int g = warp >> 2, row = threadIdx.x & 127;
+    const int g = warp >> 2, quad = warp & 3, row = threadIdx.x & 127;
     const int32_t tiles = g ? n1 : n0, rows = g ? t1.rows : t0.rows, first = g ? t1.first : t0.first;
     const int64_t r = static_cast<int64_t>(bar.q0) + first + row;  // this thread's query row
     unsigned char* qs = smem + kOffQ + g * (kQChunks * kImage);
@@ -247,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     if (tiles > 0) {
 #pragma unroll 2
       for (int i = 0; i < 32; i += 4) {
-        const int qr = 32 * (warp & 3) + i + (lane >> 3), un = lane & 7;
+        const int qr = 32 * quad + i + (lane >> 3), un = lane & 7;
         const bool in = qr < rows && static_cast<int64_t>(bar.q0) + first + qr < a.T;
         const __nv_bfloat16* src = a.q + (static_cast<int64_t>(bar.q0) + first + qr) * a.q_stride_tok + h * a.q_stride_head + 8 * un;
 #pragma unroll
@@ -263,14 +251,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
     const int32_t L = static_cast<int32_t>(max(static_cast<int64_t>(0), static_cast<int64_t>(bar.seq) - (bar.q1 - bar.q0 - 1) + first + row));
     const int32_t L_first = __shfl_sync(0xffffffffu, L, 0);  // the least of the warp's
-    const uint32_t ts = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kColS + 128u * g;
+    const uint32_t ts = tmem + (static_cast<uint32_t>(quad) << 21) + kColS + 128u * g;
     const uint32_t to = ts - kColS + kColO;
     float m = -INFINITY, l = 0.f;  // running maximum (log2, scaled) and sum
     bool ok = true, nan_row = false;
     const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2);
     for (int32_t j = 0; j < tiles; ++j) {
-      ok = mbar_wait_warp(&bar.s_full[g], j & 1) && !*stop;
-      ok = ok && mbar_wait_warp(&bar.mask_full[j % kMaskSlots], (j / kMaskSlots) & 1);
+      ok = mbar_wait_warp(&bar.mask_full[j % kMaskSlots], (j / kMaskSlots) & 1);  // (long there)
+      ok = ok && mbar_wait_warp(&bar.s_full[g], j & 1);
       if (!ok) break;
       tc_fence_after();
       float s[128];
@@ -293,6 +281,30 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           for (int k = 0; k < 32; ++k) s[32 * w + k] = (see >> k) & 1u ? s[32 * w + k] : -INFINITY;
         }
       }
+      // P and the maximum side by side: the maximum nearly always stays within
+      // 2^8 of the running one, and then P is right as it is
+      auto weigh = [&](float base) {
+        const uint64_t nb = f2_pack(-base, -base);
+        uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+        for (int part = 0; part < 4; ++part) {
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float x, y;
+            f2_unpack(f2_fma(f2_pack(s[32 * part + 2 * k], s[32 * part + 2 * k + 1]), c2, nb), x, y);
+            x = ex2_approx(x);
+            y = ex2_approx(y);
+            sum[k & 1] = f2_add(sum[k & 1], f2_pack(x, y));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+            p[k] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          tmem_st16(ts + 16 * part, p);
+        }
+        float x, y;
+        f2_unpack(f2_add(sum[0], sum[1]), x, y);
+        return x + y;
+      };
       float mx[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) mx[k] = max3(s[k], s[k + 4], s[k + 8]);
@@ -303,17 +315,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
       for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[124 + k]);
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-      // (a scale of 0 times an infinite score is NaN: such a row is NaN through its sum)
-      if (__any_sync(0xffffffffu, top > m + kRescaleLog2 || (m == -INFINITY && top > m))) {
-        const bool grow = top > m + kRescaleLog2 || (m == -INFINITY && top > m);
+      float add = weigh(m == -INFINITY ? 0.f : m);
+      const bool grow = top > m + kRescaleLog2 || (m == -INFINITY && top > m);
+      if (__any_sync(0xffffffffu, grow)) {
         const float to_m = grow ? top : m;
         const float f = grow ? ex2_approx(m - to_m) : 1.f;
         m = to_m;
         l *= f;
-        if (j > 0) {
-          ok = mbar_wait_warp(&bar.pv_done[g], (j - 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
+        if (j > 0) {  // (PV(j - 1) is complete: S(j) came after it)
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             uint32_t o[16];
@@ -324,41 +333,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             tmem_st16(to + 16 * c, o);
           }
         }
+        add = weigh(m == -INFINITY ? 0.f : m);
       }
-      const float base = m == -INFINITY ? 0.f : m;
-      const uint64_t nb = f2_pack(-base, -base);
-      uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t p[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          float x, y;
-          f2_unpack(f2_fma(f2_pack(s[64 * half + 2 * k], s[64 * half + 2 * k + 1]), c2, nb), x, y);
-          x = ex2_approx(x);
-          y = ex2_approx(y);
-          sum[k & 1] = f2_add(sum[k & 1], f2_pack(x, y));
-          const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
-          p[k] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        tmem_st32(ts + 32 * half, p);
-      }
-      float x, y;
-      f2_unpack(f2_add(sum[0], sum[1]), x, y);
-      l += x + y;
+      l += add;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.p_full[g]);
     }
     // ---- output: O / l through shared memory (Q's, which no MMA reads any more)
-    if (tiles > 0 && ok) ok = mbar_wait_warp(&bar.pv_done[g], (tiles - 1) & 1);
+    if (tiles > 0 && ok) ok = mbar_wait_warp(&bar.s_full[g], tiles & 1);
     if (!ok) failed();
     tc_fence_after();
     if (nan_row) l = __int_as_float(0x7fc00000);
     const float inv = tiles > 0 && l != 0.f ? 1.0f / l : 0.f;
     if (row < rows && r < a.T) a.lse[r * a.H + h] = tiles > 0 && l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-    const int wr = 32 * (warp & 3);  // this warp's rows
+    const int wr = 32 * quad;  // this warp's rows
     const int live = min(32, static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(rows), a.T - static_cast<int64_t>(bar.q0) - first) - wr)));
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {  // 32 dims at a time; a warp's rows are its own
@@ -371,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       for (int k = 0; k < 32; ++k) o[k] = tiles > 0 && l != 0.f ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
       unsigned char* stage = qs + wr * 128;
       const int64_t out0 = (static_cast<int64_t>(bar.q0) + first + wr) * a.H + h;
+      const int dim = 32 * c;
       __syncwarp();
       if (a.out_f32) {  // 128 bytes a row: eight lanes each
 #pragma unroll
@@ -381,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         for (int k = 0; k < 8; ++k) {
           const int q = 4 * k + (lane >> 3);
           if (q < live)
-            *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + (out0 + static_cast<int64_t>(q) * a.H) * kVDim + 32 * c + 4 * (lane & 7)) =
+            *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + (out0 + static_cast<int64_t>(q) * a.H) * kVDim + dim + 4 * (lane & 7)) =
                 *reinterpret_cast<const uint4*>(stage + image_unit(q, lane & 7));
         }
       } else {  // 64 bytes a row: four lanes each
@@ -400,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         for (int k = 0; k < 4; ++k) {
           const int q = 8 * k + (lane >> 2);
           if (q < live)
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (out0 + static_cast<int64_t>(q) * a.H) * kVDim + 32 * c + 8 * (lane & 3)) =
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (out0 + static_cast<int64_t>(q) * a.H) * kVDim + dim + 8 * (lane & 3)) =
                 *reinterpret_cast<const uint4*>(stage + image_unit(q, lane & 3));
         }
       }
@@ -413,10 +404,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       // computes what its next MMA needs falls behind the tensor pipe)
       if (elected()) {
         const uint64_t dq = smem_desc(smem_u32(smem + kOffQ), 16, 1024, kSwizzle128B);
-        const uint64_t dk = smem_desc(smem_u32(smem + kOffRing), 16, 1024, kSwizzle128B);
-        const uint64_t dv = smem_desc(smem_u32(smem + kOffRing), kImage, 1024, kSwizzle128B);
-        Issue is{bar, dq, dk, dv, n0, n1, true};
-        uint32_t k0 = 0;  // K(j)'s first image
+        // (one descriptor for K and V: the distance of 64-dim images counts for V alone)
+        const uint64_t dring = smem_desc(smem_u32(smem + kOffRing), kImage, 1024, kSwizzle128B);
+        Issue is{bar, dq, dring, n0, n1, true};
+        uint32_t k0 = 0;
         for (int32_t j = 0; j <= n && is.ok; ++j, k0 += kPerTile) {
           is.step<0>(j, k0);
           is.step<1>(j, k0);
@@ -437,32 +428,57 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const uint4* valid = a.valid + image0;
         const uint4* bad = a.bad + static_cast<int64_t>(hp) * a.tiles + image0;
         unsigned char* ring = smem + kOffRing;
-        uint32_t it = 0;
+        // K(j) takes slots of K(j - 2) and V(j - 2), V(j) of K(j - 1)
+        uint32_t slot = 0;
+        int32_t nk = 0, nv = 0;  // loaded so far
         bool ok = true;
         for (int32_t j = 0; j < n && ok; ++j) {
-#pragma unroll
-          for (int c = 0; c < kPerTile; ++c, ++it) {
-            const uint32_t s = it % kSlots;
-            ok = ok && mbar_wait(&bar.free_[s], ((it / kSlots) & 1) ^ 1);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&bar.full[s], kImage);
-            bulk_load(ring + s * kImage, c < 2 ? keys + c * kImage : c == 2 ? rope : values + (c - 3) * kImage, kImage, &bar.full[s]);
-            if (c == 0) {
-              uint64_t* mb = &bar.mask_full[j % kMaskSlots];
-              unsigned char* dst = smem + kOffMask + (j % kMaskSlots) * 32;
-              mbar_arrive_expect_tx(mb, 32);
-              bulk_load(dst, valid, 16, mb);
-              bulk_load(dst + 16, bad, 16, mb);
-            }
-          }
+          const int32_t o = j & 1, before = (j - 1) & 1;
+          if (j >= 2) ok = mbar_wait(&bar.v_free[o], ((j >> 1) - 1) & 1);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bar.k_full[o], kQChunks * kImage);
+          bulk_load(ring + slot * kImage, keys, kImage, &bar.k_full[o]);
+          bulk_load(ring + ((slot + 1) % kSlots) * kImage, keys + kImage, kImage, &bar.k_full[o]);
+          bulk_load(ring + ((slot + 2) % kSlots) * kImage, rope, kImage, &bar.k_full[o]);
+          ++nk;
+          uint64_t* mb = &bar.mask_full[j % kMaskSlots];
+          unsigned char* dst = smem + kOffMask + (j % kMaskSlots) * 32;
+          mbar_arrive_expect_tx(mb, 32);
+          bulk_load(dst, valid, 16, mb);
+          bulk_load(dst + 16, bad, 16, mb);
+          if (j >= 1) ok = mbar_wait(&bar.k_free[before], ((j - 1) >> 1) & 1);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bar.v_full[o], kVChunks * kImage);
+          bulk_load(ring + ((slot + 3) % kSlots) * kImage, values, kImage, &bar.v_full[o]);
+          bulk_load(ring + ((slot + 4) % kSlots) * kImage, values + kImage, kImage, &bar.v_full[o]);
+          ++nv;
+          slot = (slot + kPerTile) % kSlots;
           keys += 2 * kImage, values += 2 * kImage, rope += kImage, ++valid, ++bad;
         }
         if (!ok) failed();
         // nothing lands after the CTA is gone
-        for (uint32_t k = it > kSlots ? it - kSlots : 0; k < it; ++k) mbar_wait(&bar.full[k % kSlots], (k / kSlots) & 1);
-        const uint32_t masks = (it + kPerTile - 1) / kPerTile;
-        for (uint32_t k = masks > kMaskSlots ? masks - kMaskSlots : 0; k < masks; ++k)
-          mbar_wait(&bar.mask_full[k % kMaskSlots], (k / kMaskSlots) & 1);
+        for (int32_t k = max(0, nk - 2); k < nk; ++k) mbar_wait(&bar.k_full[k & 1], (k >> 1) & 1);
+        for (int32_t k = max(0, nv - 2); k < nv; ++k) mbar_wait(&bar.v_full[k & 1], (k >> 1) & 1);
+        for (int32_t k = max(0, nk - kMaskSlots); k < nk; ++k) mbar_wait(&bar.mask_full[k % kMaskSlots], (k / kMaskSlots) & 1);
+      }
+      __syncwarp();
+    } else if (warp == 11) {
+      // -------------------------------------------------- gate
+      if (elected()) {
+        bool ok = true;
+        for (int32_t j = 0; j < n && ok; ++j) {
+          ok = mbar_wait(&bar.v_full[j & 1], (j >> 1) & 1);
+          // (an arrival counts for the phase that is open: the one of tile j - 1 must be over)
+          if (j < n0) {
+            if (j > 0) ok = ok && mbar_wait(&bar.p_full[0], (j - 1) & 1);
+            if (ok) mbar_arrive(&bar.p_full[0]);
+          }
+          if (j < n1) {
+            if (j > 0) ok = ok && mbar_wait(&bar.p_full[1], (j - 1) & 1);
+            if (ok) mbar_arrive(&bar.p_full[1]);
+          }
+        }
+        if (!ok) failed();
       }
       __syncwarp();
     }
