@@ -775,9 +775,11 @@ namespace {
 // shared parts (token masks and rope images), then keys, values and masks of as
 // many heads as there is room for.
 struct ChunkPlan {
-  int64_t tiles, units;
-  size_t starts, valid, rope, per_head;  // offsets of the parts, bytes of a head's
-  size_t fixed;                          // bytes of all but the heads'
+  int64_t tiles, units;                                // images per head, units per head
+  size_t starts, pieces, valid, rope;                  // offsets of the parts
+  size_t fixed;                                        // bytes of what the heads share
+  size_t image_bytes;                                  // bytes of a head's images
+  int sms;
 };
 constexpr size_t kChunkRecommended = size_t{4} << 30;
 
@@ -785,16 +787,36 @@ size_t round256(size_t n) { return (n + 255) & ~size_t{255}; }
 
 bool chunk_plan(int32_t B, int32_t T, int32_t H, int64_t total_len, ChunkPlan* p) {
   if (B < 0 || T < 0 || H < 1 || H > 1024 || total_len < 0 || total_len > (int64_t{1} << 36)) return false;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&p->sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || p->sms <= 0) {
+    cudaGetLastError();  // clear: no device is not an error for sizing
+    p->sms = 152;        // GB300
+  }
   p->tiles = total_len / dcp::kChunkTile + B;
   p->units = T / dcp::kChunkRows + static_cast<int64_t>(B) + 2;
-  if (p->tiles * H > 0x7fffffff || p->units * H > 0x7fffffff) return false;
+  const int64_t most = p->units + dcp::added_pieces(p->sms, 1);
+  if (p->tiles * H > 0x7fffffff || most * H > 0x7fffffff) return false;
   const size_t n = static_cast<size_t>(p->tiles);
   p->starts = 0;
-  p->valid = round256(2 * (static_cast<size_t>(B) + 1) * 4);
+  p->pieces = round256((2 * (static_cast<size_t>(B) + 1) + 1) * 4);
+  p->valid = round256(p->pieces + static_cast<size_t>(most) * sizeof(dcp::Piece));
   p->rope = round256(p->valid + n * 16);
   p->fixed = p->rope + n * dcp::kImage;
-  p->per_head = n * (4 * dcp::kImage + 16);
+  p->image_bytes = n * (4 * dcp::kImage + 16);
   return true;
+}
+
+// Slots for the pieces of cut units, per head of a pass of `heads`: twice the
+// pieces that the cuts add, and none where no unit is long enough to be cut.
+int64_t chunk_slots(const ChunkPlan& p, int32_t heads) {
+  if (p.tiles <= dcp::kMinPiece) return 0;
+  const int64_t by_units = p.units * std::min<int64_t>(dcp::kMaxPieces, (p.tiles + dcp::kMinPiece - 1) / dcp::kMinPiece);
+  return std::min(by_units, 2 * dcp::added_pieces(p.sms, heads));
+}
+size_t chunk_bytes(const ChunkPlan& p, int32_t heads) {
+  const size_t slots = static_cast<size_t>(chunk_slots(p, heads)) * heads;
+  return p.fixed + round256(p.image_bytes * heads) + round256(slots * 4) + slots * dcp::kSlotBytes;
 }
 
 }  // namespace
@@ -805,9 +827,9 @@ size_t dcp_chunk_attention_workspace_size(int32_t B, int32_t T, int32_t H, int64
   ChunkPlan p{};
   if (!chunk_plan(B, T, H, total_len, &p)) return static_cast<size_t>(-1);
   if (B == 0 || T == 0) return 0;
-  size_t heads = p.per_head > 0 ? kChunkRecommended / p.per_head : 1;
+  size_t heads = p.image_bytes > 0 ? kChunkRecommended / p.image_bytes : 1;
   heads = heads < 1 ? 1 : (heads > static_cast<size_t>(H) ? static_cast<size_t>(H) : heads);
-  return p.fixed + heads * p.per_head;
+  return chunk_bytes(p, static_cast<int32_t>(heads));
 }
 
 dcp_status_t dcp_pack_kv_b(const void* w_kv_b, int32_t H, void* packed, void* stream) {
@@ -842,12 +864,13 @@ dcp_status_t dcp_mla_chunk_attention(const void* q, int64_t q_stride_tok, int64_
   if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(packed_kv_b) || !aligned16(out) || !aligned16(workspace) ||
       q_stride_tok % 8 != 0 || q_stride_head % 8 != 0)
     return DCP_ERR_MISALIGNED;
-  if (!workspace || workspace_bytes < p.fixed + p.per_head) return DCP_ERR_WORKSPACE_TOO_SMALL;
   // heads per pass: as many as fit, in passes of nearly equal size
-  const size_t fit = (workspace_bytes - p.fixed) / p.per_head;
-  int32_t heads = fit < static_cast<size_t>(H) ? static_cast<int32_t>(fit) : H;
-  const int32_t passes = (H + heads - 1) / heads;
-  heads = (H + passes - 1) / passes;
+  int32_t heads = H;
+  while (heads > 1 && chunk_bytes(p, heads) > workspace_bytes) {
+    const int32_t passes = (H + heads - 1) / heads + 1;
+    heads = std::min(heads - 1, (H + passes - 1) / passes);
+  }
+  if (!workspace || chunk_bytes(p, heads) > workspace_bytes) return DCP_ERR_WORKSPACE_TOO_SMALL;
   dcp::ChunkArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_stride_tok = q_stride_tok; a.q_stride_head = q_stride_head;
@@ -871,12 +894,19 @@ dcp_status_t dcp_mla_chunk_attention(const void* q, int64_t q_stride_tok, int64_
   a.tiles = static_cast<int32_t>(p.tiles);
   a.tile_start = reinterpret_cast<int32_t*>(ws + p.starts);
   a.block_start = a.tile_start + B + 1;
+  a.num_pieces = a.block_start + B + 1;
+  a.pieces = reinterpret_cast<dcp::Piece*>(ws + p.pieces);
   a.valid = reinterpret_cast<uint4*>(ws + p.valid);
   a.rope = ws + p.rope;
   a.keys = ws + p.fixed;
   a.values = a.keys + static_cast<size_t>(heads) * p.tiles * (2 * dcp::kImage);
   a.bad = reinterpret_cast<uint4*>(a.values + static_cast<size_t>(heads) * p.tiles * (2 * dcp::kImage));
-  a.units = static_cast<int32_t>(p.units);
+  a.sms = p.sms;
+  a.slots = static_cast<int32_t>(chunk_slots(p, heads));
+  a.max_pieces = static_cast<int32_t>(p.units + (a.slots > 0 ? dcp::added_pieces(p.sms, heads) : 0));
+  a.done = reinterpret_cast<int32_t*>(a.keys + round256(p.image_bytes * heads));
+  a.partial = reinterpret_cast<unsigned char*>(a.done) + round256(static_cast<size_t>(a.slots) * heads * 4);
+  a.heads = heads;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dcp::launch_chunk_plan(a, st) != cudaSuccess) return DCP_ERR_CUDA;
   for (a.h0 = 0; a.h0 < H; a.h0 += heads) {

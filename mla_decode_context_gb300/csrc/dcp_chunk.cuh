@@ -25,6 +25,21 @@ constexpr int kWeightStage = kUp * 128;          // packed weight: 256 rows x 64
 // Byte offset of 16-byte unit u of row r in an image (of any number of rows).
 __host__ __device__ constexpr uint32_t image_unit(uint32_t r, uint32_t u) { return r * 128u + ((u ^ (r & 7u)) << 4); }
 
+// A unit's key tiles are cut into pieces where there are too few units for the
+// SMs or some are much longer than others: at least kMinPiece tiles each, about
+// kPiecesPerSM pieces a SM if all units were cut, kMaxPieces a unit.  The last
+// piece of a unit to finish joins their outputs.
+constexpr int kMinPiece = 6, kPiecesPerSM = 2, kMaxPieces = 32;
+constexpr int kSlotBytes = kChunkRows * (kVDim + 1) * 4;  // a piece's output and log-sum-exps, fp32
+
+struct Piece {
+  int32_t b, block;       // request (-1: rows of no request), block of 256 rows
+  int32_t j0, j1;         // key tiles
+  int32_t pieces, slot;   // of the unit; its first slot (of a head's) and which of the pieces this is
+  int32_t index;
+  int32_t seg0, seg;      // pieces of similar length: the first, and how many
+};
+
 struct ChunkArgs {
   const __nv_bfloat16* q;   // [T, H, 192]
   int64_t q_stride_tok, q_stride_head;
@@ -58,7 +73,13 @@ struct ChunkArgs {
   unsigned char* values;    // the same
   uint4* bad;               // [heads of a pass][tiles]: tokens whose value is not finite (their rows are zeros)
   int32_t h0, heads;        // the heads of this pass
-  int32_t units;            // units per head (T / 256 + B + 2)
+  int32_t sms;
+  int32_t max_pieces;       // records (T / 256 + B + 2, and what the cuts add)
+  Piece* pieces;            // in launch order: long ones first
+  int32_t* num_pieces;
+  int32_t slots;            // slots of a head of a pass; 0: no cuts
+  unsigned char* partial;   // [heads of a pass][slots][kSlotBytes]
+  int32_t* done;            // [heads of a pass][slots]: pieces of a unit that are finished (at its first slot)
 };
 
 // The last b with start[b] <= n (start[0] <= n < start[count] given), by the
@@ -77,6 +98,9 @@ __device__ __forceinline__ int32_t find_range(const int32_t* start, int32_t coun
   }
   return lo;
 }
+
+// Pieces that cuts may add to the units of `heads` heads.
+DCP_HD int64_t added_pieces(int sms, int heads) { return static_cast<int64_t>(kPiecesPerSM) * sms / heads + 1; }
 
 cudaError_t launch_pack_kv_b(const void* w, int32_t H, void* packed, cudaStream_t st);
 // One pass over heads [h0, h0 + heads); the first also writes what the heads

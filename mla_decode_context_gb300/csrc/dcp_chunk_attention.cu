@@ -5,7 +5,8 @@
 //   out = sum_p exp(s - lse) v_h(p),  lse = ln sum_p exp(s)
 //
 // 2 x (192 + 128) operations per (row, token, head): bound by the tensor pipe.
-// Unit: 256 rows of one request at one head, as two MMA tiles of 128 rows that
+// Unit: 256 rows of one request at one head (cut into pieces along its tokens
+// where there are few or uneven units, dcp_chunk_plan.cu), as two MMA tiles of 128 rows that
 // share each tile of 128 keys and values in shared memory and take turns on the
 // tensor pipe: while one's scores go through the softmax, the other's products
 // run.  TMEM holds both tiles' scores (128 columns each; the weights P replace
@@ -60,7 +61,9 @@ struct Bars {
   uint64_t fin;
   uint32_t tmem;
   int32_t abort;
-  int32_t b, q0, q1, seq, r0, block;   // the unit
+  int32_t q0, q1, seq;                 // the unit's request
+  int32_t last;                        // this piece is the unit's last to finish
+  Piece piece;
 };
 constexpr int kSmemBytes = kOffBars + static_cast<int>(sizeof(Bars)) + 1024;
 static_assert(kSmemBytes <= 232448, "exceeds the 227 KB of shared memory per CTA");
@@ -77,20 +80,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// The rows of this group's tile that exist, and the images that they need.
+// The rows of this group's tile that exist, and the key tiles of this piece that
+// they need.
 struct Tile {
   int32_t first, rows;  // row of the request, number of rows
-  int32_t tiles;        // key tiles
+  int32_t tiles;
 };
-__device__ __forceinline__ Tile tile_of(const Bars& bar, int g, int32_t have) {
+__device__ __forceinline__ Tile tile_of(const Bars& bar, int g) {
   Tile t;
   const int32_t q_len = bar.q1 - bar.q0;
-  t.first = bar.block * kChunkRows + 128 * g;
-  t.rows = bar.b < 0 ? 0 : max(0, min(128, q_len - t.first));
+  t.first = bar.piece.block * kChunkRows + 128 * g;
+  t.rows = max(0, min(128, q_len - t.first));
   // what the last row sees
   const int64_t end = static_cast<int64_t>(bar.seq) - (q_len - 1) + (t.first + t.rows - 1);
-  t.tiles = t.rows > 0 && end > 0 ? static_cast<int32_t>((end + kChunkTile - 1) / kChunkTile) : 0;
-  if (t.tiles > have) t.tiles = 0;  // (its images did not fit the workspace)
+  const int32_t tiles = t.rows > 0 && end > 0 ? static_cast<int32_t>((end + kChunkTile - 1) / kChunkTile) : 0;
+  t.tiles = max(0, min(tiles, bar.piece.j1) - bar.piece.j0);
   return t;
 }
 
@@ -145,6 +149,44 @@ struct Issue {
   }
 };
 
+// The unit's output from its pieces' (normalised, with their log-sum-exps), a
+// warp per row, in the pieces' order.
+__device__ void join(const ChunkArgs& a, const Piece& p, const float* slot, int32_t q0, int32_t q1, int32_t h) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kStep = kSlotBytes / 4;
+  const int64_t first = static_cast<int64_t>(q0) + static_cast<int64_t>(p.block) * kChunkRows;
+  const int32_t rows = static_cast<int32_t>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(kChunkRows), min(static_cast<int64_t>(q1), static_cast<int64_t>(a.T)) - first)));
+  for (int32_t i = threadIdx.x >> 5; i < rows; i += 8) {
+    const float lse = lane < p.pieces ? __ldcg(slot + static_cast<int64_t>(lane) * kStep + kChunkRows * kVDim + i) : -INFINITY;
+    float top = lse;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // (all -inf: nothing to see; a NaN weighs NaN)
+    const float w = lse == -INFINITY ? 0.f : ex2_approx((lse - (top == -INFINITY ? 0.f : top)) * kLog2e);
+    float sum = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < p.pieces; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      if (wk == 0.f) continue;  // (its output may not be written)
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(slot + static_cast<int64_t>(k) * kStep + i * kVDim) + lane);
+      acc.x = fmaf(wk, v.x, acc.x), acc.y = fmaf(wk, v.y, acc.y), acc.z = fmaf(wk, v.z, acc.z), acc.w = fmaf(wk, v.w, acc.w);
+    }
+    const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+    const int64_t at = ((first + i) * a.H + h) * kVDim + 4 * lane;
+    acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+    if (a.out_f32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = acc;
+    } else {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x, acc.y), y = __floats2bfloat162_rn(acc.z, acc.w);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    }
+    if (lane == 0) a.lse[(first + i) * a.H + h] = sum != 0.f ? top + log2f(sum) * kLn2 : -INFINITY;
+  }
+}
+
 // Rows of no request: zeros and -inf.
 __device__ void pad_rows(const ChunkArgs& a, int64_t r0, int64_t r1, int32_t h) {
   for (int64_t i = threadIdx.x; i < (r1 - r0) * (kVDim / 4); i += kThreads) {
@@ -161,23 +203,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   Bars& bar = *reinterpret_cast<Bars*>(smem + kOffBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();
-  const int32_t hp = static_cast<int32_t>(blockIdx.x / static_cast<uint32_t>(a.units));
-  const int32_t h = a.h0 + hp;
-  const int32_t u = static_cast<int32_t>(blockIdx.x - static_cast<uint32_t>(hp) * a.units);
   wait_dependency();
-  // ---- the unit
+  // ---- the piece: segments of similar length, within them the heads outermost
   if (warp == 0) {
-    const int32_t blocks = a.block_start[a.B];
-    int32_t b = -1, block = u - blocks;
-    if (u < blocks) {
-      b = find_range(a.block_start, a.B, u);
-      block = u - a.block_start[b];
-    }
+    const int32_t at = static_cast<int32_t>(blockIdx.x) / a.heads;
+    const bool live = at < *a.num_pieces;
     if (lane == 0) {
-      bar.b = b;
-      bar.block = block;
-      if (b >= 0) bar.q0 = a.qsl[b], bar.q1 = a.qsl[b + 1], bar.seq = max(0, a.seq_lens[b]);
-      bar.abort = 0;
+      bar.abort = live ? 0 : -1;
+      if (live) {
+        const int32_t seg0 = a.pieces[at].seg0, seg = a.pieces[at].seg;
+        const int64_t in = static_cast<int64_t>(blockIdx.x) - static_cast<int64_t>(seg0) * a.heads;
+        bar.last = static_cast<int32_t>(in / seg);  // (the head, until the piece is done)
+        const Piece p = a.pieces[seg0 + static_cast<int32_t>(in % seg)];
+        bar.piece = p;
+        if (p.b >= 0) bar.q0 = a.qsl[p.b], bar.q1 = a.qsl[p.b + 1], bar.seq = max(0, a.seq_lens[p.b]);
+      }
     }
   }
   if (threadIdx.x == 32) {
@@ -193,15 +233,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     fence_mbar_init();
   }
   __syncthreads();
-  if (bar.b < 0) {  // rows before the first request's and from the last one's end on, 256 to a unit
-    const int64_t lead = max(0, min(a.qsl[0], a.T)), tail = max(0, min(a.qsl[a.B], a.T));
-    const int64_t n = lead + (a.T - max(tail, lead));
-    int64_t i0 = static_cast<int64_t>(bar.block) * kChunkRows, i1 = min(n, i0 + kChunkRows);
-    const int64_t skip = max(tail, lead) - lead;  // rows of requests between the two
+  if (bar.abort < 0) return;
+  const int32_t hp = bar.last, h = a.h0 + hp;
+  if (bar.piece.b < 0) {  // rows before the first request's and from the last one's end on, 256 to a unit
+    const int64_t lead = max(0, min(a.qsl[0], a.T)), tail = max(lead, static_cast<int64_t>(min(a.qsl[a.B], a.T)));
+    const int64_t n = lead + a.T - tail;
+    const int64_t i0 = static_cast<int64_t>(bar.piece.block) * kChunkRows, i1 = min(n, i0 + kChunkRows);
     if (i0 < i1) {
       const int64_t cut = min(max(lead, i0), i1);
       pad_rows(a, i0, cut, h);
-      pad_rows(a, cut + skip, i1 + skip, h);
+      pad_rows(a, cut + tail - lead, i1 + tail - lead, h);
     }
     return;
   }
@@ -213,10 +254,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = 0;  // (all 512 columns: the allocation starts at the first)
-  const int32_t image0 = a.tile_start[bar.b];
-  const int32_t have = a.tile_start[bar.b + 1] - image0;
-  const int32_t all = static_cast<int32_t>((static_cast<int64_t>(bar.seq) + kChunkTile - 1) / kChunkTile);
-  const Tile t0 = tile_of(bar, 0, have < all ? 0 : have), t1 = tile_of(bar, 1, have < all ? 0 : have);
+  const int32_t image0 = a.tile_start[bar.piece.b] + bar.piece.j0;
+  const Tile t0 = tile_of(bar, 0), t1 = tile_of(bar, 1);
   const int32_t n0 = t0.tiles, n1 = t1.tiles, n = max(n0, n1);
   volatile int32_t* stop = &bar.abort;
   auto failed = [&]() {
@@ -267,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       const uint4* masks = reinterpret_cast<const uint4*>(smem + kOffMask + (j % kMaskSlots) * 32);
       const uint4 valid = masks[0], bad = masks[1];
       tmem_wait_ld();
-      const int32_t p0 = j * kChunkTile;
+      const int32_t p0 = (bar.piece.j0 + j) * kChunkTile;
       const bool plain = (valid.x & valid.y & valid.z & valid.w) == 0xffffffffu && (bad.x | bad.y | bad.z | bad.w) == 0u &&
                          p0 + kChunkTile <= L_first;
       if (!plain) {
@@ -347,7 +386,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     tc_fence_after();
     if (nan_row) l = __int_as_float(0x7fc00000);
     const float inv = tiles > 0 && l != 0.f ? 1.0f / l : 0.f;
-    if (row < rows && r < a.T) a.lse[r * a.H + h] = tiles > 0 && l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    const float lse = tiles > 0 && l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    const bool cut = bar.piece.pieces > 1;
+    unsigned char* slot = a.partial + (static_cast<int64_t>(hp) * a.slots + bar.piece.slot) * kSlotBytes;  // the unit's first
+    unsigned char* own = slot + static_cast<int64_t>(bar.piece.index) * kSlotBytes;
+    if (cut) reinterpret_cast<float*>(own)[kChunkRows * kVDim + 128 * g + row] = lse;
+    else if (row < rows && r < a.T) a.lse[r * a.H + h] = lse;
+    const bool f32 = cut || a.out_f32;
     const int wr = 32 * quad;  // this warp's rows
     const int live = min(32, static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(rows), a.T - static_cast<int64_t>(bar.q0) - first) - wr)));
 #pragma unroll 1
@@ -363,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       const int64_t out0 = (static_cast<int64_t>(bar.q0) + first + wr) * a.H + h;
       const int dim = 32 * c;
       __syncwarp();
-      if (a.out_f32) {  // 128 bytes a row: eight lanes each
+      if (f32) {  // 128 bytes a row: eight lanes each
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           *reinterpret_cast<uint4*>(stage + image_unit(lane, k)) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
@@ -371,9 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int q = 4 * k + (lane >> 3);
-          if (q < live)
-            *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + (out0 + static_cast<int64_t>(q) * a.H) * kVDim + dim + 4 * (lane & 7)) =
-                *reinterpret_cast<const uint4*>(stage + image_unit(q, lane & 7));
+          float* dst = cut ? reinterpret_cast<float*>(own) + (128 * g + wr + q) * kVDim
+                           : static_cast<float*>(a.out) + (out0 + static_cast<int64_t>(q) * a.H) * kVDim;
+          if (q < live) *reinterpret_cast<uint4*>(dst + dim + 4 * (lane & 7)) = *reinterpret_cast<const uint4*>(stage + image_unit(q, lane & 7));
         }
       } else {  // 64 bytes a row: four lanes each
 #pragma unroll
@@ -395,6 +440,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 *reinterpret_cast<const uint4*>(stage + image_unit(q, lane & 3));
         }
       }
+    }
+    if (cut) {
+      // the last piece of the unit to get here joins them all
+      __threadfence();
+      named_barrier(1, 256);
+      if (threadIdx.x == 0) {
+        int32_t* done = a.done + static_cast<int64_t>(hp) * a.slots + bar.piece.slot;
+        const bool last = atomicAdd(done, 1) == bar.piece.pieces - 1;
+        if (last) *done = 0;  // (for the next pass)
+        bar.last = last;
+        __threadfence();
+      }
+      named_barrier(1, 256);
+      if (bar.last) join(a, bar.piece, reinterpret_cast<const float*>(slot), bar.q0, bar.q1, h);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -512,7 +571,7 @@ cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t st) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.units) * a.heads));
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.max_pieces) * a.heads));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;

@@ -374,63 +374,6 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint4* __restrict__ w, 
   *reinterpret_cast<uint4*>(packed + (row / kUp) * (kChunks * kWeightStage) + (u >> 3) * kWeightStage + image_unit(r, u & 7)) = __ldg(w + i);
 }
 
-constexpr int kPlanThreads = 1024;
-
-// First images and first units of the requests: two scans.  Requests whose
-// images do not all fit get none (and their rows nothing to see).
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ ChunkArgs a) {
-  __shared__ int64_t sums[2][32];
-  launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t base[2] = {0, 0};
-  for (int32_t b0 = 0; b0 < a.B; b0 += kPlanThreads) {
-    const int32_t b = b0 + tid;
-    int64_t x[2] = {0, 0};
-    int64_t own[2] = {0, 0};
-    if (b < a.B) {
-      const int32_t q0 = __ldg(a.qsl + b), q1 = __ldg(a.qsl + b + 1), seq = __ldg(a.seq_lens + b);
-      const bool rows = q0 >= 0 && q1 > q0;
-      if ((q1 < q0 || q0 < 0) && a.dev_error) atomicOr(a.dev_error, DCP_DEVERR_BAD_ROWS);
-      // (tokens that no row sees are not needed)
-      own[0] = rows && seq > 0 ? (static_cast<int64_t>(seq) + kChunkTile - 1) / kChunkTile : 0;
-      own[1] = rows ? (static_cast<int64_t>(q1) - q0 + kChunkRows - 1) / kChunkRows : 0;
-      x[0] = own[0], x[1] = own[1];
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x[k], o);
-        if (lane >= o) x[k] += y;
-      }
-      if (lane == 31) sums[k][warp] = x[k];
-    }
-    __syncthreads();
-    if (warp < 2) {
-      int64_t s = sums[warp][lane];
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
-      }
-      sums[warp][lane] = s;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      x[k] += base[k] + (warp > 0 ? sums[k][warp - 1] : 0);
-      base[k] += sums[k][31];
-    }
-    if (b < a.B) {
-      // ends, cut at what the workspace holds; a request past it has none
-      const int64_t end = x[0] < a.tiles ? x[0] : a.tiles;
-      if (x[0] > a.tiles && own[0] > 0 && a.dev_error) atomicOr(a.dev_error, DCP_DEVERR_SEQ_TOO_LONG);
-      a.tile_start[b + 1] = static_cast<int32_t>(end);
-      a.block_start[b + 1] = static_cast<int32_t>(x[1] < 0x7fffffff ? x[1] : 0x7fffffff);
-    }
-    __syncthreads();
-  }
-  if (tid == 0) a.tile_start[0] = a.block_start[0] = 0;
-}
-
 std::mutex g_mutex;
 bool g_ready[2][64];
 
@@ -469,11 +412,6 @@ cudaError_t launch_pack_kv_b(const void* w, int32_t H, void* packed, cudaStream_
   const int64_t units = static_cast<int64_t>(H) * kUp * (kLatent / 8);
   pack_kernel<<<static_cast<unsigned>((units + 255) / 256), 256, 0, st>>>(static_cast<const uint4*>(w),
                                                                           static_cast<unsigned char*>(packed), units);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t st) {
-  plan_kernel<<<1, kPlanThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,170 @@
+// Chunk attention, the plan: first images and first blocks of the requests, and
+// the pieces of work of the attention in launch order.  One CTA; the lengths are
+// on the device only.
+//
+// Units are (request, block of 256 rows), the same for every head.  A launch
+// takes them longest first, so that the last ones to run are short.  Units of
+// similar length (a quarter of an octave) form a segment, in which the heads are
+// outermost: the blocks of a request read one head's keys and values at about
+// the same time, out of L2.
+#include "dcp_chunk.cuh"
+
+namespace dcp {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kBuckets = 128;  // 4 per octave
+constexpr unsigned kFull = 0xffffffffu;
+
+__device__ __forceinline__ int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
+
+// longest first
+__device__ __forceinline__ int bucket_of(int32_t tiles) {
+  if (tiles <= 0) return kBuckets - 1;
+  const int e = 31 - __clz(tiles);
+  const int quarter = e >= 2 ? (tiles >> (e - 2)) & 3 : (tiles << (2 - e)) & 3;
+  return kBuckets - 2 - (4 * e + quarter);  // (4 x 30 + 3 at most)
+}
+
+// Inclusive scan over the CTA of two numbers a thread.
+__device__ __forceinline__ void scan2(int64_t (&x)[2], int64_t (*sums)[32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(kFull, x[k], o);
+      if (lane >= o) x[k] += y;
+    }
+    if (lane == 31) sums[k][warp] = x[k];
+  }
+  __syncthreads();
+  if (warp < 2) {
+    int64_t s = sums[warp][lane];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(kFull, s, o);
+      if (lane >= o) s += y;
+    }
+    sums[warp][lane] = s;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) x[k] += warp > 0 ? sums[k][warp - 1] : 0;
+}
+
+struct Unit {
+  int32_t b, block, tiles;
+};
+__device__ __forceinline__ Unit unit_of(const ChunkArgs& a, int32_t u, int32_t blocks) {
+  Unit n{-1, u - blocks, 0};
+  if (u >= blocks) return n;
+  int32_t lo = 0, hi = a.B;  // the last request whose first block is <= u
+  while (hi - lo > 1) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (a.block_start[mid] <= u) lo = mid; else hi = mid;
+  }
+  n.b = lo;
+  n.block = u - a.block_start[lo];
+  const int64_t q_len = static_cast<int64_t>(a.qsl[lo + 1]) - a.qsl[lo];
+  const int64_t rows = min(q_len, static_cast<int64_t>(kChunkRows) * (n.block + 1));  // up to this block's last
+  const int64_t seq = max(0, a.seq_lens[lo]);
+  const int64_t end = seq - q_len + rows;  // tokens that the last row sees
+  const int64_t have = a.tile_start[lo + 1] - a.tile_start[lo];
+  if (end > 0 && have >= ceil_div(seq, kChunkTile)) n.tiles = static_cast<int32_t>(ceil_div(end, kChunkTile));
+  return n;
+}
+
+__global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ ChunkArgs a) {
+  __shared__ int64_t sums[2][32];
+  __shared__ int32_t count[kBuckets], first[kBuckets];
+  __shared__ unsigned long long work;
+  __shared__ int32_t slots;
+  sm100::launch_dependents();
+  const int tid = threadIdx.x;
+  for (int i = tid; i < kBuckets; i += kThreads) count[i] = 0;
+  if (tid == 0) work = 0, slots = 0;
+  for (int64_t i = tid; i < static_cast<int64_t>(a.slots) * a.heads; i += kThreads) a.done[i] = 0;
+  // ---- first images and blocks of the requests
+  int64_t base[2] = {0, 0};
+  for (int32_t b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int32_t b = b0 + tid;
+    int64_t x[2] = {0, 0};
+    if (b < a.B) {
+      const int32_t q0 = __ldg(a.qsl + b), q1 = __ldg(a.qsl + b + 1), seq = __ldg(a.seq_lens + b);
+      const bool rows = q0 >= 0 && q1 > q0;
+      if ((q1 < q0 || q0 < 0) && a.dev_error) atomicOr(a.dev_error, DCP_DEVERR_BAD_ROWS);
+      // (tokens that no row sees are not needed)
+      x[0] = rows && seq > 0 ? ceil_div(seq, kChunkTile) : 0;
+      x[1] = rows ? ceil_div(static_cast<int64_t>(q1) - q0, kChunkRows) : 0;
+    }
+    const bool some = x[0] > 0;
+    scan2(x, sums);
+    if (b < a.B) {
+      x[0] += base[0], x[1] += base[1];
+      // ends, cut at what the workspace holds; a request past it sees nothing
+      if (x[0] > a.tiles && some && a.dev_error) atomicOr(a.dev_error, DCP_DEVERR_SEQ_TOO_LONG);
+      a.tile_start[b + 1] = static_cast<int32_t>(x[0] < a.tiles ? x[0] : a.tiles);
+      a.block_start[b + 1] = static_cast<int32_t>(x[1] < 0x7fffffff ? x[1] : 0x7fffffff);
+    }
+    base[0] += sums[0][31], base[1] += sums[1][31];
+    __syncthreads();
+  }
+  if (tid == 0) a.tile_start[0] = a.block_start[0] = 0;
+  __syncthreads();
+  // ---- the units: requests' blocks, then the rows of no request
+  const int32_t limit = a.max_pieces - (a.slots > 0 ? static_cast<int32_t>(added_pieces(a.sms, a.heads)) : 0);
+  const int32_t blocks = min(a.block_start[a.B], limit);
+  const int64_t lead = max(0, min(a.qsl[0], a.T)), tail = max(lead, static_cast<int64_t>(min(a.qsl[a.B], a.T)));
+  const int32_t units = static_cast<int32_t>(min(static_cast<int64_t>(limit), blocks + ceil_div(lead + a.T - tail, kChunkRows)));
+  unsigned long long mine = 0;
+  for (int32_t u = tid; u < units; u += kThreads) mine += unit_of(a, u, blocks).tiles;
+  if (mine) atomicAdd(&work, mine);
+  __syncthreads();
+  // tiles of a piece
+  const int64_t piece = a.slots == 0 ? 0x7fffffff
+                                     : max(static_cast<int64_t>(kMinPiece),
+                                           ceil_div(static_cast<int64_t>(work) * a.heads, static_cast<int64_t>(kPiecesPerSM) * a.sms));
+  auto cuts = [&](int32_t tiles) {
+    return static_cast<int32_t>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(kMaxPieces), ceil_div(tiles, piece))));
+  };
+  for (int32_t u = tid; u < units; u += kThreads) {
+    const int32_t tiles = unit_of(a, u, blocks).tiles, c = cuts(tiles);
+    atomicAdd(&count[bucket_of((tiles + c - 1) / c)], c);
+  }
+  __syncthreads();
+  if (tid < kBuckets) {
+    int32_t n = 0;
+    for (int i = 0; i < tid; ++i) n += count[i];
+    first[tid] = n;
+    if (tid == kBuckets - 1) *a.num_pieces = n + count[tid];
+  }
+  __syncthreads();
+  // ---- records.  `next` places a unit's pieces in its bucket; their order there
+  // and the slots' do not change results.
+  __shared__ int32_t next[kBuckets];
+  if (tid < kBuckets) next[tid] = first[tid];
+  __syncthreads();
+  for (int32_t u = tid; u < units; u += kThreads) {
+    const Unit n = unit_of(a, u, blocks);
+    const int32_t c = cuts(n.tiles), bucket = bucket_of((n.tiles + c - 1) / c);
+    const int32_t at = atomicAdd(&next[bucket], c);
+    const int32_t slot = c > 1 ? atomicAdd(&slots, c) : 0;
+    for (int32_t i = 0; i < c && at + i < a.max_pieces; ++i) {
+      Piece p;
+      p.b = n.b, p.block = n.block;
+      p.j0 = static_cast<int32_t>(static_cast<int64_t>(n.tiles) * i / c);
+      p.j1 = static_cast<int32_t>(static_cast<int64_t>(n.tiles) * (i + 1) / c);
+      p.pieces = c, p.slot = slot, p.index = i;
+      p.seg0 = first[bucket], p.seg = count[bucket];
+      a.pieces[at + i] = p;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t st) {
+  plan_kernel<<<1, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace dcp
