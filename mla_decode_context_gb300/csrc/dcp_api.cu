@@ -816,7 +816,7 @@ int64_t chunk_slots(const ChunkPlan& p, int32_t heads) {
 }
 size_t chunk_bytes(const ChunkPlan& p, int32_t heads) {
   const size_t slots = static_cast<size_t>(chunk_slots(p, heads)) * heads;
-  return p.fixed + round256(p.image_bytes * heads) + round256(slots * 4) + slots * dcp::kSlotBytes;
+  return p.fixed + round256(p.image_bytes * heads) + slots * dcp::kSlotBytes;
 }
 
 }  // namespace
@@ -904,8 +904,7 @@ dcp_status_t dcp_mla_chunk_attention(const void* q, int64_t q_stride_tok, int64_
   a.sms = p.sms;
   a.slots = static_cast<int32_t>(chunk_slots(p, heads));
   a.max_pieces = static_cast<int32_t>(p.units + (a.slots > 0 ? dcp::added_pieces(p.sms, heads) : 0));
-  a.done = reinterpret_cast<int32_t*>(a.keys + round256(p.image_bytes * heads));
-  a.partial = reinterpret_cast<unsigned char*>(a.done) + round256(static_cast<size_t>(a.slots) * heads * 4);
+  a.partial = a.keys + round256(p.image_bytes * heads);
   a.heads = heads;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dcp::launch_chunk_plan(a, st) != cudaSuccess) return DCP_ERR_CUDA;

@@ -26,19 +26,24 @@ constexpr int kWeightStage = kUp * 128;          // packed weight: 256 rows x 64
 __host__ __device__ constexpr uint32_t image_unit(uint32_t r, uint32_t u) { return r * 128u + ((u ^ (r & 7u)) << 4); }
 
 // A unit's key tiles are cut into pieces where there are too few units for the
-// SMs or some are much longer than others: at least kMinPiece tiles each, about
-// kPiecesPerSM pieces a SM if all units were cut, kMaxPieces a unit.  The last
-// piece of a unit to finish joins their outputs.
-constexpr int kMinPiece = 6, kPiecesPerSM = 2, kMaxPieces = 32;
+// SMs or some are much longer than others: at least kMinPiece tiles each,
+// kMaxPieces a unit, about one piece an SM if all units were cut (two: 12 mixed
+// requests at 16 heads 751 us instead of 742, 3 x 700 rows at 64 heads 781 instead
+// of 777; six: 818 and 917).  A second kernel joins their outputs.
+constexpr int kMinPiece = 6, kMaxPieces = 32;
 constexpr int kSlotBytes = kChunkRows * (kVDim + 1) * 4;  // a piece's output and log-sum-exps, fp32
 
-struct Piece {
+struct __align__(16) Piece {
   int32_t b, block;       // request (-1: rows of no request), block of 256 rows
+  int32_t q0, q1, seq;    // the request's rows and length
+  int32_t image;          // its image of key tile j0
   int32_t j0, j1;         // key tiles
-  int32_t pieces, slot;   // of the unit; its first slot (of a head's) and which of the pieces this is
-  int32_t index;
+  int32_t pieces, index;  // of the unit, and which of them this is
+  int32_t slot;           // the unit's first slot (of a head's)
   int32_t seg0, seg;      // pieces of similar length: the first, and how many
+  int32_t unused[3];
 };
+static_assert(sizeof(Piece) == 64, "four 16-byte units");
 
 struct ChunkArgs {
   const __nv_bfloat16* q;   // [T, H, 192]
@@ -79,7 +84,6 @@ struct ChunkArgs {
   int32_t* num_pieces;
   int32_t slots;            // slots of a head of a pass; 0: no cuts
   unsigned char* partial;   // [heads of a pass][slots][kSlotBytes]
-  int32_t* done;            // [heads of a pass][slots]: pieces of a unit that are finished (at its first slot)
 };
 
 // The last b with start[b] <= n (start[0] <= n < start[count] given), by the
@@ -100,7 +104,7 @@ __device__ __forceinline__ int32_t find_range(const int32_t* start, int32_t coun
 }
 
 // Pieces that cuts may add to the units of `heads` heads.
-DCP_HD int64_t added_pieces(int sms, int heads) { return static_cast<int64_t>(kPiecesPerSM) * sms / heads + 1; }
+DCP_HD int64_t added_pieces(int sms, int heads) { return sms / heads + 1; }
 
 cudaError_t launch_pack_kv_b(const void* w, int32_t H, void* packed, cudaStream_t st);
 // One pass over heads [h0, h0 + heads); the first also writes what the heads

@@ -61,8 +61,7 @@ struct Bars {
   uint64_t fin;
   uint32_t tmem;
   int32_t abort;
-  int32_t q0, q1, seq;                 // the unit's request
-  int32_t last;                        // this piece is the unit's last to finish
+  int32_t head;                        // of this pass
   Piece piece;
 };
 constexpr int kSmemBytes = kOffBars + static_cast<int>(sizeof(Bars)) + 1024;
@@ -80,6 +79,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// CTA `i` of a pass: segments of similar length, within them the heads outermost.
+__device__ __forceinline__ bool piece_of(const ChunkArgs& a, int32_t i, Piece& p, int32_t& head) {
+  const int32_t at = i / a.heads;
+  const int32_t n = *a.num_pieces;
+  p = a.pieces[at];  // (whatever it holds past the last one)
+  if (at >= n) return false;
+  const int32_t in = i - p.seg0 * a.heads;
+  head = in / p.seg;
+  const int32_t to = p.seg0 + (in - head * p.seg);
+  if (to != at) p = a.pieces[to];
+  return true;
+}
+
 // The rows of this group's tile that exist, and the key tiles of this piece that
 // they need.
 struct Tile {
@@ -88,11 +100,11 @@ struct Tile {
 };
 __device__ __forceinline__ Tile tile_of(const Bars& bar, int g) {
   Tile t;
-  const int32_t q_len = bar.q1 - bar.q0;
+  const int32_t q_len = bar.piece.q1 - bar.piece.q0;
   t.first = bar.piece.block * kChunkRows + 128 * g;
   t.rows = max(0, min(128, q_len - t.first));
   // what the last row sees
-  const int64_t end = static_cast<int64_t>(bar.seq) - (q_len - 1) + (t.first + t.rows - 1);
+  const int64_t end = static_cast<int64_t>(bar.piece.seq) - (q_len - 1) + (t.first + t.rows - 1);
   const int32_t tiles = t.rows > 0 && end > 0 ? static_cast<int32_t>((end + kChunkTile - 1) / kChunkTile) : 0;
   t.tiles = max(0, min(tiles, bar.piece.j1) - bar.piece.j0);
   return t;
@@ -149,44 +161,6 @@ struct Issue {
   }
 };
 
-// The unit's output from its pieces' (normalised, with their log-sum-exps), a
-// warp per row, in the pieces' order.
-__device__ void join(const ChunkArgs& a, const Piece& p, const float* slot, int32_t q0, int32_t q1, int32_t h) {
-  const int lane = threadIdx.x & 31;
-  constexpr int kStep = kSlotBytes / 4;
-  const int64_t first = static_cast<int64_t>(q0) + static_cast<int64_t>(p.block) * kChunkRows;
-  const int32_t rows = static_cast<int32_t>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(kChunkRows), min(static_cast<int64_t>(q1), static_cast<int64_t>(a.T)) - first)));
-  for (int32_t i = threadIdx.x >> 5; i < rows; i += 8) {
-    const float lse = lane < p.pieces ? __ldcg(slot + static_cast<int64_t>(lane) * kStep + kChunkRows * kVDim + i) : -INFINITY;
-    float top = lse;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // (all -inf: nothing to see; a NaN weighs NaN)
-    const float w = lse == -INFINITY ? 0.f : ex2_approx((lse - (top == -INFINITY ? 0.f : top)) * kLog2e);
-    float sum = w;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < p.pieces; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      if (wk == 0.f) continue;  // (its output may not be written)
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(slot + static_cast<int64_t>(k) * kStep + i * kVDim) + lane);
-      acc.x = fmaf(wk, v.x, acc.x), acc.y = fmaf(wk, v.y, acc.y), acc.z = fmaf(wk, v.z, acc.z), acc.w = fmaf(wk, v.w, acc.w);
-    }
-    const float inv = sum != 0.f ? 1.0f / sum : 0.f;
-    const int64_t at = ((first + i) * a.H + h) * kVDim + 4 * lane;
-    acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-    if (a.out_f32) {
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = acc;
-    } else {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x, acc.y), y = __floats2bfloat162_rn(acc.z, acc.w);
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-    }
-    if (lane == 0) a.lse[(first + i) * a.H + h] = sum != 0.f ? top + log2f(sum) * kLn2 : -INFINITY;
-  }
-}
-
 // Rows of no request: zeros and -inf.
 __device__ void pad_rows(const ChunkArgs& a, int64_t r0, int64_t r1, int32_t h) {
   for (int64_t i = threadIdx.x; i < (r1 - r0) * (kVDim / 4); i += kThreads) {
@@ -204,19 +178,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();
   wait_dependency();
-  // ---- the piece: segments of similar length, within them the heads outermost
+  // ---- the piece
   if (warp == 0) {
-    const int32_t at = static_cast<int32_t>(blockIdx.x) / a.heads;
-    const bool live = at < *a.num_pieces;
+    Piece p;
+    int32_t head;
+    const bool live = piece_of(a, static_cast<int32_t>(blockIdx.x), p, head);
     if (lane == 0) {
       bar.abort = live ? 0 : -1;
       if (live) {
-        const int32_t seg0 = a.pieces[at].seg0, seg = a.pieces[at].seg;
-        const int64_t in = static_cast<int64_t>(blockIdx.x) - static_cast<int64_t>(seg0) * a.heads;
-        bar.last = static_cast<int32_t>(in / seg);  // (the head, until the piece is done)
-        const Piece p = a.pieces[seg0 + static_cast<int32_t>(in % seg)];
+        bar.head = head;
         bar.piece = p;
-        if (p.b >= 0) bar.q0 = a.qsl[p.b], bar.q1 = a.qsl[p.b + 1], bar.seq = max(0, a.seq_lens[p.b]);
       }
     }
   }
@@ -234,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   }
   __syncthreads();
   if (bar.abort < 0) return;
-  const int32_t hp = bar.last, h = a.h0 + hp;
+  const int32_t hp = bar.head, h = a.h0 + hp;
   if (bar.piece.b < 0) {  // rows before the first request's and from the last one's end on, 256 to a unit
     const int64_t lead = max(0, min(a.qsl[0], a.T)), tail = max(lead, static_cast<int64_t>(min(a.qsl[a.B], a.T)));
     const int64_t n = lead + a.T - tail;
@@ -254,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = 0;  // (all 512 columns: the allocation starts at the first)
-  const int32_t image0 = a.tile_start[bar.piece.b] + bar.piece.j0;
+  const int32_t image0 = bar.piece.image;
   const Tile t0 = tile_of(bar, 0), t1 = tile_of(bar, 1);
   const int32_t n0 = t0.tiles, n1 = t1.tiles, n = max(n0, n1);
   volatile int32_t* stop = &bar.abort;
@@ -268,27 +239,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int g = warp >> 2, quad = warp & 3, row = threadIdx.x & 127;
     const int32_t tiles = g ? n1 : n0, rows = g ? t1.rows : t0.rows, first = g ? t1.first : t0.first;
-    const int64_t r = static_cast<int64_t>(bar.q0) + first + row;  // this thread's query row
+    const int64_t r = static_cast<int64_t>(bar.piece.q0) + first + row;  // this thread's query row
     unsigned char* qs = smem + kOffQ + g * (kQChunks * kImage);
     // ---- Q: 24 16-byte units a row, eight lanes per 128-byte line
     if (tiles > 0) {
-#pragma unroll 2
-      for (int i = 0; i < 32; i += 4) {
-        const int qr = 32 * quad + i + (lane >> 3), un = lane & 7;
-        const bool in = qr < rows && static_cast<int64_t>(bar.q0) + first + qr < a.T;
-        const __nv_bfloat16* src = a.q + (static_cast<int64_t>(bar.q0) + first + qr) * a.q_stride_tok + h * a.q_stride_head + 8 * un;
+      const int un = lane & 7;
+      const int64_t q0 = static_cast<int64_t>(bar.piece.q0) + first;
 #pragma unroll
-        for (int c = 0; c < kQChunks; ++c) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (in) v = __ldg(reinterpret_cast<const uint4*>(src + 64 * c));
+      for (int i = 0; i < 32; i += 4) {
+        const int qr = 32 * quad + i + (lane >> 3);
+        const uint32_t bytes = qr < rows && q0 + qr < a.T ? 16u : 0u;
+        const __nv_bfloat16* src = a.q + (bytes ? (q0 + qr) * a.q_stride_tok : 0) + h * a.q_stride_head + 8 * un;
+#pragma unroll
+        for (int c = 0; c < kQChunks; ++c) cp_async16_zfill(smem_u32(qs + c * kImage + image_unit(qr, un)), src + 64 * c, bytes);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      if (a.q_sign != 0u) {  // a negative scale: this thread's units with the other sign
+#pragma unroll 1
+        for (int i = 0; i < 32 * kQChunks; i += 4) {
+          uint4* p = reinterpret_cast<uint4*>(qs + (i >> 5) * kImage + image_unit(32 * quad + (i & 31) + (lane >> 3), un));
+          uint4 v = *p;
           v.x ^= a.q_sign, v.y ^= a.q_sign, v.z ^= a.q_sign, v.w ^= a.q_sign;
-          *reinterpret_cast<uint4*>(qs + c * kImage + image_unit(qr, un)) = v;
+          *p = v;
         }
       }
       fence_proxy_async_smem();
       mbar_arrive(&bar.q_full[g]);
     }
-    const int32_t L = static_cast<int32_t>(max(static_cast<int64_t>(0), static_cast<int64_t>(bar.seq) - (bar.q1 - bar.q0 - 1) + first + row));
+    const int32_t L = static_cast<int32_t>(max(static_cast<int64_t>(0), static_cast<int64_t>(bar.piece.seq) - (bar.piece.q1 - bar.piece.q0 - 1) + first + row));
     const int32_t L_first = __shfl_sync(0xffffffffu, L, 0);  // the least of the warp's
     const uint32_t ts = tmem + (static_cast<uint32_t>(quad) << 21) + kColS + 128u * g;
     const uint32_t to = ts - kColS + kColO;
@@ -394,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     else if (row < rows && r < a.T) a.lse[r * a.H + h] = lse;
     const bool f32 = cut || a.out_f32;
     const int wr = 32 * quad;  // this warp's rows
-    const int live = min(32, static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(rows), a.T - static_cast<int64_t>(bar.q0) - first) - wr)));
+    const int live = min(32, static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(rows), a.T - static_cast<int64_t>(bar.piece.q0) - first) - wr)));
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {  // 32 dims at a time; a warp's rows are its own
       uint32_t o[32];
@@ -405,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
       for (int k = 0; k < 32; ++k) o[k] = tiles > 0 && l != 0.f ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
       unsigned char* stage = qs + wr * 128;
-      const int64_t out0 = (static_cast<int64_t>(bar.q0) + first + wr) * a.H + h;
+      const int64_t out0 = (static_cast<int64_t>(bar.piece.q0) + first + wr) * a.H + h;
       const int dim = 32 * c;
       __syncwarp();
       if (f32) {  // 128 bytes a row: eight lanes each
@@ -440,20 +419,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 *reinterpret_cast<const uint4*>(stage + image_unit(q, lane & 3));
         }
       }
-    }
-    if (cut) {
-      // the last piece of the unit to get here joins them all
-      __threadfence();
-      named_barrier(1, 256);
-      if (threadIdx.x == 0) {
-        int32_t* done = a.done + static_cast<int64_t>(hp) * a.slots + bar.piece.slot;
-        const bool last = atomicAdd(done, 1) == bar.piece.pieces - 1;
-        if (last) *done = 0;  // (for the next pass)
-        bar.last = last;
-        __threadfence();
-      }
-      named_barrier(1, 256);
-      if (bar.last) join(a, bar.piece, reinterpret_cast<const float*>(slot), bar.q0, bar.q1, h);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -548,6 +513,66 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   if (warp == 10) tmem_dealloc(bar.tmem, 512);
 }
 
+// The outputs of units that were cut, from their pieces' (normalised, with their
+// log-sum-exps), in the pieces' order.  The grid is the attention's: piece i of n
+// takes the i-th of n parts of its unit's rows, a warp per row, eight pieces' rows
+// loaded at a time.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ ChunkArgs a) {
+  launch_dependents();
+  wait_dependency();
+  const int lane = threadIdx.x & 31;
+  Piece p;
+  int32_t hp;
+  if (!piece_of(a, static_cast<int32_t>(blockIdx.x), p, hp) || p.b < 0 || p.pieces == 1) return;
+  constexpr int kStep = kSlotBytes / 4, kBatch = 8;
+  const float* slot = reinterpret_cast<const float*>(a.partial + (static_cast<int64_t>(hp) * a.slots + p.slot) * kSlotBytes);
+  const int64_t first = static_cast<int64_t>(a.qsl[p.b]) + static_cast<int64_t>(p.block) * kChunkRows;
+  const int64_t end = min(static_cast<int64_t>(a.qsl[p.b + 1]), static_cast<int64_t>(a.T));
+  const int32_t rows = static_cast<int32_t>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(kChunkRows), end - first)));
+  for (int32_t i = rows * p.index / p.pieces + (threadIdx.x >> 5); i < rows * (p.index + 1) / p.pieces; i += kJoinThreads / 32) {
+    const float lse = lane < p.pieces ? __ldg(slot + static_cast<int64_t>(lane) * kStep + kChunkRows * kVDim + i) : -INFINITY;
+    float top = lse;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // (all -inf: nothing to see; a NaN weighs NaN)
+    const float w = lse == -INFINITY ? 0.f : ex2_approx((lse - (top == -INFINITY ? 0.f : top)) * kLog2e);
+    float sum = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < p.pieces; k0 += kBatch) {
+      float4 v[kBatch];
+      float wk[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        wk[k] = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+        if (k0 + k >= p.pieces) wk[k] = 0.f;
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        // (a piece without weight may not have written its output)
+        if (wk[k] != 0.f) v[k] = __ldg(reinterpret_cast<const float4*>(slot + static_cast<int64_t>(k0 + k) * kStep + i * kVDim) + lane);
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        acc.x = fmaf(wk[k], v[k].x, acc.x), acc.y = fmaf(wk[k], v[k].y, acc.y);
+        acc.z = fmaf(wk[k], v[k].z, acc.z), acc.w = fmaf(wk[k], v[k].w, acc.w);
+      }
+    }
+    const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+    const int32_t h = a.h0 + hp;
+    const int64_t at = ((first + i) * a.H + h) * kVDim + 4 * lane;
+    acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+    if (a.out_f32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = acc;
+    } else {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x, acc.y), y = __floats2bfloat162_rn(acc.z, acc.w);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    }
+    if (lane == 0) a.lse[(first + i) * a.H + h] = sum != 0.f ? top + log2f(sum) * kLn2 : -INFINITY;
+  }
+}
+
 std::mutex g_mutex;
 bool g_ready[64];
 
@@ -577,7 +602,11 @@ cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_kernel, a);
+  const cudaError_t launched = cudaLaunchKernelEx(&cfg, attention_kernel, a);
+  if (launched != cudaSuccess || a.slots == 0) return launched;
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, join_kernel, a);
 }
 
 }  // namespace dcp

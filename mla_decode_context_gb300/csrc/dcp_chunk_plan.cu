@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kBuckets = 128;  // 4 per octave
+constexpr int kFewUnits = 4;   // an SM could take this many times the units
 constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
@@ -82,7 +83,6 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
   const int tid = threadIdx.x;
   for (int i = tid; i < kBuckets; i += kThreads) count[i] = 0;
   if (tid == 0) work = 0, slots = 0;
-  for (int64_t i = tid; i < static_cast<int64_t>(a.slots) * a.heads; i += kThreads) a.done[i] = 0;
   // ---- first images and blocks of the requests
   int64_t base[2] = {0, 0};
   for (int32_t b0 = 0; b0 < a.B; b0 += kThreads) {
@@ -119,12 +119,16 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
   for (int32_t u = tid; u < units; u += kThreads) mine += unit_of(a, u, blocks).tiles;
   if (mine) atomicAdd(&work, mine);
   __syncthreads();
-  // tiles of a piece
-  const int64_t piece = a.slots == 0 ? 0x7fffffff
-                                     : max(static_cast<int64_t>(kMinPiece),
-                                           ceil_div(static_cast<int64_t>(work) * a.heads, static_cast<int64_t>(kPiecesPerSM) * a.sms));
+  // Pieces of a unit: its share of one piece an SM.  With few units they are
+  // rounded down, so that all run at once (16 units of 251 tiles on 152 SMs: 9
+  // pieces each, 144 in all; 10 would leave eight pieces for a second turn); with
+  // more, which take turns anyway, up.
+  const int64_t all = max(static_cast<int64_t>(work) * a.heads, static_cast<int64_t>(1));
+  const bool few = static_cast<int64_t>(units) * a.heads * kFewUnits <= a.sms;
   auto cuts = [&](int32_t tiles) {
-    return static_cast<int32_t>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(kMaxPieces), ceil_div(tiles, piece))));
+    if (a.slots == 0) return 1;
+    const int64_t share = (static_cast<int64_t>(tiles) * a.sms + (few ? 0 : all - 1)) / all;
+    return static_cast<int32_t>(max(static_cast<int64_t>(1), min(share, min(static_cast<int64_t>(kMaxPieces), static_cast<int64_t>(tiles) / kMinPiece))));
   };
   for (int32_t u = tid; u < units; u += kThreads) {
     const int32_t tiles = unit_of(a, u, blocks).tiles, c = cuts(tiles);
@@ -149,10 +153,14 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
     const int32_t at = atomicAdd(&next[bucket], c);
     const int32_t slot = c > 1 ? atomicAdd(&slots, c) : 0;
     for (int32_t i = 0; i < c && at + i < a.max_pieces; ++i) {
-      Piece p;
+      Piece p{};
       p.b = n.b, p.block = n.block;
+      p.q0 = n.b < 0 ? 0 : a.qsl[n.b];
+      p.q1 = n.b < 0 ? 0 : a.qsl[n.b + 1];
+      p.seq = n.b < 0 ? 0 : max(0, a.seq_lens[n.b]);
       p.j0 = static_cast<int32_t>(static_cast<int64_t>(n.tiles) * i / c);
       p.j1 = static_cast<int32_t>(static_cast<int64_t>(n.tiles) * (i + 1) / c);
+      p.image = n.b < 0 ? 0 : a.tile_start[n.b] + p.j0;
       p.pieces = c, p.slot = slot, p.index = i;
       p.seg0 = first[bucket], p.seg = count[bucket];
       a.pieces[at + i] = p;
