@@ -778,6 +778,7 @@ struct ChunkPlan {
   int64_t tiles, units;                                // images per head, units per head
   size_t starts, pieces, valid, rope;                  // offsets of the parts
   size_t fixed;                                        // bytes of what the heads share
+  int64_t lo_tiles;                                    // tiles with key remainders per head
   size_t image_bytes;                                  // bytes of a head's images
   int sms;
 };
@@ -799,11 +800,12 @@ bool chunk_plan(int32_t B, int32_t T, int32_t H, int64_t total_len, ChunkPlan* p
   if (p->tiles * H > 0x7fffffff || most * H > 0x7fffffff) return false;
   const size_t n = static_cast<size_t>(p->tiles);
   p->starts = 0;
-  p->pieces = round256((2 * (static_cast<size_t>(B) + 1) + 1) * 4);
+  p->pieces = round256((3 * (static_cast<size_t>(B) + 1) + 1) * 4);
   p->valid = round256(p->pieces + static_cast<size_t>(most) * sizeof(dcp::Piece));
   p->rope = round256(p->valid + n * 16);
   p->fixed = p->rope + n * dcp::kImage;
-  p->image_bytes = n * (4 * dcp::kImage + 16);
+  p->lo_tiles = std::min<int64_t>(p->tiles, static_cast<int64_t>(B) * dcp::kFineTiles);
+  p->image_bytes = n * (4 * dcp::kImage + 16) + static_cast<size_t>(p->lo_tiles) * 2 * dcp::kImage;
   return true;
 }
 
@@ -894,13 +896,16 @@ dcp_status_t dcp_mla_chunk_attention(const void* q, int64_t q_stride_tok, int64_
   a.tiles = static_cast<int32_t>(p.tiles);
   a.tile_start = reinterpret_cast<int32_t*>(ws + p.starts);
   a.block_start = a.tile_start + B + 1;
-  a.num_pieces = a.block_start + B + 1;
+  a.lo_start = a.block_start + B + 1;
+  a.num_pieces = a.lo_start + B + 1;
   a.pieces = reinterpret_cast<dcp::Piece*>(ws + p.pieces);
   a.valid = reinterpret_cast<uint4*>(ws + p.valid);
   a.rope = ws + p.rope;
   a.keys = ws + p.fixed;
   a.values = a.keys + static_cast<size_t>(heads) * p.tiles * (2 * dcp::kImage);
-  a.bad = reinterpret_cast<uint4*>(a.values + static_cast<size_t>(heads) * p.tiles * (2 * dcp::kImage));
+  a.lo_keys = a.values + static_cast<size_t>(heads) * p.tiles * (2 * dcp::kImage);
+  a.lo_tiles = static_cast<int32_t>(p.lo_tiles);
+  a.bad = reinterpret_cast<uint4*>(a.lo_keys + static_cast<size_t>(heads) * p.lo_tiles * (2 * dcp::kImage));
   a.sms = p.sms;
   a.slots = static_cast<int32_t>(chunk_slots(p, heads));
   a.max_pieces = static_cast<int32_t>(p.units + (a.slots > 0 ? dcp::added_pieces(p.sms, heads) : 0));

@@ -5,9 +5,16 @@
 // Keys and values pass between the two as images of shared-memory tiles: what
 // one writes with a bulk store of 16 KB, the other loads with a bulk copy, and
 // no tensor map, address arithmetic or padding is left.  An image is 128 tokens
-// (of one request, from a multiple of 128) x 64 dims of bf16: 128-byte rows,
+// (of one request, from a multiple of 128) x 64 dims of 16 bits: 128-byte rows,
 // whose 16-byte units are permuted by the row's low three bits (the 128-byte
 // swizzle of the MMAs' operands).
+//
+// Keys, values, queries and softmax weights are f16 (rope dims: bf16, as they
+// come): 11 significant bits to bf16's 8, at the same rate.  A key's rounding
+// shifts its score by ~2e-4 (bf16: ~1.5e-3), and the log-sum-exp by that over the
+// root of the number of tokens that carry it.  Where those can be few, in
+// requests of up to kFineLen tokens, keys are f16 pairs, the value and its
+// rounding's remainder, at 1.4 times the MMAs: 22 bits.
 #pragma once
 
 #include "dcp_kernels.h"
@@ -18,6 +25,8 @@ namespace dcp {
 constexpr int kChunkTile = 128;                  // tokens of an image
 constexpr int kChunkRows = 256;                  // query rows of a unit: two MMA tiles of 128
 constexpr int kImage = kChunkTile * 128;         // bytes
+constexpr int kFineLen = 1024;                   // requests up to this length have key remainders
+constexpr int kFineTiles = kFineLen / kChunkTile;
 constexpr int kNope = 128, kVDim = 128;          // a head's key dims from the latent, its value dims
 constexpr int kUp = kNope + kVDim;               // rows of the up projection's weight per head
 constexpr int kWeightStage = kUp * 128;          // packed weight: 256 rows x 64 latent dims
@@ -41,7 +50,8 @@ struct __align__(16) Piece {
   int32_t pieces, index;  // of the unit, and which of them this is
   int32_t slot;           // the unit's first slot (of a head's)
   int32_t seg0, seg;      // pieces of similar length: the first, and how many
-  int32_t unused[3];
+  int32_t lo;             // its key remainders of key tile j0; -1: none
+  int32_t unused[2];
 };
 static_assert(sizeof(Piece) == 64, "four 16-byte units");
 
@@ -72,10 +82,13 @@ struct ChunkArgs {
   int32_t tiles;            // most images per head (tokens / 128 + B)
   int32_t* tile_start;      // [B + 1]: first image of a request
   int32_t* block_start;     // [B + 1]: first unit of a request
+  int32_t* lo_start;        // [B]: first tile of a request's key remainders; -1: none
+  int32_t lo_tiles;         // most tiles of key remainders per head
   unsigned char* rope;      // [tiles] images of the rope dims
   uint4* valid;             // [tiles]: tokens that exist
   unsigned char* keys;      // [heads of a pass][tiles][2 images]
   unsigned char* values;    // the same
+  unsigned char* lo_keys;   // [heads of a pass][lo_tiles][2 images]
   uint4* bad;               // [heads of a pass][tiles]: tokens whose value is not finite (their rows are zeros)
   int32_t h0, heads;        // the heads of this pass
   int32_t sms;

@@ -27,12 +27,17 @@
 // at most 256 then, and bf16 has the same relative step there), so O is
 // rescaled a few times per unit at most.
 //
-// Roundings: keys and values to bf16 once (they are MMA operands), P to bf16
-// once, the output once.  Scores, maxima, sums and O are fp32.
+// Roundings: keys (in long requests) and values to f16 once (they are MMA
+// operands), P to f16 once, the output once.  Scores, maxima, sums and O are
+// fp32.  Queries are f16 exactly: each row is scaled by a power of 2 that makes
+// its largest element 1 to 2, and what is left behind lies 2^-25 below that.
 #include "dcp_chunk.cuh"
+
+#include <cuda_fp16.h>
 
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 namespace dcp {
 namespace {
@@ -42,14 +47,16 @@ using namespace sm100;
 constexpr int kThreads = 384;
 constexpr int kGroup = 128;       // threads of a softmax group
 constexpr uint32_t kSlots = 8;         // ring of images
-constexpr int kQChunks = 3, kVChunks = 2;
-constexpr int kPerTile = kQChunks + kVChunks;
+constexpr int kQChunks = 3, kVChunks = 2;  // images of a tile's keys (two more where they have remainders) and values
 constexpr int kMaskSlots = 4;     // ring of the tiles' token masks
 constexpr int kOffQ = 0;          // two query tiles of 3 images
 constexpr int kOffRing = 2 * kQChunks * kImage;
 constexpr int kOffMask = kOffRing + kSlots * kImage;  // kMaskSlots x (valid, bad)
 constexpr int kOffBars = kOffMask + kMaskSlots * 32;
 constexpr float kRescaleLog2 = 8.0f;
+// P carries this power of 2: with the 2^8 above, up to 2^14 (f16 ends at 2^16),
+// and down to 2^-30 of the largest weight.
+constexpr float kLift = 6.0f;
 
 struct Bars {
   uint64_t q_full[2];                  // a group's Q is in shared memory (128)
@@ -62,6 +69,7 @@ struct Bars {
   uint32_t tmem;
   int32_t abort;
   int32_t head;                        // of this pass
+  int32_t q_exp[2][128];               // row r of group g: its queries are multiplied by 2^-q_exp
   Piece piece;
 };
 constexpr int kSmemBytes = kOffBars + static_cast<int>(sizeof(Bars)) + 1024;
@@ -117,8 +125,9 @@ struct Issue {
   const int32_t n0, n1;
   bool ok;
 
-  template <int g>
-  __device__ __forceinline__ void step(int32_t j, uint32_t k0) {  // k0: K(j)'s first image
+  // k0: K(j)'s first image; fine: keys have remainders, images 3 and 4 of a tile
+  template <int g, bool fine>
+  __device__ __forceinline__ void step(int32_t j, uint32_t k0) {
     const int32_t tiles = g ? n1 : n0, n = n0 > n1 ? n0 : n1;
     if (j >= 1 && j - 1 < tiles && ok) {  // O_g += P_g(j - 1) V(j - 1)
       const uint32_t v0 = (k0 - kVChunks) % kSlots, v1 = (v0 + 1) % kSlots;
@@ -128,12 +137,12 @@ struct Issue {
       const uint64_t d = dring + ((v0 * kImage) >> 4);
       constexpr uint32_t o = kColO + 128 * g, p = kColS + 128 * g;
       if (v1 == v0 + 1) {
-        constexpr uint32_t id = idesc_bf16(128, 128, 0, 1);
+        constexpr uint32_t id = idesc_f16(128, 128, 0, 1);
         mma_ts(o, p, d, id, j > 1);
 #pragma unroll
         for (int k = 1; k < 8; ++k) mma_ts(o, p + 8 * k, d + ((2048 * k) >> 4), id, 1);
       } else {  // (64 dims each from the ring's last and first slot)
-        constexpr uint32_t id = idesc_bf16(128, 64, 0, 1);
+        constexpr uint32_t id = idesc_f16(128, 64, 0, 1);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           mma_ts(o, p + 8 * k, d + ((2048 * k) >> 4), id, j > 1 || k > 0);
@@ -151,9 +160,18 @@ struct Issue {
 #pragma unroll
       for (int c = 0; c < kQChunks; ++c) {
         const uint64_t q = dq + (((g * kQChunks + c) * kImage) >> 4), k = dring + ((((k0 + c) % kSlots) * kImage) >> 4);
-        constexpr uint32_t id = idesc_bf16(128, 128, 0, 0);
+        constexpr uint32_t nope = idesc_f16(128, 128, 0, 0), rope = idesc_bf16(128, 128, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mma_ss(kColS + 128 * g, q + 2 * i, k + 2 * i, id, (c | i) != 0);
+        for (int i = 0; i < 4; ++i) mma_ss(kColS + 128 * g, q + 2 * i, k + 2 * i, c < 2 ? nope : rope, (c | i) != 0);
+      }
+      if constexpr (fine) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint64_t q = dq + (((g * kQChunks + c) * kImage) >> 4), k = dring + ((((k0 + kQChunks + c) % kSlots) * kImage) >> 4);
+          constexpr uint32_t id = idesc_f16(128, 128, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma_ss(kColS + 128 * g, q + 2 * i, k + 2 * i, id, 1);
+        }
       }
       mma_commit(&bar.s_full[g]);
     }
@@ -228,10 +246,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   const int32_t image0 = bar.piece.image;
   const Tile t0 = tile_of(bar, 0), t1 = tile_of(bar, 1);
   const int32_t n0 = t0.tiles, n1 = t1.tiles, n = max(n0, n1);
-  volatile int32_t* stop = &bar.abort;
+  const bool fine = bar.piece.lo >= 0;  // keys have remainders
   auto failed = [&]() {
     if (a.dev_error) atomicOr(a.dev_error, DCP_DEVERR_TIMEOUT);
-    *stop = 1;
   };
 
   if (warp < 8) {
@@ -255,15 +272,49 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       }
       cp_async_commit();
       cp_async_wait<0>();
-      if (a.q_sign != 0u) {  // a negative scale: this thread's units with the other sign
+      // to f16 (rope dims: bf16), each row's largest finite element to [1, 4)
 #pragma unroll 1
-        for (int i = 0; i < 32 * kQChunks; i += 4) {
-          uint4* p = reinterpret_cast<uint4*>(qs + (i >> 5) * kImage + image_unit(32 * quad + (i & 31) + (lane >> 3), un));
-          uint4 v = *p;
-          v.x ^= a.q_sign, v.y ^= a.q_sign, v.z ^= a.q_sign, v.w ^= a.q_sign;
-          *p = v;
+      for (int i = 0; i < 32; i += 4) {
+        const int qr = 32 * quad + i + (lane >> 3);
+        uint4* at[kQChunks];
+        uint4 v[kQChunks];
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < kQChunks; ++c) {
+          at[c] = reinterpret_cast<uint4*>(qs + c * kImage + image_unit(qr, un));
+          v[c] = *at[c];
+          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t x = w[k] & 0x7fffu, y = (w[k] >> 16) & 0x7fffu;
+            top = max(top, max(x < 0x7f80u ? x : 0u, y < 0x7f80u ? y : 0u));
+          }
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // (an exponent of -126 for subnormals, 0 for a row of zeros; 127 as 126,
+        // whose power has a reciprocal)
+        const int e = top == 0 ? 0 : min(max(static_cast<int>(top >> 7), 1) - 127, 126);
+        if (un == 0) bar.q_exp[g][qr] = e;
+        const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+        for (int c = 0; c < kQChunks; ++c) {
+          uint32_t w[4] = {v[c].x ^ a.q_sign, v[c].y ^ a.q_sign, v[c].z ^ a.q_sign, v[c].w ^ a.q_sign};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x = __uint_as_float(w[k] << 16) * f, y = __uint_as_float(w[k] & 0xffff0000u) * f;
+            if (c < 2) {
+              const __half2 b = __floats2half2_rn(x, y);
+              w[k] = *reinterpret_cast<const uint32_t*>(&b);
+            } else {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+              w[k] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+          }
+          *at[c] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
+      __syncwarp();
       fence_proxy_async_smem();
       mbar_arrive(&bar.q_full[g]);
     }
@@ -273,7 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t to = ts - kColS + kColO;
     float m = -INFINITY, l = 0.f;  // running maximum (log2, scaled) and sum
     bool ok = true, nan_row = false;
-    const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2);
+    // (never 0, for 0 x -inf would be NaN)
+    const int qe = tiles > 0 ? bar.q_exp[g][row] : 0;
+    const float c1 = fmaxf(1.17549435e-38f, a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + qe) << 23));
+    const uint64_t c2 = f2_pack(c1, c1);
     for (int32_t j = 0; j < tiles; ++j) {
       ok = mbar_wait_warp(&bar.mask_full[j % kMaskSlots], (j / kMaskSlots) & 1);  // (long there)
       ok = ok && mbar_wait_warp(&bar.s_full[g], j & 1);
@@ -314,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             x = ex2_approx(x);
             y = ex2_approx(y);
             sum[k & 1] = f2_add(sum[k & 1], f2_pack(x, y));
-            const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+            const __half2 b = __floats2half2_rn(x, y);
             p[k] = *reinterpret_cast<const uint32_t*>(&b);
           }
           tmem_st16(ts + 16 * part, p);
@@ -332,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[i + k], s[i + k + 4]);
 #pragma unroll
       for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[124 + k]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-      float add = weigh(m == -INFINITY ? 0.f : m);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1;
+      float add = weigh(m == -INFINITY ? 0.f : m - kLift);
       const bool grow = top > m + kRescaleLog2 || (m == -INFINITY && top > m);
       if (__any_sync(0xffffffffu, grow)) {
         const float to_m = grow ? top : m;
@@ -351,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             tmem_st16(to + 16 * c, o);
           }
         }
-        add = weigh(m == -INFINITY ? 0.f : m);
+        add = weigh(m == -INFINITY ? 0.f : m - kLift);
       }
       l += add;
       tmem_wait_st();
@@ -365,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     tc_fence_after();
     if (nan_row) l = __int_as_float(0x7fc00000);
     const float inv = tiles > 0 && l != 0.f ? 1.0f / l : 0.f;
-    const float lse = tiles > 0 && l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    const float lse = tiles > 0 && l != 0.f ? (m - kLift + log2f(l)) * kLn2 : -INFINITY;
     const bool cut = bar.piece.pieces > 1;
     unsigned char* slot = a.partial + (static_cast<int64_t>(hp) * a.slots + bar.piece.slot) * kSlotBytes;  // the unit's first
     unsigned char* own = slot + static_cast<int64_t>(bar.piece.index) * kSlotBytes;
@@ -432,9 +486,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const uint64_t dring = smem_desc(smem_u32(smem + kOffRing), kImage, 1024, kSwizzle128B);
         Issue is{bar, dq, dring, n0, n1, true};
         uint32_t k0 = 0;
-        for (int32_t j = 0; j <= n && is.ok; ++j, k0 += kPerTile) {
-          is.step<0>(j, k0);
-          is.step<1>(j, k0);
+        if (!fine) {
+          for (int32_t j = 0; j <= n && is.ok; ++j, k0 += kQChunks + kVChunks) {
+            is.step<0, false>(j, k0);
+            is.step<1, false>(j, k0);
+          }
+        } else {
+          for (int32_t j = 0; j <= n && is.ok; ++j, k0 += kQChunks + 2 + kVChunks) {
+            is.step<0, true>(j, k0);
+            is.step<1, true>(j, k0);
+          }
         }
         if (!is.ok) failed();
         mma_commit(&bar.fin);  // the MMAs are complete before TMEM goes
@@ -449,36 +510,50 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const unsigned char* keys = a.keys + (static_cast<int64_t>(hp) * a.tiles + image0) * (2 * kImage);
         const unsigned char* values = a.values + (static_cast<int64_t>(hp) * a.tiles + image0) * (2 * kImage);
         const unsigned char* rope = a.rope + static_cast<int64_t>(image0) * kImage;
+        const unsigned char* lo = a.lo_keys + (static_cast<int64_t>(hp) * a.lo_tiles + max(0, bar.piece.lo)) * (2 * kImage);
         const uint4* valid = a.valid + image0;
         const uint4* bad = a.bad + static_cast<int64_t>(hp) * a.tiles + image0;
         unsigned char* ring = smem + kOffRing;
-        // K(j) takes slots of K(j - 2) and V(j - 2), V(j) of K(j - 1)
-        uint32_t slot = 0;
         int32_t nk = 0, nv = 0;  // loaded so far
         bool ok = true;
-        for (int32_t j = 0; j < n && ok; ++j) {
-          const int32_t o = j & 1, before = (j - 1) & 1;
-          if (j >= 2) ok = mbar_wait(&bar.v_free[o], ((j >> 1) - 1) & 1);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&bar.k_full[o], kQChunks * kImage);
-          bulk_load(ring + slot * kImage, keys, kImage, &bar.k_full[o]);
-          bulk_load(ring + ((slot + 1) % kSlots) * kImage, keys + kImage, kImage, &bar.k_full[o]);
-          bulk_load(ring + ((slot + 2) % kSlots) * kImage, rope, kImage, &bar.k_full[o]);
-          ++nk;
-          uint64_t* mb = &bar.mask_full[j % kMaskSlots];
-          unsigned char* dst = smem + kOffMask + (j % kMaskSlots) * 32;
-          mbar_arrive_expect_tx(mb, 32);
-          bulk_load(dst, valid, 16, mb);
-          bulk_load(dst + 16, bad, 16, mb);
-          if (j >= 1) ok = mbar_wait(&bar.k_free[before], ((j - 1) >> 1) & 1);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&bar.v_full[o], kVChunks * kImage);
-          bulk_load(ring + ((slot + 3) % kSlots) * kImage, values, kImage, &bar.v_full[o]);
-          bulk_load(ring + ((slot + 4) % kSlots) * kImage, values + kImage, kImage, &bar.v_full[o]);
-          ++nv;
-          slot = (slot + kPerTile) % kSlots;
-          keys += 2 * kImage, values += 2 * kImage, rope += kImage, ++valid, ++bad;
-        }
+        auto stream = [&](auto fine_c) {
+          constexpr bool kFine = decltype(fine_c)::value;
+          constexpr uint32_t kKeyImages = kQChunks + (kFine ? 2 : 0);
+          uint32_t slot = 0;
+          for (int32_t j = 0; j < n; ++j) {
+            // K(j) takes slots of K(j - 2) and V(j - 2), V(j) of K(j - 1); with
+            // remainders, K(j) of V(j - 2) and K(j - 1), V(j) of K(j - 1) and V(j - 1)
+            const int32_t o = j & 1, before = (j - 1) & 1;
+            if (j >= 2) ok = mbar_wait(&bar.v_free[o], ((j >> 1) - 1) & 1);
+            if (kFine && j >= 1) ok = ok && mbar_wait(&bar.k_free[before], ((j - 1) >> 1) & 1);
+            if (!ok) return;
+            mbar_arrive_expect_tx(&bar.k_full[o], kKeyImages * kImage);
+            bulk_load(ring + slot * kImage, keys, kImage, &bar.k_full[o]);
+            bulk_load(ring + ((slot + 1) % kSlots) * kImage, keys + kImage, kImage, &bar.k_full[o]);
+            bulk_load(ring + ((slot + 2) % kSlots) * kImage, rope, kImage, &bar.k_full[o]);
+            if constexpr (kFine) {
+              bulk_load(ring + ((slot + 3) % kSlots) * kImage, lo, kImage, &bar.k_full[o]);
+              bulk_load(ring + ((slot + 4) % kSlots) * kImage, lo + kImage, kImage, &bar.k_full[o]);
+              lo += 2 * kImage;
+            }
+            ++nk;
+            uint64_t* mb = &bar.mask_full[j % kMaskSlots];
+            unsigned char* dst = smem + kOffMask + (j % kMaskSlots) * 32;
+            mbar_arrive_expect_tx(mb, 32);
+            bulk_load(dst, valid, 16, mb);
+            bulk_load(dst + 16, bad, 16, mb);
+            if (j >= 1) ok = mbar_wait(kFine ? &bar.v_free[before] : &bar.k_free[before], ((j - 1) >> 1) & 1);
+            if (!ok) return;
+            mbar_arrive_expect_tx(&bar.v_full[o], kVChunks * kImage);
+            bulk_load(ring + ((slot + kKeyImages) % kSlots) * kImage, values, kImage, &bar.v_full[o]);
+            bulk_load(ring + ((slot + kKeyImages + 1) % kSlots) * kImage, values + kImage, kImage, &bar.v_full[o]);
+            ++nv;
+            slot = (slot + kKeyImages + kVChunks) % kSlots;
+            keys += 2 * kImage, values += 2 * kImage, rope += kImage, ++valid, ++bad;
+          }
+        };
+        if (fine) stream(std::true_type{});
+        else stream(std::false_type{});
         if (!ok) failed();
         // nothing lands after the CTA is gone
         for (int32_t k = max(0, nk - 2); k < nk; ++k) mbar_wait(&bar.k_full[k & 1], (k >> 1) & 1);

@@ -15,7 +15,7 @@
 // 851 us.)
 //
 // Warp roles (512 threads in each CTA of the pair):
-//   warps 0-3, 12-15  epilogue of the keys and of the values: accumulator -> bf16
+//   warps 0-3, 12-15  epilogue of the keys and of the values: accumulator -> f16
 //               -> images in shared memory -> bulk stores; thread = token = TMEM
 //               lane.  (By four warps for both ~3,400 cycles an item; with plain
 //               stores ~4,500, more than its MMAs' 4,096.)
@@ -63,6 +63,7 @@ struct Bars {
   uint64_t fin;               // both: the issuer's MMAs are complete
   uint32_t tmem;
   int32_t abort;
+  int32_t lo[4];              // the last tiles' key remainders (-1: none), tile by tile
 };
 constexpr int kSmemBytes = kOffBars + static_cast<int>(sizeof(Bars)) + 1024;
 static_assert(kSmemBytes <= 232448, "exceeds the 227 KB of shared memory per CTA");
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     unsigned char* images = part ? a.values : a.keys;
     const uint64_t stream = l2_stream();
     int32_t pair = work.i0 / a.heads, h = work.i0 - pair * a.heads;
+    uint32_t tile_count = 0;
     for (int32_t i = work.i0, n = 0; i < work.i1; ++i, ++n) {
       const int acc = n & 1;
       if (!mbar_wait_warp(&bar.acc_full[acc], (n >> 1) & 1)) { failed(); break; }
@@ -154,28 +156,38 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       const int32_t tile = 2 * pair + static_cast<int32_t>(rank);
       const int64_t slot = static_cast<int64_t>(h) * a.tiles + tile;
       const uint32_t col = tmem + (static_cast<uint32_t>(quad) << 21) + 256u * acc + 128u * part;
-      uint32_t v[64];  // 128 dims as bf16 pairs
+      uint32_t v[64];  // 128 dims as f16 pairs
+      const int32_t lo = part ? -1 : bar.lo[tile_count & 3];
+#pragma unroll 1
+      for (int turn = 0; turn < 1 + (lo >= 0); ++turn) {  // (keys of short requests: then what their rounding left)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        tmem_ld32(col + 32 * c, r);
-        tmem_wait_ld();
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          tmem_ld32(col + 32 * c, r);
+          tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
-          v[16 * c + k] = *reinterpret_cast<const uint32_t*>(&b);
+          for (int k = 0; k < 16; ++k) {
+            const float x = __uint_as_float(r[2 * k]), y = __uint_as_float(r[2 * k + 1]);
+            __half2 b = __floats2half2_rn(x, y);
+            if (turn) {
+              const float2 f = __half22float2(b);
+              b = __floats2half2_rn(x - f.x, y - f.y);
+            }
+            v[16 * c + k] = *reinterpret_cast<const uint32_t*>(&b);
+          }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      // (relaxed: the accumulator has been read, and no write of this warp
-      // concerns the issuer; a release waited ~3,000 cycles for them)
-      if (lane == 0) mbar_arrive_remote_relaxed(free0 + 8 * acc);
-      if (tile < tiles) {  // (the last tile may have no second one)
+        if (turn == (lo >= 0)) {
+          tc_fence_before();
+          __syncwarp();
+          // (relaxed: the accumulator has been read, and no write of this warp
+          // concerns the issuer; a release waited ~3,000 cycles for them)
+          if (lane == 0) mbar_arrive_remote_relaxed(free0 + 8 * acc);
+        }
+        if (tile >= tiles) continue;  // (the last tile may have no second one)
         if (part) {
           bool fin = true;
 #pragma unroll
-          for (int k = 0; k < 64; ++k) fin = fin && (v[k] & 0x7f80u) != 0x7f80u && (v[k] & 0x7f800000u) != 0x7f800000u;
+          for (int k = 0; k < 64; ++k) fin = fin && (v[k] & 0x7c00u) != 0x7c00u && (v[k] & 0x7c000000u) != 0x7c000000u;
           const uint32_t nan_rows = __ballot_sync(0xffffffffu, !fin);
           if (!fin) {
 #pragma unroll
@@ -183,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
           }
           if (lane == 0) reinterpret_cast<uint32_t*>(a.bad + slot)[quad] = nan_rows;
         }
-        unsigned char* dst = images + slot * (2 * kImage) + quad * kOutWarp;
+        unsigned char* dst = (turn ? a.lo_keys + (static_cast<int64_t>(h) * a.lo_tiles + lo) * (2 * kImage) : images + slot * (2 * kImage)) + quad * kOutWarp;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {  // an image's 64 dims
           if (elected()) bulk_wait_read<0>();  // (the last store has read its source)
@@ -200,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
           }
         }
       }
-      if (++h == a.heads) h = 0, ++pair;
+      if (++h == a.heads) h = 0, ++pair, ++tile_count;
     }
     if (elected()) bulk_wait<0>();
     __syncwarp();
@@ -309,8 +321,11 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       const int32_t tile = 2 * last + static_cast<int32_t>(rank);
       // this thread's token (a tile past the last is all zeros)
       int64_t src = -1;
+      int32_t lo = -1;
       if (tile < tiles) {
         const int32_t b = find_range(a.tile_start, a.B, tile);
+        lo = a.lo_start[b];
+        if (lo >= 0) lo += tile - a.tile_start[b];
         const int64_t p = static_cast<int64_t>(tile - a.tile_start[b]) * kChunkTile + 32 * lw + lane;
         if (p < a.seq_lens[b]) src = cache_row(a, b, static_cast<int32_t>(p));
       }
@@ -320,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       const uint32_t live = __ballot_sync(0xffffffffu, src >= 0);
       if (shared_too && lane == 0) reinterpret_cast<uint32_t*>(a.valid + tile)[lw] = live;
       if (loads > 0 && !mbar_wait_warp(&bar.a_free, (loads - 1) & 1)) { failed(); break; }
+      if (threadIdx.x == 8 * 32) bar.lo[loads & 3] = lo;
       ++loads;
       const int u = lane & 7;
 #pragma unroll 2

@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
   const int tid = threadIdx.x;
   for (int i = tid; i < kBuckets; i += kThreads) count[i] = 0;
   if (tid == 0) work = 0, slots = 0;
-  // ---- first images and blocks of the requests
-  int64_t base[2] = {0, 0};
+  // ---- first images and blocks of the requests, and tiles of key remainders
+  int64_t base[2] = {0, 0}, lo_base = 0;
   for (int32_t b0 = 0; b0 < a.B; b0 += kThreads) {
     const int32_t b = b0 + tid;
     int64_t x[2] = {0, 0};
@@ -106,6 +106,19 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
       a.block_start[b + 1] = static_cast<int32_t>(x[1] < 0x7fffffff ? x[1] : 0x7fffffff);
     }
     base[0] += sums[0][31], base[1] += sums[1][31];
+    __syncthreads();
+    int64_t lo[2] = {0, 0};
+    if (b < a.B) {
+      const int32_t seq = a.seq_lens[b];
+      lo[0] = some && seq <= kFineLen ? ceil_div(seq, kChunkTile) : 0;
+    }
+    const int32_t own = static_cast<int32_t>(lo[0]);
+    scan2(lo, sums);
+    if (b < a.B) {
+      const int64_t end = lo_base + lo[0];
+      a.lo_start[b] = own > 0 && end <= a.lo_tiles ? static_cast<int32_t>(end - own) : -1;
+    }
+    lo_base += sums[0][31];
     __syncthreads();
   }
   if (tid == 0) a.tile_start[0] = a.block_start[0] = 0;
@@ -161,6 +174,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
       p.j0 = static_cast<int32_t>(static_cast<int64_t>(n.tiles) * i / c);
       p.j1 = static_cast<int32_t>(static_cast<int64_t>(n.tiles) * (i + 1) / c);
       p.image = n.b < 0 ? 0 : a.tile_start[n.b] + p.j0;
+      p.lo = n.b < 0 || a.lo_start[n.b] < 0 ? -1 : a.lo_start[n.b] + p.j0;
       p.pieces = c, p.slot = slot, p.index = i;
       p.seg0 = first[bucket], p.seg = count[bucket];
       a.pieces[at + i] = p;

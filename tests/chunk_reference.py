@@ -1,20 +1,23 @@
 """Inputs and the fp64 reference of chunk attention.
 
-The reference rounds keys and values to bf16, as the operator is documented to,
-and is exact otherwise.  What may differ:
+The reference rounds values to f16, and keys of requests of more than FINE
+tokens, as the operator is documented to, and is exact otherwise.  What may
+differ:
 
-* the softmax weights, each rounded to bf16 (half a step, 2^-8 of it), and the
+* the softmax weights, each rounded to f16 (half a step, 2^-11 of it), and the
   bf16 output (2^-8 of the value);
 * keys and values that fp32 sums of 512 products left on the other side of a
-  rounding border: a step, 2^-7 of the element.  About one in a thousand does
-  (an fp32 error of 2^-20 in a step of 2^-7, twice, with room), so three of a
-  key's 128 products may, and three of the values of a sum;
+  rounding border: a step, 2^-10 of the element.  About one in 500 does (an fp32
+  error of 2^-20 on either side of a border, in steps of 2^-10), so six of a key's
+  128 products may, and six of the values of a sum.  Keys of shorter requests:
+  2^-22 of each product;
 * fp32 sums of 192 products and of the weights: 1e-5 of the sum of magnitudes.
 """
 import numpy as np
 import torch
 
 NOPE, ROPE, LATENT, KDIM, VDIM = 128, 64, 512, 576, 128
+FINE = 1024
 
 
 def owned(L, d, D, I):
@@ -91,8 +94,9 @@ def reference(st, skip_requests=()):
         see = (torch.arange(L, device=dev)[None, :] <= last[:, None]) & exists[None, :]
         for h in range(H):
             w = st["w"][256 * h:256 * h + 256].double()
-            up = (kv[:, :LATENT] @ w.T).float().to(torch.bfloat16).double()
-            k, v = torch.cat([up[:, :NOPE], kv[:, LATENT:]], 1), up[:, NOPE:]
+            up = kv[:, :LATENT] @ w.T
+            f16 = up.float().to(torch.float16).double()
+            k, v = torch.cat([(up if L <= FINE else f16)[:, :NOPE], kv[:, LATENT:]], 1), f16[:, NOPE:]
             q = st["q"][r0:r0 + n, h].double()
             s = (st["scale"] * (q @ k.T)).masked_fill(~see, -torch.inf)
             z = torch.logsumexp(s, 1)
@@ -102,11 +106,11 @@ def reference(st, skip_requests=()):
             v0 = torch.where(exists[:, None], v, torch.zeros_like(v))
             size = p @ v0.abs()
             big = torch.nan_to_num(q.abs()).amax(1) * torch.nan_to_num(k.abs()).amax()
-            ds = abs(st["scale"]) * (3 * 2.0 ** -7 * big + 1e-5 * torch.nan_to_num(q.abs()) @ torch.nan_to_num(k.abs()).amax(0))
+            ds = abs(st["scale"]) * ((6 * 2.0 ** -10 * big if L > FINE else 0.0) + 1e-5 * torch.nan_to_num(q.abs()) @ torch.nan_to_num(k.abs()).amax(0))
             peak = p.amax(1, keepdim=True) * torch.nan_to_num(v0.abs()).amax(0)[None]
             out[r0:r0 + n, h] = p @ v0
             lse[r0:r0 + n, h] = torch.where(some, z, torch.full_like(z, -torch.inf))
-            tol[r0:r0 + n, h] = size * (2 * ds[:, None] + 2.0 ** -8 + 1e-5) + 3 * 2.0 ** -7 * peak
+            tol[r0:r0 + n, h] = size * (2 * ds[:, None] + 2.0 ** -11 + 1e-5) + 6 * 2.0 ** -10 * peak
             tol_l[r0:r0 + n, h] = ds + 1e-5 * (1 + z.abs())
         r0 += n
     return out, lse, tol, tol_l
