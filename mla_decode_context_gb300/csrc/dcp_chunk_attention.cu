@@ -387,9 +387,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
       for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[124 + k]);
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1;
-      float add = weigh(m == -INFINITY ? 0.f : m - kLift);
-      const bool grow = top > m + kRescaleLog2 || (m == -INFINITY && top > m);
-      if (__any_sync(0xffffffffu, grow)) {
+      float add;
+#pragma unroll 1
+      while (true) {  // (once, or twice where a row has outgrown its maximum)
+        add = weigh(m == -INFINITY ? 0.f : m - kLift);
+        const bool grow = top > m + kRescaleLog2 || (m == -INFINITY && top > m);
+        if (!__any_sync(0xffffffffu, grow)) break;
         const float to_m = grow ? top : m;
         const float f = grow ? ex2_approx(m - to_m) : 1.f;
         m = to_m;
@@ -405,7 +408,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             tmem_st16(to + 16 * c, o);
           }
         }
-        add = weigh(m == -INFINITY ? 0.f : m - kLift);
       }
       l += add;
       tmem_wait_st();
