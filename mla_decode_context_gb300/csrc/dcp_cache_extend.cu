@@ -16,8 +16,9 @@
 // entries (a scan over the tables' needs, 1,024 at a time in shared memory;
 // then a thread per new entry finds its table by a search in the scan, so that
 // one table's thousand entries are as quick as a thousand tables' one).  Up to
-// kFusedTokens tokens follow in the same CTA, behind its own barrier; more
-// take a second grid whose launch overlaps the first (programmatic dependent
+// kFusedTokens tokens follow in the same CTA, behind its own barrier (they find
+// their requests in shared memory, where there are not too many); more take a
+// second grid whose launch overlaps the first (programmatic dependent
 // launch).
 #include "dcp_kernels.h"
 
@@ -27,6 +28,7 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kTokenThreads = 256;
 constexpr int kFusedTokens = 2048;
+constexpr int kKept = 2048;  // requests whose rows and lengths the CTA keeps for its tokens
 constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ int32_t owned(const CacheExtendArgs& a, int32_t L, int32_t d) {
@@ -72,9 +74,15 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(CacheExtendArgs a, int
   __shared__ int32_t start[kThreads + 1];  // first new entry of each of these tables, then their total
   __shared__ int32_t first_col[kThreads];
   __shared__ int32_t warp_sum[kThreads / 32];
+  __shared__ int32_t kept_qsl[kKept + 1], kept_seq[kKept];
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t tables = static_cast<int64_t>(a.B) * a.S;
+  const bool kept = fused && a.B <= kKept;
+  if (kept) {
+    for (int32_t b = tid; b < a.B; b += kThreads) kept_qsl[b] = __ldg(a.qsl + b), kept_seq[b] = __ldg(a.seq_lens + b);
+    if (tid == 0 && a.B > 0) kept_qsl[a.B] = __ldg(a.qsl + a.B);
+  }
   int32_t count = *a.free_count;
   count = count < 0 ? 0 : (count > a.num_free ? a.num_free : count);
   uint32_t err = 0;
@@ -144,7 +152,17 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(CacheExtendArgs a, int
   // (the last round's barrier, or none when there are no tables, orders the
   // entries before these reads)
   for (int32_t t = tid; t < a.T; t += kThreads) {
-    const RequestOfRow q = request_of_row(a.seq_lens, a.qsl, a.B, t);
+    RequestOfRow q{-1, 0, 0, 0};
+    if (!kept) {
+      q = request_of_row(a.seq_lens, a.qsl, a.B, t);
+    } else if (a.B > 0 && t >= kept_qsl[0] && t < kept_qsl[a.B]) {
+      int32_t lo = 0, hi = a.B;  // kept_qsl[lo] <= t < kept_qsl[hi]
+      while (hi - lo > 1) {
+        const int32_t mid = (lo + hi) >> 1;
+        if (kept_qsl[mid] <= t) lo = mid; else hi = mid;
+      }
+      q = RequestOfRow{lo, kept_qsl[lo], kept_qsl[lo + 1], kept_seq[lo]};
+    }
     place(a, t, q.b, q.q0, q.q1, q.seq);
   }
 }
