@@ -1453,7 +1453,12 @@ def chunk_attention(q, kv_cache, block_table, seq_lens, query_start_loc, packed_
     out = torch.empty((T, H, VALUE_DIM), dtype=out_dtype, device=q.device)
     lse = torch.empty((T, H), dtype=_F32, device=q.device)
     if workspace is None:
-        n = dcp_chunk_attention_workspace_size(seq_lens.shape[0], T, H, total_len)
+        sizes, index = (seq_lens.shape[0], T, H, total_len), q.get_device()
+        if index < 0 or _device_now() == index:
+            n = dcp_chunk_attention_workspace_size(*sizes)
+        else:  # (it goes by the SMs of the device that the call runs on)
+            with torch.cuda.device(index):
+                n = dcp_chunk_attention_workspace_size(*sizes)
         workspace = torch.empty(n, dtype=_U8, device=q.device) if n else None
     dcp_mla_chunk_attention(q, kv_cache, block_table, seq_lens, query_start_loc, packed_kv_b, out, lse, workspace,
                             scale=scale, total_len=total_len, kv_scale=kv_scale, D=D, interleave=interleave,

@@ -57,6 +57,7 @@ constexpr float kRescaleLog2 = 8.0f;
 // P carries this power of 2: with the 2^8 above, up to 2^14 (f16 ends at 2^16),
 // and down to 2^-30 of the largest weight.
 constexpr float kLift = 6.0f;
+constexpr float kFar = 1048576.0f;
 
 struct Bars {
   uint64_t q_full[2];                  // a group's Q is in shared memory (128)
@@ -324,6 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t to = ts - kColS + kColO;
     float m = -INFINITY, l = 0.f;  // running maximum (log2, scaled) and sum
     bool ok = true, nan_row = false;
+    // A row of the warp has a maximum past 2^20.  Then scores are scaled, and so
+    // rounded, as the maximum was, before it is taken off: s c - m in one rounding
+    // leaves what the maximum lost by its own, which is past every f16 from 2^28 on.
+    bool far = false;
     // (never 0, for 0 x -inf would be NaN)
     const int qe = tiles > 0 ? bar.q_exp[g][row] : 0;
     const float c1 = fmaxf(1.17549435e-38f, a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + qe) << 23));
@@ -353,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           for (int k = 0; k < 32; ++k) s[32 * w + k] = (see >> k) & 1u ? s[32 * w + k] : -INFINITY;
         }
       }
+      uint64_t ct = c2;
       // P and the maximum side by side: the maximum nearly always stays within
       // 2^8 of the running one, and then P is right as it is
       auto weigh = [&](float base) {
@@ -364,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             float x, y;
-            f2_unpack(f2_fma(f2_pack(s[32 * part + 2 * k], s[32 * part + 2 * k + 1]), c2, nb), x, y);
+            f2_unpack(f2_fma(f2_pack(s[32 * part + 2 * k], s[32 * part + 2 * k + 1]), ct, nb), x, y);
             x = ex2_approx(x);
             y = ex2_approx(y);
             sum[k & 1] = f2_add(sum[k & 1], f2_pack(x, y));
@@ -390,12 +396,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       float add;
 #pragma unroll 1
       while (true) {  // (once, or twice where a row has outgrown its maximum)
+        if (far && ct == c2) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) f2_unpack(f2_mul(f2_pack(s[2 * k], s[2 * k + 1]), c2), s[2 * k], s[2 * k + 1]);
+          ct = f2_pack(1.f, 1.f);
+        }
         add = weigh(m == -INFINITY ? 0.f : m - kLift);
         const bool grow = top > m + kRescaleLog2 || (m == -INFINITY && top > m);
         if (!__any_sync(0xffffffffu, grow)) break;
         const float to_m = grow ? top : m;
         const float f = grow ? ex2_approx(m - to_m) : 1.f;
         m = to_m;
+        far = __any_sync(0xffffffffu, fabsf(m) > kFar && m != -INFINITY);
         l *= f;
         if (j > 0) {  // (PV(j - 1) is complete: S(j) came after it)
 #pragma unroll 1
