@@ -57,7 +57,10 @@ constexpr float kRescaleLog2 = 8.0f;
 // P carries this power of 2: with the 2^8 above, up to 2^14 (f16 ends at 2^16),
 // and down to 2^-30 of the largest weight.
 constexpr float kLift = 6.0f;
-constexpr float kFar = 1048576.0f;
+// s c - m in one rounding leaves what m lost by its own: at most 1 up to here, and
+// past it more than f16 takes.  (Taking the maximum off before scaling has no
+// such end, and cost 7 % of the time.)
+constexpr float kFarthest = 33554432.0f;
 
 struct Bars {
   uint64_t q_full[2];                  // a group's Q is in shared memory (128)
@@ -325,10 +328,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t to = ts - kColS + kColO;
     float m = -INFINITY, l = 0.f;  // running maximum (log2, scaled) and sum
     bool ok = true, nan_row = false;
-    // A row of the warp has a maximum past 2^20.  Then scores are scaled, and so
-    // rounded, as the maximum was, before it is taken off: s c - m in one rounding
-    // leaves what the maximum lost by its own, which is past every f16 from 2^28 on.
-    bool far = false;
     // (never 0, for 0 x -inf would be NaN)
     const int qe = tiles > 0 ? bar.q_exp[g][row] : 0;
     const float c1 = fmaxf(1.17549435e-38f, a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + qe) << 23));
@@ -358,7 +357,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           for (int k = 0; k < 32; ++k) s[32 * w + k] = (see >> k) & 1u ? s[32 * w + k] : -INFINITY;
         }
       }
-      uint64_t ct = c2;
       // P and the maximum side by side: the maximum nearly always stays within
       // 2^8 of the running one, and then P is right as it is
       auto weigh = [&](float base) {
@@ -370,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             float x, y;
-            f2_unpack(f2_fma(f2_pack(s[32 * part + 2 * k], s[32 * part + 2 * k + 1]), ct, nb), x, y);
+            f2_unpack(f2_fma(f2_pack(s[32 * part + 2 * k], s[32 * part + 2 * k + 1]), c2, nb), x, y);
             x = ex2_approx(x);
             y = ex2_approx(y);
             sum[k & 1] = f2_add(sum[k & 1], f2_pack(x, y));
@@ -393,21 +391,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
       for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[124 + k]);
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1;
-      float add;
+      float add = 0.f;
 #pragma unroll 1
-      while (true) {  // (once, or twice where a row has outgrown its maximum)
-        if (far && ct == c2) {
-#pragma unroll
-          for (int k = 0; k < 64; ++k) f2_unpack(f2_mul(f2_pack(s[2 * k], s[2 * k + 1]), c2), s[2 * k], s[2 * k + 1]);
-          ct = f2_pack(1.f, 1.f);
-        }
+      for (int turn = 0; turn < 2; ++turn) {  // (the second where a row has outgrown its maximum)
         add = weigh(m == -INFINITY ? 0.f : m - kLift);
         const bool grow = top > m + kRescaleLog2 || (m == -INFINITY && top > m);
         if (!__any_sync(0xffffffffu, grow)) break;
         const float to_m = grow ? top : m;
         const float f = grow ? ex2_approx(m - to_m) : 1.f;
         m = to_m;
-        far = __any_sync(0xffffffffu, fabsf(m) > kFar && m != -INFINITY);
         l *= f;
         if (j > 0) {  // (PV(j - 1) is complete: S(j) came after it)
 #pragma unroll 1
@@ -431,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     if (tiles > 0 && ok) ok = mbar_wait_warp(&bar.s_full[g], tiles & 1);
     if (!ok) failed();
     tc_fence_after();
-    if (nan_row) l = __int_as_float(0x7fc00000);
+    if (nan_row || (fabsf(m) > kFarthest && m != -INFINITY)) l = __int_as_float(0x7fc00000);
     const float inv = tiles > 0 && l != 0.f ? 1.0f / l : 0.f;
     const float lse = tiles > 0 && l != 0.f ? (m - kLift + log2f(l)) * kLn2 : -INFINITY;
     const bool cut = bar.piece.pieces > 1;
