@@ -10,9 +10,13 @@
 // memory, all 512 dims) and the weights of head after head stream past them.
 // Two CTAs share the weights: one MMA (M = 256, N = 256) reads each CTA's 128
 // tokens and half of a head's rows from either's shared memory, so that each
-// streams 32 bytes of weights a clock instead of 64.  (A CTA by itself, with a
-// ring of two 32 KB stages, waited for its weights: 24,000 tokens at 128 heads
-// 851 us.)
+// streams 32 bytes of weights a clock instead of 64.
+//
+// 24,000 tokens at 128 heads: ~540 us, 1.5 PFLOP/s (78 % of the measured rate),
+// 2.9 TB/s of stores.  What bounds it: the weights' loads, 16 KB each and four in
+// flight, take 1,500-3,000 cycles next to the images' stores to DRAM (an item
+// 6,000-6,500 cycles; without the stores 4,105, its MMAs' 4,096).  A fifth stage,
+// or stores by another path, changed nothing.  (A CTA by itself: 851 us.)
 //
 // Warp roles (512 threads in each CTA of the pair):
 //   warps 0-3, 12-15  epilogue of the keys and of the values: accumulator -> f16
@@ -62,7 +66,6 @@ struct Bars {
   uint64_t acc_free[2];       // CTA 0: both CTAs' epilogues have read it (8 warps each)
   uint64_t fin;               // both: the issuer's MMAs are complete
   uint32_t tmem;
-  int32_t abort;
   int32_t lo[4];              // the last tiles' key remainders (-1: none), tile by tile
 };
 constexpr int kSmemBytes = kOffBars + static_cast<int>(sizeof(Bars)) + 1024;
@@ -119,7 +122,6 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     for (uint32_t i = 0; i < kWStages; ++i) mbar_init(&bar.w_full[i], rank == 0 ? 2 : 1), mbar_init(&bar.w_free[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&bar.acc_full[i], 1), mbar_init(&bar.acc_free[i], 16);
     mbar_init(&bar.fin, 1);
-    bar.abort = 0;
     fence_mbar_init();
   }
   if (warp == 6) {
@@ -134,10 +136,8 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
   wait_dependency();
   const int32_t tiles = min(a.tile_start[a.B], a.tiles);
   const Work work = my_items(a, tiles);
-  volatile int32_t* stop = &bar.abort;
   auto failed = [&]() {
     if (a.dev_error) atomicOr(a.dev_error, DCP_DEVERR_TIMEOUT);
-    *stop = 1;
   };
 
   if (warp < 4 || warp >= 12) {

@@ -1,6 +1,7 @@
 // Chunk attention, the plan: first images and first blocks of the requests, and
 // the pieces of work of the attention in launch order.  One CTA; the lengths are
-// on the device only.
+// on the device only.  A chain of scans and shared-memory searches: 6-8 us for one
+// to 12 requests (9-10 in the profiler).
 //
 // Units are (request, block of 256 rows), the same for every head.  A launch
 // takes them longest first, so that the last ones to run are short.  Units of

@@ -19,7 +19,10 @@
 // rounds of 16-byte units of ql_nope, and one in which lane = (head, rope
 // unit): its angles are loaded once), or one per 16 heads of a chunk's queries
 // (rope parts alone, four rounds with the same angles).  A pair that is 32
-// dims apart lies four lanes apart.
+// dims apart lies four lanes apart.  256 tokens with 128 heads into an FP8 cache
+// (76 MB): 13.8 us, 5.5 TB/s; the rope parts of 4,099 tokens' 128 heads in pieces
+// of 128 bytes (145 MB): 28.4 us, 5.1 TB/s; 16,381 rows alone: 13.3 us, the
+// memory's latency over 1.7 waves.
 #include "dcp_kernels.h"
 
 #include <cuda_fp8.h>
