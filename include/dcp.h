@@ -599,6 +599,8 @@ size_t dcp_decode_select_workspace_size(int32_t B, int32_t T, int32_t H, int32_t
  *                of finished requests go back by writing their ids from
  *                free_blocks[count] on and raising the count.
  *   free_left    int32 [1], how many are left afterwards; may be free_count.
+ *                Calls that share a free list or tables follow one another (one
+ *                stream, or events).
  *   positions    int32 [T]; slot_mapping int64 [T].
  */
 dcp_status_t dcp_cache_extend(

@@ -390,36 +390,50 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint4* __restrict__ w, 
   *reinterpret_cast<uint4*>(packed + (row / kUp) * (kChunks * kWeightStage) + (u >> 3) * kWeightStage + image_unit(r, u & 7)) = __ldg(w + i);
 }
 
-std::mutex g_mutex;
-bool g_ready[2][64];
+using Kernel = void (*)(ChunkArgs);
 
-template <bool kFp8>
-cudaError_t set_up() {
+cudaLaunchConfig_t pairs_config(int pairs, cudaStream_t st, cudaLaunchAttribute (&attr)[2]) {
+  attr[0] = attr[1] = cudaLaunchAttribute{};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2u * static_cast<unsigned>(pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+// Pairs of CTAs that run at once on the current device (looked up once for each
+// device and kernel); more would wait for a second turn.
+std::mutex g_mutex;
+constexpr int kMaxDevices = 64;
+int g_pairs[2][kMaxDevices];
+
+cudaError_t resident_pairs(Kernel kernel, bool fp8, int* pairs) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(g_mutex);
-  if (dev < 64 && g_ready[kFp8][dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(expand_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e == cudaSuccess && dev < 64) g_ready[kFp8][dev] = true;
-  return e;
-}
-
-cudaError_t launch_pairs(void (*kernel)(ChunkArgs), const ChunkArgs& a, int grid, int threads, int smem, cudaStream_t st) {
-  cudaLaunchAttribute attr[2]{};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  if (dev < kMaxDevices && g_pairs[fp8][dev] > 0) {
+    *pairs = g_pairs[fp8][dev];
+    return cudaSuccess;
+  }
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = pairs_config(1, nullptr, attr);
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(pairs, kernel, &cfg);
+  if (e != cudaSuccess) return e;
+  if (*pairs < 1) return cudaErrorInvalidConfiguration;
+  if (dev < kMaxDevices) g_pairs[fp8][dev] = *pairs;
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -432,14 +446,15 @@ cudaError_t launch_pack_kv_b(const void* w, int32_t H, void* packed, cudaStream_
 }
 
 cudaError_t launch_chunk_expand(const ChunkArgs& a, cudaStream_t st) {
-  int dev = 0, sms = 0;
-  cudaError_t e = a.kv_scale ? set_up<true>() : set_up<false>();
-  if (e == cudaSuccess) e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const bool fp8 = a.kv_scale != nullptr;
+  const Kernel kernel = fp8 ? expand_kernel<true> : expand_kernel<false>;
+  int pairs = 0;
+  const cudaError_t e = resident_pairs(kernel, fp8, &pairs);
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>((a.tiles + 1) / 2) * a.heads;
-  const int grid = 2 * static_cast<int>(items < sms / 2 ? items : sms / 2);
-  return launch_pairs(a.kv_scale ? expand_kernel<true> : expand_kernel<false>, a, grid, kThreads, kSmemBytes, st);
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = pairs_config(static_cast<int>(items < pairs ? items : pairs), st, attr);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace dcp

@@ -84,7 +84,7 @@ __device__ __forceinline__ Unit unit_of(const ChunkArgs& a, const Requests& r, i
 __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ ChunkArgs a) {
   __shared__ int64_t sums[3][32];
   __shared__ int32_t kept[5][kKept + 1];
-  __shared__ int32_t count[kBuckets], first[kBuckets];
+  __shared__ int32_t count[kBuckets], first[kBuckets], next[kBuckets];
   __shared__ unsigned long long work;
   __shared__ int32_t slots;
   sm100::launch_dependents();
@@ -157,19 +157,23 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
     atomicAdd(&count[bucket_of((tiles + c - 1) / c)], c);
   }
   __syncthreads();
-  if (tid < kBuckets) {
-    int32_t n = 0;
-#pragma unroll 16
-    for (int i = 0; i < kBuckets; ++i) n += i < tid ? count[i] : 0;
-    first[tid] = n;
-    if (tid == kBuckets - 1) *a.num_pieces = n + count[tid];
+  if (tid < 32) {  // four buckets a lane
+    int32_t c[4], n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = count[4 * tid + i], n += c[i];
+    int32_t x = n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(kFull, x, o);
+      if (tid >= o) x += y;
+    }
+    x -= n;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) first[4 * tid + i] = next[4 * tid + i] = x, x += c[i];
+    if (tid == 31) *a.num_pieces = x;
   }
   __syncthreads();
   // ---- records.  `next` places a unit's pieces in its bucket; their order there
   // and the slots' do not change results.
-  __shared__ int32_t next[kBuckets];
-  if (tid < kBuckets) next[tid] = first[tid];
-  __syncthreads();
   for (int32_t u = tid; u < units; u += kThreads) {
     const Unit n = unit_of(a, req, u, blocks);
     const int32_t c = cuts(n.tiles), bucket = bucket_of((n.tiles + c - 1) / c);

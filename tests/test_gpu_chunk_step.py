@@ -133,6 +133,21 @@ def test_more_requests_than_the_plan_keeps():
     ref.check(out, lse, ref.reference(st))
 
 
+@pytest.mark.parametrize("lead,T_cut", [(5, 0), (300, 0), (0, 30), (7, 50)])
+def test_rows_before_the_first_request_and_rows_cut_off(lead, T_cut):
+    """query_start_loc that starts past row 0 (rows of no request before it), or that
+    ends past the last row of the query (only the rows that exist are computed)."""
+    st = ref.make(seq=[300, 77], q=[60, 77], H=2, bs=64, seed=7)
+    want = ref.reference(st)
+    T = lead + 137 - T_cut
+    q = torch.zeros((T, 2, 192), dtype=torch.bfloat16, device="cuda")
+    q[lead:] = st["q"][:137 - T_cut]
+    out, lse = dcp.chunk_attention(q, st["cache"], st["table"], st["seq"], st["qsl"] + lead, dcp.pack_kv_b(st["w"]),
+                                   scale=st["scale"], total_len=st["total"])
+    assert (out[:lead] == 0).all() and (lse[:lead] == -torch.inf).all()
+    ref.check(out[lead:], lse[lead:], [x[:137 - T_cut] for x in want])
+
+
 def test_nothing_to_see():
     st = ref.make(seq=[0, 0], q=[3, 300], H=2, seed=3, pad=7)
     out, lse = dcp.chunk_attention(st["q"], st["cache"], st["table"], st["seq"], st["qsl"], dcp.pack_kv_b(st["w"]),
