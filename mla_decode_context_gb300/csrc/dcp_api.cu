@@ -812,7 +812,7 @@ bool chunk_plan(int32_t B, int32_t T, int32_t H, int64_t total_len, ChunkPlan* p
 // Slots for the pieces of cut units, per head of a pass of `heads`: twice the
 // pieces that the cuts add, and none where no unit is long enough to be cut.
 int64_t chunk_slots(const ChunkPlan& p, int32_t heads) {
-  if (p.tiles <= dcp::kMinPiece) return 0;
+  if (p.tiles < 2 * dcp::kMinPiece) return 0;
   const int64_t by_units = p.units * std::min<int64_t>(dcp::kMaxPieces, (p.tiles + dcp::kMinPiece - 1) / dcp::kMinPiece);
   return std::min(by_units, 2 * dcp::added_pieces(p.sms, heads));
 }
