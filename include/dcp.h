@@ -697,13 +697,13 @@ dcp_status_t dcp_pack_kv_b(const void* w_kv_b, int32_t H, void* packed, void* st
  *                Calls that may overlap need one each.
  *
  * Numbers: values, and keys of requests of more than 1,024 tokens, are rounded
- * to f16 once (keys of shorter ones are kept to 22 bits), and so are the softmax
- * weights (relative to a running maximum); everything else is fp32.  An FP8 code
- * times a scale that is no power of two is rounded to bf16.  A NaN score makes
- * the rows that see its token NaN, and no others; so does a key or value with an
- * element that is not finite or past f16's largest, 65,504.  A row whose largest
- * score is past 2e7 in magnitude (fp32 keeps no digit behind the point there) is
- * NaN.
+ * to f16 once (keys of shorter ones are kept to 22 bits; f16's steps are 2^-24
+ * below 2^-14), and so are the softmax weights (relative to a running maximum);
+ * everything else is fp32.  An FP8 code times a scale that is no power of two is
+ * rounded to bf16.  A NaN score makes the rows that see its token NaN, and no
+ * others; so does a key or value with an element that is not finite or past f16's
+ * largest, 65,504.  A row whose largest score is past 2e7 in magnitude (fp32 keeps
+ * no digit behind the point there) is NaN.
  *
  * Cost: 640 operations per row, token and head and 262,144 per token and head,
  * against 2,176 per row, token and head of the decodes: below ~170 rows of a

@@ -133,6 +133,15 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
   cluster_sync();  // (the peer's barriers are set up)
   tc_fence_after();
   const uint32_t tmem = 0;  // (all 512 columns: the allocation starts at the first)
+  // While the plan runs: this CTA's share of the weights of the pass, into L2
+  // (2,833 us instead of 2,855 for 2,048 rows on 21,952 tokens, 759 instead of 765
+  // for 12 mixed requests).
+  if (warp == 4 && elected()) {
+    const int64_t n = static_cast<int64_t>(a.heads) * (kChunks * kWeightStage / kWHalf);  // of 16 KB
+    const unsigned char* w = static_cast<const unsigned char*>(a.weight) + static_cast<int64_t>(a.h0) * (kChunks * kWeightStage);
+    for (int64_t i = blockIdx.x; i < n; i += gridDim.x) bulk_prefetch(w + i * kWHalf, kWHalf);
+  }
+  __syncwarp();
   wait_dependency();
   const int32_t tiles = min(a.tile_start[a.B], a.tiles);
   const Work work = my_items(a, tiles);
