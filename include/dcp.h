@@ -701,8 +701,10 @@ dcp_status_t dcp_pack_kv_b(const void* w_kv_b, int32_t H, void* packed, void* st
  * below 2^-14), and so are the softmax weights (relative to a running maximum);
  * everything else is fp32.  An FP8 code times a scale that is no power of two is
  * rounded to bf16.  A NaN score makes the rows that see its token NaN, and no
- * others; so does a key or value with an element that is not finite or past f16's
- * largest, 65,504.  A row whose largest score is past 2e7 in magnitude (fp32 keeps
+ * others; so does a projected key or value with an element that is not finite or
+ * past f16's largest, 65,504.  (An infinite rope element makes its token's scores
+ * what the arithmetic makes them: NaN or +inf, and the row NaN, or -inf, and the
+ * token weighs nothing.)  A row whose largest score is past 2e7 in magnitude (fp32 keeps
  * no digit behind the point there) is NaN.
  *
  * Cost: 640 operations per row, token and head and 262,144 per token and head,

@@ -32,7 +32,9 @@
 //
 // A value that is not finite would reach query rows that do not see its token
 // (0 x NaN in the product with the weights of a tile), so a token with one gets
-// a row of zeros and a bit in `bad`: rows that see it become NaN.
+// a row of zeros and a bit in `bad`: rows that see it become NaN.  A key that is
+// not finite, or past f16's largest, is made NaN: an infinite element's score
+// could be -inf, which weighs nothing.
 #include "dcp_chunk.cuh"
 
 #include <cuda_fp16.h>
@@ -193,16 +195,21 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
           if (lane == 0) mbar_arrive_remote_relaxed(free0 + 8 * acc);
         }
         if (tile >= tiles) continue;  // (the last tile may have no second one)
-        if (part) {
-          bool fin = true;
+        if (turn == 0) {
+          __half2 zero = __half2half2(__ushort_as_half(0)), sum = zero;  // 0 x (infinity or NaN) is NaN
 #pragma unroll
-          for (int k = 0; k < 64; ++k) fin = fin && (v[k] & 0x7c00u) != 0x7c00u && (v[k] & 0x7c000000u) != 0x7c000000u;
-          const uint32_t nan_rows = __ballot_sync(0xffffffffu, !fin);
-          if (!fin) {
+          for (int k = 0; k < 64; ++k) sum = __hfma2(*reinterpret_cast<const __half2*>(&v[k]), zero, sum);
+          const bool fin = (*reinterpret_cast<const uint32_t*>(&sum) & 0x7fff7fffu) == 0u;
+          if (part) {
+            const uint32_t nan_rows = __ballot_sync(0xffffffffu, !fin);
+            if (!fin) {
 #pragma unroll
-            for (int k = 0; k < 64; ++k) v[k] = 0;
+              for (int k = 0; k < 64; ++k) v[k] = 0;
+            }
+            if (lane == 0) reinterpret_cast<uint32_t*>(a.bad + slot)[quad] = nan_rows;
+          } else if (!fin) {
+            v[0] = 0x7fff7fffu;
           }
-          if (lane == 0) reinterpret_cast<uint32_t*>(a.bad + slot)[quad] = nan_rows;
         }
         unsigned char* dst = (turn ? a.lo_keys + (static_cast<int64_t>(h) * a.lo_tiles + lo) * (2 * kImage) : images + slot * (2 * kImage)) + quad * kOutWarp;
 #pragma unroll
