@@ -584,6 +584,9 @@ size_t dcp_decode_select_workspace_size(int32_t B, int32_t T, int32_t H, int32_t
  * other entries are left as they are.  A request of no tokens takes nothing.
  *   - Out of free blocks: the entries are -1 and DCP_DEVERR_NO_BLOCKS is set.
  *   - Columns at or past bt_width are not taken (DCP_DEVERR_SEQ_TOO_LONG).
+ *   - A step after rejected drafts has fewer old tokens than the table has blocks
+ *     for: the columns past them are taken anew, and what they held is lost to the
+ *     free list unless the caller puts it back.  dcp_cache_extend_v2 counts them.
  * Row i of a request is the token at position p = seq_lens[b] - q_len + i:
  *   positions[r] = p, slot_mapping[r] = entry(p) * block_size + offset(p)
  * slot_mapping -1 where the entry is negative or missing, or a shard outside
@@ -609,6 +612,31 @@ dcp_status_t dcp_cache_extend(
     const int32_t* seq_lens, const int32_t* query_start_loc, int32_t B, int32_t T, int32_t block_size,
     int32_t D, int32_t interleave, int32_t shard_begin, int32_t shard_count,
     const int32_t* free_blocks, int32_t num_free, const int32_t* free_count, int32_t* free_left,
+    int32_t* positions, int64_t* slot_mapping,
+    int32_t* dev_error, void* stream);
+
+/*
+ * dcp_cache_extend with a count of the blocks that each table holds, for steps
+ * of speculative verification, whose drafts may be rejected, and for a free list
+ * that may run out.
+ *
+ *   held  in/out int32 [B] (per_shard_tables: [shard_count, B]), dense, or NULL
+ *         (as dcp_cache_extend): the leading columns of a table that hold a
+ *         block; 0 for a new request, whatever its table's row held before.  A
+ *         request gets columns [held, ceil(len(seq) / block_size)), and held
+ *         becomes that end, or the first column without a block where the free
+ *         list ran out (the next step takes that column again).  Where the
+ *         tokens need fewer columns, none is taken and held stays: a block that a
+ *         rejected draft reached into is used by the next one.  The blocks of a
+ *         finished request are its first `held` columns.
+ */
+dcp_status_t dcp_cache_extend_v2(
+    int32_t* block_table, int32_t bt_width, int64_t bt_stride,
+    int32_t per_shard_tables, int64_t bt_shard_stride,
+    const int32_t* seq_lens, const int32_t* query_start_loc, int32_t B, int32_t T, int32_t block_size,
+    int32_t D, int32_t interleave, int32_t shard_begin, int32_t shard_count,
+    const int32_t* free_blocks, int32_t num_free, const int32_t* free_count, int32_t* free_left,
+    int32_t* held,
     int32_t* positions, int64_t* slot_mapping,
     int32_t* dev_error, void* stream);
 

@@ -90,6 +90,9 @@ EXPORTS = [
     ("dcp_decode_select_workspace_size", _SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32]),
     ("dcp_cache_extend", ctypes.c_int,
      [_P, _I32, _I64, _I32, _I64, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _P]),
+    ("dcp_cache_extend_v2", ctypes.c_int,
+     [_P, _I32, _I64, _I32, _I64, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _P,
+      _P]),
     ("dcp_norm_rope_cache", ctypes.c_int,
      [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _F, _P, _P, _I32, _I32, _P, _I32, _I32,
       _P, ctypes.c_int, _P, _I64, _P, _P]),
@@ -909,11 +912,14 @@ def _explain_read(kv_cache, block_table, cu_lens, out, seq_starts, kv_scale, sha
 
 def dcp_cache_extend(block_table, seq_lens, query_start_loc, free_blocks, free_count, free_left, positions,
                      slot_mapping, *, block_size: int, D: int = 1, interleave: int = 1, shard_begin: int = 0,
-                     shard_count: Optional[int] = None, dev_error: Optional[torch.Tensor] = None, stream=None) -> None:
+                     shard_count: Optional[int] = None, held: Optional[torch.Tensor] = None,
+                     dev_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """Build a step's block tables and slot map: block_table int32 [B, W] or
     per-shard [shard_count, B, W] (extended in place), free_blocks int32 [F],
     free_count and free_left int32 [1] (may be the same), positions int32 [T]
-    and slot_mapping int64 [T] (written)."""
+    and slot_mapping int64 [T] (written).  held int32 [B] or [shard_count, B]
+    (updated; dcp_cache_extend_v2): how many blocks each table holds, for steps
+    whose drafts may be rejected."""
     if shard_count is None:
         shard_count = D - shard_begin
     _fits32(D | interleave | block_size | shard_begin, "dcp_cache_extend")
@@ -935,31 +941,37 @@ def dcp_cache_extend(block_table, seq_lens, query_start_loc, free_blocks, free_c
             and free_left.dtype is _I32T and free_left.get_device() == device and free_left.numel() == 1
             and positions.dtype is _I32T and positions.get_device() == device and positions.is_contiguous()
             and slot_mapping.dtype is _I64T and slot_mapping.get_device() == device and slot_mapping.shape == (T,)
-            and slot_mapping.is_contiguous() and (dev_error is None or _flag_word(dev_error, device)))
+            and slot_mapping.is_contiguous()
+            and (held is None or (held.dtype is _I32T and held.get_device() == device and held.is_contiguous()
+                                  and held.shape == table[:-1]))
+            and (dev_error is None or _flag_word(dev_error, device)))
     except (AttributeError, TypeError, ValueError):
         good = False
     if not good:
         B, T, local, device = _explain_extend(block_table, seq_lens, query_start_loc, free_blocks, free_count,
-                                              free_left, positions, slot_mapping, shard_count, dev_error)
+                                              free_left, positions, slot_mapping, shard_count, held, dev_error)
         num_free = free_blocks.shape[0]
         table, table_stride = block_table.shape, block_table.stride()
-    call = (_lib or lib()).dcp_cache_extend
+    call = (_lib or lib()).dcp_cache_extend_v2
     _launch("dcp_cache_extend", device, call,
             block_table.data_ptr(), table[-1], table_stride[-2] if B > 1 else table[-1], 1 if local else 0,
             table_stride[0] if local else 0, seq_lens.data_ptr(), query_start_loc.data_ptr(), B, T, block_size, D,
             interleave, shard_begin, shard_count, free_blocks.data_ptr(), num_free, free_count.data_ptr(),
-            free_left.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(),
+            free_left.data_ptr(), None if held is None else held.data_ptr(), positions.data_ptr(),
+            slot_mapping.data_ptr(),
             None if dev_error is None else dev_error.data_ptr(), _stream_of(stream, device))
 
 
 def _explain_extend(block_table, seq_lens, query_start_loc, free_blocks, free_count, free_left, positions,
-                    slot_mapping, shard_count, dev_error):
+                    slot_mapping, shard_count, held, dev_error):
     """What is wrong with a table extension's tensors, or (B, T, local, device)."""
     i32 = torch.int32
     args = [("block_table", block_table, i32, False), ("seq_lens", seq_lens, i32, True),
             ("query_start_loc", query_start_loc, i32, True), ("free_blocks", free_blocks, i32, True),
             ("free_count", free_count, i32, False), ("free_left", free_left, i32, False),
             ("positions", positions, i32, True), ("slot_mapping", slot_mapping, torch.int64, True)]
+    if held is not None:
+        args.append(("held", held, i32, True))
     if dev_error is not None:
         args.append(("dev_error", dev_error, i32, False))
     _types(args)
@@ -974,6 +986,8 @@ def _explain_extend(block_table, seq_lens, query_start_loc, free_blocks, free_co
         raise ValueError("free_blocks must be [F], free_count and free_left [1]")
     if positions.dim() != 1 or tuple(slot_mapping.shape) != tuple(positions.shape):
         raise ValueError("positions and slot_mapping must be [T]")
+    if held is not None and held.shape != block_table.shape[:-1]:
+        raise ValueError("held must be [B] or [shard_count, B], as block_table is")
     if dev_error is not None and dev_error.numel() == 0:
         raise ValueError("dev_error must not be empty")
     return B, positions.shape[0], local, _placed(args)
@@ -1384,21 +1398,24 @@ def decode_partial_tree(q, kv_cache, block_table, seq_lens, query_start_loc, tre
 
 def cache_extend(block_table, seq_lens, query_start_loc, free_blocks, free_count, num_tokens: int, block_size: int,
                  free_left: Optional[torch.Tensor] = None, D: int = 1, interleave: int = 1, shard_begin: int = 0,
-                 shard_count: Optional[int] = None, dev_error: Optional[torch.Tensor] = None, stream=None):
+                 shard_count: Optional[int] = None, dev_error: Optional[torch.Tensor] = None, stream=None,
+                 held: Optional[torch.Tensor] = None):
     """Allocating form of dcp_cache_extend: extends block_table in place, writes
     what is left of the free list into free_left (free_count itself by
     default) and returns (positions int32, slot_mapping int64) of the step's
-    num_tokens rows."""
+    num_tokens rows.  Steps whose drafts may be rejected give held, int32 zeros
+    of block_table's leading dims at first: the blocks that each table holds."""
     if stream is not None:  # (as in _decode_select_alloc)
         with _stream_context(stream, block_table.device):
             return cache_extend(block_table, seq_lens, query_start_loc, free_blocks, free_count, num_tokens,
                                 block_size, free_left=free_left, D=D, interleave=interleave, shard_begin=shard_begin,
-                                shard_count=shard_count, dev_error=dev_error)
+                                shard_count=shard_count, dev_error=dev_error, held=held)
     positions = torch.empty(num_tokens, dtype=_I32T, device=block_table.device)
     slots = torch.empty(num_tokens, dtype=_I64T, device=block_table.device)
     dcp_cache_extend(block_table, seq_lens, query_start_loc, free_blocks, free_count,
                      free_count if free_left is None else free_left, positions, slots, block_size=block_size, D=D,
-                     interleave=interleave, shard_begin=shard_begin, shard_count=shard_count, dev_error=dev_error)
+                     interleave=interleave, shard_begin=shard_begin, shard_count=shard_count, held=held,
+                     dev_error=dev_error)
     return positions, slots
 
 

@@ -732,12 +732,12 @@ dcp_status_t dcp_norm_rope_cache(const void* ql_nope, int64_t ql_nope_stride_tok
   return dcp::launch_norm_rope(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DCP_OK : DCP_ERR_CUDA;
 }
 
-dcp_status_t dcp_cache_extend(int32_t* block_table, int32_t bt_width, int64_t bt_stride, int32_t per_shard_tables,
-                              int64_t bt_shard_stride, const int32_t* seq_lens, const int32_t* query_start_loc,
-                              int32_t B, int32_t T, int32_t block_size, int32_t D, int32_t interleave,
-                              int32_t shard_begin, int32_t shard_count, const int32_t* free_blocks, int32_t num_free,
-                              const int32_t* free_count, int32_t* free_left, int32_t* positions,
-                              int64_t* slot_mapping, int32_t* dev_error, void* stream) {
+dcp_status_t dcp_cache_extend_v2(int32_t* block_table, int32_t bt_width, int64_t bt_stride, int32_t per_shard_tables,
+                                 int64_t bt_shard_stride, const int32_t* seq_lens, const int32_t* query_start_loc,
+                                 int32_t B, int32_t T, int32_t block_size, int32_t D, int32_t interleave,
+                                 int32_t shard_begin, int32_t shard_count, const int32_t* free_blocks, int32_t num_free,
+                                 const int32_t* free_count, int32_t* free_left, int32_t* held,
+                                 int32_t* positions, int64_t* slot_mapping, int32_t* dev_error, void* stream) {
   if (B < 0 || T < 0 || D < 1 || D > DCP_MAX_SHARDS || interleave < 1 || block_size < 1 || num_free < 0)
     return DCP_ERR_INVALID_ARG;
   if (shard_begin < 0 || shard_count < 1 || shard_begin + static_cast<int64_t>(shard_count) > D) return DCP_ERR_INVALID_ARG;
@@ -762,9 +762,21 @@ dcp_status_t dcp_cache_extend(int32_t* block_table, int32_t bt_width, int64_t bt
   a.div_D = dcp::make_fastdiv(D);
   a.div_bs = dcp::make_fastdiv(block_size);
   a.free_blocks = free_blocks; a.num_free = num_free; a.free_count = free_count; a.free_left = free_left;
+  a.held = held;
   a.positions = positions; a.slot_mapping = slot_mapping;
   a.dev_error = dev_error;
   return dcp::launch_cache_extend(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DCP_OK : DCP_ERR_CUDA;
+}
+
+dcp_status_t dcp_cache_extend(int32_t* block_table, int32_t bt_width, int64_t bt_stride, int32_t per_shard_tables,
+                              int64_t bt_shard_stride, const int32_t* seq_lens, const int32_t* query_start_loc,
+                              int32_t B, int32_t T, int32_t block_size, int32_t D, int32_t interleave,
+                              int32_t shard_begin, int32_t shard_count, const int32_t* free_blocks, int32_t num_free,
+                              const int32_t* free_count, int32_t* free_left, int32_t* positions,
+                              int64_t* slot_mapping, int32_t* dev_error, void* stream) {
+  return dcp_cache_extend_v2(block_table, bt_width, bt_stride, per_shard_tables, bt_shard_stride, seq_lens,
+                             query_start_loc, B, T, block_size, D, interleave, shard_begin, shard_count, free_blocks,
+                             num_free, free_count, free_left, nullptr, positions, slot_mapping, dev_error, stream);
 }
 
 }  // extern "C"

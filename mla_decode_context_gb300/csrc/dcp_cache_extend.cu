@@ -7,7 +7,9 @@
 //   tables (one per request, or one per (request, shard) over the shard's local
 //   tokens) have ceil(len(old) / bs) entries and get those up to
 //   ceil(len(seq) / bs); new entry k, counted over (b, d, column) in order, is
-//   free_blocks[free_count - 1 - k].
+//   free_blocks[free_count - 1 - k].  With a count of the columns that a table
+//   holds, from there on instead (after rejected drafts the old tokens end before
+//   the blocks do).
 //   token i of request b: position p = seq - q_len + i, slot = entry(p) * bs +
 //   offset.
 //
@@ -93,14 +95,20 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(CacheExtendArgs a, int
   for (int64_t i0 = 0; i0 < tables; i0 += kThreads) {
     const int64_t i = i0 + tid;
     int32_t need = 0, c0 = 0;
+    int32_t* held = nullptr;
     if (i < tables) {
       const int32_t b = static_cast<int32_t>(a.S == 1 ? i : i / a.S), dd = static_cast<int32_t>(i - static_cast<int64_t>(b) * a.S);
       const int32_t q0 = __ldg(a.qsl + b), q1 = __ldg(a.qsl + b + 1);
       const int32_t seq = max(0, __ldg(a.seq_lens + b));
       if (q1 < q0) err |= DCP_DEVERR_BAD_ROWS;
-      const int64_t before = static_cast<int64_t>(seq) - max(static_cast<int64_t>(q1) - q0, static_cast<int64_t>(0));
-      const int32_t old = before > 0 ? static_cast<int32_t>(before) : 0;
-      c0 = blocks_of(a, a.local_tables ? owned(a, old, a.d0 + dd) : old);
+      if (a.held) {
+        held = a.held + static_cast<int64_t>(dd) * a.B + b;
+        c0 = max(0, *held);
+      } else {
+        const int64_t before = static_cast<int64_t>(seq) - max(static_cast<int64_t>(q1) - q0, static_cast<int64_t>(0));
+        const int32_t old = before > 0 ? static_cast<int32_t>(before) : 0;
+        c0 = blocks_of(a, a.local_tables ? owned(a, old, a.d0 + dd) : old);
+      }
       int32_t c1 = blocks_of(a, a.local_tables ? owned(a, seq, a.d0 + dd) : seq);
       if (c1 > a.bt_width) {
         err |= DCP_DEVERR_SEQ_TOO_LONG;
@@ -129,6 +137,10 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(CacheExtendArgs a, int
     if (warp > 0) x += warp_sum[warp - 1];
     start[tid] = x - need;
     first_col[tid] = c0;
+    if (held && need > 0) {  // as far as the free list reaches
+      const int64_t got = static_cast<int64_t>(count) - base - (x - need);
+      *held = c0 + (got <= 0 ? 0 : (got < need ? static_cast<int32_t>(got) : need));
+    }
     if (tid == kThreads - 1) start[kThreads] = x;
     __syncthreads();
     const int32_t total = start[kThreads];

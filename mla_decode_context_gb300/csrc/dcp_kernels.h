@@ -228,6 +228,7 @@ struct CacheExtendArgs {
   int32_t num_free;
   const int32_t* free_count;
   int32_t* free_left;
+  int32_t* held;          // [S, B] leading columns that hold a block; nullptr: those of the old tokens
   int32_t* positions;     // [T]
   int64_t* slot_mapping;  // [T]
   int32_t* dev_error;
