@@ -703,7 +703,9 @@ dcp_status_t dcp_pack_kv_b(const void* w_kv_b, int32_t H, void* packed, void* st
  *   c(p) = kv(p)[0:512],  s_p = scale * sum_{k<192} q[r,h,k] * k_h(p)[k]
  *   lse[r,h] = ln sum_{p<L} exp(s_p),  out[r,h,:] = sum_{p<L} exp(s_p - lse[r,h]) v_h(p)
  * A row with nothing to see, of no request or of a request of no tokens: 0 and
- * -inf.  Whole contexts: per-shard tables hold all D shards.
+ * -inf.  Whole contexts: per-shard tables hold all D shards.  B == 0 or T == 0
+ * returns DCP_OK without launching anything: the caller fills the rows of a step
+ * without requests (the Python binding does).
  *
  *   q            bf16 [T, H, 192], 128 dims for W_h's keys, then 64 rope dims
  *                (rotated, dcp_norm_rope_cache); token and head strides in

@@ -4,14 +4,17 @@ Argument marshalling only: every step of the path runs in the library's CUDA
 kernels.  Functions named like the C entry points take caller-allocated
 torch tensors; ``decode_partial`` and ``lse_combine`` allocate their outputs
 with torch and call the same entry points.  PyTorch provides device memory
-and streams, nothing else.
+and streams, nothing else (and fills chunk attention's outputs in a step without
+requests).
 
 The library is loaded on first use; if it has not been built the call raises
 (there is no fallback path).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -1141,7 +1144,8 @@ def dcp_mla_chunk_attention(q, kv_cache, block_table, seq_lens, query_start_loc,
     kv_scale, block_table int32 [B, W] or per-shard [D, B, W], packed_kv_b from
     dcp_pack_kv_b; writes out bf16 or fp32 [T, H, 128] and lse fp32 [T, H].
     total_len bounds the sum of seq_lens; workspace has
-    dcp_chunk_attention_workspace_size bytes (fewer: more passes)."""
+    dcp_chunk_attention_workspace_size bytes (fewer: more passes).  Without
+    requests (B = 0) the rows are zeros and -inf, as other rows of no request."""
     _fits32(D | interleave, "dcp_mla_chunk_attention")
     try:
         T, H, dim = q.shape
@@ -1188,6 +1192,10 @@ def dcp_mla_chunk_attention(q, kv_cache, block_table, seq_lens, query_start_loc,
             DTYPE_BF16 if o_dtype is _BF16 else DTYPE_F32, lse.data_ptr(),
             workspace.data_ptr() if ws_bytes else None, ws_bytes,
             None if dev_error is None else dev_error.data_ptr(), _stream_of(stream, device))
+    if B == 0 and T > 0:  # (the library's call does nothing then)
+        with contextlib.nullcontext() if stream is None else _stream_context(stream, q.device):
+            out.zero_()
+            lse.fill_(-math.inf)
 
 
 def _explain_chunk(q, kv_cache, block_table, seq_lens, query_start_loc, packed_kv_b, out, lse, workspace, kv_scale, D,
