@@ -735,7 +735,8 @@ dcp_status_t dcp_pack_kv_b(const void* w_kv_b, int32_t H, void* packed, void* st
  * past f16's largest, 65,504.  (An infinite rope element makes its token's scores
  * what the arithmetic makes them: NaN or +inf, and the row NaN, or -inf, and the
  * token weighs nothing.)  A row whose largest score is past 2e7 in magnitude (fp32 keeps
- * no digit behind the point there) is NaN.
+ * no digit behind the point there; -inf too) is NaN; scores that far below the
+ * largest weigh nothing.
  *
  * Cost: 640 operations per row, token and head and 262,144 per token and head,
  * against 2,176 per row, token and head of the decodes: below ~170 rows of a

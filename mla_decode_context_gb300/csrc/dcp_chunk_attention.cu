@@ -64,8 +64,12 @@ constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLift = 6.0f;
 // s c - m in one rounding leaves what m lost by its own: at most 1 up to here, and
 // past it more than f16 takes.  (Taking the maximum off before scaling has no
-// such end, and cost 7 % of the time.)
+// such end, and cost 7 % of the time.)  While a row's maximum is below -kFarthest,
+// its scores weigh 0, as they do next to any above it, and a row that sees no
+// others is NaN.  A piece of a cut unit cannot know: its log-sum-exp is kFar,
+// which the join takes for NaN where no piece has more.
 constexpr float kFarthest = 33554432.0f;
+constexpr float kFar = -3.402823466e38f;  // (the lowest finite number; no log-sum-exp comes near it)
 
 struct Bars {
   uint64_t q_full[2];                  // a group's Q is in shared memory (128)
@@ -196,6 +200,19 @@ __device__ void pad_rows(const ChunkArgs& a, int64_t r0, int64_t r1, int32_t h) 
     else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) = make_uint2(0u, 0u);
   }
   for (int64_t r = r0 + threadIdx.x; r < r1; r += kThreads) a.lse[r * a.H + h] = -INFINITY;
+}
+
+// Whether a row sees any of a piece's tokens; `left`: those up to its own, from the
+// piece's first.  (Rare, and a call: written out in the kernel it cost the softmax's
+// loop 2 % of the time.)
+__device__ __noinline__ bool sees_any(const uint4* valid, int32_t tiles, int32_t left) {
+  for (int32_t j = 0; j < tiles && left > 0; ++j, left -= kChunkTile) {
+    const uint4 v = valid[j];
+    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+    for (int w = 0; w < 4; ++w)
+      if ((left - 32 * w >= 32 ? vw[w] : left > 32 * w ? vw[w] & ((1u << (left - 32 * w)) - 1u) : 0u) != 0u) return true;
+  }
+  return false;
 }
 
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ ChunkArgs a) {
@@ -395,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[i + k], s[i + k + 4]);
 #pragma unroll
       for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[124 + k]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1;
+      const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1, -kFarthest);
       float add = 0.f;
 #pragma unroll 1
       for (int turn = 0; turn < 2; ++turn) {  // (the second where a row has outgrown its maximum)
@@ -428,10 +445,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     if (tiles > 0 && ok) ok = mbar_wait_warp(&bar.s_full[g], tiles & 1);
     if (!ok) failed();
     tc_fence_after();
-    if (nan_row || (fabsf(m) > kFarthest && m != -INFINITY)) l = __int_as_float(0x7fc00000);
-    const float inv = tiles > 0 && l != 0.f ? 1.0f / l : 0.f;
-    const float lse = tiles > 0 && l != 0.f ? (m - kLift + log2f(l)) * kLn2 : -INFINITY;
+    bool far = false;  // sees tokens, and all their scores are below -kFarthest
+    if (m <= -kFarthest) far = sees_any(a.valid + bar.piece.image, tiles, L - bar.piece.j0 * kChunkTile);
     const bool cut = bar.piece.pieces > 1;
+    if (nan_row || m > kFarthest || (far && !cut)) l = __int_as_float(0x7fc00000);
+    const float inv = tiles > 0 && l != 0.f ? 1.0f / l : 0.f;
+    const float lse = tiles > 0 && l != 0.f ? (m - kLift + log2f(l)) * kLn2 : far ? kFar : -INFINITY;
     unsigned char* slot = a.partial + (static_cast<int64_t>(hp) * a.slots + bar.piece.slot) * kSlotBytes;  // the unit's first
     unsigned char* own = slot + static_cast<int64_t>(bar.piece.index) * kSlotBytes;
     if (cut) reinterpret_cast<float*>(own)[kChunkRows * kVDim + 128 * g + row] = lse;
@@ -622,10 +641,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     // (all -inf: nothing to see; a NaN weighs NaN)
-    const float w = lse == -INFINITY ? 0.f : ex2_approx((lse - (top == -INFINITY ? 0.f : top)) * kLog2e);
+    const float w = lse <= kFar ? 0.f : ex2_approx((lse - top) * kLog2e);
     float sum = w;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (top == kFar) sum = __int_as_float(0x7fc00000);  // nothing but far scores
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = 0; k0 < p.pieces; k0 += kBatch) {
       float4 v[kBatch];
