@@ -898,8 +898,7 @@ dcp_status_t dcp_mla_chunk_attention(const void* q, int64_t q_stride_tok, int64_
   a.div_D = dcp::make_fastdiv(D);
   a.div_bs = dcp::make_fastdiv(block_size);
   a.seq_lens = seq_lens; a.qsl = query_start_loc; a.B = B; a.T = T; a.H = H;
-  // (a scale of 0 as a positive one that makes every score 0: 0 x -inf would be NaN)
-  a.scale_log2 = scale == 0.f ? 0x1p-120f : std::fabs(scale) * dcp::kLog2e;
+  a.scale_log2 = std::fabs(scale) * dcp::kLog2e;
   a.q_sign = scale < 0.f ? 0x80008000u : 0u;
   a.weight = packed_kv_b;
   a.out = out; a.out_f32 = out_dtype == DCP_DTYPE_F32; a.lse = lse;

@@ -350,9 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t to = ts - kColS + kColO;
     float m = -INFINITY, l = 0.f;  // running maximum (log2, scaled) and sum
     bool ok = true, nan_row = false;
-    // (never 0, for 0 x -inf would be NaN)
+    // (never 0, for 0 x -inf would be NaN: the least number, times which any finite
+    // score is next to 0)
     const int qe = tiles > 0 ? bar.q_exp[g][row] : 0;
-    const float c1 = fmaxf(1.17549435e-38f, a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + qe) << 23));
+    const float c1 = fmaxf(1.401298464e-45f, a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + qe) << 23));
     const uint64_t c2 = f2_pack(c1, c1);
     for (int32_t j = 0; j < tiles; ++j) {
       ok = mbar_wait_warp(&bar.mask_full[j % kMaskSlots], (j / kMaskSlots) & 1);  // (long there)

@@ -75,3 +75,13 @@ def test_rows_that_see_a_near_token_and_rows_before_it():
         v = st["w"][256 * h + 128:256 * h + 256].double() @ kv[:512]
         # f16 value and weight (2^-11 each), and 1e-5 of 512 products' sum of magnitudes (0.8 x 0.035 each)
         assert ((out[sees][:, h].double() - v).abs() <= 2.0 ** -10 * 1.01 * v.abs() + 1e-5 * 15).all()
+
+
+@pytest.mark.parametrize("power", [0, 60, 120, 125])
+def test_a_scale_of_zero_weighs_all_alike(power):
+    """Queries up to bf16's largest, every score 0."""
+    st = ref.make(seq=[300, 20], q=[150, 20], H=2, seed=32)
+    st["q"] = (st["q"].double() * 2.0 ** power).to(torch.bfloat16)
+    st["scale"] = 0.0
+    out, lse = run(st)
+    ref.check(out, lse, ref.reference(st))
