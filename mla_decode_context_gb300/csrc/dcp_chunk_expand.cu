@@ -23,9 +23,10 @@
 //               -> images in shared memory -> bulk stores; thread = token = TMEM
 //               lane.  (By four warps for both ~3,400 cycles an item; with plain
 //               stores ~4,500, more than its MMAs' 4,096.)
-//   warp 4      weights: 16 KB bulk copies (64 latent dims of half a head's rows)
-//   warp 5      CTA 0: MMA issuer, two accumulators; CTA 1: tells CTA 0 of its
-//               weights
+//   warp 4      weights: 16 KB tensor copies (64 latent dims of half a head's rows);
+//               both CTAs' complete on CTA 0's barrier, which is what such a copy
+//               for a pair of CTAs may do and an untiled one may not
+//   warp 5      CTA 0: MMA issuer, two accumulators
 //   warp 6      TMEM allocation
 //   warps 8-11  gather of the latents (8 lanes per 128-byte line)
 // Every wait is bounded (DCP_DEVERR_TIMEOUT).
@@ -37,6 +38,7 @@
 // could be -inf, which weighs nothing.
 #include "dcp_chunk.cuh"
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -62,7 +64,7 @@ constexpr int kOffBars = kOffOut + 8 * kOutWarp;
 struct Bars {
   uint64_t a_full;            // CTA 0: both CTAs' latents are in shared memory (every loader)
   uint64_t a_free;            // both: the tiles' MMAs are complete
-  uint64_t w_full[kWStages];  // a weight stage landed: CTA 1 its half, CTA 0 both (CTA 1 tells it)
+  uint64_t w_full[kWStages];  // CTA 0: both CTAs' halves of a weight stage have landed
   uint64_t w_free[kWStages];  // both
   uint64_t acc_full[2];       // both: an accumulator is complete
   uint64_t acc_free[2];       // CTA 0: both CTAs' epilogues have read it (8 warps each)
@@ -111,7 +113,8 @@ __device__ __forceinline__ Work my_items(const ChunkArgs& a, int32_t tiles) {
 }
 
 template <bool kFp8>
-__global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_constant__ ChunkArgs a,
+                                                             const __grid_constant__ CUtensorMap weight_map) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars& bar = *reinterpret_cast<Bars*>(smem + kOffBars);
@@ -121,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
   if (threadIdx.x == 0) {
     mbar_init(&bar.a_full, 2 * kLoadThreads);
     mbar_init(&bar.a_free, 1);
-    for (uint32_t i = 0; i < kWStages; ++i) mbar_init(&bar.w_full[i], rank == 0 ? 2 : 1), mbar_init(&bar.w_free[i], 1);
+    for (uint32_t i = 0; i < kWStages; ++i) mbar_init(&bar.w_full[i], 1), mbar_init(&bar.w_free[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&bar.acc_full[i], 1), mbar_init(&bar.acc_free[i], 16);
     mbar_init(&bar.fin, 1);
     fence_mbar_init();
@@ -241,15 +244,15 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       int32_t h = work.i0 % a.heads;
       uint32_t s = 0, phase = 0, used = 0;
       const uint64_t keep = l2_keep();  // (the images that stream out would push the weights out)
-      const unsigned char* weight = static_cast<const unsigned char*>(a.weight) + static_cast<int64_t>(a.h0) * (kChunks * kWeightStage) + rank * kWHalf;
+      const uint32_t full = map_peer(smem_u32(&bar.w_full[0]), 0);
       for (int32_t i = work.i0; i < work.i1 && ok; ++i) {
-        const unsigned char* w = weight + static_cast<int64_t>(h) * (kChunks * kWeightStage);
+        const int32_t row = (a.h0 + h) * (kChunks * kUp) + static_cast<int32_t>(rank) * (kUp / 2);  // of the packed weight
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           ok = ok && mbar_wait(&bar.w_free[s], phase ^ 1);
           if (ok) {
-            mbar_arrive_expect_tx(&bar.w_full[s], kWHalf);
-            bulk_load_hint(smem + kOffW + s * kWHalf, w + c * kWeightStage, kWHalf, &bar.w_full[s], keep);
+            if (rank == 0) mbar_arrive_expect_tx(&bar.w_full[s], kWeightStage);
+            tma_load_pair(smem + kOffW + s * kWHalf, &weight_map, 0, row + c * kUp, full + 8 * s, keep);
             ++used;
           }
           if (++s == kWStages) s = 0, phase ^= 1;
@@ -257,8 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
         h = h + 1 == a.heads ? 0 : h + 1;
       }
       if (!ok) failed();
-      // nothing lands after the CTA is gone
-      for (uint32_t k = used > kWStages ? used - kWStages : 0; k < used; ++k) mbar_wait(&bar.w_full[k % kWStages], (k / kWStages) & 1);
+      // nothing lands after the CTAs are gone (neither goes before the other)
+      if (rank == 0)
+        for (uint32_t k = used > kWStages ? used - kWStages : 0; k < used; ++k) mbar_wait_cluster(&bar.w_full[k % kWStages], (k / kWStages) & 1);
     }
     __syncwarp();
   } else if (warp == 5) {
@@ -266,23 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     // (one lane, every operand a base plus constants: an issuing thread that
     // computes what its next MMA needs falls behind the tensor pipe)
     if (rank == 1) {
-      if (elected()) {
-        bool ok = true;
-        const uint32_t to = map_peer(smem_u32(&bar.w_full[0]), 0);
-        uint32_t s = 0, phase = 0;
-        for (int32_t i = work.i0; i < work.i1 && ok; ++i) {
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            ok = ok && mbar_wait(&bar.w_full[s], phase);
-            // (relaxed: this thread has written nothing, and the copy is in
-            // shared memory once its barrier says so; a release took ~1,500 cycles)
-            if (ok) mbar_arrive_remote_relaxed(to + 8 * s);
-            if (++s == kWStages) s = 0, phase ^= 1;
-          }
-        }
-        if (!ok) failed();
-        mbar_wait(&bar.fin, 0);
-      }
+      if (elected()) mbar_wait(&bar.fin, 0);
     } else if (elected()) {
       constexpr uint32_t id = idesc_bf16(256, 256, 0, 0);
       const uint64_t da = smem_desc(smem_u32(smem + kOffA), 16, 1024, kSwizzle128B);
@@ -406,7 +394,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint4* __restrict__ w, 
   *reinterpret_cast<uint4*>(packed + (row / kUp) * (kChunks * kWeightStage) + (u >> 3) * kWeightStage + image_unit(r, u & 7)) = __ldg(w + i);
 }
 
-using Kernel = void (*)(ChunkArgs);
+using Kernel = void (*)(ChunkArgs, CUtensorMap);
 
 cudaLaunchConfig_t pairs_config(int pairs, cudaStream_t st, cudaLaunchAttribute (&attr)[2]) {
   attr[0] = attr[1] = cudaLaunchAttribute{};
@@ -452,6 +440,31 @@ cudaError_t resident_pairs(Kernel kernel, bool fp8, int* pairs) {
   return cudaSuccess;
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The packed weight as rows of 64 latent dims, in boxes of a CTA's 128 rows of a
+// stage.  (The driver's entry is looked up once: the library links no libcuda.)
+cudaError_t weight_tensor(const void* packed, int32_t H, CUtensorMap* map) {
+  static const EncodeTiled encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {64, static_cast<cuuint64_t>(H) * kChunks * kUp}, strides[1] = {128};
+  const cuuint32_t box[2] = {64, kUp / 2}, steps[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(packed), dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
 }  // namespace
 
 cudaError_t launch_pack_kv_b(const void* w, int32_t H, void* packed, cudaStream_t st) {
@@ -465,12 +478,15 @@ cudaError_t launch_chunk_expand(const ChunkArgs& a, cudaStream_t st) {
   const bool fp8 = a.kv_scale != nullptr;
   const Kernel kernel = fp8 ? expand_kernel<true> : expand_kernel<false>;
   int pairs = 0;
-  const cudaError_t e = resident_pairs(kernel, fp8, &pairs);
+  cudaError_t e = resident_pairs(kernel, fp8, &pairs);
+  if (e != cudaSuccess) return e;
+  CUtensorMap weight;
+  e = weight_tensor(a.weight, a.H, &weight);
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>((a.tiles + 1) / 2) * a.heads;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = pairs_config(static_cast<int>(items < pairs ? items : pairs), st, attr);
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a, weight);
 }
 
 }  // namespace dcp
