@@ -75,7 +75,7 @@ extern "C" {
 /* Device-side error bits ORed into *dev_error. */
 #define DCP_DEVERR_BAD_BLOCK 1    /* a referenced block id is outside [0, num_blocks) */
 #define DCP_DEVERR_SEQ_TOO_LONG 2 /* seq_len > max_seq_len (clamped to max_seq_len) */
-#define DCP_DEVERR_BAD_ROWS 4     /* query_start_loc decreasing, or q_len > max_q_len */
+#define DCP_DEVERR_BAD_ROWS 4     /* query_start_loc decreasing (chunk attention: or negative), or q_len > max_q_len */
 #define DCP_DEVERR_TIMEOUT 8      /* a bounded on-device wait gave up */
 #define DCP_DEVERR_NO_BLOCKS 16   /* the free list ran out (dcp_cache_extend) */
 #define DCP_DEVERR_BAD_POSITION 32 /* a position past the cos/sin table (dcp_norm_rope_cache) */
@@ -715,20 +715,28 @@ dcp_status_t dcp_pack_kv_b(const void* w_kv_b, int32_t H, void* packed, void* st
  *                per-shard tables only).  A token without a table column or with
  *                a block id outside the cache is skipped (DCP_DEVERR_BAD_BLOCK).
  *   H            1 .. 1024.
- *   total_len    host-known bound of the sum of seq_lens (sizes the workspace).
+ *   total_len    host-known bound of the sum of seq_lens (sizes the workspace; a
+ *                loose one costs workspace, and passes once that is 4 GiB).
  *                Requests past it see nothing (DCP_DEVERR_SEQ_TOO_LONG).
  *   packed_kv_b  from dcp_pack_kv_b.
  *   out          bf16 (round to nearest even) or fp32 [T, H, 128], dense,
  *                16-byte aligned; lse fp32 [T, H].
  *   workspace    16-byte aligned; its contents on entry are ignored.
- *                dcp_chunk_attention_workspace_size(...) bytes for the fewest
- *                passes over the heads (4 GiB at most, or what one head takes);
- *                with less, down to one head's part, more passes are made.
+ *                dcp_chunk_attention_workspace_size(...) bytes hold what the
+ *                heads share (16 KB per 128 tokens), keys and values of as many
+ *                heads as fit in 4 GiB (one at least; 64 KB per 128 tokens each)
+ *                and the outputs of cut units; the call makes as many passes
+ *                over the heads as that takes.  With less, down to one head's
+ *                part, it makes more.
  *                Calls that may overlap need one each.
  *
  * Numbers: values, and keys of requests of more than 1,024 tokens, are rounded
- * to f16 once (keys of shorter ones are kept to 22 bits; f16's steps are 2^-24
- * below 2^-14), and so are the softmax weights (relative to a running maximum);
+ * to f16 once (f16's steps are 2^-24 below 2^-14), and so are the softmax weights
+ * (relative to a running maximum).  A key's rounding shifts its score by at most
+ * 2^-11 scale sum |q k|, ~2e-4 as a rule, and the log-sum-exp of a row that sees
+ * little but that token by as much; of a row whose weight is spread over n tokens,
+ * by that over the root of n.  Requests of up to 1,024 tokens keep keys to 22 bits.
+ * Queries are f16 after a power of 2 that brings a row's largest element to 1 to 4;
  * everything else is fp32.  An FP8 code times a scale that is no power of two is
  * rounded to bf16.  A NaN score makes the rows that see its token NaN, and no
  * others; so does a projected key or value with an element that is not finite or

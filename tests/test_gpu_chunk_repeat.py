@@ -52,3 +52,36 @@ def test_packed_weights_of_several_layers_in_one_graph():
     torch.cuda.synchronize()
     for (o, l), (wo, wl) in zip(got, want):
         assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+def test_calls_from_two_threads():
+    """Threads of their own streams and workspaces; the second's first call is its first
+    use of the GPU."""
+    import threading
+    st = [ref.make(seq=[2500, 77], q=[50, 77], H=3, seed=43 + i) for i in range(2)]
+    packed = [dcp.pack_kv_b(s["w"]) for s in st]
+
+    def call(i, **kw):
+        s = st[i]
+        return dcp.chunk_attention(s["q"], s["cache"], s["table"], s["seq"], s["qsl"], packed[i], scale=s["scale"],
+                                   total_len=s["total"], **kw)
+    want = [call(i) for i in range(2)]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(20):
+                o, l = call(i, stream=stream)
+                stream.synchronize()
+                if not (torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])):
+                    failed.append(i)
+        except Exception as e:  # (a thread's exception is not the test's)
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed

@@ -56,3 +56,31 @@ def test_passes_of_unequal_heads_with_units_in_pieces(heads):
     again = run(st, workspace=ws)
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
     tight_check(*run(st), want)
+
+
+@pytest.mark.parametrize("L", [1000, 1200, 4000])
+def test_a_row_that_sees_little_but_one_token(L):
+    """Keys of requests of more than 1,024 tokens are off by half a step of f16, 2^-11 of
+    an element: a row that attends to one token has all of that in its log-sum-exp,
+    and no more; shorter requests' keys are off by 2^-22."""
+    st = ref.make(seq=[L], q=[6], H=2, bs=64, seed=54)
+    st["scale"] = 1.0
+    kv = ref.latents(st, ref.rows_of(st, 0))
+    for h in range(2):  # queries along one token's keys
+        k = kv[:, :512] @ st["w"][256 * h:256 * h + 128].double().T
+        for r in range(6):
+            t = (37 + 157 * r) % (L - 6)
+            st["q"][r, h, :128] = k[t].to(torch.bfloat16)
+            st["q"][r, h, 128:] = kv[t, 512:].to(torch.bfloat16)
+    out, lse = run(st)
+    for h in range(2):
+        k = torch.cat([kv[:, :512] @ st["w"][256 * h:256 * h + 128].double().T, kv[:, 512:]], 1)
+        q = st["q"][:, h].double()
+        s = (q @ k.T).masked_fill(torch.arange(L, device="cuda")[None, :] > L - 6 + torch.arange(6, device="cuda")[:, None], -torch.inf)
+        z = torch.logsumexp(s, 1)
+        top = s.argmax(1)
+        assert (torch.exp(s.amax(1) - z) > 0.99).all()
+        size = (q[:, :128] * k[top, :128]).abs().sum(1)
+        # fp32 sums of 192 products: 12 steps (20 with remainders), 2^-23 of up to the whole sum each
+        bound = size * (2.0 ** -11 if L > 1024 else 2.0 ** -22) + 20 * 2.0 ** -23 * (q * k[top]).abs().sum(1) + 2.0 ** -20 * z.abs()
+        assert ((lse[:, h].double() - z).abs() <= bound).all()
