@@ -742,7 +742,7 @@ dcp_status_t dcp_pack_kv_b(const void* w_kv_b, int32_t H, void* packed, void* st
  * others; so does a projected key or value with an element that is not finite or
  * past f16's largest, 65,504.  (An infinite rope element makes its token's scores
  * what the arithmetic makes them: NaN or +inf, and the row NaN, or -inf, and the
- * token weighs nothing.)  A row whose largest score is past 2e7 in magnitude (fp32 keeps
+ * token weighs nothing.)  A row whose largest score is past 2.3e7 in magnitude (fp32 keeps
  * no digit behind the point there; -inf too) is NaN; scores that far below the
  * largest weigh nothing.
  *

@@ -64,10 +64,10 @@ constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLift = 6.0f;
 // s c - m in one rounding leaves what m lost by its own: at most 1 up to here, and
 // past it more than f16 takes.  (Taking the maximum off before scaling has no
-// such end, and cost 7 % of the time.)  While a row's maximum is below -kFarthest,
-// its scores weigh 0, as they do next to any above it, and a row that sees no
-// others is NaN.  A piece of a cut unit cannot know: its log-sum-exp is kFar,
-// which the join takes for NaN where no piece has more.
+// such end, and cost 7 % of the time.)  A maximum below -kFarthest counts as that: what
+// lies there weighs nothing beside any score that may still come, and a row that
+// sees no others is NaN.  A piece of a cut unit cannot know: its log-sum-exp is
+// kFar, which the join takes for NaN where no piece has more.
 constexpr float kFarthest = 33554432.0f;
 constexpr float kFar = -3.402823466e38f;  // (the lowest finite number; no log-sum-exp comes near it)
 
@@ -449,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     bool far = false;  // sees tokens, and all their scores are below -kFarthest
     if (m <= -kFarthest) far = sees_any(a.valid + bar.piece.image, tiles, L - bar.piece.j0 * kChunkTile);
     const bool cut = bar.piece.pieces > 1;
+    if (far && cut && l == l) l = 0.f;  // (some may lie just below)
     if (nan_row || m > kFarthest || (far && !cut)) l = __int_as_float(0x7fc00000);
     const float inv = tiles > 0 && l != 0.f ? 1.0f / l : 0.f;
     const float lse = tiles > 0 && l != 0.f ? (m - kLift + log2f(l)) * kLn2 : far ? kFar : -INFINITY;

@@ -85,3 +85,21 @@ def test_a_scale_of_zero_weighs_all_alike(power):
     st["scale"] = 0.0
     out, lse = run(st)
     ref.check(out, lse, ref.reference(st))
+
+
+@pytest.mark.parametrize("L", [1300, 4000])  # in one piece, in pieces
+@pytest.mark.parametrize("past", [-40.0, -4.0, 0.0])
+def test_rows_at_the_border_are_nan_in_pieces_too(L, past):
+    """All scores (the same for every token) within a few units of the border, 2^25 in
+    base 2, on its far side."""
+    st = ref.make(seq=[L], q=[2], H=1, bs=64, seed=33)
+    st["q"].zero_()
+    st["cache"].view(-1, 576)[:, 512] = -1
+    st["q"][:, :, 128] = 2.0 ** 12
+    st["scale"] = (2.0 ** 25 - past) / 2.0 ** 12 / math.log2(math.e)
+    # the factor of a score: fp32 product of the scale and log2 e, off by 2 x 2^-24 of it: 4 at 2^25
+    out, lse = run(st)
+    if past < -4:
+        assert out.isnan().all() and lse.isnan().all()
+    else:  # either side
+        assert torch.equal(out.isnan(), out.isnan()[:1, :1, :1].expand_as(out)) and torch.equal(out.isnan()[..., 0], lse.isnan())
