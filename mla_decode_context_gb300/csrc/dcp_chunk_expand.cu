@@ -12,11 +12,12 @@
 // tokens and half of a head's rows from either's shared memory, so that each
 // streams 32 bytes of weights a clock instead of 64.
 //
-// 24,000 tokens at 128 heads: ~540 us, 1.5 PFLOP/s (78 % of the measured rate),
-// 2.9 TB/s of stores.  What bounds it: the weights' loads, 16 KB each and four in
-// flight, take 1,500-3,000 cycles next to the images' stores to DRAM (an item
-// 6,000-6,500 cycles; without the stores 4,105, its MMAs' 4,096).  A fifth stage,
-// or stores by another path, changed nothing.  (A CTA by itself: 851 us.)
+// 24,000 tokens at 128 heads: ~540 us, 1.5 PFLOP/s (77 % of what a library product
+// was measured at), 2.9 TB/s of stores.  What bounds it: the weights' loads, 16 KB
+// each and four in flight, wait behind the images' stores to DRAM: the tensor pipe is
+// busy 64 % of the time (333 us for 12 mixed requests at 16 heads), and without the
+// stores an item took 4,105 cycles, its MMAs' 4,096.  A fifth stage, or stores by
+// another path, changed nothing.  (A CTA by itself: 851 us.)
 //
 // Warp roles (512 threads in each CTA of the pair):
 //   warps 0-3, 12-15  epilogue of the keys and of the values: accumulator -> f16

@@ -12,17 +12,20 @@
 // with the row's power-of-two scale (dcp_concat_cache.cu), taken from the fp32
 // values.
 //
-// Bound by bytes, and for one token by one round trip to memory, so the work
+// Few operations a byte, and for one token one round trip to memory, so the work
 // is cut into warps without shared memory or barriers: one warp per cache row
 // (16 latent values a lane, the rope part on lanes 0-7; the sum of squares and
 // the maximum are warp reductions), one per four decode-query heads (eight
 // rounds of 16-byte units of ql_nope, and one in which lane = (head, rope
 // unit): its angles are loaded once), or one per 16 heads of a chunk's queries
 // (rope parts alone, four rounds with the same angles).  A pair that is 32
-// dims apart lies four lanes apart.  256 tokens with 128 heads into an FP8 cache
-// (76 MB): 13.8 us, 5.5 TB/s; the rope parts of 4,099 tokens' 128 heads in pieces
-// of 128 bytes (145 MB): 28.4 us, 5.1 TB/s; 16,381 rows alone: 13.3 us, the
-// memory's latency over 1.7 waves.
+// dims apart lies four lanes apart.  What bounds it is the latency of two
+// dependent trips to memory (position, then angles) under the warps that fit: 56
+// registers a thread, 64 with split halves, so nine or eight CTAs, 36 or 32 warps, an
+// SM.  256 tokens with 128 heads into an FP8 cache (76 MB read and written): 14 us,
+// of which DRAM is busy a third (the output stays in L2); the rope parts of 4,099
+// tokens' 128 heads in pieces of 128 bytes (145 MB): 28 us, DRAM 44 % busy; 16,381
+// rows alone: 13-14 us, three waves of warps, DRAM 20 % busy.
 #include "dcp_kernels.h"
 
 #include <cuda_fp8.h>
