@@ -71,7 +71,6 @@ struct Bars {
   uint64_t acc_free[2];       // CTA 0: both CTAs' epilogues have read it (8 warps each)
   uint64_t fin;               // both: the issuer's MMAs are complete
   uint32_t tmem;
-  int32_t lo[4];              // the last tiles' key remainders (-1: none), tile by tile
 };
 constexpr int kSmemBytes = kOffBars + static_cast<int>(sizeof(Bars)) + 1024;
 static_assert(kSmemBytes <= 232448, "exceeds the 227 KB of shared memory per CTA");
@@ -99,6 +98,19 @@ __device__ __forceinline__ int64_t cache_row(const ChunkArgs& a, int32_t b, int3
   }
   if (a.dev_error) atomicOr(a.dev_error, DCP_DEVERR_BAD_BLOCK);
   return -1;
+}
+
+// A tile of a request's tokens, and its key remainders (-1: none).  By the whole warp.
+struct TileOf {
+  int32_t b, index, lo;
+};
+__device__ __forceinline__ TileOf tile_of(const ChunkArgs& a, int32_t tile) {
+  TileOf t;
+  t.b = find_range(a.tile_start, a.B, tile);
+  t.index = tile - a.tile_start[t.b];
+  const int32_t lo = a.lo_start[t.b];
+  t.lo = lo >= 0 ? lo + t.index : -1;
+  return t;
 }
 
 struct Work {
@@ -163,16 +175,16 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
     unsigned char* images = part ? a.values : a.keys;
     const uint64_t stream = l2_stream();
     int32_t pair = work.i0 / a.heads, h = work.i0 - pair * a.heads;
-    uint32_t tile_count = 0;
+    int32_t lo = -1;
     for (int32_t i = work.i0, n = 0; i < work.i1; ++i, ++n) {
       const int acc = n & 1;
+      const int32_t tile = 2 * pair + static_cast<int32_t>(rank);
+      if (!part && (n == 0 || h == 0)) lo = tile < tiles ? tile_of(a, tile).lo : -1;
       if (!mbar_wait_warp(&bar.acc_full[acc], (n >> 1) & 1)) { failed(); break; }
       tc_fence_after();
-      const int32_t tile = 2 * pair + static_cast<int32_t>(rank);
       const int64_t slot = static_cast<int64_t>(h) * a.tiles + tile;
       const uint32_t col = tmem + (static_cast<uint32_t>(quad) << 21) + 256u * acc + 128u * part;
       uint32_t v[64];  // 128 dims as f16 pairs
-      const int32_t lo = part ? -1 : bar.lo[tile_count & 3];
 #pragma unroll 1
       for (int turn = 0; turn < 1 + (lo >= 0); ++turn) {  // (keys of short requests: then what their rounding left)
 #pragma unroll
@@ -232,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
           }
         }
       }
-      if (++h == a.heads) h = 0, ++pair, ++tile_count;
+      if (++h == a.heads) h = 0, ++pair;
     }
     if (elected()) bulk_wait<0>();
     __syncwarp();
@@ -326,13 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       const int32_t tile = 2 * last + static_cast<int32_t>(rank);
       // this thread's token (a tile past the last is all zeros)
       int64_t src = -1;
-      int32_t lo = -1;
       if (tile < tiles) {
-        const int32_t b = find_range(a.tile_start, a.B, tile);
-        lo = a.lo_start[b];
-        if (lo >= 0) lo += tile - a.tile_start[b];
-        const int64_t p = static_cast<int64_t>(tile - a.tile_start[b]) * kChunkTile + 32 * lw + lane;
-        if (p < a.seq_lens[b]) src = cache_row(a, b, static_cast<int32_t>(p));
+        const TileOf of = tile_of(a, tile);
+        const int64_t p = static_cast<int64_t>(of.index) * kChunkTile + 32 * lw + lane;
+        if (p < a.seq_lens[of.b]) src = cache_row(a, of.b, static_cast<int32_t>(p));
       }
       const float scale = kFp8 && src >= 0 ? __ldg(a.kv_scale + src) : 0.f;
       // what the heads share is written with the first head
@@ -340,7 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
       const uint32_t live = __ballot_sync(0xffffffffu, src >= 0);
       if (shared_too && lane == 0) reinterpret_cast<uint32_t*>(a.valid + tile)[lw] = live;
       if (loads > 0 && !mbar_wait_warp(&bar.a_free, (loads - 1) & 1)) { failed(); break; }
-      if (threadIdx.x == 8 * 32) bar.lo[loads & 3] = lo;
       ++loads;
       const int u = lane & 7;
 #pragma unroll 2
