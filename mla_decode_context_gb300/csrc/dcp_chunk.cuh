@@ -12,9 +12,11 @@
 // Keys, values, queries and softmax weights are f16 (rope dims: bf16, as they
 // come): 11 significant bits to bf16's 8, at the same rate.  A key's rounding
 // shifts its score by ~2e-4 (bf16: ~1.5e-3), and the log-sum-exp by that over the
-// root of the number of tokens that carry it.  Where those can be few, in
-// requests of up to kFineLen tokens, keys are f16 pairs, the value and its
-// rounding's remainder, at 1.4 times the MMAs: 22 bits.
+// root of the number of tokens that carry it.  In requests of up to kFineLen tokens,
+// where those are few more often, keys are f16 pairs, the value and its rounding's
+// remainder, at 1.4 times the MMAs: 22 bits.  (A row of a longer request that sees
+// little but one token has all of that token's 2e-4; its weights come too late to
+// choose by.)
 #pragma once
 
 #include "dcp_kernels.h"
